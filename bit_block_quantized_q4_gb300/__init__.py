@@ -9,6 +9,7 @@ raises.  Build it with ``python -m bit_block_quantized_q4_gb300.build`` (or
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -32,7 +33,11 @@ EXPORTS = ("q4k_abi_version", "q4k_status_str", "q4k_dequant", "q4k_gemv", "q4k_
            "q4k_moe_workspace_size", "q4k_moe_workspace_views", "q4k_moe_gemv",
            "q4k_moe_gemv_ex", "q4k_moe_gemv_noalloc", "q4k_moe_prefill",
            "q4k_moe_prefill_workspace_size",
+           "q4k_kv_plan", "q4k_kv_write", "q4k_paged_attn", "q4k_paged_attn_workspace_size",
+           "q4k_add_rmsnorm", "q4k_sample",
            "q4k_get_device_error", "q4k_selftest_wait_timeout")
+Q4K_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2}
+Q4K_KV_OK, Q4K_KV_NO_PAGES, Q4K_KV_BAD_LENGTH, Q4K_KV_NO_SLOTS = 0, 1, 2, 3
 
 _lock = threading.Lock()
 _lib = None
@@ -106,6 +111,22 @@ def lib() -> ctypes.CDLL:
         L.q4k_moe_gemv_noalloc.restype = ctypes.c_int
         L.q4k_moe_gemv_noalloc.argtypes = [P, P, P, I64, I32, I64, I64, P, I32, I64, P, P, I32, P,
                                            I64, P]
+        F32 = ctypes.c_float
+        L.q4k_kv_plan.restype = ctypes.c_int
+        L.q4k_kv_plan.argtypes = [P, P, I32, P, I64, I32, I32, P, I32, P, P, P, P, P, I64, P, P, P]
+        L.q4k_kv_write.restype = ctypes.c_int
+        L.q4k_kv_write.argtypes = [P, P, ctypes.c_int, I64, I64, P, I64, I32, I32, P, P, ctypes.c_int,
+                                   I64, I32, I64, I64, I64, P, P, P]
+        L.q4k_paged_attn_workspace_size.restype = SZ
+        L.q4k_paged_attn_workspace_size.argtypes = [I32, I32, I32, I32]
+        L.q4k_paged_attn.restype = ctypes.c_int
+        L.q4k_paged_attn.argtypes = [P, I64, I64, I32, I32, I32, I32, P, P, ctypes.c_int, I64, I32, I64,
+                                     I64, I64, P, P, P, I64, I32, P, F32, I32, P, I64, P, P, SZ, P]
+        L.q4k_add_rmsnorm.restype = ctypes.c_int
+        L.q4k_add_rmsnorm.argtypes = [P, ctypes.c_int, I64, P, ctypes.c_int, I64, P, F32, I64, I64, P,
+                                      ctypes.c_int, I64, P, I64, P, I64, P]
+        L.q4k_sample.restype = ctypes.c_int
+        L.q4k_sample.argtypes = [P, ctypes.c_int, I64, I64, I64, P, P, P, P, P, P, P, P]
         L.q4k_get_device_error.restype = ctypes.c_int
         L.q4k_get_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
         L.q4k_selftest_wait_timeout.restype = ctypes.c_int
@@ -350,6 +371,202 @@ def q4k_moe_gemv_noalloc(w_gate, w_up, w_down, expert_stride: int, n_experts: in
                                       _ptr(wts), top_k, _ptr(out), out.stride(0), _stream(stream)),
            "q4k_moe_gemv_noalloc")
     return out
+
+
+def _want(what: str, t, shape, dtypes, strided: bool = False) -> None:
+    """Raise Q4KError (Q4K_ERR_SHAPE) unless t has this shape (None: any size), one of
+    these types, and is contiguous (strided: its last dimension is)."""
+    ok = t.dim() == len(shape) and t.dtype in dtypes and \
+        all(a is None or a == b for a, b in zip(shape, t.shape)) and \
+        ((t.stride(-1) == 1 or t.shape[-1] <= 1) if strided else t.is_contiguous())
+    if not ok:
+        raise Q4KError(2, f"{what} is {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+
+
+def _ld(t, dim: int = 0) -> int:
+    """Stride of a dimension as the C ABI wants it: that of a dimension of size 1 is never used and
+    may be anything in torch, so it is given as if the tensor were contiguous."""
+    if t.shape[dim] != 1:
+        return t.stride(dim)
+    return max((t.stride(i) * t.shape[i] for i in range(dim + 1, t.dim())), default=1)
+
+
+_I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+class _alloc_on:
+    """Outputs and workspaces that a call makes belong to the stream it runs on (the
+    allocator may otherwise hand them out again while the call still uses them)."""
+
+    def __new__(cls, stream):
+        if stream is None:
+            return contextlib.nullcontext()
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        return torch.cuda.stream(stream)
+
+
+def q4k_kv_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool: torch.Tensor,
+                pool_state: torch.Tensor, page_size: int, n_slots: int, out=None, stream=None):
+    """Block tables and slot maps of a step from request lengths (int32 tensors): lens, add [n] (-1:
+    finished), table [n, max_pages] and pool [pages] (both updated in place), pool_state [2].
+    Returns (lens_out [n], cu [n + 1] int64, slots [n_slots], pos [n_slots], status [n],
+    pool_state_out [2]); out gives these six tensors (lens and pool_state may be among them)."""
+    n = lens.shape[0] if lens.dim() == 1 else -1
+    _want("lens", lens, (n,), _I32)
+    _want("add", add, (n,), _I32)
+    _want("table", table, (n, None), _I32, strided=True)
+    _want("pool", pool, (None,), _I32)
+    _want("pool_state", pool_state, (2,), _I32)
+    if out is None:
+        with _alloc_on(stream):
+            new = torch.empty(2 * n + 2 * n_slots + 2, dtype=torch.int32, device=lens.device)
+            cu = torch.empty(n + 1, dtype=torch.int64, device=lens.device)
+        lens_out, status, slots, pos, state_out = new.split((n, n, n_slots, n_slots, 2))
+    else:
+        lens_out, cu, slots, pos, status, state_out = out
+        _want("lens_out", lens_out, (n,), _I32)
+        _want("cu", cu, (n + 1,), (torch.int64,))
+        _want("slots", slots, (n_slots,), _I32)
+        _want("pos", pos, (n_slots,), _I32)
+        _want("status", status, (n,), _I32)
+        _want("pool_state_out", state_out, (2,), _I32)
+    _check(lib().q4k_kv_plan(_ptr(lens), _ptr(add), n, _ptr(table), _ld(table), table.shape[1],
+                             page_size, _ptr(pool), pool.shape[0], _ptr(pool_state), _ptr(lens_out),
+                             _ptr(cu), _ptr(slots), _ptr(pos), n_slots, _ptr(status),
+                             _ptr(state_out), _stream(stream)), "q4k_kv_plan")
+    return lens_out, cu, slots, pos, status, state_out
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale):
+    """(pages, heads, page size, dim) of the two cache buffers and their strides, after checking them."""
+    if k_cache.dim() != 4:
+        raise Q4KError(2, f"k_cache has {k_cache.dim()} dimensions, not [pages, heads, page size, dim]")
+    shape = k_cache.shape
+    _want("k_cache", k_cache, shape, (torch.bfloat16, torch.float8_e4m3fn), strided=True)
+    _want("v_cache", v_cache, shape, (k_cache.dtype,), strided=True)
+    strides = [_ld(k_cache, i) for i in range(3)]
+    if strides != [_ld(v_cache, i) for i in range(3)]:
+        raise Q4KError(2, "k_cache and v_cache have different strides")
+    if k_cache.dtype == torch.float8_e4m3fn and k_scale is not None and v_scale is not None:
+        _want("k_scale", k_scale, shape[:3], _F32)
+        _want("v_scale", v_scale, shape[:3], _F32)
+    return shape, strides
+
+
+def q4k_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                 v_cache: torch.Tensor, k_scale=None, v_scale=None, stream=None) -> None:
+    """Write rows k, v [tokens, heads, dim] (fp32 or bf16, same strides) to the slots [tokens] int32
+    (-1: skip) of the paged caches [pages, heads, page size, dim], bf16 or e4m3 (then with scales
+    [pages, heads, page size] fp32)."""
+    (pages, heads, page, dim), strides = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    tokens = slots.shape[0] if slots.dim() == 1 else -1
+    _want("slots", slots, (tokens,), _I32)
+    _want("k", k, (tokens, heads, dim), _FLOATS, strided=True)
+    _want("v", v, (tokens, heads, dim), (k.dtype,), strided=True)
+    if (_ld(k), _ld(k, 1)) != (_ld(v), _ld(v, 1)):
+        raise Q4KError(2, "k and v have different strides")
+    _check(lib().q4k_kv_write(_ptr(k), _ptr(v), Q4K_DTYPE[k.dtype], _ld(k), _ld(k, 1),
+                              _ptr(slots), tokens, heads, dim, _ptr(k_cache), _ptr(v_cache),
+                              Q4K_DTYPE[k_cache.dtype], pages, page, *strides, _ptr(k_scale),
+                              _ptr(v_scale), _stream(stream)), "q4k_kv_write")
+
+
+def q4k_paged_attn_workspace_size(n: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    return int(lib().q4k_paged_attn_workspace_size(n, q_heads, kv_heads, dim))
+
+
+def q4k_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   table: torch.Tensor, lens: torch.Tensor, softmax_scale: float, k_scale=None,
+                   v_scale=None, window: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token per request: q [n, q_heads, dim] bf16 over the paged caches
+    [pages, kv_heads, page size, dim] (bf16, or e4m3 with scales) by table [n, max_pages] and lens
+    [n] int32.  Returns (out [n, q_heads, dim] bf16, lse [n, q_heads] fp32)."""
+    (pages, heads, page, dim), strides = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    n, q_heads = q.shape[:2] if q.dim() == 3 else (-1, -1)
+    _want("q", q, (n, q_heads, dim), _BF16, strided=True)
+    _want("table", table, (n, None), _I32, strided=True)
+    _want("lens", lens, (n,), _I32)
+    L = lib()
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty((n, q_heads, dim), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((n, q_heads), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(max(L.q4k_paged_attn_workspace_size(n, q_heads, heads, dim), 16),
+                                    dtype=torch.uint8, device=q.device)
+    _want("out", out, (n, q_heads, dim), _BF16, strided=True)
+    _want("lse", lse, (n, q_heads), _F32)
+    if _ld(out, 1) != dim:
+        raise Q4KError(2, f"out has head stride {out.stride(1)}, not {dim}")
+    _check(L.q4k_paged_attn(_ptr(q), _ld(q), _ld(q, 1), n, q_heads, heads, dim, _ptr(k_cache),
+                            _ptr(v_cache), Q4K_DTYPE[k_cache.dtype], pages, page, *strides,
+                            _ptr(k_scale), _ptr(v_scale), _ptr(table), _ld(table),
+                            table.shape[1], _ptr(lens), softmax_scale, window, _ptr(out),
+                            _ld(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                            _stream(stream)), "q4k_paged_attn")
+    return out, lse
+
+
+def q4k_add_rmsnorm(x: torch.Tensor, residual, gamma: torch.Tensor, eps: float,
+                    out_dtype=torch.bfloat16, out=None, residual_out=None, scales=None, stream=None):
+    """h = x + residual; y = h * gamma / sqrt(mean(h^2) + eps) for x, residual [m, hidden] fp32 or
+    bf16 (residual may be None).  Returns (y, residual_out) with y bf16, or (y, residual_out, scales)
+    with y e4m3 (out_dtype torch.float8_e4m3fn) and scales [m, ceil(hidden / 128)] fp32; residual_out
+    may be residual itself, and is None where residual is."""
+    m, hidden = x.shape if x.dim() == 2 else (-1, -1)
+    _want("x", x, (m, hidden), _FLOATS, strided=True)
+    _want("gamma", gamma, (hidden,), _F32)
+    if residual is not None:
+        _want("residual", residual, (m, hidden), _FLOATS, strided=True)
+    e4m3 = (out_dtype if out is None else out.dtype) == torch.float8_e4m3fn
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty((m, hidden), dtype=out_dtype, device=x.device)
+        if residual_out is None and residual is not None:
+            residual_out = torch.empty((m, hidden), dtype=residual.dtype, device=x.device)
+        if scales is None and e4m3:
+            scales = torch.empty((m, (hidden + 127) // 128), dtype=torch.float32, device=x.device)
+    _want("out", out, (m, hidden), (torch.bfloat16, torch.float8_e4m3fn), strided=True)
+    if residual is not None:
+        _want("residual_out", residual_out, (m, hidden), (residual.dtype,), strided=True)
+    if e4m3:
+        _want("scales", scales, (m, (hidden + 127) // 128), _F32, strided=True)
+    _check(lib().q4k_add_rmsnorm(
+        _ptr(x), Q4K_DTYPE[x.dtype], _ld(x), _ptr(residual),
+        1 if residual is None else Q4K_DTYPE[residual.dtype], 0 if residual is None else _ld(residual),
+        _ptr(gamma), eps, m, hidden, _ptr(out), Q4K_DTYPE[out.dtype], _ld(out),
+        None if residual is None else _ptr(residual_out),
+        0 if residual is None else _ld(residual_out), _ptr(scales) if e4m3 else None,
+        _ld(scales) if e4m3 else 0, _stream(stream)), "q4k_add_rmsnorm")
+    return (out, residual_out, scales) if e4m3 else (out, residual_out)
+
+
+def q4k_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None,
+               min_p=None, out=None, logp=None, stream=None):
+    """Choose a token per row of logits [rows, vocab] (fp32 or bf16) from the random numbers u [rows]
+    fp32 in [0, 1); temperature, top_p, min_p (fp32) and top_k (int32) are [rows] or None (1, off).
+    Returns (token [rows] int32, logp [rows] fp32)."""
+    rows, vocab = logits.shape if logits.dim() == 2 else (-1, -1)
+    _want("logits", logits, (rows, vocab), _FLOATS, strided=True)
+    _want("u", u, (rows,), _F32)
+    for name, t, kind in (("temperature", temperature, _F32), ("top_k", top_k, _I32),
+                          ("top_p", top_p, _F32), ("min_p", min_p, _F32)):
+        if t is not None:
+            _want(name, t, (rows,), kind)
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        if logp is None:
+            logp = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _want("out", out, (rows,), _I32)
+    _want("logp", logp, (rows,), _F32)
+    _check(lib().q4k_sample(_ptr(logits), Q4K_DTYPE[logits.dtype], rows, vocab, _ld(logits),
+                            _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                            _ptr(out), _ptr(logp), _stream(stream)), "q4k_sample")
+    return out, logp
 
 
 def q4k_get_device_error(stream=None) -> int:

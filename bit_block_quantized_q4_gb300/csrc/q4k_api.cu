@@ -565,6 +565,183 @@ int q4k_moe_gemv_noalloc(const void *w_gate, const void *w_up, const void *w_dow
                                        static_cast<cudaStream_t>(stream)));
 }
 
+int q4k_kv_plan(const int32_t *lens, const int32_t *add, int32_t n, int32_t *table, int64_t ldt,
+                int32_t max_pages, int32_t page_size, int32_t *pool, int32_t pool_size,
+                const int32_t *pool_state, int32_t *lens_out, int64_t *cu, int32_t *slots,
+                int32_t *pos, int64_t n_slots, int32_t *status, int32_t *pool_state_out,
+                void *stream) {
+  if (n < 0 || n > 65536 || max_pages <= 0 || page_size <= 0 || pool_size <= 0 || n_slots < 0 ||
+      n_slots > INT32_MAX || ldt < max_pages || (int64_t)pool_size * page_size > INT32_MAX)
+    return Q4K_ERR_SHAPE;
+  if (n == 0) return Q4K_OK;
+  if (!lens || !add || !table || !pool || !pool_state || !lens_out || !cu || !status ||
+      !pool_state_out || (n_slots > 0 && (!slots || !pos)))
+    return Q4K_ERR_NULL;
+  if (!aligned(lens, 4) || !aligned(add, 4) || !aligned(table, 4) || !aligned(pool, 4) ||
+      !aligned(pool_state, 4) || !aligned(lens_out, 4) || !aligned(cu, 8) || !aligned(slots, 4) ||
+      !aligned(pos, 4) || !aligned(status, 4) || !aligned(pool_state_out, 4))
+    return Q4K_ERR_ALIGN;
+  int st = check_device();
+  if (st != Q4K_OK) return st;
+  st = check_device_memory({lens, add, table, pool, pool_state, lens_out, cu, slots, pos, status,
+                            pool_state_out});
+  if (st != Q4K_OK) return st;
+  return map_launch(launch_kv_plan(lens, add, n, table, ldt, max_pages, page_size, pool, pool_size,
+                                   pool_state, lens_out, cu, slots, pos, n_slots, status,
+                                   pool_state_out, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// The cache arguments that q4k_kv_write and q4k_paged_attn share.  Strides are
+// in elements, multiples of 16 bytes; no stride may make rows overlap.
+int check_cache(int32_t kv_heads, int32_t dim, int cache_dtype, int64_t n_pages, int32_t page_size,
+                int64_t page_stride, int64_t head_stride, int64_t token_stride) {
+  if (dim != 64 && dim != 128 && dim != 256) return Q4K_ERR_SHAPE;
+  if (cache_dtype != Q4K_DTYPE_BF16 && cache_dtype != Q4K_DTYPE_E4M3) return Q4K_ERR_SHAPE;
+  if (kv_heads <= 0 || kv_heads > 1024 || n_pages <= 0 || page_size <= 0 ||
+      n_pages > INT32_MAX / page_size)
+    return Q4K_ERR_SHAPE;
+  // the longest of the three strides has to step over all of the next, and so on
+  const int64_t kMax = (int64_t)1 << 40;
+  if (page_stride < dim || head_stride < dim || token_stride < dim || page_stride > kMax ||
+      head_stride > kMax || token_stride > kMax)
+    return Q4K_ERR_SHAPE;
+  const int64_t inner = head_stride > token_stride ? token_stride * page_size : head_stride * kv_heads;
+  const int64_t outer = head_stride > token_stride ? head_stride * kv_heads : token_stride * page_size;
+  if ((kv_heads > 1 && page_size > 1 && (head_stride > token_stride ? head_stride : token_stride) < inner) ||
+      (n_pages > 1 && page_stride < (kv_heads > 1 && page_size > 1 ? outer : kv_heads > 1 ? head_stride * kv_heads : token_stride * page_size)))
+    return Q4K_ERR_SHAPE;
+  const int64_t unit = cache_dtype == Q4K_DTYPE_BF16 ? 8 : 16;
+  if (page_stride % unit || head_stride % unit || token_stride % unit) return Q4K_ERR_ALIGN;
+  return Q4K_OK;
+}
+}  // namespace
+
+int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, int64_t ld_head,
+                 const int32_t *slots, int64_t tokens, int32_t kv_heads, int32_t dim, void *k_cache,
+                 void *v_cache, int cache_dtype, int64_t n_pages, int32_t page_size,
+                 int64_t page_stride, int64_t head_stride, int64_t token_stride, float *k_scale,
+                 float *v_scale, void *stream) {
+  if (in_dtype != Q4K_DTYPE_FP32 && in_dtype != Q4K_DTYPE_BF16) return Q4K_ERR_SHAPE;
+  int st = check_cache(kv_heads, dim, cache_dtype, n_pages, page_size, page_stride, head_stride,
+                       token_stride);
+  if (st != Q4K_OK) return st;
+  if (tokens < 0 || tokens > INT32_MAX / kv_heads || ld_head < dim || ld_token < 0)
+    return Q4K_ERR_SHAPE;
+  if (tokens == 0) return Q4K_OK;
+  const bool e4m3 = cache_dtype == Q4K_DTYPE_E4M3;
+  if (!k || !v || !slots || !k_cache || !v_cache || (e4m3 && (!k_scale || !v_scale)))
+    return Q4K_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || ld_token % 8 || ld_head % 8)
+    return Q4K_ERR_ALIGN;
+  st = check_device();
+  if (st != Q4K_OK) return st;
+  st = check_device_memory({k, v, slots, k_cache, v_cache, e4m3 ? k_scale : nullptr,
+                            e4m3 ? v_scale : nullptr});
+  if (st != Q4K_OK) return st;
+  return map_launch(launch_kv_write(k, v, in_dtype, ld_token, ld_head, slots, tokens, kv_heads, dim,
+                                    k_cache, v_cache, cache_dtype, n_pages, page_size, page_stride,
+                                    head_stride, token_stride, k_scale, v_scale,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+size_t q4k_paged_attn_workspace_size(int32_t n, int32_t q_heads, int32_t kv_heads, int32_t dim) {
+  if (n < 0 || q_heads <= 0 || kv_heads <= 0 || dim <= 0) return 0;
+  return paged_attn_workspace_size(n, q_heads, kv_heads, dim);
+}
+
+int q4k_paged_attn(const void *q, int64_t ldq, int64_t ldq_head, int32_t n, int32_t q_heads,
+                   int32_t kv_heads, int32_t dim, const void *k_cache, const void *v_cache,
+                   int cache_dtype, int64_t n_pages, int32_t page_size, int64_t page_stride,
+                   int64_t head_stride, int64_t token_stride, const float *k_scale,
+                   const float *v_scale, const int32_t *table, int64_t ldt, int32_t max_pages,
+                   const int32_t *lens, float softmax_scale, int32_t window, void *out, int64_t ldo,
+                   float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+  int st = check_cache(kv_heads, dim, cache_dtype, n_pages, page_size, page_stride, head_stride,
+                       token_stride);
+  if (st != Q4K_OK) return st;
+  if (n < 0 || n > 65536 || q_heads <= 0 || q_heads > 1024 || q_heads % kv_heads) return Q4K_ERR_SHAPE;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return Q4K_ERR_SHAPE;
+  if (max_pages <= 0 || max_pages > INT32_MAX / page_size || ldt < max_pages || window < 0)
+    return Q4K_ERR_SHAPE;
+  if (!(softmax_scale - softmax_scale == 0.f)) return Q4K_ERR_SHAPE;  // NaN or infinite
+  if (ldq_head < dim || ldq < 0 || ldo < (int64_t)q_heads * dim) return Q4K_ERR_SHAPE;
+  if (n == 0) return Q4K_OK;
+  const bool e4m3 = cache_dtype == Q4K_DTYPE_E4M3;
+  if (!q || !k_cache || !v_cache || !table || !lens || !out || (e4m3 && (!k_scale || !v_scale)))
+    return Q4K_ERR_NULL;
+  if (!workspace || workspace_bytes < paged_attn_workspace_size(n, q_heads, kv_heads, dim))
+    return Q4K_ERR_WORKSPACE;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(workspace, 16) || ldq % 8 || ldq_head % 8 || ldo % 8)
+    return Q4K_ERR_ALIGN;
+  st = check_device();
+  if (st != Q4K_OK) return st;
+  st = check_device_memory({q, k_cache, v_cache, table, lens, out, lse, workspace,
+                            e4m3 ? k_scale : nullptr, e4m3 ? v_scale : nullptr});
+  if (st != Q4K_OK) return st;
+  AttnArgs a = {};
+  a.q = q, a.cache[0] = k_cache, a.cache[1] = v_cache, a.scale[0] = k_scale, a.scale[1] = v_scale;
+  a.table = table, a.lens = lens, a.out = out, a.lse = lse, a.workspace = workspace;
+  a.ldq = ldq, a.ldq_head = ldq_head, a.ldo = ldo, a.ldt = ldt, a.n_pages = n_pages;
+  a.page_stride = page_stride, a.head_stride = head_stride, a.token_stride = token_stride;
+  a.n = n, a.q_heads = q_heads, a.kv_heads = kv_heads, a.dim = dim, a.page = page_size;
+  a.max_pages = max_pages, a.window = window, a.softmax_scale = softmax_scale;
+  a.cache_dtype = cache_dtype, a.err = device_error_word();
+  return map_launch(launch_paged_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+int q4k_add_rmsnorm(const void *x, int x_dtype, int64_t ldx, const void *residual, int res_dtype,
+                    int64_t ldr, const float *gamma, float eps, int64_t m, int64_t hidden, void *y,
+                    int y_dtype, int64_t ldy, void *residual_out, int64_t ldro, float *scales,
+                    int64_t lds, void *stream) {
+  const bool e4m3 = y_dtype == Q4K_DTYPE_E4M3;
+  if ((x_dtype != Q4K_DTYPE_FP32 && x_dtype != Q4K_DTYPE_BF16) ||
+      (y_dtype != Q4K_DTYPE_BF16 && !e4m3) ||
+      (residual && res_dtype != Q4K_DTYPE_FP32 && res_dtype != Q4K_DTYPE_BF16))
+    return Q4K_ERR_SHAPE;
+  if (m < 0 || m > INT32_MAX || hidden <= 0 || hidden > 32768 || hidden % 8) return Q4K_ERR_SHAPE;
+  if (!(eps >= 0.f) || !(eps - eps == 0.f)) return Q4K_ERR_SHAPE;
+  if (m == 0) return Q4K_OK;
+  if (ldx < hidden || ldy < hidden || (residual && (ldr < hidden || ldro < hidden)) ||
+      (e4m3 && lds < (hidden + 127) / 128))
+    return Q4K_ERR_SHAPE;
+  if (!x || !gamma || !y || (residual && !residual_out) || (e4m3 && !scales)) return Q4K_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(gamma, 16) || !aligned(y, 16) || ldx % 8 || ldy % 8 ||
+      (residual && (!aligned(residual, 16) || !aligned(residual_out, 16) || ldr % 8 || ldro % 8)) ||
+      (e4m3 && !aligned(scales, 4)))
+    return Q4K_ERR_ALIGN;
+  int st = check_device();
+  if (st != Q4K_OK) return st;
+  st = check_device_memory({x, residual, gamma, y, residual ? residual_out : nullptr,
+                            e4m3 ? scales : nullptr});
+  if (st != Q4K_OK) return st;
+  return map_launch(launch_add_rmsnorm(x, x_dtype, ldx, residual, res_dtype, ldr, gamma, eps, m, hidden,
+                                       y, y_dtype, ldy, residual_out, ldro, scales, lds,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+int q4k_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+               const float *u, const float *temperature, const int32_t *top_k, const float *top_p,
+               const float *min_p, int32_t *token, float *logp, void *stream) {
+  if (dtype != Q4K_DTYPE_FP32 && dtype != Q4K_DTYPE_BF16) return Q4K_ERR_SHAPE;
+  if (rows < 0 || rows > (1 << 24) || vocab <= 0 || vocab > 262144 || ld < vocab) return Q4K_ERR_SHAPE;
+  if (rows == 0) return Q4K_OK;
+  if (!logits || !u || !token) return Q4K_ERR_NULL;
+  if (!aligned(logits, dtype == Q4K_DTYPE_FP32 ? 4 : 2) || !aligned(u, 4) || !aligned(temperature, 4) ||
+      !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(token, 4) ||
+      !aligned(logp, 4))
+    return Q4K_ERR_ALIGN;
+  int st = check_device();
+  if (st != Q4K_OK) return st;
+  st = check_device_memory({logits, u, temperature, top_k, top_p, min_p, token, logp});
+  if (st != Q4K_OK) return st;
+  return map_launch(launch_sample(logits, dtype, rows, vocab, ld, u, temperature, top_k, top_p, min_p,
+                                  token, logp, static_cast<cudaStream_t>(stream)));
+}
+
 int q4k_selftest_wait_timeout(void *stream) {
   int st = check_device();
   if (st != Q4K_OK) return st;

@@ -19,6 +19,7 @@ constexpr int kQsOffset = 16;     // first quant byte within a super-block
 // kernels receive its address as an argument.
 constexpr unsigned kDevErrTimeout = 1u;
 constexpr unsigned kDevErrBadExpert = 2u;
+constexpr unsigned kDevErrBadPage = 4u;
 
 __device__ __forceinline__ void set_device_error(unsigned *err, unsigned bits) {
   if (err) atomicOr(err, bits);

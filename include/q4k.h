@@ -90,6 +90,8 @@ enum q4k_status {
 /* Bits of the device error word (q4k_get_device_error). */
 #define Q4K_DEVERR_TIMEOUT 1u    /* a bounded wait on an asynchronous copy gave up */
 #define Q4K_DEVERR_BAD_EXPERT 2u /* an expert id outside [0, n_experts) was skipped */
+#define Q4K_DEVERR_BAD_PAGE 4u   /* a page, slot or length outside the cache or the table
+                                    was skipped */
 
 int q4k_abi_version(void);
 const char *q4k_status_str(int status);
@@ -446,6 +448,195 @@ int q4k_moe_gemv_noalloc(const void *w_gate, const void *w_up, const void *w_dow
                          int64_t expert_stride, int32_t n_experts, int64_t hidden, int64_t ffn,
                          const void *x, int32_t n_tokens, int64_t ldx, const int32_t *ids,
                          const float *wts, int32_t top_k, float *y, int64_t ldy, void *stream);
+
+/*
+ * Around the projections of a decode step: the paged key-value cache, the
+ * attention of one new token per request, the norm between the projections and
+ * the choice of the next token.
+ * ("spec: specialized model runtimes", section "Architecture": attention and
+ *  norms are ops of kernel tier T0, the sampler belongs to T1; "PRD: Performant
+ *  Concurrent Distributed GGUF Runtime": hot KV state per session, DGR-012.)
+ *
+ * Element types of their arguments:
+ */
+#define Q4K_DTYPE_FP32 0
+#define Q4K_DTYPE_BF16 1
+#define Q4K_DTYPE_E4M3 2 /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448 */
+
+/*
+ * The paged cache.  K and V are two buffers of n_pages pages, each page
+ * page_size tokens of every key head: element (page, head, token, i) at
+ *     page * page_stride + head * head_stride + token * token_stride + i
+ * (in elements; i < dim contiguous; both buffers have the same strides).  The
+ * token at position p of a request is token p % page_size of page
+ * table[request][p / page_size]; its slot is page * page_size + p % page_size.
+ * bf16, or e4m3 with one fp32 scale per (page, head, token) in a contiguous
+ * [n_pages][kv_heads][page_size] array per buffer: value = e4m3 * scale.
+ */
+
+/*
+ * q4k_kv_plan -- block tables and slot maps of a step, from request lengths.
+ * For n requests with lens[r] tokens cached and add[r] tokens to append
+ * (add[r] == -1: the request is finished) and page_size tokens per page:
+ *   - pages are taken from a ring of free pages: pool[0..pool_size) holds
+ *     state[1] free pages from index state[0] on, wrapping at pool_size.
+ *     Requests are served in order; request r gets the pages it newly needs,
+ *     written to table[r][..], if all newly needed pages up to and including
+ *     its own are there (a request that needs no new page always is served).
+ *   - the pages of a finished request go to the ring's tail.  They are handed
+ *     out by later calls, not by this one, so a call repeated on the same
+ *     lens, add and state gives the same result.
+ *   - token i of request r is token cu[r] + i of the step (cu[0] = 0, cu[r+1] =
+ *     cu[r] + max(add[r], 0)); slots[] gets its slot and pos[] its position in
+ *     the request, both -1 for tokens of requests not served and past cu[n].
+ *   - lens_out[r]: lens[r] + add[r], or 0 for a finished request, or lens[r]
+ *     for one not served.
+ *   - status[r]: Q4K_KV_OK; Q4K_KV_NO_PAGES: not enough free pages;
+ *     Q4K_KV_BAD_LENGTH: lens[r] < 0, add[r] < -1 or more tokens than
+ *     max_pages * page_size; Q4K_KV_NO_SLOTS: its tokens end past n_slots.
+ *     Requests with the last two states ask for no pages.
+ *   lens, add          device, n int32
+ *   table              device, n rows of max_pages int32, row stride ldt
+ *                      (read and written)
+ *   pool               device, pool_size int32: one entry per page of the cache
+ *                      (page ids 0 .. pool_size - 1; read and written)
+ *   pool_state         device, 2 int32: first free entry, number of free pages
+ *   lens_out, status   device, n int32 (lens_out may be lens)
+ *   cu                 device, n + 1 int64
+ *   slots, pos         device, n_slots int32 each
+ *   pool_state_out     device, 2 int32 (may be pool_state)
+ * A page id outside the pool gives slot -1 and sets Q4K_DEVERR_BAD_PAGE; so
+ * does a returned page for which the ring has no entry left (a page returned
+ * twice), which is dropped.
+ * Limits: n <= 65536, pool_size * page_size < 2^31, n_slots < 2^31.
+ * Errors: NULL, SHAPE, ALIGN (4 bytes; cu 8), DEVICE, MEMORY, CUDA.
+ */
+enum q4k_kv_status {
+    Q4K_KV_OK = 0,
+    Q4K_KV_NO_PAGES = 1,
+    Q4K_KV_BAD_LENGTH = 2,
+    Q4K_KV_NO_SLOTS = 3
+};
+int q4k_kv_plan(const int32_t *lens, const int32_t *add, int32_t n, int32_t *table, int64_t ldt,
+                int32_t max_pages, int32_t page_size, int32_t *pool, int32_t pool_size,
+                const int32_t *pool_state, int32_t *lens_out, int64_t *cu, int32_t *slots,
+                int32_t *pos, int64_t n_slots, int32_t *status, int32_t *pool_state_out,
+                void *stream);
+
+/*
+ * q4k_kv_write -- write new keys and values into the paged cache.
+ * Row (t, h) of K and V goes to slot slots[t] of head h: rounded once to bf16,
+ * or to e4m3 with the scale s = max(max_i |x_i|, 2^-100) / 448 and the values
+ * e4m3(x_i * (448 / max)).  Slot -1 skips the token; any other slot outside
+ * the cache does too, and sets Q4K_DEVERR_BAD_PAGE.  Tokens of one call that
+ * share a slot leave one of their rows there, unspecified which.
+ *   k, v      device, fp32 or bf16 (in_dtype), element (t, h, i) at t * ld_token
+ *             + h * ld_head + i; 16-byte aligned, strides multiples of 8
+ *   slots     device, tokens int32
+ *   caches    as above; 16-byte aligned, strides multiples of 8 (bf16) or 16
+ *             (e4m3), page_stride >= 0 and rows not overlapping
+ *   dim       64, 128 or 256
+ *   k_scale, v_scale  fp32, for an e4m3 cache; NULL for bf16
+ * Limits: n_pages * page_size < 2^31.
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, MEMORY, CUDA.
+ */
+int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, int64_t ld_head,
+                 const int32_t *slots, int64_t tokens, int32_t kv_heads, int32_t dim, void *k_cache,
+                 void *v_cache, int cache_dtype, int64_t n_pages, int32_t page_size,
+                 int64_t page_stride, int64_t head_stride, int64_t token_stride, float *k_scale,
+                 float *v_scale, void *stream);
+
+/*
+ * q4k_paged_attn -- attention of one new token per request over the cache.
+ * For request r, query head i and key head i / (q_heads / kv_heads), with the
+ * tokens max(0, lens[r] - window) <= j < lens[r] (window 0: all of them):
+ *     z_j = softmax_scale * q . k_j,  lse = ln sum_j e^z_j,
+ *     out = sum_j e^(z_j - lse) v_j                    (bf16, rounded once)
+ * A request with no tokens (lens[r] <= 0) gets zeros and lse = -infinity.
+ * Cache rows that no request's tokens refer to are never used, whatever they
+ * hold (NaN and infinities included).  A page outside [0, n_pages) counts as
+ * absent (its tokens are skipped), and so do tokens past max_pages *
+ * page_size; both set Q4K_DEVERR_BAD_PAGE.
+ * Scores, softmax statistics and sums are fp32.  For a bf16 cache the softmax
+ * weights enter the products as two bf16 terms (16 significant bits), for an
+ * e4m3 cache as one fp16 term (11 bits) of the weight times the row's scale.
+ *   q       device, bf16, element (r, i, d) at r * ldq + i * ldq_head + d;
+ *           16-byte aligned, strides multiples of 8
+ *   caches  as above; 16-byte aligned, strides multiples of 16 bytes.  dim 64,
+ *           128 or 256; page_size 16, 32, 64, 128 or 256
+ *   scales  for an e4m3 cache: positive, finite; NULL for bf16
+ *   table   device, n rows of max_pages int32, row stride ldt
+ *   lens    device, n int32
+ *   out     device, bf16, row stride ldo >= q_heads * dim, heads contiguous;
+ *           16-byte aligned, ldo a multiple of 8
+ *   lse     device, n x q_heads fp32, or NULL
+ *   workspace  device, >= q4k_paged_attn_workspace_size(...) bytes, 16-byte
+ *           aligned; nothing in it is kept between calls
+ * Limits: n <= 65536, q_heads <= 1024 and a multiple of kv_heads.
+ * Errors: NULL, SHAPE, ALIGN, WORKSPACE, DEVICE, MEMORY, CUDA.
+ */
+size_t q4k_paged_attn_workspace_size(int32_t n, int32_t q_heads, int32_t kv_heads, int32_t dim);
+int q4k_paged_attn(const void *q, int64_t ldq, int64_t ldq_head, int32_t n, int32_t q_heads,
+                   int32_t kv_heads, int32_t dim, const void *k_cache, const void *v_cache,
+                   int cache_dtype, int64_t n_pages, int32_t page_size, int64_t page_stride,
+                   int64_t head_stride, int64_t token_stride, const float *k_scale,
+                   const float *v_scale, const int32_t *table, int64_t ldt, int32_t max_pages,
+                   const int32_t *lens, float softmax_scale, int32_t window, void *out, int64_t ldo,
+                   float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * q4k_add_rmsnorm -- residual addition and root-mean-square norm.
+ *     h = x + residual;  residual_out = h;
+ *     y = h * gamma / sqrt((1/H) sum_i h_i^2 + eps)
+ * in fp32 from the unrounded h, each output rounded once.  y is bf16, or e4m3
+ * with one fp32 scale per 128 values: scales[t][b] = max(max |y|, 2^-100) /
+ * 448, values e4m3(y * (448 / max)).
+ *   x             device, m x hidden fp32 or bf16, row stride ldx
+ *   residual      device, m x hidden fp32 or bf16, or NULL (then residual_out is
+ *                 not used)
+ *   gamma         device, hidden fp32
+ *   residual_out  same type as residual; may be residual (with the same stride)
+ *   y             device, m x hidden of y_dtype (bf16 or e4m3)
+ *   scales        device, e4m3 only: m x ceil(hidden / 128) fp32, row stride lds
+ * hidden a multiple of 8, at most 32768; pointers 16-byte aligned (scales 4),
+ * row strides multiples of 8; eps finite, >= 0.
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, MEMORY, CUDA.
+ */
+int q4k_add_rmsnorm(const void *x, int x_dtype, int64_t ldx, const void *residual, int res_dtype,
+                    int64_t ldr, const float *gamma, float eps, int64_t m, int64_t hidden, void *y,
+                    int y_dtype, int64_t ldy, void *residual_out, int64_t ldro, float *scales,
+                    int64_t lds, void *stream);
+
+/*
+ * q4k_sample -- choose a token per row of logits, from given random numbers.
+ * Row r, with e_i = exp((x_i - max x) / temperature[r]) (in exact arithmetic):
+ *   - the tokens are ordered by logit, highest first, equal ones by index;
+ *   - top-k keeps the first top_k[r] of them (<= 0 or >= vocab: all);
+ *   - top-p keeps, of these, every token whose predecessors' e sum to less than
+ *     top_p[r] times the sum over the top-k set (>= 1 or NaN: all; the first
+ *     token always stays);
+ *   - min-p keeps those with e_i >= min(min_p[r], 1) (<= 0 or NaN: all);
+ *   - token[r] is the first index i at which the sum of e over the kept tokens
+ *     0..i exceeds u[r] times the sum over all kept tokens; logp[r] =
+ *     ln(e_token / that sum).
+ * temperature[r] <= 0 or NaN: the highest logit (the lowest index of equal
+ * ones), logp 0.  Logits of -infinity and NaN are never chosen; +infinity
+ * shares the whole mass among its tokens.  A row without any other logit gives
+ * token -1 and logp -infinity.  u outside [0, 1) is taken as the nearest end.
+ * Each e_i is held to within about 2^-40 of the largest (sums are 64-bit
+ * integers, in any order the same), so that a choice differs from the exact
+ * one only where u lies that near to a border; e_i below 2^-45 count as 0.
+ *   logits  device, rows x vocab fp32 or bf16 (dtype), row stride ld
+ *   u       device, rows fp32
+ *   temperature, top_p, min_p (fp32), top_k (int32)  device, one per row, or
+ *           NULL: 1, off, off, off
+ *   token   device, rows int32;  logp  device, rows fp32, or NULL
+ * Limits: vocab <= 262144.
+ * Errors: NULL, SHAPE, ALIGN (element size), DEVICE, MEMORY, CUDA.
+ */
+int q4k_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+               const float *u, const float *temperature, const int32_t *top_k, const float *top_p,
+               const float *min_p, int32_t *token, float *logp, void *stream);
 
 /*
  * q4k_get_device_error -- synchronize `stream`, return the device error word
