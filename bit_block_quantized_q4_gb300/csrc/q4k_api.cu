@@ -663,7 +663,7 @@ int q4k_paged_attn(const void *q, int64_t ldq, int64_t ldq_head, int32_t n, int3
   if (st != Q4K_OK) return st;
   if (n < 0 || n > 65536 || q_heads <= 0 || q_heads > 1024 || q_heads % kv_heads) return Q4K_ERR_SHAPE;
   if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return Q4K_ERR_SHAPE;
-  if (max_pages <= 0 || max_pages > INT32_MAX / page_size || ldt < max_pages || window < 0)
+  if (max_pages <= 0 || max_pages > (1 << 30) / page_size || ldt < max_pages || window < 0)
     return Q4K_ERR_SHAPE;
   if (!(softmax_scale - softmax_scale == 0.f)) return Q4K_ERR_SHAPE;  // NaN or infinite
   if (ldq_head < dim || ldq < 0 || ldo < (int64_t)q_heads * dim) return Q4K_ERR_SHAPE;
@@ -673,8 +673,8 @@ int q4k_paged_attn(const void *q, int64_t ldq, int64_t ldq_head, int32_t n, int3
     return Q4K_ERR_NULL;
   if (!workspace || workspace_bytes < paged_attn_workspace_size(n, q_heads, kv_heads, dim))
     return Q4K_ERR_WORKSPACE;
-  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
-      !aligned(v_scale, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(out, 16) ||
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) ||
+      !aligned(v_scale, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(out, 16) ||
       !aligned(lse, 4) || !aligned(workspace, 16) || ldq % 8 || ldq_head % 8 || ldo % 8)
     return Q4K_ERR_ALIGN;
   st = check_device();

@@ -4,13 +4,41 @@
 // "spec: specialized model runtimes", section "Architecture": attention is an
 // op of kernel tier T0.
 //
-// One pass over the keys with the running maximum m and sum l of a softmax:
-//   z_j = scale q.k_j,  m' = max(m, z_j),  l' = l e^(m-m') + e^(z_j-m'),
-//   o' = o e^(m-m') + e^(z_j-m') v_j.
-// One block per (request, query head); its four warps take tokens in turn and
-// are joined at the end.
+// Mathematics.  One pass over the keys with the running maximum m and sum l of
+// a softmax, all in base 2 (scores carry log2 e):
+//   m' = max(m, z_j),  l' = l 2^(m-m') + 2^(z_j-m'),
+//   o' = o 2^(m-m') + 2^(z_j-m') v_j,  out = o / l;
+// two parts of a key range are joined by the same rule.
+//
+// What bounds it: bytes.  At 8 query heads per key head a bf16 cache gives 8
+// operations per byte, an e4m3 cache 16: far below the tensor rate, so the
+// design is about keeping bytes in flight.  mma.sync suffices for the arithmetic; with one new token the
+// scores of a group fill the 8 columns of its N side exactly, where a
+// tcgen05.mma would want 64 or 128 rows.
+//
+// Work split.  The (request, key head) items, each a run of tiles of TILE
+// tokens, form one list; every warp of a persistent grid takes an equal run of
+// it, whatever the requests' lengths.  The lengths are on the device, so each
+// CTA sums them itself.  An item inside one warp's run is written out directly;
+// the pieces of the others go to the workspace and a second launch joins them.
+//
+// A warp streams its own ring of tiles: one TMA tile copy per page and buffer
+// (5-D map: 128 bytes of a row, token, part of the row, head, page; 128-byte
+// swizzle), issued by its lane 0 STAGES tiles ahead across item boundaries.
+// Warps never wait for one another inside the loop.
+//
+// Products, transposed so that the query heads are the 8 columns:
+//   S^T[16 keys, 8 heads] += K[16 keys, 16 d] Q^T     (ldmatrix)
+//   O^T[16 d, 8 heads]    += V^T[16 d, 16 keys] P^T   (ldmatrix.trans; P^T from
+//                                                      S^T by movmatrix)
+// bf16 cache: P enters as two bf16 terms (hi + lo, 16 bits), because one
+// rounding of P to 8 bits would be as large as the output's own.  e4m3 cache:
+// K and V are converted exactly to fp16, q is scaled by a power of two per head
+// into fp16 (exact), and P times the row's V scale enters as one fp16 term
+// (11 bits).  Its running maximum is that of z + log2(scale), which keeps this
+// term at most 1 whatever the scales.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -23,81 +51,744 @@
 namespace q4k {
 namespace {
 
+constexpr int kMaxSms = 160;  // SMs the workspace is sized for
+
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(128) paged_attn_kernel(const AttnArgs a) {
-  constexpr int V = D / 32;  // values per lane
-  const int r = blockIdx.x, i = blockIdx.y, h = i / (a.q_heads / a.kv_heads);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ float sm[4], sl[4], so[4][D];
-  float q[V], o[V], m = -INFINITY, l = 0.f;
+struct Cfg {
+  static constexpr int kEs = E4M3 ? 1 : 2;
+  static constexpr int kTile = D * kEs >= 512 ? 16 : 32;    // tokens per tile
+  static constexpr int kRow = D * kEs >= 128 ? 128 : 64;    // bytes of a row per swizzled part
+  static constexpr int kParts = D * kEs / kRow;
+  static constexpr int kSide = kTile * D * kEs;             // bytes of K (or V) per tile
+  static constexpr int kScales = E4M3 ? kTile * 4 : 0;      // bytes of K (or V) scales per tile
+  static constexpr int kWarps = kSide >= 8192 ? 4 : 8;
+  static constexpr int kStages = kSide >= 4096 ? 3 : 4;
+  // per warp STAGES x (K | V), 1024-byte aligned as the swizzle wants it; then
+  // per warp STAGES x (K scales | V scales)
+  static constexpr int kRing = kStages * 2 * kSide, kScaleRing = kStages * 2 * kScales;
+  static constexpr int kSmem = kWarps * (kRing + kScaleRing) + 1024;
+  static_assert(kSide % 1024 == 0, "tile buffers keep the swizzle's alignment");
+};
+
+struct Params {
+  AttnArgs a;
+  int groups;      // query-head groups per key head
+  int items;       // items per request: kv_heads * groups
+  int group_size;  // query heads per key head
+  int box_rows, box_shift, page_shift;
+  int64_t warps;   // of the whole grid
+  int64_t *prefix;  // [n + 1] tiles per head before a request
+  float *slots;
+};
+
+// Fewest tiles a warp takes: below this the join costs more than the split
+// gains.
+constexpr int kMinRun = 2;
+
+__device__ __forceinline__ int64_t run_of(int64_t tiles, int64_t warps) {
+  const int64_t c = (tiles + warps - 1) / warps;
+  return c < kMinRun ? kMinRun : c;
+}
+
+template <int TILE>
+__device__ __forceinline__ void span_of(const AttnArgs &a, int len, int &start, int &t0, int &t1) {
+  start = a.window > 0 && len > a.window ? len - a.window : 0;
+  t0 = start / TILE;
+  t1 = (len + TILE - 1) / TILE;
+}
+__device__ __forceinline__ int length_of(const AttnArgs &a, int r) {
+  const int len = a.lens[r], cap = a.max_pages * a.page;
+  return len < 0 ? 0 : len > cap ? cap : len;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+// Two e4m3 values (the low 16 bits) to an fp16 pair, exact.
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t w) {
+  uint32_t y;
+  asm("{\n .reg .b16 lo;\n cvt.u16.u32 lo, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(y) : "r"(w));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The state of a piece in registers.  Thread (g = lane / 4, t = lane % 4) has
+// of every n-tile j the heads 8 j + 2t and 8 j + 2t + 1; o[dt][j] holds, of the
+// 16 values 16 dt .. 16 dt + 15 of a row, rows (d0, d1) x these two heads:
+// d0 = g, d1 = g + 8 (bf16) or d0 = 2g, d1 = 2g + 1 (e4m3).
+template <int D, int NQ>
+struct State {
+  float o[D / 16][NQ][4];
+  float m[NQ][2], l[NQ][2];
+};
+
+template <int D, bool E4M3, int NQ>
+__device__ __forceinline__ void write_out(const Params &p, State<D, NQ> &s, int r, int item, int dt0, int dt1, bool lse) {
+  const AttnArgs &a = p.a;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int kvh = item / p.groups, q0 = (item - kvh * p.groups) * 8 * NQ;
 #pragma unroll
-  for (int c = 0; c < V; ++c) {
-    q[c] = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[r * a.ldq + i * a.ldq_head + lane + 32 * c]);
-    o[c] = 0.f;
-  }
-  int64_t len = max(a.lens[r], 0);
-  if (len > (int64_t)a.max_pages * a.page) {
-    len = (int64_t)a.max_pages * a.page;
-    set_device_error(a.err, kDevErrBadPage);
-  }
-  const int64_t start = a.window ? max(len - a.window, (int64_t)0) : 0;
-  for (int64_t j = start + warp; j < len; j += 4) {
-    const int64_t page = a.table[r * a.ldt + j / a.page], off = j % a.page;
-    if (page < 0 || page >= a.n_pages) {
-      set_device_error(a.err, kDevErrBadPage);
-      continue;
+  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int q = q0 + 8 * j + 2 * t + c;
+      if (q >= p.group_size) continue;
+      const float l = s.l[j][c], inv = s.m[j][c] == -INFINITY ? 0.f : 1.f / l;
+      const int head = kvh * p.group_size + q;
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + r * a.ldo + (int64_t)head * D;
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) {
+        if (dt < dt0 || dt >= dt1) continue;
+        const float v0 = s.m[j][c] == -INFINITY ? 0.f : s.o[dt][j][c] * inv;
+        const float v1 = s.m[j][c] == -INFINITY ? 0.f : s.o[dt][j][2 + c] * inv;
+        if (E4M3) {
+          *reinterpret_cast<uint32_t *>(out + 16 * dt + 2 * g) = pack_bf16(v0, v1);
+        } else {
+          out[16 * dt + g] = __float2bfloat16(v0);
+          out[16 * dt + 8 + g] = __float2bfloat16(v1);
+        }
+      }
+      if (lse && a.lse && g == 0)
+        a.lse[(int64_t)r * a.q_heads + head] =
+            s.m[j][c] == -INFINITY ? -INFINITY : (s.m[j][c] + log2f(l)) * 0.6931471805599453f;
     }
-    const int64_t at = page * a.page_stride + h * a.head_stride + off * a.token_stride + lane;
-    const int64_t sat = (page * a.kv_heads + h) * a.page + off;
-    float z = 0.f, v[V];
+}
+
+// Floats of one workspace slot: the o registers and m, l of every lane.
+template <int D, int NQ>
+constexpr int slot_floats() {
+  return 32 * NQ * (D / 16 * 4 + 4);
+}
+
+template <int D, bool E4M3, int NQ>
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
+    paged_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D, E4M3>;
+  constexpr int TILE = C::kTile, MT = TILE / 16, W = C::kWarps, ST = C::kStages, T = W * 32;
+  constexpr int KS = D / 16;                  // k16 steps of S^T, and 16-row tiles of O^T
+  constexpr int LD = E4M3 ? D / 32 : D / 16;  // ldmatrix.x4 per 16 rows
+  constexpr int LPP = C::kRow / 32;           // of these, per 128-byte part
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[W][ST];
+  __shared__ int4 head[W][ST];
+  __shared__ int64_t sums[T];
+  __shared__ int64_t wsum[W];
+  const AttnArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  grid_launch_dependents();
+  if (lane == 0) {
+    for (int s = 0; s < ST; ++s) mbar_init(&full[warp][s], 1);
+    fence_mbar_init();
+    if (warp == 0) prefetch_tmap(&kmap), prefetch_tmap(&vmap);
+  }
+
+  // Sum the tiles of all requests: thread i takes requests [i*per, (i+1)*per).
+  const int per = (a.n + T - 1) / T, r_lo = min(tid * per, a.n), r_hi = min(r_lo + per, a.n);
+  int64_t mine = 0;
+  bool bad = false;
+  for (int r = r_lo; r < r_hi; ++r) {
+    const int len = length_of(a, r);
+    int start, t0, t1;
+    span_of<TILE>(a, len, start, t0, t1);
+    mine += t1 - t0;
+    bad |= a.lens[r] > len && a.lens[r] > 0;
+  }
+  int64_t incl = mine;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      if (E4M3) {
-        z += q[c] * (float)static_cast<const __nv_fp8_e4m3 *>(a.cache[0])[at + 32 * c];
-        v[c] = (float)static_cast<const __nv_fp8_e4m3 *>(a.cache[1])[at + 32 * c];
-      } else {
-        z += q[c] * __bfloat162float(static_cast<const __nv_bfloat16 *>(a.cache[0])[at + 32 * c]);
-        v[c] = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.cache[1])[at + 32 * c]);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) incl += wsum[w];
+    total += wsum[w];
+  }
+  sums[tid] = incl;
+  if (blockIdx.x == 0) {
+    if (bad) set_device_error(a.err, kDevErrBadPage);
+    int64_t at = incl - mine;
+    for (int r = r_lo; r < r_hi; ++r) {
+      int start, t0, t1;
+      span_of<TILE>(a, length_of(a, r), start, t0, t1);
+      p.prefix[r] = at;
+      at += t1 - t0;
+    }
+    if (tid == T - 1) p.prefix[a.n] = total;
+  }
+  __syncthreads();
+
+  // This warp's run of tiles [first, first + todo).
+  const int64_t tiles = total * p.items, run = run_of(tiles, p.warps);
+  const int64_t gw = (int64_t)blockIdx.x * W + warp, first = gw * run;
+  if (first >= tiles) return;
+  int64_t to_issue = min(run, tiles - first), to_do = to_issue;
+  int r, item, t, t0, t1, start, len;
+  {
+    const int64_t y = first / p.items;
+    int lo = 0, hi = T - 1;  // the first thread whose inclusive sum exceeds y
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sums[mid] > y) hi = mid;
+      else lo = mid + 1;
+    }
+    int64_t at = lo ? sums[lo - 1] : 0;
+    for (r = lo * per;; ++r) {
+      len = length_of(a, r);
+      span_of<TILE>(a, len, start, t0, t1);
+      if (at + (t1 - t0) > y) break;
+      at += t1 - t0;
+    }
+    const int64_t rem = first - at * p.items;
+    item = (int)(rem / (t1 - t0));
+    t = t0 + (int)(rem - (int64_t)item * (t1 - t0));
+  }
+
+  uint8_t *ring = smem + warp * C::kRing;
+  uint8_t *scales = smem + W * C::kRing + warp * C::kScaleRing;  // used for e4m3 only
+
+  // ---- producer: every lane tracks the next tile, lane 0 issues its copies.
+  // Lanes hold 32 table entries from page index tb on, and the 32 after them.
+  int tb = 0, entry = 0, entry2 = 0;
+  const auto table_at = [&](int i) {
+    return i < a.max_pages ? a.table[r * a.ldt + i] : 0;
+  };
+  const auto fetch_table = [&]() {
+    tb = (t * TILE) >> p.page_shift;
+    entry = table_at(tb + lane);
+    entry2 = table_at(tb + 32 + lane);
+  };
+  fetch_table();
+  bool piece_new = true, from_start = false;
+  const int box_bytes = p.box_rows * D * C::kEs;
+  const auto issue = [&](int slot) {
+    const int pos0 = t * TILE;
+    const int hd = item / p.groups;
+    if (piece_new) from_start = t == t0;
+    const int lo = max(start - pos0, 0), hi = max(min(len - pos0, TILE), 0);
+    uint32_t valid = (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & (0xffffffffu << lo);
+    const bool end = t + 1 == t1, last = end || to_issue == 1;
+    uint8_t *k = ring + slot * 2 * C::kSide, *v = k + C::kSide;
+    uint8_t *ks = scales + slot * 2 * C::kScales, *vs = ks + C::kScales;
+    // the boxes that hold a token, and their pages
+    const int boxes = TILE >> p.box_shift;
+    uint32_t bytes = 0;
+    int page[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      page[b] = -1;
+      if (b >= boxes) continue;
+      const uint32_t mask = (p.box_rows == 32 ? 0xffffffffu : (1u << p.box_rows) - 1u) << (b << p.box_shift);
+      if (!(valid & mask)) continue;
+      const int i = ((pos0 + (b << p.box_shift)) >> p.page_shift) - tb;
+      const int pg = __shfl_sync(0xffffffffu, i < 32 ? entry : entry2, i & 31);
+      if (pg < 0 || pg >= a.n_pages) {
+        valid &= ~mask;
+        if (lane == 0) set_device_error(a.err, kDevErrBadPage);
+        continue;
+      }
+      page[b] = pg;
+      bytes += 2 * (box_bytes + (E4M3 ? p.box_rows * 4 : 0));
+    }
+    if (lane == 0) {
+      const bool whole = from_start && end;
+      head[warp][slot] = make_int4(r, item | (piece_new ? 1 << 16 : 0) | (last ? 1 << 17 : 0) |
+                                          (whole ? 1 << 18 : 0) | (from_start ? 1 << 19 : 0),
+                                   (int)valid, 0);
+      uint64_t *bar = &full[warp][slot];
+      mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (page[b] < 0) continue;
+        const int off = (pos0 + (b << p.box_shift)) & (a.page - 1);
+        tma_load_5d(k + b * box_bytes, &kmap, bar, 0, off, 0, hd, page[b]);
+        tma_load_5d(v + b * box_bytes, &vmap, bar, 0, off, 0, hd, page[b]);
+        if (E4M3) {
+          const int64_t at = ((int64_t)page[b] * a.kv_heads + hd) * a.page + off;
+          bulk_load(ks + b * p.box_rows * 4, a.scale[0] + at, p.box_rows * 4, bar);
+          bulk_load(vs + b * p.box_rows * 4, a.scale[1] + at, p.box_rows * 4, bar);
+        }
       }
     }
+    // next tile
+    --to_issue;
+    piece_new = end;
+    if (!end) {
+      ++t;
+      if (((t * TILE) >> p.page_shift) - tb >= 32) {
+        tb += 32;
+        entry = entry2;
+        entry2 = table_at(tb + 32 + lane);
+      }
+    } else if (to_issue > 0) {
+      if (++item == p.items) {
+        item = 0;
+        t0 = t1;
+        while (t0 >= t1 && r + 1 < a.n) {
+          ++r;
+          len = length_of(a, r);
+          span_of<TILE>(a, len, start, t0, t1);
+        }
+      }
+      t = t0;
+      fetch_table();
+    }
+  };
+
+  // ---- consumer
+  const int g = lane >> 2, tq = lane & 3;
+  uint32_t qf[KS][NQ][2];
+  float qs[NQ][2];  // score factor of the thread's two heads per n-tile
+  State<D, NQ> s;
+  int cur_r = 0, cur_item = 0;
+  const auto start_piece = [&]() {
+    const int kvh = cur_item / p.groups, q0 = (cur_item - kvh * p.groups) * 8 * NQ;
+    const float f = a.softmax_scale * 1.4426950408889634f;
 #pragma unroll
-    for (int s = 16; s; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-    z *= a.softmax_scale;
-    float vs = 1.f;
-    if (E4M3) z *= a.scale[0][sat], vs = a.scale[1][sat];
-    const float mn = fmaxf(m, z), f = m == mn ? 1.f : expf(m - mn), p = expf(z - mn);
-    l = l * f + p;
-    m = mn;
+    for (int j = 0; j < NQ; ++j) {
+      const int q = q0 + 8 * j + g;
+      const bool in = q < p.group_size;
+      const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + cur_r * a.ldq +
+                                 (int64_t)(kvh * p.group_size + (in ? q : 0)) * a.ldq_head;
+      if (!E4M3) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) o[c] = o[c] * f + p * vs * v[c];
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            qf[ks][j][h] = in ? *reinterpret_cast<const uint32_t *>(src + 16 * ks + 8 * h + 2 * tq) : 0u;
+        qs[j][0] = qs[j][1] = f;
+      } else {
+        // values 16 ks + 4t .. + 3 of the row: the order in which ldmatrix on
+        // 8-bit rows and the conversions give K
+        uint2 w[KS];
+        float amax = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          w[ks] = in ? *reinterpret_cast<const uint2 *>(src + 16 * ks + 4 * tq) : make_uint2(0u, 0u);
+          amax = fmaxf(fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[ks].x << 16)), fabsf(__uint_as_float(w[ks].x & 0xffff0000u)))),
+                       fmaxf(fabsf(__uint_as_float(w[ks].y << 16)), fabsf(__uint_as_float(w[ks].y & 0xffff0000u))));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^(14 - exponent of amax): the row's largest value lands in [2^14, 2^15)
+        const int e = (int)((__float_as_uint(amax) >> 23) & 255);
+        const int up = min(max(127 + 14 - (e - 127), 1), 254);
+        const float scale = amax > 0.f && e < 255 ? __uint_as_float((uint32_t)up << 23) : 1.f;
+        const float back = f / scale;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          qf[ks][j][0] = pack_f16(__uint_as_float(w[ks].x << 16) * scale, __uint_as_float(w[ks].x & 0xffff0000u) * scale);
+          qf[ks][j][1] = pack_f16(__uint_as_float(w[ks].y << 16) * scale, __uint_as_float(w[ks].y & 0xffff0000u) * scale);
+        }
+        qs[j][0] = __shfl_sync(0xffffffffu, back, 8 * tq);
+        qs[j][1] = __shfl_sync(0xffffffffu, back, 8 * tq + 4);
+      }
+      s.m[j][0] = s.m[j][1] = -INFINITY;
+      s.l[j][0] = s.l[j][1] = 0.f;
+#pragma unroll
+      for (int dt = 0; dt < KS; ++dt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.o[dt][j][i] = 0.f;
+    }
+  };
+
+  // ldmatrix row of this lane: token (lane & 7) + 8 ((lane >> 3) & 1) of 16,
+  // 16-byte chunk 2 i + (lane >> 4) of the row, swizzled by the token.
+  const int row = lane & 15;
+  const uint32_t swz = C::kRow == 128 ? (lane & 7) : ((lane >> 1) & 3);
+  uint32_t chunk[LPP];
+#pragma unroll
+  for (int i = 0; i < LPP; ++i) chunk[i] = (uint32_t)row * C::kRow + (((2 * i + (lane >> 4)) ^ swz) << 4);
+  const uint32_t part_stride = p.box_rows * C::kRow;
+  const uint32_t mt_stride = p.box_rows == 16 ? 16 * D * C::kEs : 16 * C::kRow;
+
+  for (int i = 0; i < ST && to_issue > 0; ++i) issue(i);
+  int slot = 0;
+  uint32_t phase = 0;
+  for (; to_do > 0; --to_do) {
+    if (!mbar_wait(&full[warp][slot], phase, a.err)) {
+      // copies still under way get the same time to land before the CTA ends
+      if (lane == 0) drain_ring(full[warp], ST, slot, phase, (int)min(to_do - to_issue, (int64_t)ST));
+      __syncwarp();
+      return;
+    }
+    const int4 hd = head[warp][slot];
+    const uint32_t valid = (uint32_t)hd.z;
+    if (hd.y & (1 << 16)) {
+      cur_r = hd.x, cur_item = hd.y & 0xffff;
+      start_piece();
+    }
+    uint8_t *kt = ring + slot * 2 * C::kSide;
+    const uint32_t kb = smem_u32(kt), vb = kb + C::kSide;
+
+    // S^T
+    float z[MT][NQ][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) z[mt][j][0] = z[mt][j][1] = z[mt][j][2] = z[mt][j][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        uint32_t k4[4];
+        ldsm(k4, kb + mt * mt_stride + (i / LPP) * part_stride + chunk[i % LPP]);
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+          if (!E4M3) {
+            mma_bf16(z[mt][j], k4[0], k4[1], k4[2], k4[3], qf[i][j][0], qf[i][j][1]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_f16(z[mt][j], e4m3x2_f16(k4[2 * h]), e4m3x2_f16(k4[2 * h + 1]),
+                      e4m3x2_f16(k4[2 * h] >> 16), e4m3x2_f16(k4[2 * h + 1] >> 16),
+                      qf[2 * i + h][j][0], qf[2 * i + h][j][1]);
+          }
+        }
+      }
+    }
+
+    // scores in base 2; tokens that are not there get -infinity
+    const bool partial = valid != (TILE == 32 ? 0xffffffffu : 0xffffu);
+    float lv[MT][2], rv[MT][2];
+    const float *ksc = reinterpret_cast<const float *>(scales + slot * 2 * C::kScales), *vsc = ksc + TILE;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float ks = 1.f;
+        if (E4M3) {
+          ks = ksc[mt * 16 + 8 * h + g];
+          const float vs = fmaxf(vsc[mt * 16 + 8 * h + g], 1.1754944e-38f);
+          lv[mt][h] = lg2(vs);
+          rv[mt][h] = rcp_approx(vs);
+        }
+        const bool there = !partial || (valid >> (mt * 16 + 8 * h + g) & 1u);
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float &x = z[mt][j][2 * h + c];
+            x = E4M3 ? fmaf(x * qs[j][c], ks, lv[mt][h]) : x * qs[j][c];
+            if (!there) x = -INFINITY;
+          }
+      }
+    if (partial) {
+      // zero the V rows that are not there: 0 * (whatever they hold) must be 0
+      for (int i = lane; i < C::kSide / 16; i += 32) {
+        const int in_box = i % (box_bytes / 16);
+        const int tok = (i / (box_bytes / 16) << p.box_shift) + (in_box * 16 / C::kRow & (p.box_rows - 1));
+        if (!(valid >> tok & 1u)) *reinterpret_cast<uint4 *>(kt + C::kSide + i * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+
+    // running maximum
+    bool grew = false;
+    float mn[NQ][2];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = fmaxf(z[0][j][c], z[0][j][2 + c]);
+#pragma unroll
+        for (int mt = 1; mt < MT; ++mt) x = fmaxf(x, fmaxf(z[mt][j][c], z[mt][j][2 + c]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        mn[j][c] = fmaxf(s.m[j][c], x);
+        grew |= mn[j][c] > s.m[j][c];
+      }
+    if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+      for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float f = mn[j][c] == s.m[j][c] ? 1.f : ex2(s.m[j][c] - mn[j][c]);
+          s.m[j][c] = mn[j][c];
+          s.l[j][c] *= f;
+#pragma unroll
+          for (int dt = 0; dt < KS; ++dt) s.o[dt][j][c] *= f, s.o[dt][j][2 + c] *= f;
+        }
+    }
+
+    // weights, and the P^T fragments
+    uint32_t ph[MT][NQ][2], pl[MT][NQ][2];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      const float m0 = s.m[j][0] == -INFINITY ? 0.f : s.m[j][0], m1 = s.m[j][1] == -INFINITY ? 0.f : s.m[j][1];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float w0 = ex2(z[mt][j][2 * h] - m0), w1 = ex2(z[mt][j][2 * h + 1] - m1);
+          if (E4M3) {
+            s.l[j][0] = fmaf(w0, rv[mt][h], s.l[j][0]);
+            s.l[j][1] = fmaf(w1, rv[mt][h], s.l[j][1]);
+            ph[mt][j][h] = transpose8(pack_f16(w0, w1));
+          } else {
+            s.l[j][0] += w0;
+            s.l[j][1] += w1;
+            const uint32_t hi = pack_bf16(w0, w1);
+            ph[mt][j][h] = transpose8(hi);
+            pl[mt][j][h] = transpose8(pack_bf16(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xffff0000u)));
+          }
+        }
+    }
+
+    // O^T
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        uint32_t v4[4];
+        ldsm_t(v4, vb + mt * mt_stride + (i / LPP) * part_stride + chunk[i % LPP]);
+        if (!E4M3) {
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) {
+            mma_bf16(s.o[i][j], v4[0], v4[2], v4[1], v4[3], ph[mt][j][0], ph[mt][j][1]);
+            mma_bf16(s.o[i][j], v4[0], v4[2], v4[1], v4[3], pl[mt][j][0], pl[mt][j][1]);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // bytes (key 2t: d 2g, 2g + 1; key 2t + 1: the same) to fp16 pairs
+            // of the two keys for d 2g and for d 2g + 1
+            const uint32_t x = __byte_perm(v4[2 * h], 0, 0x3120), y = __byte_perm(v4[2 * h + 1], 0, 0x3120);
+            const uint32_t a0 = e4m3x2_f16(x), a1 = e4m3x2_f16(x >> 16), a2 = e4m3x2_f16(y), a3 = e4m3x2_f16(y >> 16);
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) mma_f16(s.o[2 * i + h][j], a0, a1, a2, a3, ph[mt][j][0], ph[mt][j][1]);
+          }
+        }
+      }
+    __syncwarp();
+    if (to_issue > 0) issue(slot);
+    if (++slot == ST) slot = 0, phase ^= 1u;
+
+    if (hd.y & (1 << 17)) {  // the piece ends
+#pragma unroll
+      for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          s.l[j][c] += __shfl_xor_sync(0xffffffffu, s.l[j][c], 4);
+          s.l[j][c] += __shfl_xor_sync(0xffffffffu, s.l[j][c], 8);
+          s.l[j][c] += __shfl_xor_sync(0xffffffffu, s.l[j][c], 16);
+        }
+      if (hd.y & (1 << 18)) {
+        write_out<D, E4M3, NQ>(p, s, cur_r, cur_item, 0, D / 16, true);
+      } else {
+        float4 *to = reinterpret_cast<float4 *>(p.slots + (2 * gw + (hd.y >> 19 & 1)) * (int64_t)slot_floats<D, NQ>()) + lane;
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+#pragma unroll
+          for (int dt = 0; dt < KS; ++dt)
+            to[(dt * NQ + j) * 32] = make_float4(s.o[dt][j][0], s.o[dt][j][1], s.o[dt][j][2], s.o[dt][j][3]);
+          to[(KS * NQ + j) * 32] = make_float4(s.m[j][0], s.m[j][1], s.l[j][0], s.l[j][1]);
+        }
+      }
+    }
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
+}
+
+// Joins the pieces of the items that several warps share, and writes the items
+// without tokens.  One CTA per item: D / 16 warps, one per 16 values of the
+// row, times `ways` warps that take the pieces in turn.  Item i covers tiles
+// [A, B) of the list, so its pieces are those of warps A / run .. (B-1) / run;
+// the first of them is its warp's slot 1 (it starts the item), the others are
+// slot 0.
+template <int D, bool E4M3, int NQ>
+__global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Params p, int ways) {
+  constexpr int KS = D / 16;
+  extern __shared__ float part[];
+  const AttnArgs &a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dt = warp % KS, way = warp / KS;
+  const int r = blockIdx.x / p.items, item = blockIdx.x % p.items;
+  grid_dependency_wait();
+  const int64_t before = p.prefix[r], nt = p.prefix[r + 1] - before, run = run_of(p.prefix[a.n] * p.items, p.warps);
+  const int64_t A = before * p.items + item * nt, w0 = A / run, w1 = nt ? (A + nt - 1) / run : w0;
+  if (nt && w0 == w1) return;
+  State<16, NQ> s;
 #pragma unroll
-  for (int c = 0; c < V; ++c) so[warp][lane + 32 * c] = o[c];
-  __syncthreads();
-  float mx = sm[0], lt = 0.f, f[4];
-  for (int w = 1; w < 4; ++w) mx = fmaxf(mx, sm[w]);
-  for (int w = 0; w < 4; ++w) f[w] = sm[w] == -INFINITY ? 0.f : expf(sm[w] - mx), lt += f[w] * sl[w];
-  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + r * a.ldo + (int64_t)i * D;
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float t = 0.f;
-    for (int w = 0; w < 4; ++w) t += f[w] * so[w][d];
-    out[d] = __float2bfloat16(lt > 0.f ? t / lt : mx == -INFINITY ? 0.f : t / lt);
+  for (int j = 0; j < NQ; ++j) {
+    s.m[j][0] = s.m[j][1] = -INFINITY;
+    s.l[j][0] = s.l[j][1] = 0.f;
+    s.o[0][j][0] = s.o[0][j][1] = s.o[0][j][2] = s.o[0][j][3] = 0.f;
   }
-  if (a.lse && threadIdx.x == 0) a.lse[(int64_t)r * a.q_heads + i] = mx == -INFINITY ? -INFINITY : mx + logf(lt);
+  const auto add = [&](float4 o, float4 ml, int j) {
+    const float m2[2] = {ml.x, ml.y}, l2[2] = {ml.z, ml.w}, o2[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float m = fmaxf(s.m[j][c], m2[c]);
+      const float f = s.m[j][c] == m ? 1.f : ex2(s.m[j][c] - m), f2 = m2[c] == m ? 1.f : ex2(m2[c] - m);
+      s.m[j][c] = m;
+      s.l[j][c] = s.l[j][c] * f + l2[c] * f2;
+      s.o[0][j][c] = s.o[0][j][c] * f + o2[c] * f2;
+      s.o[0][j][2 + c] = s.o[0][j][2 + c] * f + o2[2 + c] * f2;
+    }
+  };
+  if (nt) {
+    constexpr int U = 4;  // pieces loaded at a time
+    for (int64_t w = w0 + way; w <= w1; w += U * ways) {
+      float4 o[U][NQ], ml[U][NQ];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t x = min(w + u * ways, w1);
+        const float4 *from = reinterpret_cast<const float4 *>(p.slots + (2 * x + (x == w0)) * (int64_t)slot_floats<D, NQ>()) + lane;
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) o[u][j] = from[(dt * NQ + j) * 32], ml[u][j] = from[(KS * NQ + j) * 32];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (w + u * ways <= w1) {
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) add(o[u][j], ml[u][j], j);
+        }
+    }
+  }
+  if (ways > 1) {
+    float4 *mine = reinterpret_cast<float4 *>(part) + warp * NQ * 64 + lane;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      mine[j * 64] = make_float4(s.o[0][j][0], s.o[0][j][1], s.o[0][j][2], s.o[0][j][3]);
+      mine[j * 64 + 32] = make_float4(s.m[j][0], s.m[j][1], s.l[j][0], s.l[j][1]);
+    }
+    __syncthreads();
+    if (way) return;
+    for (int v = 1; v < ways; ++v) {
+      const float4 *from = reinterpret_cast<const float4 *>(part) + (warp + v * KS) * NQ * 64 + lane;
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) add(from[j * 64], from[j * 64 + 32], j);
+    }
+  }
+  // written by the code of a whole item, this warp's 16 values in place of all
+  State<D, NQ> all;
+#pragma unroll
+  for (int j = 0; j < NQ; ++j) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) all.m[j][c] = s.m[j][c], all.l[j][c] = s.l[j][c];
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) all.o[i][j][c] = s.o[0][j][c];
+  }
+  write_out<D, E4M3, NQ>(p, all, r, item, dt, dt + 1, dt == 0);
+}
+
+struct Shape {
+  int nq, groups, warps_per_cta, slot;
+};
+
+template <int D, bool E4M3>
+constexpr int warps_of() {
+  return Cfg<D, E4M3>::kWarps;
+}
+int query_tiles(int dim, int group) { return group > 8 && dim <= 128 ? 2 : 1; }
+size_t slot_bytes(int dim, int nq) { return (size_t)32 * nq * (dim / 16 * 4 + 4) * 4; }
+size_t prefix_bytes(int n) { return ((size_t)(n + 1) * 8 + 255) / 256 * 256; }
+
+template <int D, bool E4M3, int NQ>
+cudaError_t launch_cfg(Params &p, cudaStream_t stream) {
+  using C = Cfg<D, E4M3>;
+  const AttnArgs &a = p.a;
+  const DeviceFacts *f = device_facts();
+  // Kernel attributes are per device; set once for each.
+  static bool ready[kMaxDevices];
+  if (!ready[f->device]) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, E4M3, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    ready[f->device] = true;
+  }
+  CUtensorMap maps[2];
+  p.box_rows = a.page < C::kTile ? a.page : C::kTile;
+  p.box_shift = p.box_rows == 32 ? 5 : 4;
+  p.page_shift = 31 - __builtin_clz((unsigned)a.page);
+  const int inner = C::kRow / C::kEs;
+  const uint64_t dims[5] = {(uint64_t)inner, (uint64_t)a.page, (uint64_t)C::kParts, (uint64_t)a.kv_heads, (uint64_t)a.n_pages};
+  const uint64_t strides[4] = {(uint64_t)a.token_stride * C::kEs, (uint64_t)C::kRow, (uint64_t)a.head_stride * C::kEs,
+                               (uint64_t)a.page_stride * C::kEs};
+  const uint32_t box[5] = {(uint32_t)inner, (uint32_t)p.box_rows, (uint32_t)C::kParts, 1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (encode_tiled(&maps[i], E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                     const_cast<void *>(a.cache[i]), dims, strides, box,
+                     C::kRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  const int grid = f->sm_count < kMaxSms ? f->sm_count : kMaxSms;
+  p.warps = (int64_t)grid * C::kWarps;
+  paged_attn_kernel<D, E4M3, NQ><<<grid, C::kWarps * 32, C::kSmem, stream>>>(p, maps[0], maps[1]);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // Few items: their pieces are many, so several warps share them.
+  const int64_t items = (int64_t)a.n * p.items;
+  const int ways = items <= 2 * f->sm_count ? 512 / (D / 16 * 32) : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)items);
+  cfg.blockDim = dim3(D / 16 * 32 * ways);
+  cfg.dynamicSmemBytes = ways > 1 ? (size_t)D / 16 * ways * NQ * 64 * 16 : 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, join_kernel<D, E4M3, NQ>, p, ways);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_nq(Params &p, int nq, cudaStream_t s) {
+  if constexpr (D <= 128) {
+    if (nq == 2) return launch_cfg<D, E4M3, 2>(p, s);
+  }
+  return launch_cfg<D, E4M3, 1>(p, s);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace_size(int32_t, int32_t, int32_t, int32_t) { return 16; }
+size_t paged_attn_workspace_size(int32_t n, int32_t q_heads, int32_t kv_heads, int32_t dim) {
+  const int nq = query_tiles(dim, q_heads / (kv_heads < q_heads ? kv_heads : q_heads));
+  return prefix_bytes(n) + (size_t)kMaxSms * 8 * 2 * slot_bytes(dim, nq);
+}
 
 cudaError_t launch_paged_attn(const AttnArgs &a, cudaStream_t s) {
-  const dim3 grid(a.n, a.q_heads);
+  Params p = {};
+  p.a = a;
+  p.group_size = a.q_heads / a.kv_heads;
+  const int nq = query_tiles(a.dim, p.group_size);
+  p.groups = (p.group_size + 8 * nq - 1) / (8 * nq);
+  p.items = a.kv_heads * p.groups;
+  p.prefix = static_cast<int64_t *>(a.workspace);
+  p.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + prefix_bytes(a.n));
   const bool e = a.cache_dtype == Q4K_DTYPE_E4M3;
-  if (a.dim == 64) e ? paged_attn_kernel<64, true><<<grid, 128, 0, s>>>(a) : paged_attn_kernel<64, false><<<grid, 128, 0, s>>>(a);
-  else if (a.dim == 128) e ? paged_attn_kernel<128, true><<<grid, 128, 0, s>>>(a) : paged_attn_kernel<128, false><<<grid, 128, 0, s>>>(a);
-  else e ? paged_attn_kernel<256, true><<<grid, 128, 0, s>>>(a) : paged_attn_kernel<256, false><<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.dim == 64) return e ? launch_nq<64, true>(p, nq, s) : launch_nq<64, false>(p, nq, s);
+  if (a.dim == 128) return e ? launch_nq<128, true>(p, nq, s) : launch_nq<128, false>(p, nq, s);
+  return e ? launch_nq<256, true>(p, nq, s) : launch_nq<256, false>(p, nq, s);
 }
 
 }  // namespace q4k

@@ -564,7 +564,7 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
  *           16-byte aligned, strides multiples of 8
  *   caches  as above; 16-byte aligned, strides multiples of 16 bytes.  dim 64,
  *           128 or 256; page_size 16, 32, 64, 128 or 256
- *   scales  for an e4m3 cache: positive, finite; NULL for bf16
+ *   scales  for an e4m3 cache: positive, finite, 16-byte aligned; NULL for bf16
  *   table   device, n rows of max_pages int32, row stride ldt
  *   lens    device, n int32
  *   out     device, bf16, row stride ldo >= q_heads * dim, heads contiguous;
@@ -572,7 +572,8 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
  *   lse     device, n x q_heads fp32, or NULL
  *   workspace  device, >= q4k_paged_attn_workspace_size(...) bytes, 16-byte
  *           aligned; nothing in it is kept between calls
- * Limits: n <= 65536, q_heads <= 1024 and a multiple of kv_heads.
+ * Limits: n <= 65536, q_heads <= 1024 and a multiple of kv_heads, max_pages *
+ * page_size <= 2^30.
  * Errors: NULL, SHAPE, ALIGN, WORKSPACE, DEVICE, MEMORY, CUDA.
  */
 size_t q4k_paged_attn_workspace_size(int32_t n, int32_t q_heads, int32_t kv_heads, int32_t dim);
