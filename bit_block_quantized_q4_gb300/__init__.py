@@ -9,7 +9,6 @@ raises.  Build it with ``python -m bit_block_quantized_q4_gb300.build`` (or
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -36,7 +35,7 @@ EXPORTS = ("q4k_abi_version", "q4k_status_str", "q4k_dequant", "q4k_gemv", "q4k_
            "q4k_kv_plan", "q4k_kv_write", "q4k_paged_attn", "q4k_paged_attn_workspace_size",
            "q4k_add_rmsnorm", "q4k_sample",
            "q4k_get_device_error", "q4k_selftest_wait_timeout")
-Q4K_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2}
+Q4K_DTYPE_FP32, Q4K_DTYPE_BF16, Q4K_DTYPE_E4M3 = 0, 1, 2
 Q4K_KV_OK, Q4K_KV_NO_PAGES, Q4K_KV_BAD_LENGTH, Q4K_KV_NO_SLOTS = 0, 1, 2, 3
 
 _lock = threading.Lock()
@@ -373,38 +372,55 @@ def q4k_moe_gemv_noalloc(w_gate, w_up, w_down, expert_stride: int, n_experts: in
     return out
 
 
-def _want(what: str, t, shape, dtypes, strided: bool = False) -> None:
-    """Raise Q4KError (Q4K_ERR_SHAPE) unless t has this shape (None: any size), one of
-    these types, and is contiguous (strided: its last dimension is)."""
-    ok = t.dim() == len(shape) and t.dtype in dtypes and \
-        all(a is None or a == b for a, b in zip(shape, t.shape)) and \
-        ((t.stride(-1) == 1 or t.shape[-1] <= 1) if strided else t.is_contiguous())
-    if not ok:
-        raise Q4KError(2, f"{what} is {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+# ---- Around the projections.  A decode step makes hundreds of these calls, and a call of some
+# microseconds on the device should not wait for its arguments: the checks below are plain
+# comparisons, and the current stream is asked for by device index (3.0 us less per call than
+# torch.cuda.current_stream() on the GB300's host).
+
+_I32, _I64, _F32, _BF16, _E4M3 = (torch.int32, torch.int64, torch.float32, torch.bfloat16,
+                                  torch.float8_e4m3fn)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _ld(t, dim: int = 0) -> int:
-    """Stride of a dimension as the C ABI wants it: that of a dimension of size 1 is never used and
-    may be anything in torch, so it is given as if the tensor were contiguous."""
-    if t.shape[dim] != 1:
-        return t.stride(dim)
-    return max((t.stride(i) * t.shape[i] for i in range(dim + 1, t.dim())), default=1)
+def _refuse(what: str, t) -> None:
+    raise Q4KError(2, f"{what} is {t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}"
+                   if isinstance(t, torch.Tensor) else f"{what} is {type(t).__name__}, not a tensor")
 
 
-_I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
-_FLOATS = (torch.float32, torch.bfloat16)
+def _vec(what: str, t: torch.Tensor, n: int, dtype) -> int:
+    """The address of a contiguous vector of n values of this type; raises Q4KError otherwise."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        _refuse(what, t)
+    return t.data_ptr()
 
 
-class _alloc_on:
-    """Outputs and workspaces that a call makes belong to the stream it runs on (the
-    allocator may otherwise hand them out again while the call still uses them)."""
+def _rows(what: str, t: torch.Tensor, m: int, n: int, dtype) -> int:
+    """The row stride of an m x n matrix of this type with contiguous rows.  (The stride of a single
+    row is never used and may be anything in torch: n stands in for it.)"""
+    if t.dtype is not dtype or t.shape != (m, n) or (n > 1 and t.stride(1) != 1):
+        _refuse(what, t)
+    return t.stride(0) if m != 1 else n
 
-    def __new__(cls, stream):
-        if stream is None:
-            return contextlib.nullcontext()
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        return torch.cuda.stream(stream)
+
+def _call_stream(stream, t: torch.Tensor) -> int:
+    if stream is not None or _raw_stream is None or not t.is_cuda:
+        return _stream(stream)
+    return _raw_stream(t.get_device())
+
+
+def _on(stream):
+    """Outputs and workspaces that a call makes belong to the stream it runs on (the allocator may
+    otherwise hand them out again while the call still uses them)."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, like: torch.Tensor, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def q4k_kv_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool: torch.Tensor,
@@ -413,46 +429,58 @@ def q4k_kv_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool
     finished), table [n, max_pages] and pool [pages] (both updated in place), pool_state [2].
     Returns (lens_out [n], cu [n + 1] int64, slots [n_slots], pos [n_slots], status [n],
     pool_state_out [2]); out gives these six tensors (lens and pool_state may be among them)."""
-    n = lens.shape[0] if lens.dim() == 1 else -1
-    _want("lens", lens, (n,), _I32)
-    _want("add", add, (n,), _I32)
-    _want("table", table, (n, None), _I32, strided=True)
-    _want("pool", pool, (None,), _I32)
-    _want("pool_state", pool_state, (2,), _I32)
+    n, width, pages = lens.numel(), table.shape[-1], pool.numel()
     if out is None:
-        with _alloc_on(stream):
-            new = torch.empty(2 * n + 2 * n_slots + 2, dtype=torch.int32, device=lens.device)
-            cu = torch.empty(n + 1, dtype=torch.int64, device=lens.device)
-        lens_out, status, slots, pos, state_out = new.split((n, n, n_slots, n_slots, 2))
+        if n_slots < 0:
+            raise Q4KError(2, f"n_slots is {n_slots}")
+        new = _empty(2 * n + 2 * n_slots + 2, _I32, lens, stream)
+        cu = _empty(n + 1, _I64, lens, stream)
+        lens_out, status, slots, pos, state_out = torch.split_with_sizes(
+            new, (n, n, n_slots, n_slots, 2))
+        at = new.data_ptr()
+        to = (at, cu.data_ptr(), at + 8 * n, at + 8 * n + 4 * n_slots, at + 4 * n,
+              at + 8 * (n + n_slots))
     else:
         lens_out, cu, slots, pos, status, state_out = out
-        _want("lens_out", lens_out, (n,), _I32)
-        _want("cu", cu, (n + 1,), (torch.int64,))
-        _want("slots", slots, (n_slots,), _I32)
-        _want("pos", pos, (n_slots,), _I32)
-        _want("status", status, (n,), _I32)
-        _want("pool_state_out", state_out, (2,), _I32)
-    _check(lib().q4k_kv_plan(_ptr(lens), _ptr(add), n, _ptr(table), _ld(table), table.shape[1],
-                             page_size, _ptr(pool), pool.shape[0], _ptr(pool_state), _ptr(lens_out),
-                             _ptr(cu), _ptr(slots), _ptr(pos), n_slots, _ptr(status),
-                             _ptr(state_out), _stream(stream)), "q4k_kv_plan")
+        to = (_vec("lens_out", lens_out, n, _I32), _vec("cu", cu, n + 1, _I64),
+              _vec("slots", slots, n_slots, _I32), _vec("pos", pos, n_slots, _I32),
+              _vec("status", status, n, _I32), _vec("pool_state_out", state_out, 2, _I32))
+    ldt = _rows("table", table, n, width, _I32)
+    _check((_lib or lib()).q4k_kv_plan(
+        _vec("lens", lens, n, _I32), _vec("add", add, n, _I32), n, table.data_ptr(), ldt, width,
+        page_size, _vec("pool", pool, pages, _I32), pages, _vec("pool_state", pool_state, 2, _I32),
+        to[0], to[1], to[2], to[3], n_slots, to[4], to[5], _call_stream(stream, lens)), "q4k_kv_plan")
     return lens_out, cu, slots, pos, status, state_out
 
 
-def _cache_args(k_cache, v_cache, k_scale, v_scale):
-    """(pages, heads, page size, dim) of the two cache buffers and their strides, after checking them."""
-    if k_cache.dim() != 4:
-        raise Q4KError(2, f"k_cache has {k_cache.dim()} dimensions, not [pages, heads, page size, dim]")
-    shape = k_cache.shape
-    _want("k_cache", k_cache, shape, (torch.bfloat16, torch.float8_e4m3fn), strided=True)
-    _want("v_cache", v_cache, shape, (k_cache.dtype,), strided=True)
-    strides = [_ld(k_cache, i) for i in range(3)]
-    if strides != [_ld(v_cache, i) for i in range(3)]:
+def _outer_strides(t: torch.Tensor):
+    """Strides of all dimensions but the last (which has to be contiguous).  The stride of a dimension
+    of size 1 is never used and may be anything in torch: it is given as if t were contiguous there."""
+    st, shape = list(t.stride()), t.shape
+    if shape[-1] > 1 and st[-1] != 1:
+        _refuse("a tensor with a strided last dimension", t)
+    for i in range(len(st) - 1):
+        if shape[i] == 1:
+            st[i] = max(shape[j] * (st[j] if j < len(st) - 1 else 1) for j in range(i + 1, len(st)))
+    return st[:-1]
+
+
+def _caches(k_cache, v_cache, k_scale, v_scale):
+    """(shape, strides, type code, scale addresses) of the two cache buffers, after checking them."""
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or (dtype is not _BF16 and dtype is not _E4M3):
+        _refuse("k_cache", k_cache)
+    if v_cache.shape != shape or v_cache.dtype is not dtype:
+        _refuse("v_cache", v_cache)
+    strides = _outer_strides(k_cache)
+    if strides != _outer_strides(v_cache):
         raise Q4KError(2, "k_cache and v_cache have different strides")
-    if k_cache.dtype == torch.float8_e4m3fn and k_scale is not None and v_scale is not None:
-        _want("k_scale", k_scale, shape[:3], _F32)
-        _want("v_scale", v_scale, shape[:3], _F32)
-    return shape, strides
+    if dtype is _BF16:
+        return shape, strides, 1, None, None
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None and (t.dtype is not _F32 or t.shape != shape[:3] or not t.is_contiguous()):
+            _refuse(name, t)
+    return shape, strides, 2, _ptr(k_scale), _ptr(v_scale)
 
 
 def q4k_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
@@ -460,17 +488,21 @@ def q4k_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache:
     """Write rows k, v [tokens, heads, dim] (fp32 or bf16, same strides) to the slots [tokens] int32
     (-1: skip) of the paged caches [pages, heads, page size, dim], bf16 or e4m3 (then with scales
     [pages, heads, page size] fp32)."""
-    (pages, heads, page, dim), strides = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    tokens = slots.shape[0] if slots.dim() == 1 else -1
-    _want("slots", slots, (tokens,), _I32)
-    _want("k", k, (tokens, heads, dim), _FLOATS, strided=True)
-    _want("v", v, (tokens, heads, dim), (k.dtype,), strided=True)
-    if (_ld(k), _ld(k, 1)) != (_ld(v), _ld(v, 1)):
+    shape, strides, code, ks, vs = _caches(k_cache, v_cache, k_scale, v_scale)
+    pages, heads, page, dim = shape
+    tokens, dtype = slots.numel(), k.dtype
+    if k.shape != (tokens, heads, dim) or (dtype is not _F32 and dtype is not _BF16):
+        _refuse("k", k)
+    if v.shape != k.shape or v.dtype is not dtype:
+        _refuse("v", v)
+    ld = _outer_strides(k)
+    if ld != _outer_strides(v):
         raise Q4KError(2, "k and v have different strides")
-    _check(lib().q4k_kv_write(_ptr(k), _ptr(v), Q4K_DTYPE[k.dtype], _ld(k), _ld(k, 1),
-                              _ptr(slots), tokens, heads, dim, _ptr(k_cache), _ptr(v_cache),
-                              Q4K_DTYPE[k_cache.dtype], pages, page, *strides, _ptr(k_scale),
-                              _ptr(v_scale), _stream(stream)), "q4k_kv_write")
+    _check((_lib or lib()).q4k_kv_write(
+        k.data_ptr(), v.data_ptr(), 1 if dtype is _BF16 else 0, ld[0], ld[1],
+        _vec("slots", slots, tokens, _I32), tokens, heads, dim, k_cache.data_ptr(),
+        v_cache.data_ptr(), code, pages, page, strides[0], strides[1], strides[2], ks, vs,
+        _call_stream(stream, k)), "q4k_kv_write")
 
 
 def q4k_paged_attn_workspace_size(n: int, q_heads: int, kv_heads: int, dim: int) -> int:
@@ -483,30 +515,37 @@ def q4k_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     """Attention of one new token per request: q [n, q_heads, dim] bf16 over the paged caches
     [pages, kv_heads, page size, dim] (bf16, or e4m3 with scales) by table [n, max_pages] and lens
     [n] int32.  Returns (out [n, q_heads, dim] bf16, lse [n, q_heads] fp32)."""
-    (pages, heads, page, dim), strides = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    n, q_heads = q.shape[:2] if q.dim() == 3 else (-1, -1)
-    _want("q", q, (n, q_heads, dim), _BF16, strided=True)
-    _want("table", table, (n, None), _I32, strided=True)
-    _want("lens", lens, (n,), _I32)
-    L = lib()
-    with _alloc_on(stream):
-        if out is None:
-            out = torch.empty((n, q_heads, dim), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((n, q_heads), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(max(L.q4k_paged_attn_workspace_size(n, q_heads, heads, dim), 16),
-                                    dtype=torch.uint8, device=q.device)
-    _want("out", out, (n, q_heads, dim), _BF16, strided=True)
-    _want("lse", lse, (n, q_heads), _F32)
-    if _ld(out, 1) != dim:
-        raise Q4KError(2, f"out has head stride {out.stride(1)}, not {dim}")
-    _check(L.q4k_paged_attn(_ptr(q), _ld(q), _ld(q, 1), n, q_heads, heads, dim, _ptr(k_cache),
-                            _ptr(v_cache), Q4K_DTYPE[k_cache.dtype], pages, page, *strides,
-                            _ptr(k_scale), _ptr(v_scale), _ptr(table), _ld(table),
-                            table.shape[1], _ptr(lens), softmax_scale, window, _ptr(out),
-                            _ld(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-                            _stream(stream)), "q4k_paged_attn")
+    shape, strides, code, ks, vs = _caches(k_cache, v_cache, k_scale, v_scale)
+    pages, heads, page, dim = shape
+    L = _lib or lib()
+    if q.dtype is not _BF16 or len(q.shape) != 3 or q.shape[2] != dim:
+        _refuse("q", q)
+    n, q_heads = q.shape[0], q.shape[1]
+    ldq = _outer_strides(q)
+    width = table.shape[-1]
+    ldt = _rows("table", table, n, width, _I32)
+    if out is None:
+        out = _empty((n, q_heads, dim), _BF16, q, stream)
+        ldo = q_heads * dim
+    else:
+        if out.dtype is not _BF16 or out.shape != q.shape:
+            _refuse("out", out)
+        ldo, inner = _outer_strides(out)
+        if inner != dim:
+            raise Q4KError(2, f"out has head stride {inner}, not {dim}")
+    if lse is None:
+        lse = _empty((n, q_heads), _F32, q, stream)
+    elif lse.dtype is not _F32 or lse.shape != (n, q_heads) or not lse.is_contiguous():
+        _refuse("lse", lse)
+    if workspace is None:
+        size = L.q4k_paged_attn_workspace_size(n, q_heads, heads, dim)
+        workspace = _empty(max(size, 16), torch.uint8, q, stream)
+    _check(L.q4k_paged_attn(
+        q.data_ptr(), ldq[0], ldq[1], n, q_heads, heads, dim, k_cache.data_ptr(),
+        v_cache.data_ptr(), code, pages, page, strides[0], strides[1], strides[2], ks, vs,
+        table.data_ptr(), ldt, width, _vec("lens", lens, n, _I32), softmax_scale, window,
+        out.data_ptr(), ldo, lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _call_stream(stream, q)), "q4k_paged_attn")
     return out, lse
 
 
@@ -516,32 +555,47 @@ def q4k_add_rmsnorm(x: torch.Tensor, residual, gamma: torch.Tensor, eps: float,
     bf16 (residual may be None).  Returns (y, residual_out) with y bf16, or (y, residual_out, scales)
     with y e4m3 (out_dtype torch.float8_e4m3fn) and scales [m, ceil(hidden / 128)] fp32; residual_out
     may be residual itself, and is None where residual is."""
-    m, hidden = x.shape if x.dim() == 2 else (-1, -1)
-    _want("x", x, (m, hidden), _FLOATS, strided=True)
-    _want("gamma", gamma, (hidden,), _F32)
+    dtype = x.dtype
+    if len(x.shape) != 2 or (dtype is not _F32 and dtype is not _BF16):
+        _refuse("x", x)
+    m, hidden = x.shape
+    ldx = _rows("x", x, m, hidden, dtype)
+    res = res_out = res_dtype = None
+    ldr = ldro = 0
     if residual is not None:
-        _want("residual", residual, (m, hidden), _FLOATS, strided=True)
-    e4m3 = (out_dtype if out is None else out.dtype) == torch.float8_e4m3fn
-    with _alloc_on(stream):
-        if out is None:
-            out = torch.empty((m, hidden), dtype=out_dtype, device=x.device)
-        if residual_out is None and residual is not None:
-            residual_out = torch.empty((m, hidden), dtype=residual.dtype, device=x.device)
-        if scales is None and e4m3:
-            scales = torch.empty((m, (hidden + 127) // 128), dtype=torch.float32, device=x.device)
-    _want("out", out, (m, hidden), (torch.bfloat16, torch.float8_e4m3fn), strided=True)
-    if residual is not None:
-        _want("residual_out", residual_out, (m, hidden), (residual.dtype,), strided=True)
-    if e4m3:
-        _want("scales", scales, (m, (hidden + 127) // 128), _F32, strided=True)
-    _check(lib().q4k_add_rmsnorm(
-        _ptr(x), Q4K_DTYPE[x.dtype], _ld(x), _ptr(residual),
-        1 if residual is None else Q4K_DTYPE[residual.dtype], 0 if residual is None else _ld(residual),
-        _ptr(gamma), eps, m, hidden, _ptr(out), Q4K_DTYPE[out.dtype], _ld(out),
-        None if residual is None else _ptr(residual_out),
-        0 if residual is None else _ld(residual_out), _ptr(scales) if e4m3 else None,
-        _ld(scales) if e4m3 else 0, _stream(stream)), "q4k_add_rmsnorm")
-    return (out, residual_out, scales) if e4m3 else (out, residual_out)
+        res_dtype = residual.dtype
+        if res_dtype is not _F32 and res_dtype is not _BF16:
+            _refuse("residual", residual)
+        ldr = _rows("residual", residual, m, hidden, res_dtype)
+        res = residual.data_ptr()
+        if residual_out is None:
+            residual_out, ldro = _empty((m, hidden), res_dtype, x, stream), hidden
+        else:
+            ldro = _rows("residual_out", residual_out, m, hidden, res_dtype)
+        res_out = residual_out.data_ptr()
+    else:
+        residual_out = None
+    if out is None:
+        out, ldy = _empty((m, hidden), out_dtype, x, stream), hidden
+    else:
+        out_dtype = out.dtype
+        ldy = _rows("out", out, m, hidden, out_dtype)
+    if out_dtype is _BF16:
+        code, sc, lds = 1, None, 0
+    elif out_dtype is _E4M3:
+        code, blocks = 2, (hidden + 127) // 128
+        if scales is None:
+            scales, lds = _empty((m, blocks), _F32, x, stream), blocks
+        else:
+            lds = _rows("scales", scales, m, blocks, _F32)
+        sc = scales.data_ptr()
+    else:
+        _refuse("out", out)
+    _check((_lib or lib()).q4k_add_rmsnorm(
+        x.data_ptr(), 1 if dtype is _BF16 else 0, ldx, res, 1 if res_dtype is _BF16 else 0, ldr,
+        _vec("gamma", gamma, hidden, _F32), eps, m, hidden, out.data_ptr(), code, ldy, res_out, ldro,
+        sc, lds, _call_stream(stream, x)), "q4k_add_rmsnorm")
+    return (out, residual_out) if code == 1 else (out, residual_out, scales)
 
 
 def q4k_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None,
@@ -549,23 +603,23 @@ def q4k_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=No
     """Choose a token per row of logits [rows, vocab] (fp32 or bf16) from the random numbers u [rows]
     fp32 in [0, 1); temperature, top_p, min_p (fp32) and top_k (int32) are [rows] or None (1, off).
     Returns (token [rows] int32, logp [rows] fp32)."""
-    rows, vocab = logits.shape if logits.dim() == 2 else (-1, -1)
-    _want("logits", logits, (rows, vocab), _FLOATS, strided=True)
-    _want("u", u, (rows,), _F32)
-    for name, t, kind in (("temperature", temperature, _F32), ("top_k", top_k, _I32),
-                          ("top_p", top_p, _F32), ("min_p", min_p, _F32)):
-        if t is not None:
-            _want(name, t, (rows,), kind)
-    with _alloc_on(stream):
-        if out is None:
-            out = torch.empty(rows, dtype=torch.int32, device=logits.device)
-        if logp is None:
-            logp = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _want("out", out, (rows,), _I32)
-    _want("logp", logp, (rows,), _F32)
-    _check(lib().q4k_sample(_ptr(logits), Q4K_DTYPE[logits.dtype], rows, vocab, _ld(logits),
-                            _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-                            _ptr(out), _ptr(logp), _stream(stream)), "q4k_sample")
+    dtype = logits.dtype
+    if len(logits.shape) != 2 or (dtype is not _F32 and dtype is not _BF16):
+        _refuse("logits", logits)
+    rows, vocab = logits.shape
+    ld = _rows("logits", logits, rows, vocab, dtype)
+    t = None if temperature is None else _vec("temperature", temperature, rows, _F32)
+    k = None if top_k is None else _vec("top_k", top_k, rows, _I32)
+    p = None if top_p is None else _vec("top_p", top_p, rows, _F32)
+    mp = None if min_p is None else _vec("min_p", min_p, rows, _F32)
+    if out is None:
+        out = _empty(rows, _I32, logits, stream)
+    if logp is None:
+        logp = _empty(rows, _F32, logits, stream)
+    _check((_lib or lib()).q4k_sample(
+        logits.data_ptr(), 1 if dtype is _BF16 else 0, rows, vocab, ld, _vec("u", u, rows, _F32), t, k,
+        p, mp, _vec("out", out, rows, _I32), _vec("logp", logp, rows, _F32),
+        _call_stream(stream, logits)), "q4k_sample")
     return out, logp
 
 

@@ -51,7 +51,8 @@
 namespace q4k {
 namespace {
 
-constexpr int kMaxSms = 160;  // SMs the workspace is sized for
+constexpr int kMaxSms = 160;   // SMs and warps per SM that the workspace is
+constexpr int kMaxWarps = 12;  // sized for
 
 template <int D, bool E4M3>
 struct Cfg {
@@ -61,12 +62,13 @@ struct Cfg {
   static constexpr int kParts = D * kEs / kRow;
   static constexpr int kSide = kTile * D * kEs;             // bytes of K (or V) per tile
   static constexpr int kScales = E4M3 ? kTile * 4 : 0;      // bytes of K (or V) scales per tile
-  static constexpr int kWarps = kSide >= 8192 ? 4 : 8;
-  static constexpr int kStages = kSide >= 4096 ? 3 : 4;
+  static constexpr int kWarps = kSide >= 8192 ? 6 : 12;
+  static constexpr int kStages = kSide >= 4096 ? 2 : 3;
   // per warp STAGES x (K | V), 1024-byte aligned as the swizzle wants it; then
   // per warp STAGES x (K scales | V scales)
   static constexpr int kRing = kStages * 2 * kSide, kScaleRing = kStages * 2 * kScales;
   static constexpr int kSmem = kWarps * (kRing + kScaleRing) + 1024;
+  static_assert(kWarps <= kMaxWarps, "the workspace has two slots for each of kMaxWarps warps");
   static_assert(kSide % 1024 == 0, "tile buffers keep the swizzle's alignment");
 };
 
@@ -81,13 +83,11 @@ struct Params {
   float *slots;
 };
 
-// Fewest tiles a warp takes: below this the join costs more than the split
-// gains.
-constexpr int kMinRun = 2;
-
+// Tiles per warp.  Even a run of one tile pays: for 22 tiles per head (one
+// request of 700 tokens) runs of 1, 2, 4 and 8 took 9.6, 10.9, 14.0 and 19.7 us.
 __device__ __forceinline__ int64_t run_of(int64_t tiles, int64_t warps) {
   const int64_t c = (tiles + warps - 1) / warps;
-  return c < kMinRun ? kMinRun : c;
+  return c < 1 ? 1 : c;
 }
 
 template <int TILE>
@@ -431,47 +431,68 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
   const uint32_t mt_stride = p.box_rows == 16 ? 16 * D * C::kEs : 16 * C::kRow;
 
   for (int i = 0; i < ST && to_issue > 0; ++i) issue(i);
+  __syncwarp();
   int slot = 0;
   uint32_t phase = 0;
   for (; to_do > 0; --to_do) {
+    const int4 hd = head[warp][slot];
+    const uint32_t valid = (uint32_t)hd.z;
+    if (hd.y & (1 << 16)) {  // a piece begins: its q is fetched while its first tile arrives
+      cur_r = hd.x, cur_item = hd.y & 0xffff;
+      start_piece();
+    }
     if (!mbar_wait(&full[warp][slot], phase, a.err)) {
       // copies still under way get the same time to land before the CTA ends
       if (lane == 0) drain_ring(full[warp], ST, slot, phase, (int)min(to_do - to_issue, (int64_t)ST));
       __syncwarp();
       return;
     }
-    const int4 hd = head[warp][slot];
-    const uint32_t valid = (uint32_t)hd.z;
-    if (hd.y & (1 << 16)) {
-      cur_r = hd.x, cur_item = hd.y & 0xffff;
-      start_piece();
-    }
     uint8_t *kt = ring + slot * 2 * C::kSide;
     const uint32_t kb = smem_u32(kt), vb = kb + C::kSide;
 
-    // S^T
+    // S^T, each 16 x 8 tile as the sum of CH chains of products (a chain waits
+    // for its previous product; four chains in all keep the tensor pipe fed)
+    constexpr int CH = MT * NQ >= 4 ? 1 : 4 / (MT * NQ);
     float z[MT][NQ][4];
+    {
+      float zc[CH][MT][NQ][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int j = 0; j < NQ; ++j) z[mt][j][0] = z[mt][j][1] = z[mt][j][2] = z[mt][j][3] = 0.f;
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int i = 0; i < LD; ++i) {
-        uint32_t k4[4];
-        ldsm(k4, kb + mt * mt_stride + (i / LPP) * part_stride + chunk[i % LPP]);
+          for (int j = 0; j < NQ; ++j) zc[c][mt][j][0] = zc[c][mt][j][1] = zc[c][mt][j][2] = zc[c][mt][j][3] = 0.f;
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) {
+      for (int i = 0; i < LD; ++i)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t k4[4];
+          ldsm(k4, kb + mt * mt_stride + (i / LPP) * part_stride + chunk[i % LPP]);
           if (!E4M3) {
-            mma_bf16(z[mt][j], k4[0], k4[1], k4[2], k4[3], qf[i][j][0], qf[i][j][1]);
+#pragma unroll
+            for (int j = 0; j < NQ; ++j)
+              mma_bf16(zc[i % CH][mt][j], k4[0], k4[1], k4[2], k4[3], qf[i][j][0], qf[i][j][1]);
           } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              mma_f16(z[mt][j], e4m3x2_f16(k4[2 * h]), e4m3x2_f16(k4[2 * h + 1]),
-                      e4m3x2_f16(k4[2 * h] >> 16), e4m3x2_f16(k4[2 * h + 1] >> 16),
-                      qf[2 * i + h][j][0], qf[2 * i + h][j][1]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a0 = e4m3x2_f16(k4[2 * h]), a1 = e4m3x2_f16(k4[2 * h + 1]);
+              const uint32_t a2 = e4m3x2_f16(k4[2 * h] >> 16), a3 = e4m3x2_f16(k4[2 * h + 1] >> 16);
+#pragma unroll
+              for (int j = 0; j < NQ; ++j)
+                mma_f16(zc[(2 * i + h) % CH][mt][j], a0, a1, a2, a3, qf[2 * i + h][j][0], qf[2 * i + h][j][1]);
+            }
           }
         }
-      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            z[mt][j][x] = zc[0][mt][j][x];
+#pragma unroll
+            for (int c = 1; c < CH; ++c) z[mt][j][x] += zc[c][mt][j][x];
+          }
     }
 
     // scores in base 2; tokens that are not there get -infinity
@@ -563,20 +584,31 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
         }
     }
 
-    // O^T
+    // O^T.  The products of two d-tiles are interleaved: hi and lo of one tile
+    // add to the same registers.
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      if (!E4M3) {
 #pragma unroll
-      for (int i = 0; i < LD; ++i) {
-        uint32_t v4[4];
-        ldsm_t(v4, vb + mt * mt_stride + (i / LPP) * part_stride + chunk[i % LPP]);
-        if (!E4M3) {
+        for (int i = 0; i < LD; i += 2) {
+          uint32_t v4[2][4];
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) {
-            mma_bf16(s.o[i][j], v4[0], v4[2], v4[1], v4[3], ph[mt][j][0], ph[mt][j][1]);
-            mma_bf16(s.o[i][j], v4[0], v4[2], v4[1], v4[3], pl[mt][j][0], pl[mt][j][1]);
-          }
-        } else {
+          for (int x = 0; x < 2; ++x)
+            ldsm_t(v4[x], vb + mt * mt_stride + ((i + x) / LPP) * part_stride + chunk[(i + x) % LPP]);
+#pragma unroll
+          for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int j = 0; j < NQ; ++j)
+                mma_bf16(s.o[i + x][j], v4[x][0], v4[x][2], v4[x][1], v4[x][3],
+                         lo ? pl[mt][j][0] : ph[mt][j][0], lo ? pl[mt][j][1] : ph[mt][j][1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+          uint32_t v4[4];
+          ldsm_t(v4, vb + mt * mt_stride + (i / LPP) * part_stride + chunk[i % LPP]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // bytes (key 2t: d 2g, 2g + 1; key 2t + 1: the same) to fp16 pairs
@@ -588,8 +620,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
           }
         }
       }
+    }
     __syncwarp();
     if (to_issue > 0) issue(slot);
+    __syncwarp();  // the tile's header, written by lane 0, is read before its barrier
     if (++slot == ST) slot = 0, phase ^= 1u;
 
     if (hd.y & (1 << 17)) {  // the piece ends
@@ -618,17 +652,18 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
 }
 
 // Joins the pieces of the items that several warps share, and writes the items
-// without tokens.  One CTA per item: D / 16 warps, one per 16 values of the
-// row, times `ways` warps that take the pieces in turn.  Item i covers tiles
+// without tokens.  A warp joins 16 of an item's D values; a CTA has `dts` such
+// warps, times `ways` that take the pieces in turn.  Item i covers tiles
 // [A, B) of the list, so its pieces are those of warps A / run .. (B-1) / run;
 // the first of them is its warp's slot 1 (it starts the item), the others are
 // slot 0.
 template <int D, bool E4M3, int NQ>
-__global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Params p, int ways) {
+__global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Params p, int dts, int ways) {
   constexpr int KS = D / 16;
   extern __shared__ float part[];
   const AttnArgs &a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dt = warp % KS, way = warp / KS;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp / dts;
+  const int dt = blockIdx.y * dts + warp % dts;
   const int r = blockIdx.x / p.items, item = blockIdx.x % p.items;
   grid_dependency_wait();
   const int64_t before = p.prefix[r], nt = p.prefix[r + 1] - before, run = run_of(p.prefix[a.n] * p.items, p.warps);
@@ -682,7 +717,7 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Param
     __syncthreads();
     if (way) return;
     for (int v = 1; v < ways; ++v) {
-      const float4 *from = reinterpret_cast<const float4 *>(part) + (warp + v * KS) * NQ * 64 + lane;
+      const float4 *from = reinterpret_cast<const float4 *>(part) + (warp + v * dts) * NQ * 64 + lane;
 #pragma unroll
       for (int j = 0; j < NQ; ++j) add(from[j * 64], from[j * 64 + 32], j);
     }
@@ -701,14 +736,6 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Param
   write_out<D, E4M3, NQ>(p, all, r, item, dt, dt + 1, dt == 0);
 }
 
-struct Shape {
-  int nq, groups, warps_per_cta, slot;
-};
-
-template <int D, bool E4M3>
-constexpr int warps_of() {
-  return Cfg<D, E4M3>::kWarps;
-}
 int query_tiles(int dim, int group) { return group > 8 && dim <= 128 ? 2 : 1; }
 size_t slot_bytes(int dim, int nq) { return (size_t)32 * nq * (dim / 16 * 4 + 4) * 4; }
 size_t prefix_bytes(int n) { return ((size_t)(n + 1) * 8 + 255) / 256 * 256; }
@@ -744,20 +771,24 @@ cudaError_t launch_cfg(Params &p, cudaStream_t stream) {
   paged_attn_kernel<D, E4M3, NQ><<<grid, C::kWarps * 32, C::kSmem, stream>>>(p, maps[0], maps[1]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // Few items: their pieces are many, so several warps share them.
-  const int64_t items = (int64_t)a.n * p.items;
-  const int ways = items <= 2 * f->sm_count ? 512 / (D / 16 * 32) : 1;
+  // An item has about warps / items pieces; a warp takes 4 to 8 of them.  (One
+  // CTA per item with its D / 16 warps alone took 11 us for 16 items of 114
+  // pieces; 16 ways for every item took 40 us for 256 items of 4.)
+  const int64_t items = (int64_t)a.n * p.items, pieces = p.warps / items;
+  int ways = 1;
+  while (ways < 16 && ways * 4 < pieces) ways *= 2;
+  const int dts = D / 16 < 16 / ways ? D / 16 : 16 / ways;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)items);
-  cfg.blockDim = dim3(D / 16 * 32 * ways);
-  cfg.dynamicSmemBytes = ways > 1 ? (size_t)D / 16 * ways * NQ * 64 * 16 : 0;
+  cfg.gridDim = dim3((unsigned)items, D / 16 / dts);
+  cfg.blockDim = dim3(dts * ways * 32);
+  cfg.dynamicSmemBytes = ways > 1 ? (size_t)dts * ways * NQ * 64 * 16 : 0;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<D, E4M3, NQ>, p, ways);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<D, E4M3, NQ>, p, dts, ways);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -773,7 +804,7 @@ cudaError_t launch_nq(Params &p, int nq, cudaStream_t s) {
 
 size_t paged_attn_workspace_size(int32_t n, int32_t q_heads, int32_t kv_heads, int32_t dim) {
   const int nq = query_tiles(dim, q_heads / (kv_heads < q_heads ? kv_heads : q_heads));
-  return prefix_bytes(n) + (size_t)kMaxSms * 8 * 2 * slot_bytes(dim, nq);
+  return prefix_bytes(n) + (size_t)kMaxSms * kMaxWarps * 2 * slot_bytes(dim, nq);
 }
 
 cudaError_t launch_paged_attn(const AttnArgs &a, cudaStream_t s) {
