@@ -571,7 +571,8 @@ int q4k_kv_plan(const int32_t *lens, const int32_t *add, int32_t n, int32_t *tab
                 int32_t *pos, int64_t n_slots, int32_t *status, int32_t *pool_state_out,
                 void *stream) {
   if (n < 0 || n > 65536 || max_pages <= 0 || page_size <= 0 || pool_size <= 0 || n_slots < 0 ||
-      n_slots > INT32_MAX || ldt < max_pages || (int64_t)pool_size * page_size > INT32_MAX)
+      n_slots > INT32_MAX || ldt < max_pages || (int64_t)pool_size * page_size > INT32_MAX ||
+      (int64_t)max_pages * page_size > (1 << 30))
     return Q4K_ERR_SHAPE;
   if (n == 0) return Q4K_OK;
   if (!lens || !add || !table || !pool || !pool_state || !lens_out || !cu || !status ||

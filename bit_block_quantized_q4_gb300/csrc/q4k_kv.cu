@@ -30,9 +30,9 @@ namespace {
 // state gives the same result.
 //
 // What bounds it: latency (a few hundred KB at most).  One cluster of 1..8
-// CTAs: every CTA scans all requests, 1024 at a time (cheaper than passing
-// sums between CTAs), and the requests' writes are divided among them.  A
-// cluster barrier between the reads and the writes of a chunk is what allows
+// CTAs: every CTA scans all requests, a block's width at a time (cheaper than
+// passing sums between CTAs), and the requests' writes are divided among them.
+// A cluster barrier between the reads and the writes of a chunk is what allows
 // lens_out == lens and state_out == state.
 
 constexpr int kPlanThreads = 1024;
@@ -47,198 +47,211 @@ struct PlanArgs {
   int64_t *cu;
   int32_t *slots, *pos, *status, *state_out;
   int64_t n_slots;
-  int n, width, page, pool_size;
+  int n, capacity;  // capacity: tokens of a table row, < 2^31
+  uint32_t pool_size;
+  FastDiv page;
   unsigned *err;
 };
 
-struct Sums {
-  int64_t tokens, need, back;
-};
-__device__ __forceinline__ Sums operator+(const Sums &a, const Sums &b) {
-  return {a.tokens + b.tokens, a.need + b.need, a.back + b.back};
+// Inclusive sum over the block, and the block's total.  `part` holds one value
+// per warp; the caller's barriers separate its uses.
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
 }
-__device__ __forceinline__ Sums shfl_up(const Sums &s, int o) {
-  return {__shfl_up_sync(0xffffffffu, s.tokens, o), __shfl_up_sync(0xffffffffu, s.need, o),
-          __shfl_up_sync(0xffffffffu, s.back, o)};
+__device__ __forceinline__ int64_t before_warp(const int64_t *part, int warps, int warp, int64_t &total) {
+  const int lane = threadIdx.x & 31;
+  const int64_t incl = warp_scan(lane < warps ? part[lane] : 0);
+  total = __shfl_sync(0xffffffffu, incl, 31);
+  const int64_t prev = __shfl_sync(0xffffffffu, incl, warp ? warp - 1 : 0);
+  return warp ? prev : 0;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a) {
-  __shared__ Sums warp_sums[32];
-  __shared__ unsigned long long taken_max;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int64_t part[3][32];
+  __shared__ unsigned taken_max;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int rank = (int)cluster_ctarank(), ranks = (int)gridDim.x;
-  const int64_t size = a.pool_size;
-  const int64_t head = ((a.state[0] % size) + size) % size;
-  const int64_t count = min(max((int64_t)a.state[1], (int64_t)0), size);
-  const int ps = a.page;
+  const uint32_t size = a.pool_size, ps = a.page.d;
+  const int64_t head_in = a.state[0] % (int64_t)size;
+  const uint32_t head = (uint32_t)(head_in < 0 ? head_in + size : head_in);
+  const uint32_t count = (uint32_t)min(max((int64_t)a.state[1], (int64_t)0), (int64_t)size);
+  const auto ring = [&](uint32_t i) {  // i < 2 size: head + an offset into the ring
+    return i >= size ? i - size : i;
+  };
   if (tid == 0) taken_max = 0;
-  Sums carry = {0, 0, 0};
+  int64_t tokens0 = 0, need0 = 0, back0 = 0;  // of the chunks before
   bool bad_page = false;
 
-  for (int r0 = 0; r0 < a.n; r0 += kPlanThreads) {
+  for (int r0 = 0; r0 < a.n; r0 += blockDim.x) {
     const int r = r0 + tid;
     const bool in = r < a.n;
-    const int64_t len = in ? a.lens[r] : 0, add = in ? a.add[r] : 0;
-    const int64_t more = max(add, (int64_t)0);
-    const bool bad = len < 0 || add < -1 || len + more > (int64_t)a.width * ps;
+    const int len = in ? a.lens[r] : 0, add = in ? a.add[r] : 0, more = max(add, 0);
+    const bool bad = len < 0 || add < -1 || (int64_t)len + more > a.capacity;
     const bool done = add == -1;
-    const int64_t have = bad ? 0 : (len + ps - 1) / ps;
-    // prefix of the tokens first: a request whose tokens do not fit the slot
-    // map asks for no pages
-    int64_t t = more;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += u;
-    }
-    if (lane == 31) warp_sums[warp].tokens = t;
+    const int have = bad ? 0 : (int)a.page.div(len + ps - 1);
+    // tokens first: a request whose tokens do not fit the slot map asks for no pages
+    int64_t t = warp_scan(more);
+    if (lane == 31) part[0][warp] = t;
     __syncthreads();
-    int64_t chunk_tokens = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) t += warp_sums[w].tokens;
-      chunk_tokens += warp_sums[w].tokens;
-    }
-    const int64_t cu1 = carry.tokens + t, cu0 = cu1 - more;
+    int64_t chunk_tokens, chunk_need, chunk_back;
+    t += before_warp(part[0], warps, warp, chunk_tokens);
+    const int64_t cu1 = tokens0 + t, cu0 = cu1 - more;
     const bool lng = !bad && more > 0 && cu1 > a.n_slots;
-    const int64_t need = bad || done || lng ? 0 : (len + more + ps - 1) / ps - have;
-    const int64_t back = done && !bad ? have : 0;
-    int64_t p = need, q = back;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, p, o), v = __shfl_up_sync(0xffffffffu, q, o);
-      if (lane >= o) p += u, q += v;
-    }
-    if (lane == 31) warp_sums[warp].need = p, warp_sums[warp].back = q;
+    const int need = bad || done || lng ? 0 : (int)a.page.div(len + more + ps - 1) - have;
+    const int back = done && !bad ? have : 0;
+    int64_t p = warp_scan(need), q = warp_scan(back);
+    if (lane == 31) part[1][warp] = p, part[2][warp] = q;
     // every lens, add and state value of this chunk has been read by every CTA
     // before any CTA writes outputs that may be the same buffers
     cluster_sync();
-    Sums chunk = {chunk_tokens, 0, 0};
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) p += warp_sums[w].need, q += warp_sums[w].back;
-      chunk.need += warp_sums[w].need, chunk.back += warp_sums[w].back;
-    }
-    const int64_t upto = carry.need + p, first = upto - need, back0 = carry.back + q - back;
+    p += before_warp(part[1], warps, warp, chunk_need);
+    q += before_warp(part[2], warps, warp, chunk_back);
+    const int64_t upto = need0 + p, given = back0 + q - back;
     const bool granted = !bad && !lng && !done && (need == 0 || upto <= count);
-    if (granted && need > 0) atomicMax(&taken_max, (unsigned long long)upto);
+    if (granted && need > 0) atomicMax(&taken_max, (unsigned)upto);
+    // ring index of its first new page; only used where upto <= count <= size
+    const uint32_t first = granted && need ? ring(head + (uint32_t)(upto - need)) : 0u;
+    // tokens that the slot map has room for
+    const int room = (int)max(min((int64_t)more, a.n_slots - cu0), (int64_t)0);
 
     // Small outputs of the warp's 32 requests: one CTA of the cluster.
     if (in && warp % ranks == rank) {
       a.status[r] = bad ? Q4K_KV_BAD_LENGTH : lng ? Q4K_KV_NO_SLOTS : granted || done ? Q4K_KV_OK : Q4K_KV_NO_PAGES;
-      a.lens_out[r] = (int32_t)(granted ? len + more : done && !bad ? 0 : len);
+      a.lens_out[r] = granted ? len + more : done && !bad ? 0 : len;
       a.cu[r] = cu0;
       if (r == a.n - 1) a.cu[a.n] = cu1;
     }
     // Tokens and pages.  Requests with at most 4 tokens or pages to move are
     // written by their own lane; the others by the warp together, their
     // elements divided among the CTAs of the cluster.
-    const int64_t work = max(max(more, granted ? need : (int64_t)0), back);
-    const bool small = in && work <= 4;
-    auto token = [&](int64_t i, int64_t at, int64_t ln, int64_t hv, int64_t fst, int64_t row, bool ok) {
-      if (at >= a.n_slots) return;
+    const auto token = [&](int i, int64_t at, int ln, int hv, uint32_t fst, int64_t row, bool ok) {
       int32_t slot = -1, where = -1;
       if (ok) {
-        const int64_t pp = ln + i, pg = pp / ps;
-        const int32_t id = pg < hv ? a.table[row * a.ldt + pg] : a.pool[(head + fst + pg - hv) % size];
+        const uint32_t pp = ln + i, pg = a.page.div(pp);
+        const int32_t id = (int)pg < hv ? a.table[row * a.ldt + pg] : a.pool[ring(fst + (pg - hv))];
         where = (int32_t)pp;
-        if (id >= 0 && id < a.pool_size) slot = id * ps + (int32_t)(pp - pg * ps);
+        if ((uint32_t)id < size) slot = id * ps + (pp - pg * ps);
         else bad_page = true;
       }
       a.slots[at] = slot;
       a.pos[at] = where;
     };
-    auto fresh = [&](int64_t j, int64_t hv, int64_t fst, int64_t row) {
-      a.table[row * a.ldt + hv + j] = a.pool[(head + fst + j) % size];
+    const auto fresh = [&](int j, int hv, uint32_t fst, int64_t row) {
+      a.table[row * a.ldt + hv + j] = a.pool[ring(fst + j)];
     };
-    auto give = [&](int64_t j, int64_t b0, int64_t row) {
-      if (b0 + j < size - count) a.pool[(head + count + b0 + j) % size] = a.table[row * a.ldt + j];
+    const auto give = [&](int j, int64_t b0, int64_t row) {
+      // the ring has size - count entries left; the rest is dropped
+      if (b0 + j < size - count) a.pool[ring(ring(head + count) + (uint32_t)(b0 + j))] = a.table[row * a.ldt + j];
       else bad_page = true;
     };
+    const int pages = granted ? need : 0;
+    const bool small = in && max(max(room, pages), back) <= 4;
     if (small && warp % ranks == rank) {
-      for (int64_t i = 0; i < more; ++i) token(i, cu0 + i, len, have, first, r, granted);
-      if (granted)
-        for (int64_t j = 0; j < need; ++j) fresh(j, have, first, r);
-      for (int64_t j = 0; j < back; ++j) give(j, back0, r);
+      for (int i = 0; i < room; ++i) token(i, cu0 + i, len, have, first, r, granted);
+      for (int j = 0; j < pages; ++j) fresh(j, have, first, r);
+      for (int j = 0; j < back; ++j) give(j, given, r);
     }
     unsigned big = __ballot_sync(0xffffffffu, in && !small);
     while (big) {
       const int src = __ffs(big) - 1;
       big &= big - 1;
       const int64_t rr = r0 + warp * 32 + src;
-      const int64_t m = __shfl_sync(0xffffffffu, more, src), nd = __shfl_sync(0xffffffffu, granted ? need : 0, src);
-      const int64_t bk = __shfl_sync(0xffffffffu, back, src), c0 = __shfl_sync(0xffffffffu, cu0, src);
-      const int64_t ln = __shfl_sync(0xffffffffu, len, src), hv = __shfl_sync(0xffffffffu, have, src);
-      const int64_t fs = __shfl_sync(0xffffffffu, first, src), b0 = __shfl_sync(0xffffffffu, back0, src);
-      const bool ok = __shfl_sync(0xffffffffu, (int)granted, src);
-      const int64_t m_in = min(m, max(a.n_slots - c0, (int64_t)0));
-      for (int64_t i = rank * 32 + lane; i < m_in; i += 32 * ranks) token(i, c0 + i, ln, hv, fs, rr, ok);
-      for (int64_t j = rank * 32 + lane; j < nd; j += 32 * ranks) fresh(j, hv, fs, rr);
-      for (int64_t j = rank * 32 + lane; j < bk; j += 32 * ranks) give(j, b0, rr);
+      const int m = __shfl_sync(0xffffffffu, room, src), nd = __shfl_sync(0xffffffffu, pages, src);
+      const int bk = __shfl_sync(0xffffffffu, back, src), ln = __shfl_sync(0xffffffffu, len, src);
+      const int hv = __shfl_sync(0xffffffffu, have, src), ok = __shfl_sync(0xffffffffu, (int)granted, src);
+      const int64_t c0 = __shfl_sync(0xffffffffu, cu0, src), b0 = __shfl_sync(0xffffffffu, given, src);
+      const uint32_t fs = __shfl_sync(0xffffffffu, first, src);
+      const int step = 32 * ranks, i0 = rank * 32 + lane;
+      for (int i = i0; i < m; i += step) token(i, c0 + i, ln, hv, fs, rr, ok);
+      for (int j = i0; j < nd; j += step) fresh(j, hv, fs, rr);
+      for (int j = i0; j < bk; j += step) give(j, b0, rr);
     }
-    carry = carry + chunk;
-    __syncthreads();  // warp_sums are rewritten in the next chunk
+    tokens0 += chunk_tokens, need0 += chunk_need, back0 += chunk_back;
+    __syncthreads();  // part[] is rewritten in the next chunk
   }
-  for (int64_t t = carry.tokens + rank * kPlanThreads + tid; t < a.n_slots; t += (int64_t)ranks * kPlanThreads)
+  for (int64_t t = tokens0 + rank * blockDim.x + tid; t < a.n_slots; t += (int64_t)ranks * blockDim.x)
     a.slots[t] = -1, a.pos[t] = -1;
   if (rank == 0 && tid == 0) {
-    const int64_t taken = (int64_t)taken_max;
-    a.state_out[0] = (int32_t)((head + taken) % size);
-    a.state_out[1] = (int32_t)(count - taken + min(carry.back, size - count));
+    a.state_out[0] = (int32_t)ring(head + taken_max);
+    a.state_out[1] = (int32_t)(count - taken_max + min(back0, (int64_t)(size - count)));
   }
   if (bad_page) set_device_error(a.err, kDevErrBadPage);
 }
 
 // --------------------------------------------------------------------- write
 //
-// One row (token, head) of K or V: D/8 lanes of 8 values each.  Bound by
-// bytes: inputs read once, cache rows written once.
+// One row (token, head) of K or V: D/8 lanes of 8 values each; a block takes
+// rows of one head, a lane kWriteRows of them so that as many loads are under
+// way.  Bound by bytes (inputs read once, cache rows written once), with the
+// instructions of a row close behind: with the token and the page from 64-bit
+// divisions the 16001 x 8 x 128 bf16 -> e4m3 write took 71 us, with 32-bit ones
+// 42 us.
+
+constexpr int kWriteRows = 4;
 
 struct WriteArgs {
   const void *in[2];
   void *cache[2];
   float *scale[2];
   const int32_t *slots;
-  int64_t tokens, ld_token, ld_head, page_stride, head_stride, token_stride, n_slots;
-  int heads, page;
+  int64_t ld_token, ld_head, page_stride, head_stride, token_stride;
+  uint32_t tokens, heads, n_slots;
+  FastDiv page;
   unsigned *err;
 };
 
 template <int D, typename TI, bool E4M3>
 __global__ void __launch_bounds__(256) kv_write_kernel(const WriteArgs a) {
-  constexpr int LPR = D / 8;  // lanes per row
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
-  const int c = threadIdx.x % LPR;
-  const int64_t t = row / a.heads;
-  const int h = (int)(row - t * a.heads), kv = blockIdx.y;
-  if (t >= a.tokens) return;  // whole warps or whole rows: the shuffles below stay within a row
-  const int64_t slot = a.slots[t];
-  if (slot < 0 || slot >= a.n_slots) {
-    if (slot != -1 && c == 0) set_device_error(a.err, kDevErrBadPage);
-    return;
+  constexpr int LPR = D / 8, RPB = 256 / LPR;  // lanes per row, rows per block and step
+  const int c = threadIdx.x % LPR, kv = blockIdx.z;
+  const uint32_t h = blockIdx.y, t0 = blockIdx.x * (RPB * kWriteRows) + threadIdx.x / LPR;
+  const TI *in = static_cast<const TI *>(a.in[kv]) + h * a.ld_head + c * 8;
+  float v[kWriteRows][8];
+  int32_t slot[kWriteRows];
+#pragma unroll
+  for (int i = 0; i < kWriteRows; ++i) {
+    const uint32_t t = t0 + i * RPB;
+    slot[i] = -1;
+    if (t < a.tokens) {
+      slot[i] = a.slots[t];
+      load8(in + t * a.ld_token, v[i]);
+    }
   }
-  const int64_t page = slot / a.page, off = slot - page * a.page;
-  float v[8];
-  load8(static_cast<const TI *>(a.in[kv]) + t * a.ld_token + h * a.ld_head + c * 8, v);
-  const int64_t to = page * a.page_stride + h * a.head_stride + off * a.token_stride + c * 8;
-  if (!E4M3) {
-    store8(static_cast<__nv_bfloat16 *>(a.cache[kv]) + to, v);
-  } else {
-    float amax = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    const unsigned mask = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << ((threadIdx.x & 31) / LPR * LPR);
+  for (int i = 0; i < kWriteRows; ++i) {
+    // all lanes of a row agree on its slot, so the shuffles below are complete
+    if ((uint32_t)slot[i] >= a.n_slots) {
+      if (slot[i] != -1 && c == 0) set_device_error(a.err, kDevErrBadPage);
+      continue;
+    }
+    const uint32_t page = a.page.div(slot[i]), off = slot[i] - page * a.page.d;
+    const int64_t to = page * a.page_stride + h * a.head_stride + off * a.token_stride + c * 8;
+    if (!E4M3) {
+      store8(static_cast<__nv_bfloat16 *>(a.cache[kv]) + to, v[i]);
+    } else {
+      float amax = 0.f;
 #pragma unroll
-    for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
-    amax = fmaxf(amax, kAmaxFloor);
-    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.cache[kv]) + to) = to_e4m3x8(v, 448.f / amax);
-    if (c == 0) a.scale[kv][(page * a.heads + h) * a.page + off] = amax / 448.f;
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[i][j]));
+      const unsigned mask = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << ((threadIdx.x & 31) / LPR * LPR);
+#pragma unroll
+      for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
+      amax = fmaxf(amax, kAmaxFloor);
+      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.cache[kv]) + to) = to_e4m3x8(v[i], 448.f / amax);
+      if (c == 0) a.scale[kv][((int64_t)page * a.heads + h) * a.page.d + off] = amax / 448.f;
+    }
   }
 }
 
 template <int D>
 void launch_write_d(const WriteArgs &a, bool bf16_in, bool e4m3, cudaStream_t s) {
-  const int64_t rows = a.tokens * a.heads;
-  constexpr int kRows = 256 / (D / 8);
-  const dim3 grid((unsigned)((rows + kRows - 1) / kRows), 2);
+  constexpr uint32_t kRows = 256 / (D / 8) * kWriteRows;
+  const dim3 grid((a.tokens + kRows - 1) / kRows, a.heads, 2);
   if (bf16_in && e4m3) kv_write_kernel<D, __nv_bfloat16, true><<<grid, 256, 0, s>>>(a);
   else if (bf16_in) kv_write_kernel<D, __nv_bfloat16, false><<<grid, 256, 0, s>>>(a);
   else if (e4m3) kv_write_kernel<D, float, true><<<grid, 256, 0, s>>>(a);
@@ -253,13 +266,14 @@ cudaError_t launch_kv_plan(const int32_t *lens, const int32_t *add, int32_t n, i
                            int32_t *slots, int32_t *pos, int64_t n_slots, int32_t *status,
                            int32_t *state_out, cudaStream_t stream) {
   const PlanArgs a = {lens, add, table, ldt, pool, state, lens_out, cu, slots, pos, status, state_out,
-                      n_slots, n, width, page, pool_size, device_error_word()};
-  // One CTA writes about 4096 tokens in the time that a wider cluster's
-  // barriers take.
+                      n_slots, n, width * page, (uint32_t)pool_size, FastDiv(page), device_error_word()};
   const int ranks = n_slots <= 4096 ? 1 : n_slots <= 16384 ? 4 : 8;
+  // a block as wide as the requests, and wide enough for the slots
+  const int64_t wide = n > n_slots / 8 ? n : n_slots / 8;
+  const int threads = wide >= kPlanThreads ? kPlanThreads : ((int)wide + 31) / 32 * 32;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -277,9 +291,9 @@ cudaError_t launch_kv_write(const void *k, const void *v, int in_dtype, int64_t 
                             int64_t n_pages, int32_t page, int64_t page_stride, int64_t head_stride,
                             int64_t token_stride, float *k_scale, float *v_scale,
                             cudaStream_t stream) {
-  const WriteArgs a = {{k, v}, {k_cache, v_cache}, {k_scale, v_scale}, slots, tokens, ld_token,
-                       ld_head, page_stride, head_stride, token_stride, n_pages * page, heads, page,
-                       device_error_word()};
+  const WriteArgs a = {{k, v}, {k_cache, v_cache}, {k_scale, v_scale}, slots, ld_token, ld_head,
+                       page_stride, head_stride, token_stride, (uint32_t)tokens, (uint32_t)heads,
+                       (uint32_t)(n_pages * page), FastDiv(page), device_error_word()};
   const bool b = in_dtype == Q4K_DTYPE_BF16, e = cache_dtype == Q4K_DTYPE_E4M3;
   if (dim == 64) launch_write_d<64>(a, b, e, stream);
   else if (dim == 128) launch_write_d<128>(a, b, e, stream);

@@ -25,6 +25,9 @@
 namespace q4k {
 namespace {
 
+constexpr int kMinBlocks = 1;
+constexpr int kThreadsPerRow = 640;
+
 struct NormArgs {
   const void *x;
   const void *res;
@@ -41,8 +44,8 @@ struct NormArgs {
 // is vector t + i * tpr of the row, so the 16 vectors of a 128-value block lie
 // in one half-warp (tpr is a multiple of 32).
 template <int NV, typename TX, typename TR, bool E4M3>
-__global__ void __launch_bounds__(512) add_rmsnorm_kernel(const NormArgs a) {
-  __shared__ float part[16];
+__global__ void __launch_bounds__(1024, NV <= 2 ? kMinBlocks : 1) add_rmsnorm_kernel(const NormArgs a) {
+  __shared__ float part[32];
   const int tpr = blockDim.x;
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < a.m;
@@ -136,16 +139,16 @@ void launch_nv(const NormArgs &a, bool e4m3, dim3 grid, dim3 block, cudaStream_t
 template <typename TX, typename TR>
 void launch_types(const NormArgs &a, bool e4m3, cudaStream_t s) {
   const int nvec = a.h / 8;
-  // One vector per thread while 512 threads cover the row, then 2, 4 or 8.
-  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8;
+  int nv = (nvec + kThreadsPerRow - 1) / kThreadsPerRow;
+  if (nv > 4) nv = 4;
   const int tpr = ((nvec + nv - 1) / nv + 31) / 32 * 32;
   const int rows = tpr >= 256 ? 1 : 256 / tpr;
   const dim3 block(tpr, rows), grid((unsigned)((a.m + rows - 1) / rows));
   switch (nv) {
     case 1: launch_nv<1, TX, TR>(a, e4m3, grid, block, s); break;
     case 2: launch_nv<2, TX, TR>(a, e4m3, grid, block, s); break;
-    case 4: launch_nv<4, TX, TR>(a, e4m3, grid, block, s); break;
-    default: launch_nv<8, TX, TR>(a, e4m3, grid, block, s); break;
+    case 3: launch_nv<3, TX, TR>(a, e4m3, grid, block, s); break;
+    default: launch_nv<4, TX, TR>(a, e4m3, grid, block, s); break;
   }
 }
 

@@ -10,6 +10,25 @@
 
 namespace q4k {
 
+// Division of 0 <= x < 2^31 by a fixed 1 <= d < 2^31 with one multiplication:
+// with s = ceil(log2 d) and m = floor(2^(31+s) / d) + 1 (< 2^32 + 1; d = 1 and
+// other powers of two are shifts), x m / 2^(31+s) exceeds x / d by less than
+// 1 / d for x < 2^31, so its floor is the quotient.
+struct FastDiv {
+  uint32_t d, m, s;  // m = 0: shift by s
+  explicit FastDiv(uint32_t div) : d(div), m(0), s(0) {
+    while (s < 31 && (1u << s) < d) ++s;
+    if ((1u << s) != d) {
+      m = (uint32_t)(((uint64_t)1 << (31 + s)) / d + 1);
+      --s;
+    }
+  }
+  __host__ __device__ uint32_t div(uint32_t x) const {
+    if (!m) return x >> s;
+    return (uint32_t)(((uint64_t)x * m) >> 32) >> s;
+  }
+};
+
 // The smallest block maximum a scale is derived from: keeps 448 / max finite
 // and the scale a normal number, so a block of zeros has a scale of its own.
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100

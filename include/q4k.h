@@ -508,7 +508,8 @@ int q4k_moe_gemv_noalloc(const void *w_gate, const void *w_up, const void *w_dow
  * A page id outside the pool gives slot -1 and sets Q4K_DEVERR_BAD_PAGE; so
  * does a returned page for which the ring has no entry left (a page returned
  * twice), which is dropped.
- * Limits: n <= 65536, pool_size * page_size < 2^31, n_slots < 2^31.
+ * Limits: n <= 65536, pool_size * page_size < 2^31, max_pages * page_size <=
+ * 2^30, n_slots < 2^31.
  * Errors: NULL, SHAPE, ALIGN (4 bytes; cu 8), DEVICE, MEMORY, CUDA.
  */
 enum q4k_kv_status {
