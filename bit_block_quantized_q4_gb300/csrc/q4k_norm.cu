@@ -25,8 +25,9 @@
 namespace q4k {
 namespace {
 
-constexpr int kMinBlocks = 1;
-constexpr int kThreadsPerRow = 640;
+constexpr int kMaxStages = 4;
+constexpr int kRowsSmThreads = 1536;  // threads per SM of the many-rows kernel
+constexpr int kRingBytes = 200 << 10;  // shared memory of an SM given to rings
 
 struct NormArgs {
   const void *x;
@@ -38,13 +39,41 @@ struct NormArgs {
   int64_t m, ldx, ldr, ldy, ldro, lds;
   int h;
   float eps;
+  unsigned *err;
 };
 
-// Block (tpr, rows): tpr threads (whole warps) per row.  Vector i of thread t
-// is vector t + i * tpr of the row, so the 16 vectors of a 128-value block lie
-// in one half-warp (tpr is a multiple of 32).
+// y of one 8-value vector: `in` is false for lanes past the end of the row,
+// which take part in the half-warp's block maximum with 0.
+template <bool E4M3>
+__device__ __forceinline__ void write_y(const NormArgs &a, int64_t row, int vec, bool in, float rinv, float (&v)[8]) {
+  float amax = 0.f;
+  if (in) {
+    float g[8];
+    load8(a.gamma + vec * 8, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = v[j] * rinv * g[j];
+      if (E4M3) amax = fmaxf(amax, fabsf(v[j]));
+    }
+  }
+  if constexpr (E4M3) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    amax = fmaxf(amax, kAmaxFloor);
+    if (in) {
+      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.y) + row * a.ldy + vec * 8) = to_e4m3x8(v, 448.f / amax);
+      if ((vec & 15) == 0) a.scales[row * a.lds + (vec >> 4)] = amax / 448.f;
+    }
+  } else if (in) {
+    store8(static_cast<__nv_bfloat16 *>(a.y) + row * a.ldy + vec * 8, v);
+  }
+}
+
+// Few rows: a block (tpr, rows) loads its rows straight into registers, tpr
+// threads (whole warps) per row.  Vector i of thread t is vector t + i * tpr of
+// the row, so the 16 vectors of a 128-value block lie in one half-warp.
 template <int NV, typename TX, typename TR, bool E4M3>
-__global__ void __launch_bounds__(1024, NV <= 2 ? kMinBlocks : 1) add_rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
   __shared__ float part[32];
   const int tpr = blockDim.x;
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -54,36 +83,32 @@ __global__ void __launch_bounds__(1024, NV <= 2 ? kMinBlocks : 1) add_rmsnorm_ke
   float ss = 0.f;
   if (live) {
     const TX *x = static_cast<const TX *>(a.x) + row * a.ldx;
+    const TR *r = static_cast<const TR *>(a.res) + row * a.ldr;
+    Raw8<TX> xv[NV];
+    Raw8<TR> rv[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int vec = threadIdx.x + i * tpr;
-      if (vec < nvec) load8(x + vec * 8, v[i]);
-    }
-    if (a.res) {
-      const TR *r = static_cast<const TR *>(a.res) + row * a.ldr;
-      TR *ro = static_cast<TR *>(a.res_out) + row * a.ldro;
-      float w[NV][8];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int vec = threadIdx.x + i * tpr;
-        if (vec < nvec) load8(r + vec * 8, w[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int vec = threadIdx.x + i * tpr;
-        if (vec < nvec) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] += w[i][j];
-          store8(ro + vec * 8, v[i]);
-        }
+      if (vec < nvec) {
+        xv[i].load(x + vec * 8);
+        if (a.res) rv[i].load(r + vec * 8);
       }
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (threadIdx.x + i * tpr < nvec) {
+    for (int i = 0; i < NV; ++i) {
+      const int vec = threadIdx.x + i * tpr;
+      if (vec >= nvec) continue;
+      xv[i].to(v[i]);
+      if (a.res) {
+        float w[8];
+        rv[i].to(w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+        for (int j = 0; j < 8; ++j) v[i][j] += w[j];
+        store8(static_cast<TR *>(a.res_out) + row * a.ldro + vec * 8, v[i]);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -99,32 +124,85 @@ __global__ void __launch_bounds__(1024, NV <= 2 ? kMinBlocks : 1) add_rmsnorm_ke
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int vec = threadIdx.x + i * tpr;
-    const bool in = vec < nvec;
-    float amax = 0.f;
-    if (in) {
-      float g[8];
-      load8(a.gamma + vec * 8, g);
+    write_y<E4M3>(a, row, vec, vec < nvec, rinv, v[i]);
+  }
+}
+
+// Many rows: persistent blocks, each with a ring of rows in shared memory that
+// bulk copies fill `stages` rows ahead (x, then the residual).  A row is read
+// twice from shared memory (sum of squares, then y), so nothing is held in
+// registers and the loads of the next rows never stop.  One barrier per row:
+// behind it every thread has its part of the sum, and every thread has left
+// the row before, whose stage is then refilled.
+template <typename TX, typename TR, bool E4M3>
+__global__ void __launch_bounds__(512) add_rmsnorm_rows_kernel(const NormArgs a, int stages) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float part[2][16];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5;
+  const int nvec = a.h >> 3, loops = (nvec + threads - 1) / threads;
+  const uint32_t xb = a.h * sizeof(TX), rb = a.res ? a.h * sizeof(TR) : 0;
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  int64_t next = blockIdx.x;  // thread 0: the next row to fetch
+  const auto fetch = [&](int slot) {
+    if (next >= a.m) return;
+    uint8_t *to = ring + slot * (xb + rb);
+    mbar_arrive_expect_tx(&full[slot], xb + rb);
+    bulk_load(to, static_cast<const TX *>(a.x) + next * a.ldx, xb, &full[slot]);
+    if (rb) bulk_load(to + xb, static_cast<const TR *>(a.res) + next * a.ldr, rb, &full[slot]);
+    next += gridDim.x;
+  };
+  if (tid == 0)
+    for (int s = 0; s < stages; ++s) fetch(s);
+  int slot = 0, prev = -1, flip = 0;
+  uint32_t phase = 0;
+  for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
+    const bool ok = mbar_wait(&full[slot], phase, a.err);
+    const TX *x = reinterpret_cast<const TX *>(ring + slot * (xb + rb));
+    const TR *r = reinterpret_cast<const TR *>(ring + slot * (xb + rb) + xb);
+    const auto load_h = [&](int vec, float (&v)[8]) {
+      load8(x + vec * 8, v);
+      if (rb) {
+        float w[8];
+        load8(r + vec * 8, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] = v[i][j] * rinv * g[j];
-        if (E4M3) amax = fmaxf(amax, fabsf(v[i][j]));
+        for (int j = 0; j < 8; ++j) v[j] += w[j];
       }
-    }
-    if (!E4M3) {
-      if (in) store8(static_cast<__nv_bfloat16 *>(a.y) + row * a.ldy + vec * 8, v[i]);
-    } else {
-      // the half-warp that holds a block takes part as a whole: lanes past the
-      // end of the row bring 0
+    };
+    float ss = 0.f;
+    if (ok)
+      for (int vec = tid; vec < nvec; vec += threads) {
+        float v[8];
+        load_h(vec, v);
+        if (rb) store8(static_cast<TR *>(a.res_out) + row * a.ldro + vec * 8, v);
 #pragma unroll
-      for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      amax = fmaxf(amax, kAmaxFloor);
-      if (in) {
-        const float inv = 448.f / amax;
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.y) + row * a.ldy + vec * 8) =
-            to_e4m3x8(v[i], inv);
-        if ((vec & 15) == 0) a.scales[row * a.lds + (vec >> 4)] = amax / 448.f;
+        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
       }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if ((tid & 31) == 0) part[flip][tid >> 5] = ss;
+    if (__syncthreads_or(!ok)) {
+      // a copy did not arrive in time: give the others the same time, then end
+      if (tid == 0) drain_ring(full, stages, slot, phase, stages);
+      return;
     }
+    if (tid == 0 && prev >= 0) fetch(prev);
+    ss = 0.f;
+    for (int i = 0; i < warps; ++i) ss += part[flip][i];
+    const float rinv = rsqrtf(ss / (float)a.h + a.eps);
+    for (int i = 0; i < loops; ++i) {
+      const int vec = tid + i * threads;
+      float v[8];
+      if (vec < nvec) load_h(vec, v);
+      write_y<E4M3>(a, row, vec, vec < nvec, rinv, v);
+    }
+    prev = slot;
+    flip ^= 1;
+    if (++slot == stages) slot = 0, phase ^= 1u;
   }
 }
 
@@ -136,11 +214,45 @@ void launch_nv(const NormArgs &a, bool e4m3, dim3 grid, dim3 block, cudaStream_t
     add_rmsnorm_kernel<NV, TX, TR, false><<<grid, block, 0, s>>>(a);
 }
 
+template <typename TX, typename TR, bool E4M3>
+cudaError_t launch_rows(const NormArgs &a, int stage, cudaStream_t s) {
+  const DeviceFacts *f = device_facts();
+  static bool ready[kMaxDevices];  // the attribute is per device
+  if (!ready[f->device]) {
+    const cudaError_t e = cudaFuncSetAttribute(add_rmsnorm_rows_kernel<TX, TR, E4M3>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    ready[f->device] = true;
+  }
+  // 8192 rows of 5120 bf16 to e4m3: 320 threads 50.8 us, 256 53.7, 160 56.6;
+  // 2000 rows of 17408: 512 threads 32.0 us, 320 34.4, 160 44.7.
+  const int nvec = a.h / 8, most = nvec > 2048 ? 512 : 320, loops = (nvec + most - 1) / most;
+  const int threads = ((nvec + loops - 1) / loops + 31) / 32 * 32;
+  // blocks per SM: as many as keep two rows each in flight, up to 1536 threads
+  int blocks = kRowsSmThreads / threads;
+  if (blocks > kRingBytes / (2 * stage)) blocks = kRingBytes / (2 * stage);
+  if (blocks > 16) blocks = 16;
+  if (blocks < 1) blocks = 1;
+  int stages = kRingBytes / blocks / stage;
+  if (stages > 4) stages = 4;
+  int64_t grid = (int64_t)f->sm_count * blocks;
+  if (grid > a.m) grid = a.m;
+  add_rmsnorm_rows_kernel<TX, TR, E4M3><<<(unsigned)grid, threads, stages * stage, s>>>(a, stages);
+  return cudaGetLastError();
+}
+
 template <typename TX, typename TR>
-void launch_types(const NormArgs &a, bool e4m3, cudaStream_t s) {
-  const int nvec = a.h / 8;
-  int nv = (nvec + kThreadsPerRow - 1) / kThreadsPerRow;
-  if (nv > 4) nv = 4;
+cudaError_t launch_types(const NormArgs &a, bool e4m3, cudaStream_t s) {
+  const int nvec = a.h / 8, sms = device_facts()->sm_count;
+  const int stage = a.h * (int)(sizeof(TX) + (a.res ? sizeof(TR) : 0));
+  // Rows of up to 4096 values fit the registers of a block often enough to keep
+  // the memory busy (30000 x 1024: 37.4 us against 45.1 through the ring; 8192 x
+  // 4096 from fp32: 47.0 against 51.6); longer ones do not (8191 x 5120 to e4m3:
+  // 56.8 against 50.8; 2000 x 17408: 42.7 against 32.0).  With fewer than 4 rows
+  // per SM there is nothing to fetch ahead.
+  if (nvec > 512 && a.m > 4 * sms && 2 * stage <= kRingBytes)
+    return e4m3 ? launch_rows<TX, TR, true>(a, stage, s) : launch_rows<TX, TR, false>(a, stage, s);
+  const int nv = nvec > 256 && nvec <= 512 ? 2 : (nvec + 1023) / 1024;
   const int tpr = ((nvec + nv - 1) / nv + 31) / 32 * 32;
   const int rows = tpr >= 256 ? 1 : 256 / tpr;
   const dim3 block(tpr, rows), grid((unsigned)((a.m + rows - 1) / rows));
@@ -150,6 +262,7 @@ void launch_types(const NormArgs &a, bool e4m3, cudaStream_t s) {
     case 3: launch_nv<3, TX, TR>(a, e4m3, grid, block, s); break;
     default: launch_nv<4, TX, TR>(a, e4m3, grid, block, s); break;
   }
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -159,14 +272,14 @@ cudaError_t launch_add_rmsnorm(const void *x, int x_dtype, int64_t ldx, const vo
                                int64_t m, int64_t h, void *y, int y_dtype, int64_t ldy,
                                void *res_out, int64_t ldro, float *scales, int64_t lds,
                                cudaStream_t stream) {
-  const NormArgs a = {x, res, gamma, y, res_out, scales, m, ldx, ldr, ldy, ldro, lds, (int)h, eps};
+  const NormArgs a = {x, res, gamma, y, res_out, scales, m, ldx, ldr, ldy, ldro, lds, (int)h, eps,
+                      device_error_word()};
   const bool e4m3 = y_dtype == Q4K_DTYPE_E4M3;
   const bool xb = x_dtype == Q4K_DTYPE_BF16, rb = !res || res_dtype == Q4K_DTYPE_BF16;
-  if (xb && rb) launch_types<__nv_bfloat16, __nv_bfloat16>(a, e4m3, stream);
-  else if (xb) launch_types<__nv_bfloat16, float>(a, e4m3, stream);
-  else if (rb) launch_types<float, __nv_bfloat16>(a, e4m3, stream);
-  else launch_types<float, float>(a, e4m3, stream);
-  return cudaGetLastError();
+  if (xb && rb) return launch_types<__nv_bfloat16, __nv_bfloat16>(a, e4m3, stream);
+  if (xb) return launch_types<__nv_bfloat16, float>(a, e4m3, stream);
+  if (rb) return launch_types<float, __nv_bfloat16>(a, e4m3, stream);
+  return launch_types<float, float>(a, e4m3, stream);
 }
 
 }  // namespace q4k
