@@ -18,16 +18,21 @@
 // 32 | ~i that order is the descending one of distinct integers, a filter is the
 // smallest c_i kept, and the kept set is c_i >= the largest of these.
 //
-// Selection.  A histogram over (max - x) in kBins equal steps of the 46 binary
-// orders in which weights are not 0, with the count and the exact weight of
-// each bin, gives the bin in which the k-th token lies, or in which the
-// cumulative weight reaches top_p of the total.  The bin's tokens are listed
-// and ranked by comparing all pairs.  A bin of more than kList tokens is first
-// split further, by histograms over ranges of c_i, whatever the ties.
+// Selection.  A cluster of up to 8 CTAs holds a row in its shared memory.  A
+// histogram over (max - x) in kBins equal steps of the 46 binary orders in which
+// weights are not 0 (counts, and the exact weight of each bin where top-p needs
+// it) gives the bin in which the k-th token lies, or in which the cumulative
+// weight reaches top_p of the total.
+//   - Up to kShort tokens in that bin and above (nearly always with a top-k):
+//     they are sent to the cluster's first CTA, which sorts them and does the
+//     rest on the list.
+//   - Else each filter's smallest key is found (the bin's tokens compared in
+//     pairs; a bin of more than kList tokens is split further by histograms over
+//     ranges of c_i, whatever the ties), and the draw goes over all tokens.
 //
-// What bounds it: the logits are read once from memory (a cluster of up to 8
-// CTAs holds a row in its shared memory, all passes run from there), then the
-// instructions of the weights, about 60 per token and pass that needs them.
+// What bounds it: the logits are read once from memory; after that a row with a
+// top-k is bound by latency (barriers of the cluster, about 0.5 us each), and a
+// row whose weights are all needed by their instructions.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -42,7 +47,7 @@ namespace {
 
 using u64 = unsigned long long;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 1024, kList = 512;
+constexpr int kBins = 1024, kList = 512, kShort = 1024;
 constexpr float kOrders = 46.f;
 constexpr int kMaxCluster = 8, kMaxVocab = 262144;
 constexpr u64 kOne = 1ull << 44;
@@ -92,6 +97,31 @@ struct Scale {
   const float2 *pow;  // 2^(-j/256) in shared memory
 };
 
+// 2^-y for 0 <= y = yh + yl < 64 as (wh + wl) 2^-e, to about 2^-42; wh in (0.49,
+// 1.01).
+struct Pow {
+  float wh, wl;
+  int e;
+};
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves an integer in the low bits
+constexpr int kMagicBits = 0x4B400000;
+__device__ __forceinline__ Pow pow_of(const float2 *table, float yh, float yl) {
+  // y = n / 256 + r, |r| <= 1/512 and a little
+  const float nm = fmaf(yh, 256.f, kMagic), nf = nm - kMagic;
+  const int n = __float_as_int(nm) - kMagicBits;
+  const float r0 = fmaf(nf, -1.f / 256.f, yh), r = r0 + yl, rl = yl - (r - r0);
+  // 2^-r - 1 = z + z^2/2 + ... as eh + el, z = -r ln 2
+  constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654300e-9f;
+  const float zh = -r * kLn2h;
+  const float zl = fmaf(-r, kLn2h, -zh) - fmaf(r, kLn2l, rl * kLn2h);
+  const float q = zh * zh * fmaf(zh, fmaf(zh, 1.f / 24.f, 1.f / 6.f), 0.5f);
+  const float eh = zh + q, el = (q - (eh - zh)) + zl;
+  const float2 p = table[n & 255];
+  // 2^-(n mod 256)/256 (1 + eh + el)
+  const float ph = p.x * eh, wh = p.x + ph;
+  return {wh, (ph - (wh - p.x)) + (fmaf(p.x, eh, -ph) + fmaf(p.x, el, fmaf(p.y, eh, p.y))), n >> 8};
+}
+
 // rint(2^44 exp((x - max) / temperature)) to about 2^-42 relative.
 __device__ __forceinline__ u64 weight(const Scale &s, float x) {
   if (x == s.high) return kOne;
@@ -102,30 +132,27 @@ __device__ __forceinline__ u64 weight(const Scale &s, float x) {
   // y = d c in binary orders, as yh + yl
   const float yh = dh * s.ch;
   const float yl = fmaf(dl, s.ch, fmaf(dh, s.cl, fmaf(dh, s.ch, -yh)));
-  // y = n / 256 + r, |r| <= 1/512 and a little
-  // (conversions by adding 1.5 * 2^23, which leaves an integer in the low bits:
-  // the conversion instructions run at a quarter of this rate or less)
-  constexpr float kMagic = 12582912.f;
-  const float nm = fmaf(yh, 256.f, kMagic), nf = nm - kMagic;
-  const int n = __float_as_int(nm) - 0x4B400000;
-  const float r0 = fmaf(nf, -1.f / 256.f, yh), r = r0 + yl, rl = yl - (r - r0);
-  // 2^-r - 1 = z + z^2/2 + ... as eh + el, z = -r ln 2
-  constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654323148236017e-9f;
-  const float zh = -r * kLn2h;
-  const float zl = fmaf(-r, kLn2h, -zh) - fmaf(r, kLn2l, rl * kLn2h);
-  const float q = zh * zh * fmaf(zh, fmaf(zh, 1.f / 24.f, 1.f / 6.f), 0.5f);
-  const float eh = zh + q, el = (q - (eh - zh)) + zl;
-  const float2 p = s.pow[n & 255];
-  // 2^-(n mod 256)/256 (1 + eh + el) as wh + wl
-  const float ph = p.x * eh;
-  const float wh = p.x + ph;
-  const float wl = (ph - (wh - p.x)) + (fmaf(p.x, eh, -ph) + fmaf(p.x, el, fmaf(p.y, eh, p.y)));
-  // wh in (0.49, 1.01) is its 24-bit mantissa times 2^-25, 2^-24 or 2^-23
-  const uint32_t bits = __float_as_uint(wh);
+  const Pow p = pow_of(s.pow, yh, yl);
+  // wh is its 24-bit mantissa times 2^-25, 2^-24 or 2^-23; |wl| 2^44 < 2^21
+  const uint32_t bits = __float_as_uint(p.wh);
   const uint32_t wi = ((bits & 0x7fffffu) | 0x800000u) << ((bits >> 23) - 125);
-  const int64_t m = ((int64_t)wi << 19) + (__float_as_int(fmaf(wl, 17592186044416.f, kMagic)) - 0x4B400000);
-  const int e = n >> 8;
-  return (u64)(e ? (m + (1ll << (e - 1))) >> e : m);
+  const int64_t m = ((int64_t)wi << 19) + (__float_as_int(fmaf(p.wl, 17592186044416.f, kMagic)) - kMagicBits);
+  return (u64)(p.e ? (m + (1ll << (p.e - 1))) >> p.e : m);
+}
+
+// ln(w / total) for 0 < w <= total, rounded once but for about 2^-40: y0 from
+// fp32, then y0 + (w - total e^y0) / w, e^y0 in fp32 pairs and the difference in
+// fp64 (a 64-bit division and logarithm cost 2 us here).
+__device__ __forceinline__ float log_share(const float2 *table, u64 w, u64 total) {
+  if (w == total) return 0.f;
+  const float y0 = fminf(logf((float)w / (float)total), 0.f);
+  constexpr float kLog2eh = 1.44269502162933349609375f, kLog2el = 1.925962991e-8f;
+  const float yh = -y0 * kLog2eh, yl = fmaf(-y0, kLog2eh, -yh) - y0 * kLog2el;
+  const Pow p = pow_of(table, yh, yl);
+  const float f = __int_as_float((127 - p.e) << 23);  // 2^-e
+  const double t = (double)total;
+  const double d = fma(-t, (double)(p.wl * f), fma(-t, (double)(p.wh * f), (double)w));
+  return y0 + (float)d / (float)w;
 }
 
 // Bin of a token: 0 for the largest, kBins and above for those of weight 0.
@@ -147,6 +174,24 @@ __device__ __forceinline__ u64 ld_peer64(const void *p, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ uint4 ld_peer128(const void *p, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(peer_smem(smem_u32(p), rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_peer64(void *p, uint32_t rank, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(peer_smem(smem_u32(p), rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t add_peer32(uint32_t *p, uint32_t rank, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;\n" : "=r"(old) : "r"(peer_smem(smem_u32(p), rank)), "r"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ void min_peer32(uint32_t *p, uint32_t rank, uint32_t v) {
+  asm volatile("red.shared::cluster.min.u32 [%0], %1;\n" ::"r"(peer_smem(smem_u32(p), rank)), "r"(v) : "memory");
+}
+
 // All threads of the cluster.  The barrier's instruction wants whole warps.
 __device__ __forceinline__ void sync_cluster() {
   __syncwarp();
@@ -158,7 +203,13 @@ struct Hist {  // counts and weights of all bins, over the cluster
   u64 weight[kBins];
 };
 struct __align__(16) Shared {
-  Hist top, split;
+  Hist top;
+  union {
+    Hist split;
+    struct {
+      u64 key[kShort], weight[kShort];
+    } sorted;  // the short list, in the cluster's first CTA
+  };
   // One use after the other, a cluster barrier between: the CTA's own sums (the
   // weights in three parts of 16 bits or less, so that 32768 tokens add up in 32
   // bits with the native atomics), then the lists.
@@ -175,8 +226,8 @@ struct __align__(16) Shared {
   u64 found[4];   // bin, count before, weight before, count in it
   u64 cut, kept_weight, total;
   float high;
-  uint32_t listed;
-  double c, log_min_p;
+  uint32_t listed, counts[kMaxCluster];
+  uint32_t best;  // the first token of the highest logit; in the draw, the warp of the target
 };
 
 struct Ctx {
@@ -209,28 +260,26 @@ struct Ctx {
       }
     }
     sync_cluster();
-    // CTA r sums bins [r, r + 1) * kBins / ranks of all CTAs, then all exchange
-    const int share = kBins / ranks, first = rank * share;
-    for (int b = first + tid; b < first + share; b += kThreads) {
-      uint32_t c = 0;
-      u64 w = 0;
+    // every CTA sums all CTAs' bins itself, 4 bins per thread: cheaper than a
+    // second barrier
+    if (tid < kBins / 4) {
+      uint32_t c[4] = {};
+      u64 w[4] = {};
+#pragma unroll 4
       for (uint32_t p = 0; p < ranks; ++p) {
-        c += ld_peer32(&s.own.count[b], p);
-        if (weights)
-          w += ld_peer32(&s.own.w[0][b], p) + ((u64)ld_peer32(&s.own.w[1][b], p) << 16) +
-               ((u64)ld_peer32(&s.own.w[2][b], p) << 32);
+        const uint4 v = ld_peer128(&s.own.count[tid * 4], p);
+        c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
+        if (weights) {
+          const uint4 a0 = ld_peer128(&s.own.w[0][tid * 4], p), a1 = ld_peer128(&s.own.w[1][tid * 4], p),
+                      a2 = ld_peer128(&s.own.w[2][tid * 4], p);
+          w[0] += a0.x + ((u64)a1.x << 16) + ((u64)a2.x << 32);
+          w[1] += a0.y + ((u64)a1.y << 16) + ((u64)a2.y << 32);
+          w[2] += a0.z + ((u64)a1.z << 16) + ((u64)a2.z << 32);
+          w[3] += a0.w + ((u64)a1.w << 16) + ((u64)a2.w << 32);
+        }
       }
-      h.count[b] = c;
-      h.weight[b] = w;
-    }
-    sync_cluster();
-    for (int b = tid; b < kBins; b += kThreads)
-      if ((uint32_t)(b / share) != rank) {
-        h.count[b] = ld_peer32(&h.count[b], b / share);
-        if (weights) h.weight[b] = ld_peer64(&h.weight[b], b / share);
-      }
-    if (!weights) {
-      for (int b = tid; b < kBins; b += kThreads) h.weight[b] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h.count[tid * 4 + j] = c[j], h.weight[tid * 4 + j] = w[j];
     }
     __syncthreads();
   }
@@ -308,6 +357,7 @@ struct Ctx {
       lo = hi - lo > width ? hi - width : lo;
     }
     // list the tokens of the bin: each CTA its own, then all of them everywhere
+    sync_cluster();  // the sums that shared this memory, and earlier lists, are read
     if (tid == 0) s.listed = 0, s.cut = ~0ull, s.kept_weight = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
@@ -322,18 +372,18 @@ struct Ctx {
       if (in) s.list.mine[atomicAdd(&s.listed, 1u)] = comp(i, v);
     }
     sync_cluster();
-    uint32_t at = 0;
-    for (uint32_t p = 0; p < ranks; ++p) {
-      const uint32_t m = ld_peer32(&s.listed, p);
-      for (uint32_t i = tid; i < m && at + i < kList; i += kThreads) {
-        const u64 k = ld_peer64(&s.list.mine[i], p);
-        s.list.all[at + i] = k;
-        s.list.weights[at + i] = weights ? weight(sc, of_key((uint32_t)(k >> 32))) : 0;
-      }
-      at += m;
+    if (tid < (int)ranks) s.counts[tid] = ld_peer32(&s.listed, tid);
+    __syncthreads();
+    const uint32_t at = (uint32_t)count;
+    if (tid < (int)at) {
+      uint32_t p = 0, i = tid;
+      while (p + 1 < ranks && i >= s.counts[p]) i -= s.counts[p++];
+      const u64 k = ld_peer64(&s.list.mine[min(i, (uint32_t)kList - 1)], p);
+      s.list.all[tid] = k;
+      s.list.weights[tid] = weights ? weight(sc, of_key((uint32_t)(k >> 32))) : 0;
     }
     __syncthreads();
-    if (tid < (int)at && tid < kList) {
+    if (tid < (int)at) {
       const u64 k = s.list.all[tid];
       u64 before = by_weight ? w0 : c0;
       for (uint32_t j = 0; j < at; ++j)
@@ -350,14 +400,60 @@ struct Ctx {
   }
 };
 
+// Sort key[0..size) descending, size a power of two up to kShort.
+__device__ void sort_down(u64 *key, int size) {
+  const int tid = threadIdx.x;
+  const bool one = size <= 64;  // one warp's pairs
+  if (!one || tid < 32) {
+    for (int k = 2; k <= size; k *= 2)
+      for (int j = k / 2; j; j /= 2) {
+        for (int i = tid; i < size / 2; i += kThreads) {
+          const int lo = (i & ~(j - 1)) * 2 | (i & (j - 1)), hi = lo | j;
+          const u64 a = key[lo], b = key[hi];
+          if ((a < b) == ((lo & k) == 0)) key[lo] = b, key[hi] = a;
+        }
+        if (one) __syncwarp();
+        else __syncthreads();
+      }
+  }
+  __syncthreads();
+}
+
+// Sum over the block of the values before this thread's, and of all.
+__device__ u64 scan_block(u64 *part, u64 v, u64 &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  __syncthreads();  // earlier uses of part
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  u64 w = lane < kWarps ? part[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const u64 u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  total = __shfl_sync(0xffffffffu, w, kWarps - 1);
+  const u64 prev = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+  return (warp ? prev : 0) + incl - v;
+}
+
 template <typename T>
 __device__ __forceinline__ float widen(T v) {
   const float f = (float)v;
   return f == f ? f : -INFINITY;  // NaN is never chosen
 }
 
+__device__ __forceinline__ u64 share_of(float part, u64 total) {  // floor(part * total), part in [0, 1]
+  return (u64)((double)part * (double)total);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared &s = *reinterpret_cast<Shared *>(raw);
   float *x = reinterpret_cast<float *>(raw + sizeof(Shared));
@@ -368,6 +464,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
   const T *in = static_cast<const T *>(a.logits) + row * a.ld + base;
   const float t = a.temperature ? a.temperature[row] : 1.f;
   const float mp = a.min_p ? a.min_p[row] : 0.f;
+  const int k = a.top_k ? a.top_k[row] : 0;
+  const float p = a.top_p ? a.top_p[row] : 1.f;
+  const float u = fminf(fmaxf(a.u[row], 0.f), 1.f);
 
   // ---- the row's slice into shared memory, and its maximum
   float high = -INFINITY;
@@ -378,13 +477,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     for (int i = tid; i < full; i += U * kThreads) {
       uint4 w[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u * kThreads < full) w[u] = reinterpret_cast<const uint4 *>(in)[i + u * kThreads];
+      for (int j = 0; j < U; ++j)
+        if (i + j * kThreads < full) w[j] = reinterpret_cast<const uint4 *>(in)[i + j * kThreads];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i + u * kThreads >= full) continue;
-        const T *e = reinterpret_cast<const T *>(&w[u]);
-        float4 *to = reinterpret_cast<float4 *>(x + (i + u * kThreads) * V);
+      for (int l = 0; l < U; ++l) {
+        if (i + l * kThreads >= full) continue;
+        const T *e = reinterpret_cast<const T *>(&w[l]);
+        float4 *to = reinterpret_cast<float4 *>(x + (i + l * kThreads) * V);
 #pragma unroll
         for (int j = 0; j < V / 4; ++j) {
           const float4 f = make_float4(widen(e[4 * j]), widen(e[4 * j + 1]), widen(e[4 * j + 2]), widen(e[4 * j + 3]));
@@ -398,10 +497,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     for (int i = tid; i < n; i += kThreads) high = fmaxf(high, x[i] = widen(in[i]));
   }
   for (int i = tid; i < 256; i += kThreads) s.pow[i] = make_float2(kPow.hi[i], kPow.lo[i]);
-  if (tid == kThreads - 1) {  // in fp64, once per row
-    s.c = 2.0 * 1.4426950408889634074 / (double)t;
-    s.log_min_p = mp > 0.f ? (double)t * log((double)fminf(mp, 1.f)) : 0.0;
-  }
+  if (tid == 0) s.listed = 0, s.best = 0xffffffffu;
 #pragma unroll
   for (int o = 16; o; o >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
   if (lane == 0) s.part[0][warp] = __float_as_uint(high);
@@ -413,70 +509,140 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     if (lane == 0) s.high = high;
   }
   sync_cluster();
-  high = -INFINITY;
-  for (uint32_t p = 0; p < ranks; ++p) high = fmaxf(high, __uint_as_float(ld_peer32(&s.high, p)));
+  high = __uint_as_float(ld_peer32(&s.high, lane & (ranks - 1)));  // ranks is a power of two
+#pragma unroll
+  for (int o = kMaxCluster / 2; o; o >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
 
   const bool none = high == -INFINITY;
   if (none || !(t > 0.f)) {
-    // the first token of the highest logit
+    // the first token of the highest logit, sent to the first CTA
     uint32_t best = 0xffffffffu;
     for (int i = tid; i < n; i += kThreads)
       if (x[i] == high) best = min(best, (uint32_t)(base + i));
     best = __reduce_min_sync(0xffffffffu, best);
-    if (lane == 0) s.part[1][warp] = best;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kWarps; ++w) best = min(best, (uint32_t)s.part[1][w]);
-      s.listed = best;
-    }
+    if (lane == 0 && best != 0xffffffffu) min_peer32(&s.best, 0, best);
     sync_cluster();
     if (rank == 0 && tid == 0) {
-      for (uint32_t p = 0; p < ranks; ++p) best = min(best, ld_peer32(&s.listed, p));
-      a.token[row] = none ? -1 : (int32_t)best;
+      a.token[row] = none ? -1 : (int32_t)s.best;
       if (a.logp) a.logp[row] = none ? -INFINITY : 0.f;
     }
-    sync_cluster();  // no CTA leaves while its memory is read
     return;
   }
 
-  const float ch = (float)s.c;
-  Ctx c = {s, a, x, n, base, rank, ranks, {high, 0.5f * high, ch, (float)(s.c - (double)ch), ch * (kBins / kOrders), s.pow}};
-  if (!(fabsf(ch) < INFINITY)) c.sc.cl = 0.f;
+  // c = 2 log2(e) / t as two fp32 numbers
+  constexpr float kLh = 2.8853900432586669922f, kLl = 3.851925982e-8f;
+  const float ch = kLh / t;
+  const bool plain = ch > 0.f && ch < INFINITY;
+  const float cl = plain ? (fmaf(-ch, t, kLh) + kLl) / t : 0.f;
+  Ctx c = {s, a, x, n, base, rank, ranks, {high, 0.5f * high, ch, cl, ch * (kBins / kOrders), s.pow}};
+  // min-p: e_i >= min_p, as weights
+  const u64 least = mp > 0.f ? max(1ull, (u64)ceilf(fminf(mp, 1.f) * 17592186044416.f)) : 0;
 
   // ---- the filters, each as the smallest key it keeps
   u64 cut = 0;
-  const int k = a.top_k ? a.top_k[row] : 0;
-  const float p = a.top_p ? a.top_p[row] : 1.f;
   const bool use_k = k > 0 && k < a.vocab, use_p = p < 1.f;
   if (use_k || use_p) {
-    c.histogram(s.top, use_p, [&](int, float v) { return bin_of(c.sc, v); });
+    const auto bins = [&](int, float v) { return bin_of(c.sc, v); };
     u64 total = 0;
-    bool whole = true;  // the top-k set is everything of any weight
+    c.histogram(s.top, !use_k, bins);
+    if (!use_k) {
+      u64 w = 0;
+      for (int b = tid; b < kBins; b += kThreads) w += s.top.weight[b];
+      scan_block(s.part[0], w, total);
+      __syncthreads();
+    }
+    // before < top_p * total, and at least the first token: before < want
+    u64 want = use_k ? (u64)k : max(1ull, (u64)ceil((double)fmaxf(p, 0.f) * (double)total));
+    const bool reached = c.find(s.top, !use_k, want, 0, 0);
+    int b = reached ? (int)s.found[0] : kBins - 1;
+    u64 count = reached ? s.found[1] + s.found[3] : 0;
+    if (!reached) {  // fewer than k tokens of any weight: all of them
+      u64 m = 0;
+      for (int i = tid; i < kBins; i += kThreads) m += s.top.count[i];
+      scan_block(s.part[0], m, count);
+    }
+    if (count <= kShort) {
+      for (int i = tid; i < n; i += kThreads) {
+        const float v = x[i];
+        if (bin_of(c.sc, v) <= b) st_peer64(&s.sorted.key[add_peer32(&s.listed, 0, 1)], 0, c.comp(i, v));
+      }
+      sync_cluster();
+      if (rank != 0) return;
+      // two tokens per thread, in order
+      const int m = (int)count;
+      int size = 2;
+      while (size < m) size *= 2;
+      for (int i = m + tid; i < size; i += kThreads) s.sorted.key[i] = 0;
+      __syncthreads();
+      sort_down(s.sorted.key, size);
+      const int kept_k = use_k ? min(m, k) : m;
+      u64 w[2], key[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = 2 * tid + j;
+        key[j] = i < kept_k ? s.sorted.key[i] : 0;
+        w[j] = i < kept_k ? weight(c.sc, of_key((uint32_t)(key[j] >> 32))) : 0;
+      }
+      u64 all, before = scan_block(s.part[0], w[0] + w[1], all);
+      if (use_p) {
+        if (use_k) want = max(1ull, (u64)ceil((double)fmaxf(p, 0.f) * (double)all));
+        if (before + w[0] >= want) w[1] = 0;
+        if (before >= want) w[0] = 0;
+      }
+      if (w[0] < least) w[0] = 0;
+      if (w[1] < least) w[1] = 0;
+      const int kept = __syncthreads_count(w[0] != 0) + __syncthreads_count(w[1] != 0);  // the first `kept` of the order
+      size = 2;
+      while (size < kept) size *= 2;
+      // by index: ~i high, the place in the order low
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = 2 * tid + j;
+        if (i < size) {
+          s.sorted.weight[i] = w[j];
+          s.sorted.key[i] = w[j] ? key[j] << 32 | (uint32_t)i : 0;
+        }
+      }
+      __syncthreads();
+      sort_down(s.sorted.key, size);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = 2 * tid + j;
+        key[j] = i < kept ? s.sorted.key[i] : 0;
+        w[j] = i < kept ? s.sorted.weight[(uint32_t)key[j]] : 0;
+      }
+      before = scan_block(s.part[0], w[0] + w[1], all);
+      u64 target = share_of(u, all);
+      if (target >= all) target = all - 1;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (before <= target && target < before + w[j]) {
+          a.token[row] = (int32_t)~(uint32_t)(key[j] >> 32);
+          if (a.logp) a.logp[row] = log_share(s.pow, w[j], all);
+        }
+        before += w[j];
+      }
+      return;
+    }
+    if (use_k && use_p) {
+      sync_cluster();  // the sums are read
+      c.histogram(s.top, true, bins);
+    }
     if (use_k) {
       cut = c.select(false, (u64)k, use_p);
-      whole = cut == 0;
-      total = whole ? 0 : s.kept_weight;
-    }
-    if (use_p) {
-      if (whole) {
-        u64 w = 0;
-        for (int b = tid; b < kBins; b += kThreads) w += s.top.weight[b];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-        if (lane == 0) s.part[0][warp] = w;
-        __syncthreads();
-        for (int v = 0; v < kWarps; ++v) total += s.part[0][v];
+      if (use_p) {
+        if (cut) {
+          total = s.kept_weight;
+        } else {  // the top-k set is everything of any weight
+          u64 w = 0;
+          for (int i = tid; i < kBins; i += kThreads) w += s.top.weight[i];
+          scan_block(s.part[0], w, total);
+        }
+        want = max(1ull, (u64)ceil((double)fmaxf(p, 0.f) * (double)total));
         __syncthreads();
       }
-      // before < top_p * total, and at least the first token: before < want
-      const u64 want = max(1ull, (u64)ceil((double)fmaxf(p, 0.f) * (double)total));
-      sync_cluster();  // the lists of the first selection are read
-      cut = max(cut, c.select(true, want, true));
     }
-  }
-  if (mp > 0.f) {
-    const float least = high == INFINITY ? high : __double2float_ru((double)high + s.log_min_p);
-    cut = max(cut, (u64)key_of(least) << 32);
+    if (use_p) cut = max(cut, c.select(true, want, true));
   }
 
   // ---- the draw.  A warp's tokens are contiguous, 32 at a time, so the order
@@ -484,65 +650,54 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
   const int run = (n + kThreads - 1) / kThreads * 32, i0 = min(n, warp * run), i1 = min(n, i0 + run);
   const auto kept = [&](int i) -> u64 {
     const float v = x[i];
-    return c.comp(i, v) >= cut ? weight(c.sc, v) : 0;
+    const u64 w = c.comp(i, v) >= cut ? weight(c.sc, v) : 0;
+    return w >= least ? w : 0;
   };
   u64 sum = 0;
   for (int i = i0 + lane; i < i1; i += 32) sum += kept(i);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s.part[0][warp] = sum;
-  __syncthreads();
-  u64 before = 0, mine = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s.part[0][w];
-    mine += s.part[0][w];
-  }
+  u64 mine, before = scan_block(s.part[0], lane == 0 ? sum : 0, mine);
+  before = __shfl_sync(0xffffffffu, before, 0);  // before this warp's tokens
   if (tid == 0) s.total = mine;
   sync_cluster();
-  u64 total = 0;
-  for (uint32_t q = 0; q < ranks; ++q) {
-    const u64 w = ld_peer64(&s.total, q);
-    if (q < rank) before += w;
-    total += w;
+  u64 total = ld_peer64(&s.total, lane & (ranks - 1));
+  {
+    u64 less = lane < (int)rank ? total : 0;
+    total = lane < (int)ranks ? total : 0;
+#pragma unroll
+    for (int o = kMaxCluster / 2; o; o >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      less += __shfl_xor_sync(0xffffffffu, less, o);
+    }
+    total = __shfl_sync(0xffffffffu, total, 0);
+    before += __shfl_sync(0xffffffffu, less, 0);
   }
+  sync_cluster();  // all totals are read: from here on the CTAs are on their own
   // cumulative > u * total, for an integer: cumulative > floor(u * total)
-  const float u = fminf(fmaxf(a.u[row], 0.f), 1.f);
-  u64 target = (u64)((double)u * (double)total);
+  u64 target = share_of(u, total);
   if (target >= total) target = total - 1;
   // The warp whose tokens reach the target tells the block, which goes through
   // them again together (one warp alone took 6 us for its 1024).
-  if (tid == 0) s.listed = 0xffffffffu;
+  if (lane == 0 && before <= target && target < before + sum) s.best = warp, s.cut = before;
   __syncthreads();
-  if (lane == 0 && before <= target && target < before + sum) s.listed = warp, s.cut = before;
-  __syncthreads();
-  if (s.listed != 0xffffffffu) {
-    const int from = min(n, (int)s.listed * run), to = min(n, from + run);
-    const int per = (run + kThreads - 1) / kThreads, j0 = min(to, from + tid * per), j1 = min(to, j0 + per);
-    u64 own = 0;
-    for (int i = j0; i < j1; ++i) own += kept(i);
-    u64 incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) s.part[1][warp] = incl;
-    __syncthreads();
-    u64 at = s.cut + incl - own;
-    for (int w = 0; w < warp; ++w) at += s.part[1][w];
-    if (at <= target && target < at + own) {
-      for (int i = j0; i < j1; ++i) {
-        const u64 w = kept(i);
-        at += w;
-        if (at > target) {
-          a.token[row] = base + i;
-          if (a.logp) a.logp[row] = (float)log((double)w / (double)total);
-          break;
-        }
+  if (s.best == 0xffffffffu) return;
+  const int from = min(n, (int)s.best * run), to = min(n, from + run);
+  const int per = (run + kThreads - 1) / kThreads, j0 = min(to, from + tid * per), j1 = min(to, j0 + per);
+  u64 own = 0;
+  for (int i = j0; i < j1; ++i) own += kept(i);
+  u64 at = s.cut + scan_block(s.part[1], own, mine);
+  if (at <= target && target < at + own) {
+    for (int i = j0; i < j1; ++i) {
+      const u64 w = kept(i);
+      at += w;
+      if (at > target) {
+        a.token[row] = base + i;
+        if (a.logp) a.logp[row] = log_share(s.pow, w, total);
+        break;
       }
     }
   }
-  sync_cluster();  // no CTA leaves while its memory is read
 }
 
 template <typename T>
