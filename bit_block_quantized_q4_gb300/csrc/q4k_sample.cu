@@ -8,10 +8,10 @@
 // temperature) with borders, and in a flat row of 10^5 tokens a border lies
 // within 10^-5 of any point: with weights good to 2^-23 about one row in a
 // hundred would give another token than exact arithmetic.  So a weight is the
-// integer rint(2^44 e_i), computed in pairs of fp32 numbers to about 2^-42 (fp64
+// integer rint(2^43 e_i), computed in pairs of fp32 numbers to about 2^-42 (fp64
 // has 1/64 of the fp32 rate here and would take over a millisecond for 256 rows
 // of 131072).  Integer sums are exact, the same in any order; 2^18 tokens sum
-// below 2^62.
+// below 2^61.
 //
 // Order.  Every filter keeps a prefix of the tokens in the order (logit
 // descending, index ascending).  With c_i = (monotone integer image of x_i) <<
@@ -47,15 +47,18 @@ namespace {
 
 using u64 = unsigned long long;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 1024, kList = 512, kShort = 1024;
+constexpr int kBins = 1024, kList = 512, kShort = 2048;
 constexpr float kOrders = 46.f;
 constexpr int kMaxCluster = 8, kMaxVocab = 262144;
-constexpr u64 kOne = 1ull << 44;
+// Tokens per CTA: few rows are spread as thin as kSliceLeast, many rows take as
+// few CTAs as hold them with two CTAs per SM.
+constexpr int kSliceMost = 16384, kSliceLeast = 2048;
+constexpr float kOne = 8796093022208.f;  // weight of the highest logit, 2^43
 
 struct SampleArgs {
   const void *logits;
   int64_t ld;
-  int vocab, slice;  // slice: tokens per CTA, a multiple of 32
+  int vocab, slice;  // slice: tokens per CTA, a multiple of 64
   const float *u, *temperature, *top_p, *min_p;
   const int32_t *top_k;
   int32_t *token;
@@ -97,47 +100,99 @@ struct Scale {
   const float2 *pow;  // 2^(-j/256) in shared memory
 };
 
+// Two fp32 numbers in one instruction.
+struct F2 {
+  u64 v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ float2 parts(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator-(F2 a, F2 b) { return fma2(b, f2(-1.f), a); }
+
 // 2^-y for 0 <= y = yh + yl < 64 as (wh + wl) 2^-e, to about 2^-42; wh in (0.49,
-// 1.01).
-struct Pow {
-  float wh, wl;
-  int e;
+// 1.01).  Two at a time.
+struct Pow2 {
+  F2 wh, wl;
+  int e0, e1;
 };
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves an integer in the low bits
 constexpr int kMagicBits = 0x4B400000;
-__device__ __forceinline__ Pow pow_of(const float2 *table, float yh, float yl) {
+__device__ __forceinline__ int magic_int(float x) { return __float_as_int(x) - kMagicBits; }
+__device__ __forceinline__ Pow2 pow_of(const float2 *table, F2 yh, F2 yl) {
   // y = n / 256 + r, |r| <= 1/512 and a little
-  const float nm = fmaf(yh, 256.f, kMagic), nf = nm - kMagic;
-  const int n = __float_as_int(nm) - kMagicBits;
-  const float r0 = fmaf(nf, -1.f / 256.f, yh), r = r0 + yl, rl = yl - (r - r0);
+  const F2 nm = fma2(yh, f2(256.f), f2(kMagic)), nf = nm + f2(-kMagic);
+  const float2 nn = parts(nm);
+  const int n0 = magic_int(nn.x), n1 = magic_int(nn.y);
+  const F2 r0 = fma2(nf, f2(-1.f / 256.f), yh), r = r0 + yl, rl = yl - (r - r0);
   // 2^-r - 1 = z + z^2/2 + ... as eh + el, z = -r ln 2
   constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654300e-9f;
-  const float zh = -r * kLn2h;
-  const float zl = fmaf(-r, kLn2h, -zh) - fmaf(r, kLn2l, rl * kLn2h);
-  const float q = zh * zh * fmaf(zh, fmaf(zh, 1.f / 24.f, 1.f / 6.f), 0.5f);
-  const float eh = zh + q, el = (q - (eh - zh)) + zl;
-  const float2 p = table[n & 255];
+  const F2 zh = r * f2(-kLn2h);
+  const F2 zl = fma2(r, f2(-kLn2h), zh * f2(-1.f)) + fma2(r, f2(-kLn2l), rl * f2(-kLn2h));
+  const F2 q = zh * zh * fma2(zh, fma2(zh, f2(1.f / 24.f), f2(1.f / 6.f)), f2(0.5f));
+  const F2 eh = zh + q, el = (q - (eh - zh)) + zl;
   // 2^-(n mod 256)/256 (1 + eh + el)
-  const float ph = p.x * eh, wh = p.x + ph;
-  return {wh, (ph - (wh - p.x)) + (fmaf(p.x, eh, -ph) + fmaf(p.x, el, fmaf(p.y, eh, p.y))), n >> 8};
+  const float2 p0 = table[n0 & 255], p1 = table[n1 & 255];
+  const F2 px = f2(p0.x, p1.x), py = f2(p0.y, p1.y);
+  const F2 ph = px * eh, wh = px + ph;
+  const F2 wl = (ph - (wh - px)) + (fma2(px, eh, ph * f2(-1.f)) + fma2(px, el, fma2(py, eh, py)));
+  return {wh, wl, n0 >> 8, n1 >> 8};
 }
 
-// rint(2^44 exp((x - max) / temperature)) to about 2^-42 relative.
-__device__ __forceinline__ u64 weight(const Scale &s, float x) {
-  if (x == s.high) return kOne;
+// rint(2^43 exp((x - max) / temperature)) of two logits, to about 2^-42 relative.
+__device__ __forceinline__ void weights(const Scale &s, float x0, float x1, u64 &w0, u64 &w1) {
   // d = (max - x) / 2 as dh + dl, exactly
-  const float b = -0.5f * x, dh = s.half + b, bb = dh - s.half;
-  if (!(dh * s.ch < kOrders)) return 0;  // also -infinity, and all but the largest where that is +infinity
-  const float dl = (s.half - (dh - bb)) + (b - bb);
+  const F2 half = f2(s.half), b = f2(x0, x1) * f2(-0.5f);
+  const F2 d = half + b;
+  const float2 dd = parts(d);
+  // 0 below 2^-46 (and for -infinity, for which the rest would be NaN)
+  const bool in0 = dd.x * s.ch < kOrders, in1 = dd.y * s.ch < kOrders;
+  if (!in0 && !in1) {
+    w0 = w1 = 0;
+    return;
+  }
+  const F2 dh = f2(in0 ? dd.x : 0.f, in1 ? dd.y : 0.f), c = f2(s.ch);
+  const F2 bs = f2(in0 ? -0.5f * x0 : -s.half, in1 ? -0.5f * x1 : -s.half), bb = dh - half;
+  const F2 dl = (half - (dh - bb)) + (bs - bb);
   // y = d c in binary orders, as yh + yl
-  const float yh = dh * s.ch;
-  const float yl = fmaf(dl, s.ch, fmaf(dh, s.cl, fmaf(dh, s.ch, -yh)));
-  const Pow p = pow_of(s.pow, yh, yl);
-  // wh is its 24-bit mantissa times 2^-25, 2^-24 or 2^-23; |wl| 2^44 < 2^21
-  const uint32_t bits = __float_as_uint(p.wh);
-  const uint32_t wi = ((bits & 0x7fffffu) | 0x800000u) << ((bits >> 23) - 125);
-  const int64_t m = ((int64_t)wi << 19) + (__float_as_int(fmaf(p.wl, 17592186044416.f, kMagic)) - kMagicBits);
-  return (u64)(p.e ? (m + (1ll << (p.e - 1))) >> p.e : m);
+  const F2 yh = dh * c;
+  const F2 yl = fma2(dl, c, fma2(dh, f2(s.cl), fma2(dh, c, yh * f2(-1.f))));
+  const Pow2 p = pow_of(s.pow, yh, yl);
+  // 2^43 2^-e (wh + wl) = 2^22 (i1 + f), i1 an integer below 2^22, |f| <= 9/16
+  const F2 scale = f2(__int_as_float((148 - p.e0) << 23), __int_as_float((148 - p.e1) << 23));  // 2^(21-e)
+  const F2 am = fma2(p.wh, scale, f2(kMagic)), ai = am + f2(-kMagic);
+  const F2 f = fma2(p.wl, scale, fma2(p.wh, scale, ai * f2(-1.f)));
+  const F2 fm = fma2(f, f2(4194304.f), f2(kMagic));
+  const float2 i1 = parts(am), i2 = parts(fm);
+  w0 = in0 ? (u64)((int64_t)magic_int(i1.x) * 4194304 + magic_int(i2.x)) : 0;
+  w1 = in1 ? (u64)((int64_t)magic_int(i1.y) * 4194304 + magic_int(i2.y)) : 0;
+}
+__device__ __forceinline__ u64 weight(const Scale &s, float x) {
+  u64 w0, w1;
+  weights(s, x, x, w0, w1);
+  return w0;
 }
 
 // ln(w / total) for 0 < w <= total, rounded once but for about 2^-40: y0 from
@@ -148,18 +203,17 @@ __device__ __forceinline__ float log_share(const float2 *table, u64 w, u64 total
   const float y0 = fminf(logf((float)w / (float)total), 0.f);
   constexpr float kLog2eh = 1.44269502162933349609375f, kLog2el = 1.925962991e-8f;
   const float yh = -y0 * kLog2eh, yl = fmaf(-y0, kLog2eh, -yh) - y0 * kLog2el;
-  const Pow p = pow_of(table, yh, yl);
-  const float f = __int_as_float((127 - p.e) << 23);  // 2^-e
+  const Pow2 p = pow_of(table, f2(yh), f2(yl));
+  const float f = __int_as_float((127 - p.e0) << 23);  // 2^-e
   const double t = (double)total;
-  const double d = fma(-t, (double)(p.wl * f), fma(-t, (double)(p.wh * f), (double)w));
+  const double d = fma(-t, (double)(parts(p.wl).x * f), fma(-t, (double)(parts(p.wh).x * f), (double)w));
   return y0 + (float)d / (float)w;
 }
 
-// Bin of a token: 0 for the largest, kBins and above for those of weight 0.
-// Not increasing in x.
+// Bin of a token: 0 for the largest, kBins and above for those of weight 0 (and
+// for -infinity).  Not increasing in x.
 __device__ __forceinline__ int bin_of(const Scale &s, float x) {
-  if (x == s.high) return 0;
-  const float t = (s.half + -0.5f * x) * s.cb;
+  const float t = fmaf(-0.5f, x, s.half) * s.cb;
   return t < (float)kBins ? (int)t : kBins;
 }
 
@@ -206,13 +260,11 @@ struct __align__(16) Shared {
   Hist top;
   union {
     Hist split;
-    struct {
-      u64 key[kShort], weight[kShort];
-    } sorted;  // the short list, in the cluster's first CTA
+    u64 short_list[kShort];  // in the cluster's first CTA
   };
   // One use after the other, a cluster barrier between: the CTA's own sums (the
   // weights in three parts of 16 bits or less, so that 32768 tokens add up in 32
-  // bits with the native atomics), then the lists.
+  // bits with the native atomics), then the lists, or the short list's weights.
   union {
     struct {
       uint32_t count[kBins], w[3][kBins];
@@ -220,6 +272,7 @@ struct __align__(16) Shared {
     struct {
       u64 mine[kList], all[kList], weights[kList];
     } list;
+    u64 short_weight[kShort];
   };
   float2 pow[256];
   u64 part[2][kWarps];
@@ -242,21 +295,28 @@ struct Ctx {
 
   // Fill h with the cluster's histogram of bin(i, x_i) (bins >= kBins: none).
   template <typename F>
-  __device__ void histogram(Hist &h, bool weights, F bin) {
+  __device__ void histogram(Hist &h, bool with_weights, F bin) {
     const int tid = threadIdx.x;
     uint32_t *zero = reinterpret_cast<uint32_t *>(&s.own);
     for (int i = tid; i < (int)(sizeof(s.own) / 4); i += kThreads) zero[i] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const float v = x[i];
-      const int b = bin(i, v);
-      if (b >= kBins) continue;
-      atomicAdd(&s.own.count[b], 1u);
-      if (weights) {
-        const u64 w = weight(sc, v);
-        atomicAdd(&s.own.w[0][b], (uint32_t)w & 0xffffu);
-        atomicAdd(&s.own.w[1][b], (uint32_t)(w >> 16) & 0xffffu);
-        atomicAdd(&s.own.w[2][b], (uint32_t)(w >> 32));
+    for (int i = 2 * tid; i < n; i += 2 * kThreads) {
+      const float2 v = *reinterpret_cast<const float2 *>(x + i);
+      const int b0 = bin(i, v.x), b1 = bin(i + 1, v.y);
+      if (b0 >= kBins && b1 >= kBins) continue;
+      u64 w0 = 0, w1 = 0;
+      if (with_weights) weights(sc, v.x, v.y, w0, w1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int b = j ? b1 : b0;
+        const u64 w = j ? w1 : w0;
+        if (b >= kBins) continue;
+        atomicAdd(&s.own.count[b], 1u);
+        if (with_weights) {
+          atomicAdd(&s.own.w[0][b], (uint32_t)w & 0xffffu);
+          atomicAdd(&s.own.w[1][b], (uint32_t)(w >> 16) & 0xffffu);
+          atomicAdd(&s.own.w[2][b], (uint32_t)(w >> 32));
+        }
       }
     }
     sync_cluster();
@@ -269,7 +329,7 @@ struct Ctx {
       for (uint32_t p = 0; p < ranks; ++p) {
         const uint4 v = ld_peer128(&s.own.count[tid * 4], p);
         c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
-        if (weights) {
+        if (with_weights) {
           const uint4 a0 = ld_peer128(&s.own.w[0][tid * 4], p), a1 = ld_peer128(&s.own.w[1][tid * 4], p),
                       a2 = ld_peer128(&s.own.w[2][tid * 4], p);
           w[0] += a0.x + ((u64)a1.x << 16) + ((u64)a2.x << 32);
@@ -318,7 +378,7 @@ struct Ctx {
   // The smallest key kept when a token is kept if the sum of counts (or
   // weights) of those before it is less than `want` > 0; 0 if all are.
   // s.kept_weight: the weight of the kept ones (0 unless h has weights).
-  __device__ u64 select(bool by_weight, u64 want, bool weights) {
+  __device__ u64 select(bool by_weight, u64 want, bool with_weights) {
     const int tid = threadIdx.x;
     if (!find(s.top, by_weight, want, 0, 0)) return 0;
     int b = (int)s.found[0];
@@ -346,7 +406,7 @@ struct Ctx {
       const int bits = 64 - __clzll((long long)range);
       const int shift = bits > 10 ? bits - 10 : 0;
       sync_cluster();  // the lists or sums that shared this memory are read
-      histogram(s.split, weights, [&](int i, float v) {
+      histogram(s.split, with_weights, [&](int i, float v) {
         const u64 k = comp(i, v);
         return k >= lo && k <= hi ? (int)((hi - k) >> shift) : kBins;
       });
@@ -380,7 +440,7 @@ struct Ctx {
       while (p + 1 < ranks && i >= s.counts[p]) i -= s.counts[p++];
       const u64 k = ld_peer64(&s.list.mine[min(i, (uint32_t)kList - 1)], p);
       s.list.all[tid] = k;
-      s.list.weights[tid] = weights ? weight(sc, of_key((uint32_t)(k >> 32))) : 0;
+      s.list.weights[tid] = with_weights ? weight(sc, of_key((uint32_t)(k >> 32))) : 0;
     }
     __syncthreads();
     if (tid < (int)at) {
@@ -390,7 +450,7 @@ struct Ctx {
         if (s.list.all[j] > k) before += by_weight ? s.list.weights[j] : 1;
       if (before < want) {
         atomicMin(&s.cut, k);
-        if (weights) atomicAdd(&s.kept_weight, s.list.weights[tid]);
+        if (with_weights) atomicAdd(&s.kept_weight, s.list.weights[tid]);
       }
     }
     __syncthreads();
@@ -460,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_ctarank(), ranks = gridDim.y;
   const int row = blockIdx.x;
-  const int base = (int)rank * a.slice, n = max(0, min(a.vocab - base, a.slice));
+  const int base = (int)rank * a.slice, n = a.slice, live = max(0, min(a.vocab - base, n));
   const T *in = static_cast<const T *>(a.logits) + row * a.ld + base;
   const float t = a.temperature ? a.temperature[row] : 1.f;
   const float mp = a.min_p ? a.min_p[row] : 0.f;
@@ -472,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   float high = -INFINITY;
   constexpr int V = 16 / sizeof(T);
   if ((reinterpret_cast<uintptr_t>(in) & 15) == 0) {
-    const int full = n / V;
+    const int full = live / V;
     constexpr int U = 4;
     for (int i = tid; i < full; i += U * kThreads) {
       uint4 w[U];
@@ -492,10 +552,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
       }
     }
-    for (int i = full * V + tid; i < n; i += kThreads) high = fmaxf(high, x[i] = widen(in[i]));
+    for (int i = full * V + tid; i < live; i += kThreads) high = fmaxf(high, x[i] = widen(in[i]));
   } else {
-    for (int i = tid; i < n; i += kThreads) high = fmaxf(high, x[i] = widen(in[i]));
+    for (int i = tid; i < live; i += kThreads) high = fmaxf(high, x[i] = widen(in[i]));
   }
+  for (int i = live + tid; i < n; i += kThreads) x[i] = -INFINITY;
   for (int i = tid; i < 256; i += kThreads) s.pow[i] = make_float2(kPow.hi[i], kPow.lo[i]);
   if (tid == 0) s.listed = 0, s.best = 0xffffffffu;
 #pragma unroll
@@ -529,14 +590,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return;
   }
 
-  // c = 2 log2(e) / t as two fp32 numbers
+  if (high == INFINITY) {  // its tokens share everything: they are the row's only ones
+    for (int i = tid; i < n; i += kThreads) x[i] = x[i] == high ? 0.f : -INFINITY;
+    high = 0.f;
+    __syncthreads();
+  }
+  // c = 2 log2(e) / t as two fp32 numbers (a temperature so small that it is
+  // not finite separates all logits that differ all the same)
   constexpr float kLh = 2.8853900432586669922f, kLl = 3.851925982e-8f;
-  const float ch = kLh / t;
-  const bool plain = ch > 0.f && ch < INFINITY;
-  const float cl = plain ? (fmaf(-ch, t, kLh) + kLl) / t : 0.f;
+  const float ch = fminf(kLh / t, 3e38f);
+  const float cl = ch > 0.f && ch < 3e38f ? (fmaf(-ch, t, kLh) + kLl) / t : 0.f;
   Ctx c = {s, a, x, n, base, rank, ranks, {high, 0.5f * high, ch, cl, ch * (kBins / kOrders), s.pow}};
+  if (!(c.sc.cb < 3e38f)) c.sc.cb = 3e38f;
   // min-p: e_i >= min_p, as weights
-  const u64 least = mp > 0.f ? max(1ull, (u64)ceilf(fminf(mp, 1.f) * 17592186044416.f)) : 0;
+  const u64 least = mp > 0.f ? max(1ull, (u64)ceilf(fminf(mp, 1.f) * kOne)) : 0;
 
   // ---- the filters, each as the smallest key it keeps
   u64 cut = 0;
@@ -564,58 +631,64 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (count <= kShort) {
       for (int i = tid; i < n; i += kThreads) {
         const float v = x[i];
-        if (bin_of(c.sc, v) <= b) st_peer64(&s.sorted.key[add_peer32(&s.listed, 0, 1)], 0, c.comp(i, v));
+        if (bin_of(c.sc, v) <= b) st_peer64(&s.short_list[add_peer32(&s.listed, 0, 1)], 0, c.comp(i, v));
       }
       sync_cluster();
       if (rank != 0) return;
-      // two tokens per thread, in order
+      constexpr int PER = kShort / kThreads;  // tokens per thread, in order
       const int m = (int)count;
       int size = 2;
       while (size < m) size *= 2;
-      for (int i = m + tid; i < size; i += kThreads) s.sorted.key[i] = 0;
+      for (int i = m + tid; i < size; i += kThreads) s.short_list[i] = 0;
       __syncthreads();
-      sort_down(s.sorted.key, size);
+      sort_down(s.short_list, size);
       const int kept_k = use_k ? min(m, k) : m;
-      u64 w[2], key[2];
+      u64 w[PER], key[PER], sum = 0;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 2 * tid + j;
-        key[j] = i < kept_k ? s.sorted.key[i] : 0;
+      for (int j = 0; j < PER; ++j) {
+        const int i = PER * tid + j;
+        key[j] = i < kept_k ? s.short_list[i] : 0;
         w[j] = i < kept_k ? weight(c.sc, of_key((uint32_t)(key[j] >> 32))) : 0;
+        sum += w[j];
       }
-      u64 all, before = scan_block(s.part[0], w[0] + w[1], all);
-      if (use_p) {
-        if (use_k) want = max(1ull, (u64)ceil((double)fmaxf(p, 0.f) * (double)all));
-        if (before + w[0] >= want) w[1] = 0;
-        if (before >= want) w[0] = 0;
+      u64 all, before = scan_block(s.part[0], sum, all);
+      if (use_p && use_k) want = max(1ull, (u64)ceil((double)fmaxf(p, 0.f) * (double)all));
+      int mine = 0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const u64 e = w[j];
+        if ((use_p && before >= want) || e < least) w[j] = 0;
+        before += e;
+        mine += w[j] != 0;
       }
-      if (w[0] < least) w[0] = 0;
-      if (w[1] < least) w[1] = 0;
-      const int kept = __syncthreads_count(w[0] != 0) + __syncthreads_count(w[1] != 0);  // the first `kept` of the order
+      u64 kept;  // the first `kept` of the order
+      scan_block(s.part[1], mine, kept);
       size = 2;
-      while (size < kept) size *= 2;
+      while (size < (int)kept) size *= 2;
       // by index: ~i high, the place in the order low
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 2 * tid + j;
+      for (int j = 0; j < PER; ++j) {
+        const int i = PER * tid + j;
         if (i < size) {
-          s.sorted.weight[i] = w[j];
-          s.sorted.key[i] = w[j] ? key[j] << 32 | (uint32_t)i : 0;
+          s.short_weight[i] = w[j];
+          s.short_list[i] = w[j] ? key[j] << 32 | (uint32_t)i : 0;
         }
       }
       __syncthreads();
-      sort_down(s.sorted.key, size);
+      sort_down(s.short_list, size);
+      sum = 0;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 2 * tid + j;
-        key[j] = i < kept ? s.sorted.key[i] : 0;
-        w[j] = i < kept ? s.sorted.weight[(uint32_t)key[j]] : 0;
+      for (int j = 0; j < PER; ++j) {
+        const int i = PER * tid + j;
+        key[j] = i < (int)kept ? s.short_list[i] : 0;
+        w[j] = i < (int)kept ? s.short_weight[(uint32_t)key[j]] : 0;
+        sum += w[j];
       }
-      before = scan_block(s.part[0], w[0] + w[1], all);
+      before = scan_block(s.part[0], sum, all);
       u64 target = share_of(u, all);
       if (target >= all) target = all - 1;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < PER; ++j) {
         if (before <= target && target < before + w[j]) {
           a.token[row] = (int32_t)~(uint32_t)(key[j] >> 32);
           if (a.logp) a.logp[row] = log_share(s.pow, w[j], all);
@@ -645,16 +718,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (use_p) cut = max(cut, c.select(true, want, true));
   }
 
-  // ---- the draw.  A warp's tokens are contiguous, 32 at a time, so the order
-  // of the sums is that of the indexes.
-  const int run = (n + kThreads - 1) / kThreads * 32, i0 = min(n, warp * run), i1 = min(n, i0 + run);
-  const auto kept = [&](int i) -> u64 {
-    const float v = x[i];
-    const u64 w = c.comp(i, v) >= cut ? weight(c.sc, v) : 0;
-    return w >= least ? w : 0;
+  // ---- the draw.  A warp's tokens are contiguous, so the order of the sums is
+  // that of the indexes.
+  const int run = (n + 2 * kThreads - 1) / (2 * kThreads) * 64, i0 = min(n, warp * run), i1 = min(n, i0 + run);
+  const auto kept = [&](int i) -> u64 {  // of tokens i and i + 1, i even
+    const float2 v = *reinterpret_cast<const float2 *>(x + i);
+    u64 w0, w1;
+    weights(c.sc, v.x, v.y, w0, w1);
+    if (w0 < least || c.comp(i, v.x) < cut) w0 = 0;
+    if (w1 < least || c.comp(i + 1, v.y) < cut) w1 = 0;
+    return w0 + w1;
   };
   u64 sum = 0;
-  for (int i = i0 + lane; i < i1; i += 32) sum += kept(i);
+  for (int i = i0 + 2 * lane; i < i1; i += 64) sum += kept(i);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   u64 mine, before = scan_block(s.part[0], lane == 0 ? sum : 0, mine);
@@ -683,13 +759,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   __syncthreads();
   if (s.best == 0xffffffffu) return;
   const int from = min(n, (int)s.best * run), to = min(n, from + run);
-  const int per = (run + kThreads - 1) / kThreads, j0 = min(to, from + tid * per), j1 = min(to, j0 + per);
+  const int per = (run + 2 * kThreads - 1) / (2 * kThreads) * 2, j0 = min(to, from + tid * per), j1 = min(to, j0 + per);
   u64 own = 0;
-  for (int i = j0; i < j1; ++i) own += kept(i);
+  for (int i = j0; i < j1; i += 2) own += kept(i);
   u64 at = s.cut + scan_block(s.part[1], own, mine);
   if (at <= target && target < at + own) {
     for (int i = j0; i < j1; ++i) {
-      const u64 w = kept(i);
+      const u64 e = weight(c.sc, x[i]), w = e < least || c.comp(i, x[i]) < cut ? 0 : e;
       at += w;
       if (at > target) {
         a.token[row] = base + i;
@@ -732,10 +808,9 @@ cudaError_t launch_sample(const void *logits, int dtype, int64_t rows, int64_t v
                           const float *u, const float *temperature, const int32_t *top_k,
                           const float *top_p, const float *min_p, int32_t *token, float *logp,
                           cudaStream_t stream) {
-  // A CTA's slice is at least 4096 tokens; 8 CTAs hold the largest row.
   int ranks = 1;
-  while (ranks < kMaxCluster && vocab > ranks * 4096) ranks *= 2;
-  const int slice = (int)((vocab + ranks - 1) / ranks + 31) / 32 * 32;
+  while (ranks < kMaxCluster && (vocab > ranks * kSliceMost || (vocab > ranks * kSliceLeast && rows * ranks < 2 * device_facts()->sm_count))) ranks *= 2;
+  const int slice = (int)((vocab + ranks - 1) / ranks + 63) / 64 * 64;
   const SampleArgs a = {logits, ld, (int)vocab, slice, u, temperature, top_p, min_p, top_k, token, logp};
   return dtype == Q4K_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, rows, ranks, stream) : launch_t<float>(a, rows, ranks, stream);
 }

@@ -627,7 +627,7 @@ int q4k_add_rmsnorm(const void *x, int x_dtype, int64_t ldx, const void *residua
  * token -1 and logp -infinity.  u outside [0, 1) is taken as the nearest end.
  * Each e_i is held to within about 2^-40 of the largest (sums are 64-bit
  * integers, in any order the same), so that a choice differs from the exact
- * one only where u lies that near to a border; e_i below 2^-45 count as 0.
+ * one only where u lies that near to a border; e_i below 2^-44 count as 0.
  *   logits  device, rows x vocab fp32 or bf16 (dtype), row stride ld
  *   u       device, rows fp32
  *   temperature, top_p, min_p (fp32), top_k (int32)  device, one per row, or
