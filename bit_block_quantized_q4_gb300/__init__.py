@@ -433,13 +433,11 @@ def q4k_kv_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool
     if out is None:
         if n_slots < 0:
             raise Q4KError(2, f"n_slots is {n_slots}")
-        new = _empty(2 * n + 2 * n_slots + 2, _I32, lens, stream)
-        cu = _empty(n + 1, _I64, lens, stream)
-        lens_out, status, slots, pos, state_out = torch.split_with_sizes(
-            new, (n, n, n_slots, n_slots, 2))
-        at = new.data_ptr()
-        to = (at, cu.data_ptr(), at + 8 * n, at + 8 * n + 4 * n_slots, at + 4 * n,
-              at + 8 * (n + n_slots))
+        lens_out, status = _empty(n, _I32, lens, stream), _empty(n, _I32, lens, stream)
+        slots, pos = _empty(n_slots, _I32, lens, stream), _empty(n_slots, _I32, lens, stream)
+        cu, state_out = _empty(n + 1, _I64, lens, stream), _empty(2, _I32, lens, stream)
+        to = (lens_out.data_ptr(), cu.data_ptr(), slots.data_ptr(), pos.data_ptr(),
+              status.data_ptr(), state_out.data_ptr())
     else:
         lens_out, cu, slots, pos, status, state_out = out
         to = (_vec("lens_out", lens_out, n, _I32), _vec("cu", cu, n + 1, _I64),
@@ -456,13 +454,18 @@ def q4k_kv_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool
 def _outer_strides(t: torch.Tensor):
     """Strides of all dimensions but the last (which has to be contiguous).  The stride of a dimension
     of size 1 is never used and may be anything in torch: it is given as if t were contiguous there."""
-    st, shape = list(t.stride()), t.shape
+    st, shape = t.stride(), t.shape
+    if 1 not in shape:
+        if st[-1] != 1:
+            _refuse("a tensor with a strided last dimension", t)
+        return st[:-1]
+    st = list(st)
     if shape[-1] > 1 and st[-1] != 1:
         _refuse("a tensor with a strided last dimension", t)
     for i in range(len(st) - 1):
         if shape[i] == 1:
             st[i] = max(shape[j] * (st[j] if j < len(st) - 1 else 1) for j in range(i + 1, len(st)))
-    return st[:-1]
+    return tuple(st[:-1])
 
 
 def _caches(k_cache, v_cache, k_scale, v_scale):

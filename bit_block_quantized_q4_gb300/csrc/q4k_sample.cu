@@ -46,8 +46,9 @@ namespace q4k {
 namespace {
 
 using u64 = unsigned long long;
+constexpr int kUnroll = 1;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 1024, kList = 512, kShort = 2048;
+constexpr int kBins = 1024, kList = kThreads, kShort = 2048;
 constexpr float kOrders = 46.f;
 constexpr int kMaxCluster = 8, kMaxVocab = 262144;
 // Tokens per CTA: few rows are spread as thin as kSliceLeast, many rows take as
@@ -730,7 +731,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return w0 + w1;
   };
   u64 sum = 0;
-  for (int i = i0 + 2 * lane; i < i1; i += 64) sum += kept(i);
+  if (cut == 0 && least == 0) {
+#pragma unroll kUnroll
+    for (int i = i0 + 2 * lane; i < i1; i += 64) {
+      const float2 v = *reinterpret_cast<const float2 *>(x + i);
+      u64 w0, w1;
+      weights(c.sc, v.x, v.y, w0, w1);
+      sum += w0 + w1;
+    }
+  } else {
+    for (int i = i0 + 2 * lane; i < i1; i += 64) sum += kept(i);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   u64 mine, before = scan_block(s.part[0], lane == 0 ? sum : 0, mine);
