@@ -25,8 +25,8 @@
 // bounds all sums of weights from both sides, and with them the bins in which
 // the cumulative weight can reach top_p of the total.
 //   - Up to kShort tokens down to the last of these bins (nearly always): they
-//     are sent to the cluster's first CTA, which sorts them and does the rest on
-//     the list.  Top-p without top-k needs the exact total of all weights too.
+//     are sent to the cluster's first CTA, which compares all pairs of them (up to
+//     kThreads) or sorts them, and does the rest on the list.  Top-p without top-k needs the exact total of all weights too.
 //   - Else each filter's smallest key is found by histograms over ever smaller
 //     ranges of c_i, counts and exact weights, until at most kList tokens are
 //     left, which are compared in pairs (whatever the ties); the draw then goes
@@ -166,11 +166,12 @@ __device__ __forceinline__ float log_share(const float2 *table, u64 w, u64 total
   return y0 + (float)d / (float)w;
 }
 
-// Bin of a token: 0 for the largest, kBins and above for those of weight 0 (and
-// for -infinity and NaN).  Not increasing in x.
+// Bin of a token, b for (max - x) in [b - 1/2, b + 1/2] steps: 0 for the largest,
+// kBins and above for those of weight 0 (and for -infinity and NaN).  Not
+// increasing in x.
 __device__ __forceinline__ int bin_of(const Scale &s, float x) {
   const float t = __fmul_rn(__fmaf_rn(-0.5f, x, s.half), s.cb);
-  return t < (float)kBins ? (int)t : kBins;
+  return t < (float)kBins ? magic_int(__fadd_rn(t, kMagic)) : kBins;
 }
 
 __device__ __forceinline__ uint32_t ld_peer32(const void *p, uint32_t rank) {
@@ -290,10 +291,11 @@ struct Ctx {
     for (int i = threadIdx.x; i < (int)(sizeof(s.own) / 4); i += kThreads) zero[i] = 0;
   }
 
-  // s.top: tokens per bin, over the cluster.  s.own is zero before.
+  // s.top: tokens per bin, over the cluster.  s.own and s.top are zero before.
   __device__ __forceinline__ void count_bins() {
     const int tid = threadIdx.x;
     const uint32_t at = smem_u32(s.own.count);
+#pragma unroll 4
     for (int i = 2 * tid; i < n; i += 2 * kThreads) {
       const float2 v = load2(x, i);
       const int b0 = bin_of(sc, v.x), b1 = bin_of(sc, v.y);
@@ -301,16 +303,23 @@ struct Ctx {
       if (b1 < kBins) add_own32(at, b1, 1);
     }
     sync_cluster();
-    // every CTA sums all CTAs' bins itself: cheaper than a second barrier
-    if (tid < kBins / 4) {
-      uint4 c = {0, 0, 0, 0};
-#pragma unroll 4
-      for (uint32_t p = 0; p < ranks; ++p) {
-        const uint4 v = ld_peer128(&s.own.count[tid * 4], p);
-        c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
-      }
-      *reinterpret_cast<uint4 *>(&s.top[tid * 4]) = c;
+    // Every CTA sums all CTAs' bins itself, which is cheaper than a second
+    // barrier: 4 bins per thread, of half of the CTAs.
+    static_assert(kThreads == kBins / 2, "two threads for 4 bins");
+    const int v4 = tid & (kBins / 4 - 1), half = tid / (kBins / 4);
+    uint4 c = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < kMaxCluster / 2; ++j) {
+      const uint32_t p = 2 * j + half;
+      if (p >= ranks) break;
+      const uint4 v = ld_peer128(&s.own.count[v4 * 4], p);
+      c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
     }
+    const uint32_t to = smem_u32(s.top);
+    if (c.x) add_own32(to, v4 * 4, c.x);
+    if (c.y) add_own32(to, v4 * 4 + 1, c.y);
+    if (c.z) add_own32(to, v4 * 4 + 2, c.z);
+    if (c.w) add_own32(to, v4 * 4 + 3, c.w);
     __syncthreads();
   }
 
@@ -554,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const float u = fminf(fmaxf(a.u[row], 0.f), 1.f);
   for (int i = bulk + tid; i < n; i += kThreads) x[i] = i < live ? in[i] : kNone;
   for (int i = tid; i < 256; i += kThreads) s.pow[i] = make_float2(kPow.hi[i], kPow.lo[i]);
+  for (int i = tid; i < kBins; i += kThreads) s.top[i] = 0;
   c.zero_own();
   __syncthreads();
   // a copy that does not arrive in time ends the whole cluster, at the barrier
@@ -628,17 +638,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     // bins' rounded borders.
     constexpr int PER = kBins / kThreads;
     const float step = kOrders / kBins;
-    u64 have[PER], tokens = 0, all;
+    uint32_t have[PER], tokens = 0, all;
 #pragma unroll
     for (int j = 0; j < PER; ++j) have[j] = s.top[tid * PER + j], tokens += have[j];
-    const u64 first = scan_block(s.part, tokens, all);
-    const bool whole = !use_k || all <= (u64)k;  // the top-k set is everything of any weight
-    const u64 most = whole ? all : (u64)k;
-    int bk = kBins - 1;      // the bin of the last of them
-    u64 upto_k = all, before_k = 0;  // tokens up to and before that bin
+    const uint32_t first = scan_block(reinterpret_cast<uint32_t *>(s.partf), tokens, all);
+    const bool whole = !use_k || all <= (uint32_t)k;  // the top-k set is everything of any weight
+    const uint32_t most = whole ? all : (uint32_t)k;
     if (tid == 0) s.found[0] = kBins - 1, s.found[1] = 0, s.found[2] = all;
     __syncthreads();
-    u64 at = first;
+    uint32_t at = first;
     float kept_in[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -647,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       at += have[j];
     }
     __syncthreads();
-    bk = (int)s.found[0], before_k = s.found[1], upto_k = s.found[2];
+    const int bk = (int)s.found[0];  // the bin of the last of them, and the tokens before and up to it
+    const uint32_t before_k = (uint32_t)s.found[1], upto_k = (uint32_t)s.found[2];
     // The first bin up to which the sum over bins of tokens times
     // 2^-((b + shift) step) reaches `part` of the sum over all bins with all_shift
     // (the highest logit itself counts 1); at most bk.
@@ -657,9 +666,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       for (int j = 0; j < PER; ++j) {
         const int b = tid * PER + j;
         const float most_one = b == 0 ? fminf(kept_in[j], 1.f) : 0.f;
-        v[j] = (kept_in[j] - most_one) * exp2f(-(b + shift) * step) + most_one;
+        v[j] = (kept_in[j] - most_one) * exp2f(-fmaxf(b + shift, 0.f) * step) + most_one;
         sum += v[j];
-        other += (kept_in[j] - most_one) * exp2f(-(b + all_shift) * step) + most_one;
+        other += (kept_in[j] - most_one) * exp2f(-fmaxf(b + all_shift, 0.f) * step) + most_one;
       }
       float c0 = scan_block(s.partf, sum, total);
       scan_block(s.partf, other, other_total);
@@ -676,8 +685,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       return b;
     };
     // tokens before bin b0 and up to bin b1
-    const auto span = [&](int b0, int b1, u64 &before, u64 &upto) {
-      u64 sum = first;
+    const auto span = [&](int b0, int b1, uint32_t &before, uint32_t &upto) {
+      uint32_t sum = first;
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
@@ -686,13 +695,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (tid * PER + j == b1) s.found[3] = sum;
       }
       __syncthreads();
-      before = s.found[0], upto = s.found[3];
+      before = (uint32_t)s.found[0], upto = (uint32_t)s.found[3];
     };
     const float pp = fmaxf(p, 0.f);
     int b1 = bk;  // the last bin in which the last kept token can lie
-    u64 count = upto_k, unused;
+    uint32_t count = upto_k, unused;
     if (use_p && whole) {  // the weights of a bin are at least those of its end, all at most those of their bins' beginnings
-      b1 = reach(1.01f, -0.01f, pp * 1.001f);
+      b1 = reach(0.51f, -0.51f, pp * 1.001f);
       span(0, b1, unused, count);
     }
     bool have_total = false;
@@ -704,8 +713,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       // up to bin b1, at first for the bins next to where the middles of all
       // bins put the border, then for the bins that are sure to hold it.
       for (int round = 0; round < 2; ++round) {
-        b0 = round ? reach(-0.01f, 1.01f, pp * 0.999f) : reach(0.5f, 0.5f, pp * 0.996f);
-        b1 = round ? reach(1.01f, -0.01f, pp * 1.001f) : reach(0.5f, 0.5f, pp * 1.004f);
+        b0 = round ? reach(-0.51f, 0.51f, pp * 0.999f) : reach(0.f, 0.f, pp * 0.996f);
+        b1 = round ? reach(0.51f, -0.51f, pp * 1.001f) : reach(0.f, 0.f, pp * 1.004f);
         b0 = min(b0, b1);
         u64 sum = 0, less = 0, in = 0, mine;
         for (int i = 2 * tid; i < n; i += 2 * kThreads) {
@@ -734,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (less_p < want && want <= in) break;
       }
       have_total = true;
-      u64 before_p, upto_p;
+      uint32_t before_p, upto_p;
       span(b0, b1, before_p, upto_p);
       if (whole && upto_p <= kShort) {
         count = upto_p;
@@ -747,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       // Top-p without top-k: its total is that of all tokens.
       const bool sum_all = use_p && whole && !have_total;
       u64 sum = 0, total;
+#pragma unroll 4
       for (int i = 2 * tid; i < n; i += 2 * kThreads) {
         const float2 v = load2(x, i);
         if (bin_of(c.sc, v.x) <= last) st_peer64(&s.short_list[add_peer32(&s.listed, 0, 1)], 0, c.comp(i, v.x));
@@ -759,8 +769,55 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       sync_cluster();
       if (rank != 0) return;
-      constexpr int PS = kShort / kThreads;  // tokens per thread, in order
       const int m = (int)count;
+      if (m <= kThreads) {
+        // One token per thread, compared with all others: of those before it
+        // (larger keys) the number and the weight; then of the kept ones the
+        // weight up to it in the order of the indexes.
+        const u64 key = tid < m ? s.short_list[tid] : 0;
+        u64 w = tid < m ? weight(c.sc, of_key((uint32_t)(key >> 32))) : 0;
+        if (tid < m) s.short_weight[tid] = w;
+        if (tid == 0) s.cut = have_total ? total_p : 0;
+        __syncthreads();
+        u64 before = 0;
+        uint32_t place = 0;
+        const bool mine = warp * 32 < m;  // the warp has tokens
+        if (mine) {
+#pragma unroll 4
+          for (int j = 0; j < m; ++j)
+            if (s.short_list[j] > key) ++place, before += s.short_weight[j];
+        }
+        if (use_p) {
+          // the total of the top-k set: up to its last token
+          if (!whole && tid < m && place == (uint32_t)k - 1) s.cut = before + w;
+          if (sum_all && tid == 0)
+            for (uint32_t q = 0; q < ranks; ++q) s.cut += s.total[q];
+          __syncthreads();
+          if (before >= want_of(p, s.cut)) w = 0;
+        }
+        if (use_k && place >= (uint32_t)k) w = 0;
+        if (w < least) w = 0;
+        __syncthreads();
+        if (tid < m) s.short_weight[tid] = w;
+        __syncthreads();
+        if (!mine) return;
+        u64 upto = 0;
+        total = 0;
+#pragma unroll 4
+        for (int j = 0; j < m; ++j) {
+          const u64 e = s.short_weight[j];
+          total += e;
+          if ((uint32_t)s.short_list[j] >= (uint32_t)key) upto += e;  // the low half is ~index
+        }
+        u64 target = share_of(u, total);
+        if (target >= total) target = total - 1;
+        if (w && upto > target && upto - w <= target) {
+          a.token[row] = (int32_t)~(uint32_t)key;
+          if (a.logp) a.logp[row] = log_share(s.pow, w, total);
+        }
+        return;
+      }
+      constexpr int PS = kShort / kThreads;  // tokens per thread, in order
       int size = 2;
       while (size < m) size *= 2;
       for (int i = m + tid; i < size; i += kThreads) s.short_list[i] = 0;
