@@ -467,30 +467,30 @@ struct Ctx {
 
 // Sort key[0 .. E * kThreads) descending by a bitonic network, E keys per
 // thread: steps within a thread in registers, within a warp by shuffles, and
-// the few across warps through shared memory.  Only the first `size` keys (a
-// power of two) are sorted.
+// the few across warps through shared memory.  Unrolled, so that the steps'
+// directions are constants or one predicate (as loops a step of 1024 keys took
+// 270 cycles).
 template <int E>
-__device__ void sort_keys(u64 *key, int size) {
+__device__ __noinline__ void sort_keys(u64 *key) {
   const int tid = threadIdx.x;
   u64 e[E];
 #pragma unroll
-  for (int a = 0; a < E; ++a) e[a] = tid * E + a < size ? key[tid * E + a] : 0;
-  for (int k = 2; k <= size; k *= 2) {
+  for (int a = 0; a < E; ++a) e[a] = key[tid * E + a];
+#pragma unroll
+  for (int k = 2; k <= E * kThreads; k *= 2) {
+#pragma unroll
     for (int j = k / 2; j; j /= 2) {
       if (j < E) {
 #pragma unroll
         for (int a = 0; a < E; ++a) {
-          // (constant register indices: a's partner is a ^ 1 or a ^ 2)
-#pragma unroll
-          for (int d = 1; d < E; d *= 2) {
-            if (j != d || (a & d)) continue;
-            const bool down = ((tid * E + a) & k) == 0;
-            const u64 p = e[a], q = e[a | d];
-            if ((p < q) == down) e[a] = q, e[a | d] = p;
-          }
+          if (a & j) continue;
+          const bool down = k < E ? (a & k) == 0 : ((tid * E) & k) == 0;
+          const u64 p = e[a], q = e[(a | j) % E];
+          if ((p < q) == down) e[a] = q, e[(a | j) % E] = p;
         }
       } else {
         const int m = j / E;  // distance of the partner thread
+        const bool larger = (((tid * E) & k) == 0) == ((tid & m) == 0);  // this one keeps the larger
         if (m >= 32) {
           __syncthreads();
 #pragma unroll
@@ -500,23 +500,24 @@ __device__ void sort_keys(u64 *key, int size) {
 #pragma unroll
         for (int a = 0; a < E; ++a) {
           const u64 q = m >= 32 ? key[(tid ^ m) * E + a] : __shfl_xor_sync(0xffffffffu, e[a], m & 31);
-          const bool down = ((tid * E + a) & k) == 0, first = (tid & m) == 0;
-          const bool larger = down == first;  // this one keeps the larger
-          e[a] = (e[a] > q) == larger ? e[a] : q;
+          if ((q > e[a]) == larger) e[a] = q;
         }
       }
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int a = 0; a < E; ++a)
-    if (tid * E + a < size) key[tid * E + a] = e[a];
+  for (int a = 0; a < E; ++a) key[tid * E + a] = e[a];
   __syncthreads();
 }
-__device__ void sort_down(u64 *key, int size) {
-  if (size <= kThreads) sort_keys<1>(key, size);
-  else if (size <= 2 * kThreads) sort_keys<2>(key, size);
-  else sort_keys<4>(key, size);
+// Sort the first m of kShort keys; the keys behind them are made 0.
+__device__ __forceinline__ void sort_down(u64 *key, int m) {
+  const int size = m <= 2 * kThreads ? 2 * kThreads : 4 * kThreads;
+  static_assert(kShort == 4 * kThreads, "the list is what 4 keys per thread sort");
+  for (int i = m + threadIdx.x; i < size; i += kThreads) key[i] = 0;
+  __syncthreads();
+  if (size == 2 * kThreads) sort_keys<2>(key);
+  else sort_keys<4>(key);
 }
 
 __device__ __forceinline__ u64 share_of(float part, u64 total) {  // floor(part * total), part in [0, 1]
@@ -818,11 +819,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         return;
       }
       constexpr int PS = kShort / kThreads;  // tokens per thread, in order
-      int size = 2;
-      while (size < m) size *= 2;
-      for (int i = m + tid; i < size; i += kThreads) s.short_list[i] = 0;
-      __syncthreads();
-      sort_down(s.short_list, size);
+      sort_down(s.short_list, m);
       const int kept_k = use_k ? min(m, k) : m;
       u64 w[PS], key[PS];
       sum = 0;
@@ -850,19 +847,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       int kept;  // the first `kept` of the order
       scan_block(reinterpret_cast<int *>(s.partf), mine, kept);
-      size = 2;
-      while (size < kept) size *= 2;
       // by index: ~i high, the place in the order low
 #pragma unroll
       for (int j = 0; j < PS; ++j) {
         const int i = PS * tid + j;
-        if (i < size) {
+        if (i < kept) {
           s.short_weight[i] = w[j];
-          s.short_list[i] = w[j] ? key[j] << 32 | (uint32_t)i : 0;
+          s.short_list[i] = key[j] << 32 | (uint32_t)i;
         }
       }
-      __syncthreads();
-      sort_down(s.short_list, size);
+      sort_down(s.short_list, kept);
       sum = 0;
 #pragma unroll
       for (int j = 0; j < PS; ++j) {
