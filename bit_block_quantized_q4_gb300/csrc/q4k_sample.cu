@@ -310,8 +310,8 @@ struct Ctx {
     uint4 c = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < kMaxCluster / 2; ++j) {
-      const uint32_t p = 2 * j + half;
-      if (p >= ranks) break;
+      if (2 * j + half >= ranks) break;
+      const uint32_t p = (rank + 2 * j + half) & (ranks - 1);  // not all from the same CTA at once
       const uint4 v = ld_peer128(&s.own.count[v4 * 4], p);
       c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
     }
@@ -324,35 +324,43 @@ struct Ctx {
   }
 
   // s.split: counts and weights of kBins steps of 2^shift keys down from hi, of
-  // the keys in [lo, hi].
+  // the keys in [lo, hi].  (The members are copied first: the additions to shared
+  // memory would have them loaded again for every token.)
   __device__ void split_range(u64 lo, u64 hi, int shift, bool with_weights) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, n = this->n, base = this->base;
+    const uint32_t rank = this->rank, ranks = this->ranks, lo32 = (uint32_t)(lo >> 32), hi32 = (uint32_t)(hi >> 32);
+    const Scale sc = this->sc;
+    const T *const x = this->x;
+    Shared &s = this->s;
     zero_own();
     __syncthreads();
     const uint32_t at = smem_u32(&s.own);
+    const auto add = [&](int i, float e) {
+      const uint32_t k32 = key_of(e);
+      if (k32 < lo32 || k32 > hi32) return;
+      const u64 k = (u64)k32 << 32 | (uint32_t)~(base + i);
+      if (k < lo || k > hi) return;
+      const int b = (int)((hi - k) >> shift);
+      add_own32(at, b, 1);
+      if (with_weights) {
+        const u64 w = weight(sc, e);
+        add_own32(at, kBins + b, (uint32_t)w & 0xffffu);
+        add_own32(at, 2 * kBins + b, (uint32_t)(w >> 16) & 0xffffu);
+        add_own32(at, 3 * kBins + b, (uint32_t)(w >> 32));
+      }
+    };
     for (int i = 2 * tid; i < n; i += 2 * kThreads) {
       const float2 v = load2(x, i);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float e = j ? v.y : v.x;
-        const u64 k = comp(i + j, e);
-        if (k < lo || k > hi) continue;
-        const int b = (int)((hi - k) >> shift);
-        add_own32(at, b, 1);
-        if (with_weights) {
-          const u64 w = weight(sc, e);
-          add_own32(at, kBins + b, (uint32_t)w & 0xffffu);
-          add_own32(at, 2 * kBins + b, (uint32_t)(w >> 16) & 0xffffu);
-          add_own32(at, 3 * kBins + b, (uint32_t)(w >> 32));
-        }
-      }
+      add(i, v.x);
+      add(i + 1, v.y);
     }
     sync_cluster();
     if (tid < kBins / 4) {
       uint32_t c[4] = {};
       u64 w[4] = {};
 #pragma unroll 2
-      for (uint32_t p = 0; p < ranks; ++p) {
+      for (uint32_t j = 0; j < ranks; ++j) {
+        const uint32_t p = (rank + j) & (ranks - 1);  // not all from the same CTA at once
         const uint4 v = ld_peer128(&s.own.count[tid * 4], p);
         c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
         if (with_weights) {
@@ -392,13 +400,19 @@ struct Ctx {
     __syncthreads();
   }
 
-  // The smallest key of a bin <= b.
+  // The smallest key of a bin <= b: bins do not increase with the key, so 32
+  // keys at a time tell between which two it lies.
   __device__ uint32_t least_key(int b) const {
-    uint32_t l = 0, r = key_of(sc.high);
+    const uint32_t lane = threadIdx.x & 31;
+    const Scale sc = this->sc;
+    uint32_t l = 0, r = key_of(sc.high);  // the answer is in [l, r]
     while (l < r) {
-      const uint32_t m = l + (r - l) / 2;
-      if (bin_of(sc, of_key(m)) <= b) r = m;
-      else l = m + 1;
+      const uint32_t step = (r - l) / 33 + 1, m = l + min((r - l), step * lane);
+      const unsigned in = __ballot_sync(0xffffffffu, bin_of(sc, of_key(m)) <= b);
+      const int f = in ? __ffs(in) - 1 : 32;  // the first key that is
+      if (f < 32) r = l + min(r - l, step * f);
+      if (f > 0) l = min(l + min(r - l, step * (f - 1)) + 1, r);
+      else r = l;
     }
     return l;
   }
@@ -408,7 +422,11 @@ struct Ctx {
   // which hold `count` tokens, with c0 tokens and weight w0 before them.
   // s.kept_weight: the weight of the kept ones, if with_weights.
   __device__ u64 select(bool by_weight, u64 want, bool with_weights, int b0, int b1, u64 c0, u64 w0, u64 count) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, n = this->n, base = this->base;
+    const uint32_t ranks = this->ranks;
+    const Scale sc = this->sc;
+    const T *const x = this->x;
+    Shared &s = this->s;
     u64 lo = (u64)least_key(b1) << 32;
     u64 hi = b0 ? ((u64)least_key(b0 - 1) << 32) - 1 : (u64)key_of(sc.high) << 32 | 0xffffffffu;
     while (count > kList) {
@@ -428,13 +446,18 @@ struct Ctx {
     sync_cluster();
     if (tid == 0) s.listed = 0, s.cut = ~0ull, s.kept_weight = 0;
     __syncthreads();
+    const uint32_t lo32 = (uint32_t)(lo >> 32), hi32 = (uint32_t)(hi >> 32);
+    const auto list = [&](int i, float e) {
+      const uint32_t k32 = key_of(e);
+      if (k32 < lo32 || k32 > hi32) return;
+      const u64 k = (u64)k32 << 32 | (uint32_t)~(base + i);
+      if (k >= lo && k <= hi) s.list.mine[atomicAdd(&s.listed, 1u)] = k;
+    };
+#pragma unroll 4
     for (int i = 2 * tid; i < n; i += 2 * kThreads) {
       const float2 v = load2(x, i);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const u64 k = comp(i + j, j ? v.y : v.x);
-        if (k >= lo && k <= hi) s.list.mine[atomicAdd(&s.listed, 1u)] = k;
-      }
+      list(i, v.x);
+      list(i + 1, v.y);
     }
     sync_cluster();
     if (tid < (int)ranks) s.counts[tid] = ld_peer32(&s.listed, tid);
@@ -723,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float e = j ? v.y : v.x;
-            const u64 w = c.comp(i + j, e) >= cut ? weight(c.sc, e) : 0;
+            const u64 w = !cut || c.comp(i + j, e) >= cut ? weight(c.sc, e) : 0;
             const int b = bin_of(c.sc, e);
             sum += w;
             if (b < b0) less += w;
