@@ -506,6 +506,36 @@ def test_norm(q4k, m, h, src, res, out):
         assert bool(((back - block).abs() <= H8 * block.abs() * 1.001 + 2.0 ** -10 * s[:, b, None] + 1.2 * slip[:, part]).all())
 
 
+@pytest.mark.parametrize("out", [BF16, E4M3])
+@pytest.mark.parametrize("m,h,src,res", [(700, 5120, BF16, BF16), (611, 8200, F32, BF16), (1300, 4104, BF16, None), (650, 17408, BF16, BF16), (640, 16384, F32, F32)])
+def test_norm_many_rows(q4k, m, h, src, res, out):
+    """More rows than the GPU holds at once, of more values than a block keeps in registers: against the same rows in
+    calls of a few."""
+    g = torch.Generator(device=DEV).manual_seed(h)
+    x = torch.randn((m, h), generator=g, device=DEV).to(src)
+    r = None if res is None else torch.randn((m, h), generator=g, device=DEV).to(res)
+    gamma = torch.rand(h, generator=g, device=DEV) + 0.5
+    got = q4k.q4k_add_rmsnorm(x, r, gamma, 1e-6, out_dtype=out)
+    assert q4k.q4k_get_device_error() == 0
+    hh = x.double() if r is None else x.double() + r.double()
+    y = hh / torch.sqrt((hh * hh).mean(-1, keepdim=True) + 1e-6) * gamma.double()
+    rel = (h / 32 + 24) * H32 + 8 * H32
+    if res is not None:
+        size = x.double().abs() + r.double().abs()
+        assert bool(((got[1].double() - hh).abs() <= (HB if res == BF16 else 0) * hh.abs() * 1.001 + 2 * H32 * size).all())
+    slip = rel * y.abs() + H32 * (x.double().abs() + (0 if r is None else r.double().abs())) / torch.sqrt((hh * hh).mean(-1, keepdim=True) + 1e-6) * gamma.double()
+    if out == BF16:
+        assert bool(((got[0].double() - y).abs() <= HB * y.abs() + 1.01 * slip).all())
+        return
+    s = got[2].double().repeat_interleave(128, 1)[:, :h]
+    assert bool(((got[0].double() * s - y).abs() <= H8 * y.abs() * 1.001 + 2.0 ** -10 * s + 1.2 * slip).all())
+    top = torch.nn.functional.pad(y.abs(), (0, -h % 128)).view(m, -1, 128).amax(-1) / 448
+    assert bool(((got[2].double() - top).abs() <= (2 * rel + 16 * H32) * top + 1e-6 * top).all())
+    again = q4k.q4k_add_rmsnorm(x[3:9], None if r is None else r[3:9], gamma, 1e-6, out_dtype=out)
+    off = (again[0].float() - got[0][3:9].float()).abs()
+    assert float((off > 0).float().mean()) < 0.01  # another order of the sums: a rounding here and there
+
+
 def test_norm_in_place_zero_rows_and_streams(q4k):
     g = gen(9)
     x, r, gamma = torch.randn((6, 512), generator=g), torch.randn((6, 512), generator=g).to(BF16), torch.ones(512)
@@ -590,6 +620,19 @@ def test_sample_mixed(q4k, vocab, src):
     check_sample(q4k, x.to(src), u, t, k, p, m)
     check_sample(q4k, x.to(src), u)
     check_sample(q4k, x.to(src), u, t=torch.full((rows,), 5.0), p=torch.full((rows,), 0.8))
+
+
+@pytest.mark.parametrize("rows,vocab", [(200, 3000), (160, 20011), (40, 70000)])
+def test_sample_many_rows(q4k, rows, vocab):
+    """Other cluster sizes than few rows take, and every way through the filters."""
+    x, u = peaked(rows, vocab, rows)
+    i = torch.arange(rows)
+    t = torch.tensor([1.0, 0.6, 1.5, 3.0])[i % 4]
+    k = torch.tensor([0, 0, 1500, 300, 2500, 12])[i % 6]
+    p = torch.tensor([0.9, 0.5, 0.99, 1.0, 0.9999])[i % 5]
+    m = torch.tensor([0.0, 0.0, 0.001])[i % 3]
+    check_sample(q4k, x, u, t, k, p, m)
+    check_sample(q4k, (x * 4).round().div(4).to(BF16), u, t, k, p, m)  # many ties
 
 
 def test_sample_strided_rows_of_any_alignment(q4k):

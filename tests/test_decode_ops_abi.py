@@ -31,7 +31,7 @@ PLAN = dict(lens=P, add=P, n=4, table=P, ldt=8, max_pages=8, page=16, pool=P, po
 
 @pytest.mark.parametrize("change,status", [
     (dict(n=-1), SHAPE), (dict(n=65537), SHAPE), (dict(max_pages=0), SHAPE), (dict(ldt=7), SHAPE), (dict(page=0), SHAPE),
-    (dict(pool_size=0), SHAPE), (dict(pool_size=1 << 28, page=16), SHAPE), (dict(n_slots=-1), SHAPE), (dict(n_slots=1 << 31), SHAPE),
+    (dict(max_pages=1 << 27, ldt=1 << 27), SHAPE), (dict(pool_size=0), SHAPE), (dict(pool_size=1 << 28, page=16), SHAPE), (dict(n_slots=-1), SHAPE), (dict(n_slots=1 << 31), SHAPE),
     (dict(n=0, lens=None), OK), (dict(lens=None), NULL), (dict(add=None), NULL), (dict(table=None), NULL), (dict(pool=None), NULL),
     (dict(state=None), NULL), (dict(lens_out=None), NULL), (dict(cu=None), NULL), (dict(slots=None), NULL), (dict(pos=None), NULL),
     (dict(status=None), NULL), (dict(state_out=None), NULL), (dict(cu=P + 4), ALIGN), (dict(lens=P + 2), ALIGN), (dict(slots=P + 1), ALIGN)])
@@ -66,8 +66,8 @@ ATTN = dict(q=P, ldq=1024, ldq_head=128, n=4, q_heads=8, heads=8, dim=128, k_cac
 
 @pytest.mark.parametrize("change,status", CACHE_REFUSALS + [
     (dict(page=8, page_stride=1 << 20), SHAPE), (dict(page=512, page_stride=1 << 20, head_stride=1 << 17), SHAPE), (dict(page=24, head_stride=24 * 128, page_stride=1 << 20), SHAPE),
-    (dict(n=-1), SHAPE), (dict(n=65537), SHAPE), (dict(q_heads=12), SHAPE), (dict(q_heads=2048), SHAPE), (dict(max_pages=0), SHAPE), (dict(ldt=7), SHAPE),
-    (dict(window=-1), SHAPE), (dict(scale=float("nan")), SHAPE), (dict(scale=float("inf")), SHAPE), (dict(ldq_head=64), SHAPE), (dict(ldo=1016), SHAPE),
+    (dict(n=-1), SHAPE), (dict(n=65537), SHAPE), (dict(q_heads=12), SHAPE), (dict(q_heads=2048), SHAPE), (dict(max_pages=0), SHAPE), (dict(max_pages=1 << 27, ldt=1 << 27), SHAPE), (dict(ldt=7), SHAPE),
+    (dict(cache_dtype=2, k_scale=P + 8, v_scale=P), ALIGN), (dict(window=-1), SHAPE), (dict(scale=float("nan")), SHAPE), (dict(scale=float("inf")), SHAPE), (dict(ldq_head=64), SHAPE), (dict(ldo=1016), SHAPE),
     (dict(n=0, q=None), OK), (dict(q=None), NULL), (dict(k_cache=None), NULL), (dict(v_cache=None), NULL), (dict(table=None), NULL), (dict(lens=None), NULL),
     (dict(out=None), NULL), (dict(cache_dtype=2, k_scale=P), NULL), (dict(ws=None), WORKSPACE), (dict(ws_bytes=0), WORKSPACE), (dict(q=P + 8), ALIGN), (dict(ldq=1028), ALIGN),
     (dict(ldo=1028), ALIGN), (dict(lens=P + 2), ALIGN), (dict(ws=P + 8), ALIGN), (dict(lse=P + 2), ALIGN)])
