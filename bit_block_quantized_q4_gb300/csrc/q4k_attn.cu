@@ -77,6 +77,7 @@ struct Params {
   int groups;      // query-head groups per key head
   int items;       // items per request: kv_heads * groups
   int group_size;  // query heads per key head
+  int heads_per_item;  // of them in an item: 8 per n-tile
   int box_rows, box_shift, page_shift;
   int64_t warps;   // of the whole grid
   int64_t *prefix;  // [n + 1] tiles per head before a request
@@ -145,25 +146,25 @@ struct State {
   float m[NQ][2], l[NQ][2];
 };
 
+// Writes D values of a head's row of `row` values, from d0 on, for the heads of
+// n-tiles j0 .. j0 + NQ - 1 of an item.  No token: l is 0.
 template <int D, bool E4M3, int NQ>
-__device__ __forceinline__ void write_out(const Params &p, State<D, NQ> &s, int r, int item, int dt0, int dt1, bool lse) {
+__device__ __forceinline__ void write_out(const Params &p, const State<D, NQ> &s, int r, int item, int j0, int d0, int row, bool lse) {
   const AttnArgs &a = p.a;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int kvh = item / p.groups, q0 = (item - kvh * p.groups) * 8 * NQ;
+  const int kvh = item / p.groups, q0 = (item - kvh * p.groups) * p.heads_per_item + 8 * j0;
 #pragma unroll
   for (int j = 0; j < NQ; ++j)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int q = q0 + 8 * j + 2 * t + c;
       if (q >= p.group_size) continue;
-      const float l = s.l[j][c], inv = s.m[j][c] == -INFINITY ? 0.f : 1.f / l;
+      const float l = s.l[j][c], inv = l == 0.f ? 0.f : 1.f / l;
       const int head = kvh * p.group_size + q;
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + r * a.ldo + (int64_t)head * D;
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + r * a.ldo + (int64_t)head * row + d0;
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt) {
-        if (dt < dt0 || dt >= dt1) continue;
-        const float v0 = s.m[j][c] == -INFINITY ? 0.f : s.o[dt][j][c] * inv;
-        const float v1 = s.m[j][c] == -INFINITY ? 0.f : s.o[dt][j][2 + c] * inv;
+        const float v0 = s.o[dt][j][c] * inv, v1 = s.o[dt][j][2 + c] * inv;
         if (E4M3) {
           *reinterpret_cast<uint32_t *>(out + 16 * dt + 2 * g) = pack_bf16(v0, v1);
         } else {
@@ -172,8 +173,7 @@ __device__ __forceinline__ void write_out(const Params &p, State<D, NQ> &s, int 
         }
       }
       if (lse && a.lse && g == 0)
-        a.lse[(int64_t)r * a.q_heads + head] =
-            s.m[j][c] == -INFINITY ? -INFINITY : (s.m[j][c] + log2f(l)) * 0.6931471805599453f;
+        a.lse[(int64_t)r * a.q_heads + head] = l == 0.f ? -INFINITY : (s.m[j][c] + log2f(l)) * 0.6931471805599453f;
     }
 }
 
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
           s.l[j][c] += __shfl_xor_sync(0xffffffffu, s.l[j][c], 16);
         }
       if (hd.y & (1 << 18)) {
-        write_out<D, E4M3, NQ>(p, s, cur_r, cur_item, 0, D / 16, true);
+        write_out<D, E4M3, NQ>(p, s, cur_r, cur_item, 0, 0, D, true);
       } else {
         float4 *to = reinterpret_cast<float4 *>(p.slots + (2 * gw + (hd.y >> 19 & 1)) * (int64_t)slot_floats<D, NQ>()) + lane;
 #pragma unroll
@@ -652,88 +652,79 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
 }
 
 // Joins the pieces of the items that several warps share, and writes the items
-// without tokens.  A warp joins 16 of an item's D values; a CTA has `dts` such
-// warps, times `ways` that take the pieces in turn.  Item i covers tiles
-// [A, B) of the list, so its pieces are those of warps A / run .. (B-1) / run;
-// the first of them is its warp's slot 1 (it starts the item), the others are
-// slot 0.
+// without tokens.  A warp joins one unit, 16 of an item's D values of 8 heads;
+// `ways` warps of a CTA take a unit's pieces in turn.  Item i covers tiles [A, B)
+// of the list, so its pieces are those of warps A / run .. (B-1) / run; the
+// first of them is its warp's slot 1 (it starts the item), the others are slot 0.
+constexpr int kJoinWarps = 8;
+
 template <int D, bool E4M3, int NQ>
-__global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Params p, int dts, int ways) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p, int ways) {
   constexpr int KS = D / 16;
-  extern __shared__ float part[];
+  __shared__ float4 part[kJoinWarps][2][32];
   const AttnArgs &a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp / dts;
-  const int dt = blockIdx.y * dts + warp % dts;
-  const int r = blockIdx.x / p.items, item = blockIdx.x % p.items;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, units = kJoinWarps / ways, way = warp / units;
+  const int64_t unit = (int64_t)blockIdx.x * units + warp % units;
+  const int64_t it = unit / (KS * NQ);
+  const int dj = (int)(unit - it * (KS * NQ)), dt = dj / NQ, j = dj % NQ;
+  const int r = (int)(it / p.items), item = (int)(it - (int64_t)r * p.items);
   grid_dependency_wait();
-  const int64_t before = p.prefix[r], nt = p.prefix[r + 1] - before, run = run_of(p.prefix[a.n] * p.items, p.warps);
-  const int64_t A = before * p.items + item * nt, w0 = A / run, w1 = nt ? (A + nt - 1) / run : w0;
-  if (nt && w0 == w1) return;
-  State<16, NQ> s;
-#pragma unroll
-  for (int j = 0; j < NQ; ++j) {
-    s.m[j][0] = s.m[j][1] = -INFINITY;
-    s.l[j][0] = s.l[j][1] = 0.f;
-    s.o[0][j][0] = s.o[0][j][1] = s.o[0][j][2] = s.o[0][j][3] = 0.f;
+  int64_t w0 = 0, w1 = 0, nt = 1;  // what is left so has nothing to join
+  if (r < a.n) {
+    const int64_t before = p.prefix[r], total = p.prefix[a.n] * p.items;
+    nt = p.prefix[r + 1] - before;
+    const int64_t A = before * p.items + item * nt, run = run_of(total, p.warps);
+    if (total <= INT32_MAX) {  // 64-bit divisions take as long as the loads
+      w0 = (uint32_t)A / (uint32_t)run;
+      w1 = nt ? (uint32_t)(A + nt - 1) / (uint32_t)run : w0;
+    } else {
+      w0 = A / run;
+      w1 = nt ? (A + nt - 1) / run : w0;
+    }
   }
-  const auto add = [&](float4 o, float4 ml, int j) {
+  const bool joined = w1 > w0 || nt == 0;
+  if (ways == 1 && !joined) return;
+  State<16, 1> s;
+  s.m[0][0] = s.m[0][1] = -INFINITY;
+  s.l[0][0] = s.l[0][1] = 0.f;
+  s.o[0][0][0] = s.o[0][0][1] = s.o[0][0][2] = s.o[0][0][3] = 0.f;
+  const auto add = [&](float4 o, float4 ml) {
     const float m2[2] = {ml.x, ml.y}, l2[2] = {ml.z, ml.w}, o2[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const float m = fmaxf(s.m[j][c], m2[c]);
-      const float f = s.m[j][c] == m ? 1.f : ex2(s.m[j][c] - m), f2 = m2[c] == m ? 1.f : ex2(m2[c] - m);
-      s.m[j][c] = m;
-      s.l[j][c] = s.l[j][c] * f + l2[c] * f2;
-      s.o[0][j][c] = s.o[0][j][c] * f + o2[c] * f2;
-      s.o[0][j][2 + c] = s.o[0][j][2 + c] * f + o2[2 + c] * f2;
+      const float m = fmaxf(s.m[0][c], m2[c]);
+      const float f = s.m[0][c] == m ? 1.f : ex2(s.m[0][c] - m), f2 = m2[c] == m ? 1.f : ex2(m2[c] - m);
+      s.m[0][c] = m;
+      s.l[0][c] = s.l[0][c] * f + l2[c] * f2;
+      s.o[0][0][c] = s.o[0][0][c] * f + o2[c] * f2;
+      s.o[0][0][2 + c] = s.o[0][0][2 + c] * f + o2[2 + c] * f2;
     }
   };
-  if (nt) {
+  if (w1 > w0) {
     constexpr int U = 4;  // pieces loaded at a time
     for (int64_t w = w0 + way; w <= w1; w += U * ways) {
-      float4 o[U][NQ], ml[U][NQ];
+      float4 o[U], ml[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t x = min(w + u * ways, w1);
         const float4 *from = reinterpret_cast<const float4 *>(p.slots + (2 * x + (x == w0)) * (int64_t)slot_floats<D, NQ>()) + lane;
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) o[u][j] = from[(dt * NQ + j) * 32], ml[u][j] = from[(KS * NQ + j) * 32];
+        o[u] = from[(dt * NQ + j) * 32], ml[u] = from[(KS * NQ + j) * 32];
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (w + u * ways <= w1) {
-#pragma unroll
-          for (int j = 0; j < NQ; ++j) add(o[u][j], ml[u][j], j);
-        }
+        if (w + u * ways <= w1) add(o[u], ml[u]);
     }
   }
-  if (ways > 1) {
-    float4 *mine = reinterpret_cast<float4 *>(part) + warp * NQ * 64 + lane;
-#pragma unroll
-    for (int j = 0; j < NQ; ++j) {
-      mine[j * 64] = make_float4(s.o[0][j][0], s.o[0][j][1], s.o[0][j][2], s.o[0][j][3]);
-      mine[j * 64 + 32] = make_float4(s.m[j][0], s.m[j][1], s.l[j][0], s.l[j][1]);
+  for (int half = ways / 2; half; half /= 2) {  // the upper half of the ways to the lower
+    if (way >= half && way < 2 * half) {
+      part[warp][0][lane] = make_float4(s.o[0][0][0], s.o[0][0][1], s.o[0][0][2], s.o[0][0][3]);
+      part[warp][1][lane] = make_float4(s.m[0][0], s.m[0][1], s.l[0][0], s.l[0][1]);
     }
     __syncthreads();
-    if (way) return;
-    for (int v = 1; v < ways; ++v) {
-      const float4 *from = reinterpret_cast<const float4 *>(part) + (warp + v * dts) * NQ * 64 + lane;
-#pragma unroll
-      for (int j = 0; j < NQ; ++j) add(from[j * 64], from[j * 64 + 32], j);
-    }
+    if (way < half) add(part[warp + half * units][0][lane], part[warp + half * units][1][lane]);
   }
-  // written by the code of a whole item, this warp's 16 values in place of all
-  State<D, NQ> all;
-#pragma unroll
-  for (int j = 0; j < NQ; ++j) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) all.m[j][c] = s.m[j][c], all.l[j][c] = s.l[j][c];
-#pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) all.o[i][j][c] = s.o[0][j][c];
-  }
-  write_out<D, E4M3, NQ>(p, all, r, item, dt, dt + 1, dt == 0);
+  if (!joined || way) return;
+  write_out<16, E4M3, 1>(p, s, r, item, j, dt * 16, D, dt == 0);
 }
 
 int query_tiles(int dim, int group) { return group > 8 && dim <= 128 ? 2 : 1; }
@@ -771,24 +762,23 @@ cudaError_t launch_cfg(Params &p, cudaStream_t stream) {
   paged_attn_kernel<D, E4M3, NQ><<<grid, C::kWarps * 32, C::kSmem, stream>>>(p, maps[0], maps[1]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // An item has about warps / items pieces; a warp takes 4 to 8 of them.  (One
-  // CTA per item with its D / 16 warps alone took 11 us for 16 items of 114
-  // pieces; 16 ways for every item took 40 us for 256 items of 4.)
+  // An item has about warps / items pieces; a warp takes 4 to 8 of them.  (With
+  // one CTA per item the join of 16 items of 114 pieces alone took 11 us; 16 ways
+  // for every item took 40 us for 256 items of 4.)
   const int64_t items = (int64_t)a.n * p.items, pieces = p.warps / items;
   int ways = 1;
-  while (ways < 16 && ways * 4 < pieces) ways *= 2;
-  const int dts = D / 16 < 16 / ways ? D / 16 : 16 / ways;
+  while (ways < kJoinWarps && ways * 4 < pieces) ways *= 2;
+  const int units = kJoinWarps / ways;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)items, D / 16 / dts);
-  cfg.blockDim = dim3(dts * ways * 32);
-  cfg.dynamicSmemBytes = ways > 1 ? (size_t)dts * ways * NQ * 64 * 16 : 0;
+  cfg.gridDim = dim3((unsigned)((items * (D / 16) * NQ + units - 1) / units));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<D, E4M3, NQ>, p, dts, ways);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<D, E4M3, NQ>, p, ways);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -812,6 +802,7 @@ cudaError_t launch_paged_attn(const AttnArgs &a, cudaStream_t s) {
   p.a = a;
   p.group_size = a.q_heads / a.kv_heads;
   const int nq = query_tiles(a.dim, p.group_size);
+  p.heads_per_item = 8 * nq;
   p.groups = (p.group_size + 8 * nq - 1) / (8 * nq);
   p.items = a.kv_heads * p.groups;
   p.prefix = static_cast<int64_t *>(a.workspace);
