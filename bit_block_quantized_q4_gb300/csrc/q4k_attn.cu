@@ -125,11 +125,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
 }
-// Two e4m3 values (the low 16 bits) to an fp16 pair, exact.
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t w) {
-  uint32_t y;
-  asm("{\n .reg .b16 lo;\n cvt.u16.u32 lo, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(y) : "r"(w));
-  return y;
+// Four e4m3 values to two fp16 pairs (the lower two, the upper two), exact.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(lo), "=r"(hi) : "r"(w));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -475,8 +474,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = e4m3x2_f16(k4[2 * h]), a1 = e4m3x2_f16(k4[2 * h + 1]);
-              const uint32_t a2 = e4m3x2_f16(k4[2 * h] >> 16), a3 = e4m3x2_f16(k4[2 * h + 1] >> 16);
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_f16(k4[2 * h], a0, a2);
+              e4m3x4_f16(k4[2 * h + 1], a1, a3);
 #pragma unroll
               for (int j = 0; j < NQ; ++j)
                 mma_f16(zc[(2 * i + h) % CH][mt][j], a0, a1, a2, a3, qf[2 * i + h][j][0], qf[2 * i + h][j][1]);
@@ -510,17 +510,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
           lv[mt][h] = lg2(vs);
           rv[mt][h] = rcp_approx(vs);
         }
-        const bool there = !partial || (valid >> (mt * 16 + 8 * h + g) & 1u);
 #pragma unroll
         for (int j = 0; j < NQ; ++j)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float &x = z[mt][j][2 * h + c];
             x = E4M3 ? fmaf(x * qs[j][c], ks, lv[mt][h]) : x * qs[j][c];
-            if (!there) x = -INFINITY;
           }
       }
     if (partial) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (!(valid >> (mt * 16 + 8 * h + g) & 1u)) {
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) z[mt][j][2 * h] = z[mt][j][2 * h + 1] = -INFINITY;
+          }
       // zero the V rows that are not there: 0 * (whatever they hold) must be 0
       for (int i = lane; i < C::kSide / 16; i += 32) {
         const int in_box = i % (box_bytes / 16);
@@ -613,8 +619,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
           for (int h = 0; h < 2; ++h) {
             // bytes (key 2t: d 2g, 2g + 1; key 2t + 1: the same) to fp16 pairs
             // of the two keys for d 2g and for d 2g + 1
-            const uint32_t x = __byte_perm(v4[2 * h], 0, 0x3120), y = __byte_perm(v4[2 * h + 1], 0, 0x3120);
-            const uint32_t a0 = e4m3x2_f16(x), a1 = e4m3x2_f16(x >> 16), a2 = e4m3x2_f16(y), a3 = e4m3x2_f16(y >> 16);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_f16(__byte_perm(v4[2 * h], 0, 0x3120), a0, a1);
+            e4m3x4_f16(__byte_perm(v4[2 * h + 1], 0, 0x3120), a2, a3);
 #pragma unroll
             for (int j = 0; j < NQ; ++j) mma_f16(s.o[2 * i + h][j], a0, a1, a2, a3, ph[mt][j][0], ph[mt][j][1]);
           }
