@@ -249,8 +249,10 @@ __global__ void __launch_bounds__(256, kWriteBlocks) kv_write_kernel(const Write
 #pragma unroll
       for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
       amax = fmaxf(amax, kAmaxFloor);
-      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + to) = to_e4m3x8(v, 448.f / amax);
-      if (c == 0) scale[((int64_t)page * a.heads + h) * a.page.d + off] = amax / 448.f;
+      float factor;
+      const float inv = block_factor(amax, c, mask, factor);
+      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + to) = to_e4m3x8(v, inv);
+      if (c == 0) scale[((int64_t)page * a.heads + h) * a.page.d + off] = factor;
     }
   }
 }

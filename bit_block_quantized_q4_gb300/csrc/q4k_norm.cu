@@ -42,14 +42,15 @@ struct NormArgs {
   unsigned *err;
 };
 
-// y of one 8-value vector: `in` is false for lanes past the end of the row,
-// which take part in the half-warp's block maximum with 0.
+// y of one 8-value vector, to row pointers y and scales: `in` is false for lanes
+// past the end of the row, which take part in the half-warp's block maximum with
+// 0.
 template <bool E4M3>
-__device__ __forceinline__ void write_y(const NormArgs &a, int64_t row, int vec, bool in, float rinv, float (&v)[8]) {
+__device__ __forceinline__ void write_y(const float *gamma, uint8_t *y, float *scales, int vec, bool in, float rinv, float (&v)[8]) {
   float amax = 0.f;
   if (in) {
     float g[8];
-    load8(a.gamma + vec * 8, g);
+    load8(gamma + vec * 8, g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       v[j] = v[j] * rinv * g[j];
@@ -59,14 +60,19 @@ __device__ __forceinline__ void write_y(const NormArgs &a, int64_t row, int vec,
   if constexpr (E4M3) {
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    amax = fmaxf(amax, kAmaxFloor);
+    float scale;
+    const float inv = block_factor(fmaxf(amax, kAmaxFloor), threadIdx.x & 15, 0xffffffffu, scale);
     if (in) {
-      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.y) + row * a.ldy + vec * 8) = to_e4m3x8(v, 448.f / amax);
-      if ((vec & 15) == 0) a.scales[row * a.lds + (vec >> 4)] = amax / 448.f;
+      *reinterpret_cast<uint2 *>(y + vec * 8) = to_e4m3x8(v, inv);
+      if ((vec & 15) == 0) scales[vec >> 4] = scale;
     }
   } else if (in) {
-    store8(static_cast<__nv_bfloat16 *>(a.y) + row * a.ldy + vec * 8, v);
+    store8(reinterpret_cast<__nv_bfloat16 *>(y) + vec * 8, v);
   }
+}
+template <bool E4M3>
+__device__ __forceinline__ uint8_t *row_of_y(const NormArgs &a, int64_t row) {
+  return static_cast<uint8_t *>(a.y) + row * a.ldy * (E4M3 ? 1 : 2);
 }
 
 // Few rows: a block (tpr, rows) loads its rows straight into registers, tpr
@@ -121,20 +127,25 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
   }
   if (!live) return;
   const float rinv = rsqrtf(ss / (float)a.h + a.eps);
+  uint8_t *y = row_of_y<E4M3>(a, row);
+  float *scales = E4M3 ? a.scales + row * a.lds : nullptr;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int vec = threadIdx.x + i * tpr;
-    write_y<E4M3>(a, row, vec, vec < nvec, rinv, v[i]);
+    write_y<E4M3>(a.gamma, y, scales, vec, vec < nvec, rinv, v[i]);
   }
 }
 
 // Many rows: persistent blocks, each with a ring of rows in shared memory that
-// bulk copies fill `stages` rows ahead (x, then the residual).  A row is read
-// twice from shared memory (sum of squares, then y), so nothing is held in
-// registers and the loads of the next rows never stop.  One barrier per row:
-// behind it every thread has its part of the sum, and every thread has left
-// the row before, whose stage is then refilled.
-template <typename TX, typename TR, bool E4M3>
+// bulk copies fill `stages` rows ahead (x, then the residual), so that the loads
+// of the next rows never stop.  A thread takes up to KEEP vectors of a row, which
+// it keeps in registers between the sum of squares and y; with KEEP = 0 it takes
+// any number and reads them again.  One barrier per row: behind it every thread
+// has its part of the sum, and every thread has left the row before, whose stage
+// is then refilled.  (8191 x 5120 to e4m3: 47.3 us kept, 49.3 read again; 2000 x
+// 17408: 31.6 us read again, 35.6 with 8 kept, whose registers leave room for one
+// block per SM only.)
+template <typename TX, typename TR, bool E4M3, int KEEP>
 __global__ void __launch_bounds__(512) add_rmsnorm_rows_kernel(const NormArgs a, int stages) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float part[2][16];
@@ -160,28 +171,38 @@ __global__ void __launch_bounds__(512) add_rmsnorm_rows_kernel(const NormArgs a,
     for (int s = 0; s < stages; ++s) fetch(s);
   int slot = 0, prev = -1, flip = 0;
   uint32_t phase = 0;
+  const float inv_h = 1.f / (float)a.h;
   for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
     const bool ok = mbar_wait(&full[slot], phase, a.err);
     const TX *x = reinterpret_cast<const TX *>(ring + slot * (xb + rb));
     const TR *r = reinterpret_cast<const TR *>(ring + slot * (xb + rb) + xb);
-    const auto load_h = [&](int vec, float (&v)[8]) {
+    TR *res_out = rb ? static_cast<TR *>(a.res_out) + row * a.ldro : nullptr;
+    float ss = 0.f;
+    // h of a vector: x + residual, added to the sum and stored where `first`
+    const auto load_h = [&](int vec, float (&v)[8], bool first) {
       load8(x + vec * 8, v);
       if (rb) {
         float w[8];
         load8(r + vec * 8, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += w[j];
+        if (first) store8(res_out + vec * 8, v);
       }
-    };
-    float ss = 0.f;
-    if (ok)
-      for (int vec = tid; vec < nvec; vec += threads) {
-        float v[8];
-        load_h(vec, v);
-        if (rb) store8(static_cast<TR *>(a.res_out) + row * a.ldro + vec * 8, v);
+      if (first) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
       }
+    };
+    float v[KEEP ? KEEP : 1][8];
+    if (ok) {
+      if constexpr (KEEP > 0) {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+          if (tid + i * threads < nvec) load_h(tid + i * threads, v[i], true);
+      } else {
+        for (int vec = tid; vec < nvec; vec += threads) load_h(vec, v[0], true);
+      }
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if ((tid & 31) == 0) part[flip][tid >> 5] = ss;
@@ -193,12 +214,19 @@ __global__ void __launch_bounds__(512) add_rmsnorm_rows_kernel(const NormArgs a,
     if (tid == 0 && prev >= 0) fetch(prev);
     ss = 0.f;
     for (int i = 0; i < warps; ++i) ss += part[flip][i];
-    const float rinv = rsqrtf(ss / (float)a.h + a.eps);
-    for (int i = 0; i < loops; ++i) {
-      const int vec = tid + i * threads;
-      float v[8];
-      if (vec < nvec) load_h(vec, v);
-      write_y<E4M3>(a, row, vec, vec < nvec, rinv, v);
+    const float rinv = rsqrtf(ss * inv_h + a.eps);
+    uint8_t *y = row_of_y<E4M3>(a, row);
+    float *scales = E4M3 ? a.scales + row * a.lds : nullptr;
+    if constexpr (KEEP > 0) {
+#pragma unroll
+      for (int i = 0; i < KEEP; ++i)
+        write_y<E4M3>(a.gamma, y, scales, tid + i * threads, tid + i * threads < nvec, rinv, v[i]);
+    } else {
+      for (int i = 0; i < loops; ++i) {
+        const int vec = tid + i * threads;
+        if (vec < nvec) load_h(vec, v[0], false);
+        write_y<E4M3>(a.gamma, y, scales, vec, vec < nvec, rinv, v[0]);
+      }
     }
     prev = slot;
     flip ^= 1;
@@ -214,31 +242,38 @@ void launch_nv(const NormArgs &a, bool e4m3, dim3 grid, dim3 block, cudaStream_t
     add_rmsnorm_kernel<NV, TX, TR, false><<<grid, block, 0, s>>>(a);
 }
 
-template <typename TX, typename TR, bool E4M3>
-cudaError_t launch_rows(const NormArgs &a, int stage, cudaStream_t s) {
+template <typename TX, typename TR, bool E4M3, int KEEP>
+cudaError_t launch_rows_kept(const NormArgs &a, int stage, int threads, cudaStream_t s) {
   const DeviceFacts *f = device_facts();
   static bool ready[kMaxDevices];  // the attribute is per device
   if (!ready[f->device]) {
-    const cudaError_t e = cudaFuncSetAttribute(add_rmsnorm_rows_kernel<TX, TR, E4M3>,
+    const cudaError_t e = cudaFuncSetAttribute(add_rmsnorm_rows_kernel<TX, TR, E4M3, KEEP>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     if (e != cudaSuccess) return e;
     ready[f->device] = true;
   }
-  // 8192 rows of 5120 bf16 to e4m3: 320 threads 50.8 us, 256 53.7, 160 56.6;
-  // 2000 rows of 17408: 512 threads 32.0 us, 320 34.4, 160 44.7.
-  const int nvec = a.h / 8, most = nvec > 2048 ? 512 : 320, loops = (nvec + most - 1) / most;
-  const int threads = ((nvec + loops - 1) / loops + 31) / 32 * 32;
   // blocks per SM: as many as keep two rows each in flight, up to 1536 threads
   int blocks = kRowsSmThreads / threads;
   if (blocks > kRingBytes / (2 * stage)) blocks = kRingBytes / (2 * stage);
   if (blocks > 16) blocks = 16;
   if (blocks < 1) blocks = 1;
   int stages = kRingBytes / blocks / stage;
-  if (stages > 4) stages = 4;
+  if (stages > kMaxStages) stages = kMaxStages;
   int64_t grid = (int64_t)f->sm_count * blocks;
   if (grid > a.m) grid = a.m;
-  add_rmsnorm_rows_kernel<TX, TR, E4M3><<<(unsigned)grid, threads, stages * stage, s>>>(a, stages);
+  add_rmsnorm_rows_kernel<TX, TR, E4M3, KEEP><<<(unsigned)grid, threads, stages * stage, s>>>(a, stages);
   return cudaGetLastError();
+}
+template <typename TX, typename TR, bool E4M3>
+cudaError_t launch_rows(const NormArgs &a, int stage, cudaStream_t s) {
+  // Threads per row, before vectors were kept: 8192 rows of 5120 bf16 to e4m3 took
+  // 50.8 us with 320, 53.7 with 256, 56.6 with 160; 2000 rows of 17408 32.0 us with
+  // 512, 34.4 with 320, 44.7 with 160.
+  const int nvec = a.h / 8, most = nvec > 2048 ? 512 : 320, loops = (nvec + most - 1) / most;
+  const int threads = ((nvec + loops - 1) / loops + 31) / 32 * 32;
+  if (loops <= 2) return launch_rows_kept<TX, TR, E4M3, 2>(a, stage, threads, s);
+  if (loops <= 4) return launch_rows_kept<TX, TR, E4M3, 4>(a, stage, threads, s);
+  return launch_rows_kept<TX, TR, E4M3, 0>(a, stage, threads, s);
 }
 
 template <typename TX, typename TR>
@@ -248,7 +283,7 @@ cudaError_t launch_types(const NormArgs &a, bool e4m3, cudaStream_t s) {
   // Rows of up to 4096 values fit the registers of a block often enough to keep
   // the memory busy (30000 x 1024: 37.4 us against 45.1 through the ring; 8192 x
   // 4096 from fp32: 47.0 against 51.6); longer ones do not (8191 x 5120 to e4m3:
-  // 56.8 against 50.8; 2000 x 17408: 42.7 against 32.0).  With fewer than 4 rows
+  // 56.8 against 47.3; 2000 x 17408: 42.7 against 31.6).  With fewer than 4 rows
   // per SM there is nothing to fetch ahead.
   if (nvec > 512 && a.m > 4 * sms && 2 * stage <= kRingBytes)
     return e4m3 ? launch_rows<TX, TR, true>(a, stage, s) : launch_rows<TX, TR, false>(a, stage, s);

@@ -79,6 +79,16 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
+// The scale of a block, max / 448, in the block's first lane and the factor of
+// its values, 448 / max, in all others and returned to all: one division.  Lanes
+// of a block are consecutive, `place` is the lane's in it; `mask` are the lanes
+// that take part.
+__device__ __forceinline__ float block_factor(float amax, int place, unsigned mask, float &scale) {
+  const bool first = place == 0;
+  const float q = (first ? amax : 448.f) / (first ? 448.f : amax);
+  scale = q;
+  return __shfl_sync(mask, q, (int)(threadIdx.x & 31) - place + 1);
+}
 // e4m3(v * inv), nearest even, finite overflow saturating to 448, NaN kept.
 __device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], float inv) {
   uint32_t w[2];
