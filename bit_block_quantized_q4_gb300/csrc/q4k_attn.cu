@@ -47,6 +47,7 @@
 #include "q4k_device.cuh"
 #include "q4k_internal.h"
 #include "q4k_step.cuh"
+#include "q4k_step.h"
 
 namespace q4k {
 namespace {
@@ -506,7 +507,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
         float ks = 1.f;
         if (E4M3) {
           ks = ksc[mt * 16 + 8 * h + g];
-          const float vs = fmaxf(vsc[mt * 16 + 8 * h + g], 1.1754944e-38f);
+          // (a floor of 2^-96 keeps the sum of 1 / scale finite for any number of tokens)
+          const float vs = fmaxf(vsc[mt * 16 + 8 * h + g], 1.2621774e-29f);
           lv[mt][h] = lg2(vs);
           rv[mt][h] = rcp_approx(vs);
         }

@@ -21,6 +21,7 @@
 #include "q4k_device.cuh"
 #include "q4k_internal.h"
 #include "q4k_step.cuh"
+#include "q4k_step.h"
 
 namespace q4k {
 namespace {

@@ -46,6 +46,7 @@
 #include "../../include/q4k.h"
 #include "q4k_device.cuh"
 #include "q4k_internal.h"
+#include "q4k_step.h"
 
 namespace q4k {
 namespace {

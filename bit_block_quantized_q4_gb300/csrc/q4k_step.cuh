@@ -8,7 +8,23 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "q4k_device.cuh"
+
 namespace q4k {
+
+// Device error word: a page, slot or length outside the cache or the table.
+constexpr unsigned kDevErrBadPage = 4u;
+
+// Tiled tensor copy global -> shared, completion counted on `bar` in bytes.
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "r"(c4)
+      : "memory");
+}
 
 // Division of 0 <= x < 2^31 by a fixed 1 <= d < 2^31 with one multiplication:
 // with s = ceil(log2 d) and m = floor(2^(31+s) / d) + 1 (< 2^32 + 1; d = 1 and

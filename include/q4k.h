@@ -561,11 +561,14 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
  * Scores, softmax statistics and sums are fp32.  For a bf16 cache the softmax
  * weights enter the products as two bf16 terms (16 significant bits), for an
  * e4m3 cache as one fp16 term (11 bits) of the weight times the row's scale.
+ * Values that are not finite in rows that take part show in the result; an
+ * infinite value of V may do so as NaN.
  *   q       device, bf16, element (r, i, d) at r * ldq + i * ldq_head + d;
  *           16-byte aligned, strides multiples of 8
  *   caches  as above; 16-byte aligned, strides multiples of 16 bytes.  dim 64,
  *           128 or 256; page_size 16, 32, 64, 128 or 256
- *   scales  for an e4m3 cache: positive, finite, 16-byte aligned; NULL for bf16
+ *   scales  for an e4m3 cache: positive, finite, 16-byte aligned (V scales below
+ *           2^-96 count as 2^-96); NULL for bf16
  *   table   device, n rows of max_pages int32, row stride ldt
  *   lens    device, n int32
  *   out     device, bf16, row stride ldo >= q_heads * dim, heads contiguous;

@@ -431,6 +431,35 @@ def test_attn_pages_outside_the_cache_count_as_absent(q4k, kind):
     check_attn(q4k, c, 0.1)
 
 
+def test_attn_rows_of_zeros_and_values_that_are_not_finite(q4k):
+    """Zero rows of an e4m3 cache have the smallest scale; what is not finite in a row that counts shows."""
+    n, h, page, d = 3000, 2, 64, 128
+    x = torch.zeros((n, 2, h, d))
+    x[:, 0] = torch.randn((n, h, d), generator=gen(1))
+    caches = [torch.zeros((n // page + 1, h, page, d), dtype=torch.uint8, device=DEV).view(E4M3) for _ in range(2)]
+    sc = [torch.zeros((n // page + 1, h, page), device=DEV) for _ in range(2)]
+    q4k.q4k_kv_write(x[:, 0].to(DEV), x[:, 1].to(DEV), torch.arange(n, dtype=torch.int32, device=DEV), *caches, *sc)
+    table = torch.arange(n // page + 1, dtype=torch.int32, device=DEV)[None]
+    q = torch.randn((1, 4, d), generator=gen(2)).to(BF16)
+    out, lse = q4k.q4k_paged_attn(q.to(DEV), *caches, table, torch.tensor([n], dtype=torch.int32, device=DEV), 0.1, *sc)
+    assert not out.any()
+    k = caches[0].double().cpu().transpose(1, 2).reshape(-1, h, d)[:n] * sc[0].double().cpu().transpose(1, 2).reshape(-1, h)[:n, :, None]
+    want = torch.logsumexp(torch.einsum("hd,thd->ht", q[0].double(), k.repeat_interleave(2, 1)) * 0.1, 1)
+    assert bool(((lse[0].double().cpu() - want).abs() <= 2.0 ** -16).all())  # scores of some units in fp32, 3000 terms
+    c = make_attn(3, [40, 1, 33, 20], 4, 2, 64, 16, BF16)
+    for r, kv, t, v in ((0, 0, 7, math.nan), (1, 0, 0, math.nan), (2, 1, 32, math.inf), (3, 0, 3, -math.inf)):
+        c["caches"][kv][c["table"][r, t // 16], 1, t % 16, 5] = v
+    out, lse = q4k.q4k_paged_attn(c["q"].to(DEV), *[to_dev(x) for x in c["caches"]], c["table"].to(DEV), c["lens"].to(DEV), 0.1)
+    out, lse = out.float().cpu(), lse.cpu()
+    assert bool(torch.isfinite(out[:, :2]).all()) and bool(torch.isfinite(lse[:, :2]).all())  # the other key head
+    assert bool(torch.isnan(out[:2, 2:]).all()) and bool(torch.isnan(lse[:2, 2:]).all())
+    # (an infinite value times a weight in two terms: an infinity or no number, as the header says)
+    assert not bool(torch.isfinite(out[2, 2:, 5]).any()) and bool(torch.isfinite(out[2, 2:, :5]).all())
+    qk = c["q"][3, 2:, 5].float()  # a score of -inf takes no part, one of +inf leaves no number
+    for i in range(2):
+        assert bool(torch.isfinite(out[3, 2 + i]).all()) if qk[i] > 0 else bool(torch.isnan(out[3, 2 + i]).all())
+
+
 def test_attn_offsets_past_32_bits(q4k):
     """A cache of over 2^32 bytes, used at its end."""
     pages, heads, page, dim = 70000, 2, 128, 128
