@@ -455,17 +455,16 @@ def _outer_strides(t: torch.Tensor):
     """Strides of all dimensions but the last (which has to be contiguous).  The stride of a dimension
     of size 1 is never used and may be anything in torch: it is given as if t were contiguous there."""
     st, shape = t.stride(), t.shape
-    if 1 not in shape:
-        if st[-1] != 1:
-            _refuse("a tensor with a strided last dimension", t)
-        return st[:-1]
-    st = list(st)
-    if shape[-1] > 1 and st[-1] != 1:
+    if st[-1] != 1 and shape[-1] > 1:
         _refuse("a tensor with a strided last dimension", t)
-    for i in range(len(st) - 1):
+    if 1 not in shape:
+        return st[:-1]
+    out, span = list(st[:-1]), shape[-1]
+    for i in range(len(out) - 1, -1, -1):
         if shape[i] == 1:
-            st[i] = max(shape[j] * (st[j] if j < len(st) - 1 else 1) for j in range(i + 1, len(st)))
-    return tuple(st[:-1])
+            out[i] = span
+        span = max(span, out[i] * shape[i])
+    return tuple(out)
 
 
 def _caches(k_cache, v_cache, k_scale, v_scale):
@@ -476,7 +475,7 @@ def _caches(k_cache, v_cache, k_scale, v_scale):
     if v_cache.shape != shape or v_cache.dtype is not dtype:
         _refuse("v_cache", v_cache)
     strides = _outer_strides(k_cache)
-    if strides != _outer_strides(v_cache):
+    if v_cache.stride() != k_cache.stride() and strides != _outer_strides(v_cache):
         raise Q4KError(2, "k_cache and v_cache have different strides")
     if dtype is _BF16:
         return shape, strides, 1, None, None
@@ -499,7 +498,7 @@ def q4k_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache:
     if v.shape != k.shape or v.dtype is not dtype:
         _refuse("v", v)
     ld = _outer_strides(k)
-    if ld != _outer_strides(v):
+    if v.stride() != k.stride() and ld != _outer_strides(v):
         raise Q4KError(2, "k and v have different strides")
     _check((_lib or lib()).q4k_kv_write(
         k.data_ptr(), v.data_ptr(), 1 if dtype is _BF16 else 0, ld[0], ld[1],
