@@ -664,6 +664,20 @@ def test_sample_many_rows(q4k, rows, vocab):
     check_sample(q4k, (x * 4).round().div(4).to(BF16), u, t, k, p, m)  # many ties
 
 
+@pytest.mark.parametrize("rows,vocab", [(6, 9001), (170, 40003), (6, 131071)])
+def test_sample_long_kept_sets_with_masked_tokens(q4k, rows, vocab):
+    """More tokens kept than are sorted, with -inf and NaN between them."""
+    x, u = peaked(rows, vocab, vocab + 1, 1.0)
+    x[:, 5::11] = -math.inf
+    x[:, 3::17] = math.nan
+    i = torch.arange(rows)
+    k = torch.tensor([0, 2100, vocab // 2, 7000])[i % 4]
+    p = torch.tensor([0.97, 0.9, 0.999])[i % 3]
+    for src in (F32, BF16):
+        check_sample(q4k, x.to(src), u, torch.full((rows,), 3.0), k, p)
+        check_sample(q4k, x.to(src), u, torch.full((rows,), 3.0), k, p, torch.full((rows,), 1e-3))
+
+
 def test_sample_strided_rows_of_any_alignment(q4k):
     for src in (F32, BF16):
         x, u = peaked(5, 1111, 3)
