@@ -8,6 +8,7 @@
 // length and error-path behaviour is tested.
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <algorithm>
 
 #include <initializer_list>
 #include <mutex>
@@ -614,16 +615,22 @@ int check_cache(int32_t kv_heads, int32_t dim, int cache_dtype, int64_t n_pages,
   if (kv_heads <= 0 || kv_heads > 1024 || n_pages <= 0 || page_size <= 0 ||
       n_pages > INT32_MAX / page_size)
     return Q4K_ERR_SHAPE;
-  // the longest of the three strides has to step over all of the next, and so on
   const int64_t kMax = (int64_t)1 << 40;
   if (page_stride < dim || head_stride < dim || token_stride < dim || page_stride > kMax ||
       head_stride > kMax || token_stride > kMax)
     return Q4K_ERR_SHAPE;
-  const int64_t inner = head_stride > token_stride ? token_stride * page_size : head_stride * kv_heads;
-  const int64_t outer = head_stride > token_stride ? head_stride * kv_heads : token_stride * page_size;
-  if ((kv_heads > 1 && page_size > 1 && (head_stride > token_stride ? head_stride : token_stride) < inner) ||
-      (n_pages > 1 && page_stride < (kv_heads > 1 && page_size > 1 ? outer : kv_heads > 1 ? head_stride * kv_heads : token_stride * page_size)))
-    return Q4K_ERR_SHAPE;
+  // By size, whatever their order, each stride has to step over all of the next
+  // smaller one (dimensions of 1 have no stride to speak of).
+  struct Dim {
+    int64_t stride, extent;
+  } d[3] = {{token_stride, page_size}, {head_stride, kv_heads}, {page_stride, n_pages}};
+  std::sort(d, d + 3, [](const Dim &x, const Dim &y) { return x.stride < y.stride; });
+  const Dim *inner = nullptr;
+  for (const Dim &x : d) {
+    if (x.extent == 1) continue;
+    if (inner && x.stride / inner->stride < inner->extent) return Q4K_ERR_SHAPE;
+    inner = &x;
+  }
   const int64_t unit = cache_dtype == Q4K_DTYPE_BF16 ? 8 : 16;
   if (page_stride % unit || head_stride % unit || token_stride % unit) return Q4K_ERR_ALIGN;
   return Q4K_OK;

@@ -468,6 +468,8 @@ int q4k_moe_gemv_noalloc(const void *w_gate, const void *w_up, const void *w_dow
  * page_size tokens of every key head: element (page, head, token, i) at
  *     page * page_stride + head * head_stride + token * token_stride + i
  * (in elements; i < dim contiguous; both buffers have the same strides).  The
+ * three strides may come in any order; each steps over the whole of the next
+ * smaller one (over a row: dim), so that no rows overlap.  The
  * token at position p of a request is token p % page_size of page
  * table[request][p / page_size]; its slot is page * page_size + p % page_size.
  * bf16, or e4m3 with one fp32 scale per (page, head, token) in a contiguous
@@ -535,7 +537,7 @@ int q4k_kv_plan(const int32_t *lens, const int32_t *add, int32_t n, int32_t *tab
  *             + h * ld_head + i; 16-byte aligned, strides multiples of 8
  *   slots     device, tokens int32
  *   caches    as above; 16-byte aligned, strides multiples of 8 (bf16) or 16
- *             (e4m3), page_stride >= 0 and rows not overlapping
+ *             (e4m3)
  *   dim       64, 128 or 256
  *   k_scale, v_scale  fp32, for an e4m3 cache; NULL for bf16
  * Limits: n_pages * page_size < 2^31.

@@ -394,6 +394,35 @@ def test_attn_layouts_and_strides(q4k, layout, kind):
 
 
 @pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("order", [(0, 2, 1, 3), (1, 0, 2, 3), (1, 2, 0, 3), (2, 0, 1, 3), (2, 1, 0, 3)])
+def test_cache_dimensions_in_any_order(q4k, order, kind):
+    """Cache buffers that lie heads first, tokens first and so on: the bits of a head-major one."""
+    c = make_attn(17, LENS, 8, 4, 128, 32, kind)
+    table, lens, q = c["table"].to(DEV), c["lens"].to(DEV), c["q"].to(DEV)
+    scales = [s.to(DEV) for s in c["scales"]] if c["scales"] else []
+    back = [order.index(i) for i in range(4)]
+    slots = torch.tensor([3, 0, -1, 70, 64], dtype=torch.int32, device=DEV)
+    rows = [torch.randn((5, 4, 128), generator=gen(18 + i)).to(DEV) for i in range(2)]
+
+    def both(caches):
+        sc = [s.clone() for s in scales]
+        caches = [x.view(E4M3) for x in caches] if kind == E4M3 else caches
+        first = q4k.q4k_paged_attn(q, *caches, table, lens, 0.09, *sc)
+        q4k.q4k_kv_write(*rows, slots, *caches, *sc)
+        return first, [x.view(torch.uint8).contiguous() if kind == E4M3 else x.contiguous() for x in caches], sc
+
+    plain = [x.to(DEV) for x in c["caches"]]
+    other = [x.permute(order).contiguous().permute(back) for x in plain]
+    assert other[0].stride() != plain[0].stride()
+    (o0, l0), c0, s0 = both(plain)
+    (o1, l1), c1, s1 = both(other)
+    assert torch.equal(o0, o1) and torch.equal(l0, l1)
+    for x, y in zip(c0 + s0, c1 + s1):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))  # bytes: unused rows hold NaN
+    assert q4k.q4k_get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
 def test_attn_long_and_many(q4k, kind):
     check_attn(q4k, make_attn(11, [20011], 16, 2, 128, 64, kind), 0.08)
     check_attn(q4k, make_attn(12, [(i * 37) % 190 for i in range(400)], 4, 2, 64, 16, kind), 0.125)

@@ -75,6 +75,34 @@ def test_attn_refusals(L, change, status):
     assert _call(L.q4k_paged_attn, ATTN, **change) == status
 
 
+def _strides(order, page=16, heads=8, pages=64, dim=128):
+    """Strides of a dense cache whose dimensions lie in this order, the outermost first."""
+    extent, out, at = dict(page=page, head=heads, pages=pages), {}, dim
+    for name in reversed(order):
+        out[{"page": "token_stride", "head": "head_stride", "pages": "page_stride"}[name]] = at
+        at *= extent[name]
+    return out
+
+
+ORDERS = [("pages", "head", "page"), ("pages", "page", "head"), ("head", "pages", "page"), ("head", "page", "pages"), ("page", "pages", "head"), ("page", "head", "pages")]
+
+
+@pytest.mark.parametrize("order", ORDERS)
+def test_cache_strides_in_any_order(L, order):
+    """Dense caches pass the checks of strides in every order (there is no device, or the memory is
+    not a device's); eight elements less in any but the innermost stride are an overlap."""
+    good = _strides(order)
+    for fn, base in ((L.q4k_kv_write, WRITE), (L.q4k_paged_attn, ATTN)):
+        assert _call(fn, base, **good) not in (OK, NULL, SHAPE, ALIGN, WORKSPACE)
+        for name in good:
+            assert _call(fn, base, **{**good, name: good[name] - 8}) == SHAPE
+
+
+def test_cache_strides_whose_product_passes_64_bits(L):
+    """2^24 tokens of stride 2^40 do not fit a page of 2^40, though the product is 0 in 64 bits."""
+    assert _call(L.q4k_kv_write, WRITE, heads=1, page=1 << 24, n_pages=4, token_stride=1 << 40, page_stride=1 << 40) == SHAPE
+
+
 NORM = dict(x=P, x_dtype=0, ldx=512, res=P, res_dtype=1, ldr=512, gamma=P, eps=1e-6, m=4, hidden=512, y=P, y_dtype=1, ldy=512, res_out=P, ldro=512,
             scales=None, lds=0, stream=None)
 
