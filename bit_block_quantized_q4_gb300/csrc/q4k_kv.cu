@@ -187,16 +187,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
 
 // --------------------------------------------------------------------- write
 //
-// One row (token, head) of K or V: D/8 lanes of 8 values each; a block takes
-// rows of one head, a lane kWriteRows of them so that as many loads are under
-// way.  Bound by bytes (inputs read once, cache rows written once), with the
-// instructions of a row close behind: with the token and the page from 64-bit
-// divisions the 16001 x 8 x 128 bf16 -> e4m3 write took 71 us, with 32-bit ones
-// 42, now 21 us (4.7 TB/s).  Two rows in 40 registers and 6 blocks per SM were
-// best or within 4% of it for every pair of types (4 rows: the fp32 -> bf16
-// write 16.1 -> 17.8 us).
-
-constexpr int kWriteRows = 2, kWriteBlocks = 6;
+// A token's rows of K and V of one head: D/8 lanes of 8 values each; a block
+// takes tokens of one head.  Bound by bytes (inputs read once, cache rows written
+// once), with the instructions of a row close behind: the 16001 x 8 x 128 bf16 ->
+// e4m3 write took 71 us with the token and the page from 64-bit divisions, 42
+// with 32-bit ones, 21.3 without and with two rows of K or of V per lane, and
+// 18.1 us (5.5 TB/s) now that K and V share the slot and the place.  6 blocks
+// per SM: 19.9 us.  Two tokens per lane: 18.3, and 64-wide fp32 rows 8.9 -> 12.6.
 
 struct WriteArgs {
   const void *in[2];
@@ -210,38 +207,29 @@ struct WriteArgs {
 };
 
 template <int D, typename TI, bool E4M3>
-__global__ void __launch_bounds__(256, kWriteBlocks) kv_write_kernel(const WriteArgs a) {
-  constexpr int LPR = D / 8, RPB = 256 / LPR;  // lanes per row, rows per block and step
+__global__ void __launch_bounds__(256, 8) kv_write_kernel(const WriteArgs a) {
+  constexpr int LPR = D / 8, TPB = 256 / LPR;  // lanes per row, tokens per block
   const int c = threadIdx.x % LPR;
-  const bool kv = blockIdx.z;  // K or V; selected without indexing, which would copy the arguments
-  const uint32_t h = blockIdx.y, t0 = blockIdx.x * (RPB * kWriteRows) + threadIdx.x / LPR;
-  void *const cache = kv ? a.cache[1] : a.cache[0];
-  float *const scale = kv ? a.scale[1] : a.scale[0];
-  const TI *in = static_cast<const TI *>(kv ? a.in[1] : a.in[0]) + h * a.ld_head + c * 8;
-  Raw8<TI> raw[kWriteRows];
-  int32_t slot[kWriteRows];
-#pragma unroll
-  for (int i = 0; i < kWriteRows; ++i) {
-    const uint32_t t = t0 + i * RPB;
-    slot[i] = -1;
-    if (t < a.tokens) {
-      slot[i] = a.slots[t];
-      raw[i].load(in + t * a.ld_token);
-    }
+  const uint32_t h = blockIdx.y, t = blockIdx.x * TPB + threadIdx.x / LPR;
+  // all lanes of a row leave together, so the shuffles below are complete
+  if (t >= a.tokens) return;
+  const int32_t slot = a.slots[t];
+  const int64_t from = t * a.ld_token + h * a.ld_head + c * 8;
+  Raw8<TI> raw[2];  // K and V
+  raw[0].load(static_cast<const TI *>(a.in[0]) + from);
+  raw[1].load(static_cast<const TI *>(a.in[1]) + from);
+  if ((uint32_t)slot >= a.n_slots) {
+    if (slot != -1 && c == 0) set_device_error(a.err, kDevErrBadPage);
+    return;
   }
+  const uint32_t page = a.page.div(slot), off = slot - page * a.page.d;
+  const int64_t to = page * a.page_stride + h * a.head_stride + off * a.token_stride + c * 8;
 #pragma unroll
-  for (int i = 0; i < kWriteRows; ++i) {
-    // all lanes of a row agree on its slot, so the shuffles below are complete
-    if ((uint32_t)slot[i] >= a.n_slots) {
-      if (slot[i] != -1 && c == 0) set_device_error(a.err, kDevErrBadPage);
-      continue;
-    }
+  for (int kv = 0; kv < 2; ++kv) {
     float v[8];
-    raw[i].to(v);
-    const uint32_t page = a.page.div(slot[i]), off = slot[i] - page * a.page.d;
-    const int64_t to = page * a.page_stride + h * a.head_stride + off * a.token_stride + c * 8;
+    raw[kv].to(v);
     if (!E4M3) {
-      store8(static_cast<__nv_bfloat16 *>(cache) + to, v);
+      store8(static_cast<__nv_bfloat16 *>(a.cache[kv]) + to, v);
     } else {
       float amax = 0.f;
 #pragma unroll
@@ -252,16 +240,16 @@ __global__ void __launch_bounds__(256, kWriteBlocks) kv_write_kernel(const Write
       amax = fmaxf(amax, kAmaxFloor);
       float factor;
       const float inv = block_factor(amax, c, mask, factor);
-      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + to) = to_e4m3x8(v, inv);
-      if (c == 0) scale[((int64_t)page * a.heads + h) * a.page.d + off] = factor;
+      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.cache[kv]) + to) = to_e4m3x8(v, inv);
+      if (c == 0) a.scale[kv][((int64_t)page * a.heads + h) * a.page.d + off] = factor;
     }
   }
 }
 
 template <int D>
 void launch_write_d(const WriteArgs &a, bool bf16_in, bool e4m3, cudaStream_t s) {
-  constexpr uint32_t kRows = 256 / (D / 8) * kWriteRows;
-  const dim3 grid((a.tokens + kRows - 1) / kRows, a.heads, 2);
+  constexpr uint32_t kTokens = 256 / (D / 8);
+  const dim3 grid((a.tokens + kTokens - 1) / kTokens, a.heads);
   if (bf16_in && e4m3) kv_write_kernel<D, __nv_bfloat16, true><<<grid, 256, 0, s>>>(a);
   else if (bf16_in) kv_write_kernel<D, __nv_bfloat16, false><<<grid, 256, 0, s>>>(a);
   else if (e4m3) kv_write_kernel<D, float, true><<<grid, 256, 0, s>>>(a);
