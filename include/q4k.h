@@ -574,7 +574,7 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
  *   table   device, n rows of max_pages int32, row stride ldt
  *   lens    device, n int32
  *   out     device, bf16, row stride ldo >= q_heads * dim, heads contiguous;
- *           16-byte aligned, ldo a multiple of 8
+ *           16-byte aligned, ldo a multiple of 8; may not overlap q
  *   lse     device, n x q_heads fp32, or NULL
  *   workspace  device, >= q4k_paged_attn_workspace_size(...) bytes, 16-byte
  *           aligned; nothing in it is kept between calls
