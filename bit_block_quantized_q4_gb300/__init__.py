@@ -430,6 +430,8 @@ def q4k_kv_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool
     Returns (lens_out [n], cu [n + 1] int64, slots [n_slots], pos [n_slots], status [n],
     pool_state_out [2]); out gives these six tensors (lens and pool_state may be among them)."""
     n, width, pages = lens.numel(), table.shape[-1], pool.numel()
+    if n == 0 and not pool_state.is_cuda:  # (without a GPU the library's empty calls succeed and write nothing)
+        raise Q4KError(8, "pool_state")
     if out is None:
         if n_slots < 0:
             raise Q4KError(2, f"n_slots is {n_slots}")

@@ -69,6 +69,14 @@ int check_device() {
   return Q4K_OK;
 }
 
+// No GPU at all, so that no pointer can be device memory.
+bool no_device() {
+  int count = 0;
+  const cudaError_t e = cudaGetDeviceCount(&count);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e == cudaErrorNoDevice || e == cudaErrorInsufficientDriver || (e == cudaSuccess && count == 0);
+}
+
 int map_launch(cudaError_t e) { return e == cudaSuccess ? Q4K_OK : Q4K_ERR_CUDA; }
 
 // Q4K_OK when every non-null pointer is memory of the current device
@@ -587,8 +595,9 @@ int q4k_kv_plan(const int32_t *lens, const int32_t *add, int32_t n, int32_t *tab
       n_slots > INT32_MAX || ldt < max_pages || (int64_t)pool_size * page_size > INT32_MAX ||
       (int64_t)max_pages * page_size > (1 << 30))
     return Q4K_ERR_SHAPE;
-  if (n == 0) return Q4K_OK;
-  if (!lens || !add || !table || !pool || !pool_state || !lens_out || !cu || !status ||
+  // Without requests nothing of theirs is touched, but the state, cu[0] and the
+  // slot map are outputs all the same.
+  if ((n > 0 && (!lens || !add || !table || !pool || !lens_out || !status)) || !pool_state || !cu ||
       !pool_state_out || (n_slots > 0 && (!slots || !pos)))
     return Q4K_ERR_NULL;
   if (!aligned(lens, 4) || !aligned(add, 4) || !aligned(table, 4) || !aligned(pool, 4) ||
@@ -596,9 +605,13 @@ int q4k_kv_plan(const int32_t *lens, const int32_t *add, int32_t n, int32_t *tab
       !aligned(pos, 4) || !aligned(status, 4) || !aligned(pool_state_out, 4))
     return Q4K_ERR_ALIGN;
   int st = check_device();
-  if (st != Q4K_OK) return st;
-  st = check_device_memory({lens, add, table, pool, pool_state, lens_out, cu, slots, pos, status,
-                            pool_state_out});
+  // (an empty call succeeds on a machine without a GPU, as all others do)
+  if (st != Q4K_OK) return n == 0 && no_device() ? Q4K_OK : st;
+  if (n == 0)
+    st = check_device_memory({pool_state, cu, n_slots ? slots : nullptr, n_slots ? pos : nullptr, pool_state_out});
+  else
+    st = check_device_memory({lens, add, table, pool, pool_state, lens_out, cu, slots, pos, status,
+                              pool_state_out});
   if (st != Q4K_OK) return st;
   return map_launch(launch_kv_plan(lens, add, n, table, ldt, max_pages, page_size, pool, pool_size,
                                    pool_state, lens_out, cu, slots, pos, n_slots, status,

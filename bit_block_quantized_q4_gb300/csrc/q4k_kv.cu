@@ -34,7 +34,8 @@ namespace {
 // CTAs: every CTA scans all requests, a block's width at a time (cheaper than
 // passing sums between CTAs), and the requests' writes are divided among them.
 // A cluster barrier between the reads and the writes of a chunk is what allows
-// lens_out == lens and state_out == state.
+// lens_out == lens and state_out == state; without requests there is no chunk,
+// and one barrier of its own before the outputs that are defined all the same.
 
 constexpr int kPlanThreads = 1024;
 
@@ -176,6 +177,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
     tokens0 += chunk_tokens, need0 += chunk_need, back0 += chunk_back;
     __syncthreads();  // part[] is rewritten in the next chunk
   }
+  if (a.n == 0) {
+    cluster_sync();  // every CTA has read the state
+    if (rank == 0 && tid == 0) a.cu[0] = 0;
+  }
   for (int64_t t = tokens0 + rank * blockDim.x + tid; t < a.n_slots; t += (int64_t)ranks * blockDim.x)
     a.slots[t] = -1, a.pos[t] = -1;
   if (rank == 0 && tid == 0) {
@@ -266,8 +271,8 @@ cudaError_t launch_kv_plan(const int32_t *lens, const int32_t *add, int32_t n, i
   const PlanArgs a = {lens, add, table, ldt, pool, state, lens_out, cu, slots, pos, status, state_out,
                       n_slots, n, width * page, (uint32_t)pool_size, FastDiv(page), device_error_word()};
   const int ranks = n_slots <= 4096 ? 1 : n_slots <= 16384 ? 4 : 8;
-  // a block as wide as the requests, and wide enough for the slots
-  const int64_t wide = n > n_slots / 8 ? n : n_slots / 8;
+  // a block as wide as the requests, and wide enough for the slots; a warp at least
+  const int64_t most = n > n_slots / 8 ? n : n_slots / 8, wide = most > 0 ? most : 1;
   const int threads = wide >= kPlanThreads ? kPlanThreads : ((int)wide + 31) / 32 * 32;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);

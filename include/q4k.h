@@ -46,7 +46,7 @@
  *   - Strides (ldx, ldy) are in elements.
  *   - Argument errors are reported before anything is launched (nothing runs).
  *     An empty problem (n == 0, batch/m/tokens == 0) returns Q4K_OK and
- *     launches nothing.
+ *     launches nothing (but q4k_kv_plan, whose outputs are not empty then).
  *   - Kernels never trap.  Bad data found on the device (an expert id out of
  *     range, a wait that gave up) sets a device-side error word, read and
  *     cleared with q4k_get_device_error.
@@ -507,6 +507,9 @@ int q4k_moe_gemv_noalloc(const void *w_gate, const void *w_up, const void *w_dow
  *   cu                 device, n + 1 int64
  *   slots, pos         device, n_slots int32 each
  *   pool_state_out     device, 2 int32 (may be pool_state)
+ * With n == 0 the call still writes pool_state_out, cu[0] and slots and pos;
+ * lens, add, table, pool, lens_out and status may be NULL then.  (On a machine
+ * without a GPU it returns Q4K_OK and writes nothing, as every empty call.)
  * A page id outside the pool gives slot -1 and sets Q4K_DEVERR_BAD_PAGE; so
  * does a returned page for which the ring has no entry left (a page returned
  * twice), which is dropped.
