@@ -92,15 +92,16 @@ __device__ __forceinline__ int64_t run_of(int64_t tiles, int64_t warps) {
   return c < 1 ? 1 : c;
 }
 
+// A request's tokens start .. len - 1 and their tiles t0 .. t1 - 1.  The window
+// ends at lens[r] itself; tokens past the table are absent, so that a request
+// far longer than its table may have none.
 template <int TILE>
-__device__ __forceinline__ void span_of(const AttnArgs &a, int len, int &start, int &t0, int &t1) {
-  start = a.window > 0 && len > a.window ? len - a.window : 0;
+__device__ __forceinline__ void span_of(const AttnArgs &a, int r, int &len, int &start, int &t0, int &t1) {
+  const int told = a.lens[r], cap = a.max_pages * a.page;
+  len = told < 0 ? 0 : told > cap ? cap : told;
+  start = a.window > 0 && told > a.window ? told - a.window : 0;
   t0 = start / TILE;
-  t1 = (len + TILE - 1) / TILE;
-}
-__device__ __forceinline__ int length_of(const AttnArgs &a, int r) {
-  const int len = a.lens[r], cap = a.max_pages * a.page;
-  return len < 0 ? 0 : len > cap ? cap : len;
+  t1 = start < len ? (len + TILE - 1) / TILE : t0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -212,11 +213,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
   int64_t mine = 0;
   bool bad = false;
   for (int r = r_lo; r < r_hi; ++r) {
-    const int len = length_of(a, r);
-    int start, t0, t1;
-    span_of<TILE>(a, len, start, t0, t1);
+    int len, start, t0, t1;
+    span_of<TILE>(a, r, len, start, t0, t1);
     mine += t1 - t0;
-    bad |= a.lens[r] > len && a.lens[r] > 0;
+    bad |= a.lens[r] > len;
   }
   int64_t incl = mine;
 #pragma unroll
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
     if (bad) set_device_error(a.err, kDevErrBadPage);
     int64_t at = incl - mine;
     for (int r = r_lo; r < r_hi; ++r) {
-      int start, t0, t1;
-      span_of<TILE>(a, length_of(a, r), start, t0, t1);
+      int len, start, t0, t1;
+      span_of<TILE>(a, r, len, start, t0, t1);
       p.prefix[r] = at;
       at += t1 - t0;
     }
@@ -262,8 +262,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
     }
     int64_t at = lo ? sums[lo - 1] : 0;
     for (r = lo * per;; ++r) {
-      len = length_of(a, r);
-      span_of<TILE>(a, len, start, t0, t1);
+      span_of<TILE>(a, r, len, start, t0, t1);
       if (at + (t1 - t0) > y) break;
       at += t1 - t0;
     }
@@ -354,8 +353,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kWarps * 32, 1)
         t0 = t1;
         while (t0 >= t1 && r + 1 < a.n) {
           ++r;
-          len = length_of(a, r);
-          span_of<TILE>(a, len, start, t0, t1);
+          span_of<TILE>(a, r, len, start, t0, t1);
         }
       }
       t = t0;

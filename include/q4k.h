@@ -562,7 +562,7 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
  * Cache rows that no request's tokens refer to are never used, whatever they
  * hold (NaN and infinities included).  A page outside [0, n_pages) counts as
  * absent (its tokens are skipped), and so do tokens past max_pages *
- * page_size; both set Q4K_DEVERR_BAD_PAGE.
+ * page_size (the window still ends at lens[r]); both set Q4K_DEVERR_BAD_PAGE.
  * Scores, softmax statistics and sums are fp32.  For a bf16 cache the softmax
  * weights enter the products as two bf16 terms (16 significant bits), for an
  * e4m3 cache as one fp16 term (11 bits) of the weight times the row's scale.

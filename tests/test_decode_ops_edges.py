@@ -6,12 +6,14 @@ Tolerances count roundings: half a step of a type is eps / 2 relative (bf16 2^-8
 """
 from __future__ import annotations
 
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from _gpu import DEV
-from test_decode_ops import plain_plan
+from test_decode_ops import BAD_PAGE, BF16, E4M3, make_attn, plain_attn, plain_plan, to_dev
 
 gpu = pytest.mark.gpu
 NULL, SHAPE, ALIGN, MEMORY = 1, 2, 3, 8
@@ -69,3 +71,31 @@ def test_plan_of_no_requests_refusals(q4k):
     with pytest.raises(q4k.Q4KError) as e:  # on host tensors it would leave its outputs unwritten
         q4k.q4k_kv_plan(none, none, torch.zeros((0, 4), dtype=torch.int32), torch.zeros(9, dtype=torch.int32), state, 16, 3)
     assert e.value.status == MEMORY
+
+
+# ------------------------------------------------------------------------------------------ window and lengths past the table
+
+
+@gpu
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("dim,q_heads,kv_heads,page", [(128, 8, 2, 16), (64, 6, 1, 64), (256, 4, 2, 32)])
+def test_attn_window_of_lengths_past_the_table(q4k, dim, q_heads, kv_heads, page, kind):
+    """The window ends at the length, not at the table's end: tokens max(0, len - window) <= j < len, of which
+    those past the table are absent."""
+    cap = 512
+    top = 2 ** 31 - 1
+    for window in (0, 1, 100, 488, 489, 600, 1000, top - 500, top - 512, top):
+        raw = [1000, 300, cap, top, 513, 0, 1100]
+        c = make_attn(31, [min(v, cap) for v in raw], q_heads, kv_heads, dim, page, kind, extra=0)
+        assert c["table"].shape[1] * page == cap
+        caches = [to_dev(x, kind) for x in c["caches"]]
+        scales = [s.to(DEV) for s in c["scales"]] if c["scales"] else [None, None]
+        lens = torch.tensor(raw, dtype=torch.int32, device=DEV)
+        out, lse = q4k.q4k_paged_attn(c["q"].to(DEV), *caches, c["table"].to(DEV), lens, dim ** -0.5, *scales, window=window)
+        assert q4k.q4k_get_device_error() == BAD_PAGE
+        want, wl, bo, bl = plain_attn(c, dim ** -0.5, skip=lambda r, n: torch.arange(n) < (raw[r] - window if window else 0))
+        assert bool(((out.double().cpu() - want).abs() <= bo).all()), window
+        lse = lse.double().cpu()
+        assert torch.equal(lse == -math.inf, wl == -math.inf), window
+        fin = wl != -math.inf
+        assert bool(((lse - wl)[fin].abs() <= bl[fin]).all()), window
