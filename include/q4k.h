@@ -565,7 +565,8 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
  * page_size (the window still ends at lens[r]); both set Q4K_DEVERR_BAD_PAGE.
  * Scores, softmax statistics and sums are fp32.  For a bf16 cache the softmax
  * weights enter the products as two bf16 terms (16 significant bits), for an
- * e4m3 cache as one fp16 term (11 bits) of the weight times the row's scale.
+ * e4m3 cache as one fp16 term of the weight times the row's scale: 11 bits down
+ * to 2^-29 of the largest such term, an error of at most 2^-40 of it below.
  * Values that are not finite in rows that take part show in the result; an
  * infinite value of V may do so as NaN.
  *   q       device, bf16, element (r, i, d) at r * ldq + i * ldq_head + d;

@@ -13,7 +13,7 @@ import pytest
 import torch
 
 from _gpu import DEV
-from test_decode_ops import BAD_PAGE, BF16, E4M3, make_attn, plain_attn, plain_plan, to_dev
+from test_decode_ops import BAD_PAGE, BF16, E4M3, H16, H32, HB, gen, make_attn, plain_attn, plain_plan, quantize, to_dev
 
 gpu = pytest.mark.gpu
 NULL, SHAPE, ALIGN, MEMORY = 1, 2, 3, 8
@@ -99,3 +99,79 @@ def test_attn_window_of_lengths_past_the_table(q4k, dim, q_heads, kv_heads, page
         assert torch.equal(lse == -math.inf, wl == -math.inf), window
         fin = wl != -math.inf
         assert bool(((lse - wl)[fin].abs() <= bl[fin]).all()), window
+
+
+# ------------------------------------------------------------------------------------------ weights far below the largest
+
+
+def attn_bounds(q, k, v, scale, e4m3, keep=None):
+    """(out, lse, bound of out, bound of lse) in 64 bits of q [n, hq, d] over k, v [n, t, h, d], keep [n, t].
+
+    Roundings: fp32 scores (a product's rounding and d additions of up to the sum of |q k| each, and the
+    scaling), exp2 and its argument 2^-20 relative, sums of t terms, the weights: two bf16 terms (2^-16), or
+    one fp16 term: half a step 2^-11 of those down to 2^-29 of the largest weight times scale, and 2^-40 of it
+    below (half of fp16's smallest step 2^-24, the largest being 2^15); the output's bf16."""
+    n, hq, d = q.shape
+    t = k.shape[1]
+    group = hq // k.shape[2]
+    k, v = k.repeat_interleave(group, 2), v.repeat_interleave(group, 2)
+    z = torch.einsum("nhd,nthd->nht", q, k) * scale
+    size = torch.einsum("nhd,nthd->nht", q.abs(), k.abs()) * abs(scale)
+    if keep is not None:
+        z = z.masked_fill(~keep[:, None], -math.inf)
+        size = size.masked_fill(~keep[:, None], 0.0)
+        v = v.masked_fill(~keep[:, :, None, None], 0.0)
+    lse = torch.logsumexp(z, 2)
+    some = lse > -math.inf
+    p = torch.exp(z - lse.masked_fill(~some, 0.0)[:, :, None])
+    out = torch.einsum("nht,nthd->nhd", p, v)
+    pv = torch.einsum("nht,nthd->nhd", p, v.abs())
+    far = z.masked_fill(z == -math.inf, 0.0).abs().amax(2)
+    dz = (d + 8) * H32 * size.amax(2) + 2.0 ** -20 * (1 + far * 2 ** -2)
+    count = keep.sum(1).double()[:, None] if keep is not None else torch.full((n, 1), float(t), dtype=torch.float64, device=q.device)
+    sums = (count.sqrt() + 40) * H32 * 2
+    rel = 2 * dz + sums + (H16 if e4m3 else 2.0 ** -16)
+    bo = HB * out.abs() + rel[:, :, None] * pv * 1.01
+    if e4m3:
+        largest = (p.unsqueeze(-1) * v.abs().permute(0, 2, 1, 3)).amax((2, 3))
+        bo = bo + 2.0 ** -40 * count[:, :, None] * largest[:, :, None] * 1.01
+    return out, lse, bo, dz + sums + H32 * lse.masked_fill(~some, 0.0).abs()
+
+
+@gpu
+@pytest.mark.parametrize("gap", [10, 14, 17, 20, 24, 27, 32])
+@pytest.mark.parametrize("dim,q_heads", [(64, 2), (64, 16), (128, 4), (128, 16), (256, 8)])
+def test_attn_weights_far_below_the_largest(q4k, dim, q_heads, gap):
+    """One token takes nearly all the weight and the others, `gap` binary orders below it, all of the value in
+    every column but the first."""
+    page, h = 32, 2
+    g = gen(gap + dim)
+    for length in (32, 33, 700, 9000):
+        k, v = torch.zeros((length, h, dim)), torch.randn((length, h, dim), generator=g).abs() + 0.5
+        # scores of the others: -gap ln 2 and less, by up to one binary order
+        k[:, :, 1] = -(gap + torch.rand((length, h), generator=g)) * math.log(2.0)
+        v[:, :, 0] = 0.0
+        sink = length * 2 // 3
+        k[sink] = 0.0
+        v[sink] = 0.0
+        v[sink, :, 0] = 1.5
+        q = torch.zeros((1, h * q_heads, dim))
+        q[:, :, 1] = 1.0
+        pages = -(-length // page)
+        table = torch.randperm(pages, generator=g).to(torch.int32)
+        caches, scales, dense = [], [], []
+        for x in (k, v):
+            b, s = quantize(x)
+            dense.append((b.view(E4M3).double() * s.double()[..., None])[None].to(DEV))
+            c, cs = torch.zeros((pages * page, h, dim), dtype=torch.uint8), torch.ones((pages * page, h))
+            c[:length], cs[:length] = b, s
+            c, cs = c.view(pages, page, h, dim).transpose(1, 2), cs.view(pages, page, h).transpose(1, 2)
+            inv = torch.argsort(table)
+            caches.append(c[inv].contiguous().to(DEV).view(E4M3)), scales.append(cs[inv].contiguous().to(DEV))
+        qb = q.to(BF16).to(DEV)
+        out, lse = q4k.q4k_paged_attn(qb, *caches, table[None].to(DEV), torch.tensor([length], dtype=torch.int32, device=DEV), 1.0, *scales)
+        want, wl, bo, bl = attn_bounds(qb.double(), *dense, 1.0, True)
+        off = (out.double() - want).abs()
+        assert bool((off <= bo).all()), (length, float((off / bo).max()))
+        assert bool(((lse.double() - wl).abs() <= bl).all()), length
+    assert q4k.q4k_get_device_error() == 0
