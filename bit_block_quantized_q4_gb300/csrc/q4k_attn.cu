@@ -752,13 +752,9 @@ cudaError_t launch_cfg(Params &p, cudaStream_t stream) {
   using C = Cfg<D, E4M3>;
   const AttnArgs &a = p.a;
   const DeviceFacts *f = device_facts();
-  // Kernel attributes are per device; set once for each.
-  static bool ready[kMaxDevices];
-  if (!ready[f->device]) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, E4M3, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    ready[f->device] = true;
-  }
+  static SmemLimit limit;
+  cudaError_t e = raise_smem_limit(limit, paged_attn_kernel<D, E4M3, NQ>, C::kSmem);
+  if (e != cudaSuccess) return e;
   CUtensorMap maps[2];
   p.box_rows = a.page < C::kTile ? a.page : C::kTile;
   p.box_shift = p.box_rows == 32 ? 5 : 4;
@@ -776,7 +772,7 @@ cudaError_t launch_cfg(Params &p, cudaStream_t stream) {
   const int grid = f->sm_count < kMaxSms ? f->sm_count : kMaxSms;
   p.warps = (int64_t)grid * C::kWarps;
   paged_attn_kernel<D, E4M3, NQ><<<grid, C::kWarps * 32, C::kSmem, stream>>>(p, maps[0], maps[1]);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // An item has about warps / items pieces; a warp takes up to 8 of them.  (With
   // one CTA per item the join of 16 items of 114 pieces alone took 11 us; 16 ways

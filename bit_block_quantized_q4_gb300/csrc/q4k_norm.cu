@@ -246,13 +246,9 @@ void launch_nv(const NormArgs &a, bool e4m3, dim3 grid, dim3 block, cudaStream_t
 template <typename TX, typename TR, bool E4M3, int KEEP>
 cudaError_t launch_rows_kept(const NormArgs &a, int stage, int threads, cudaStream_t s) {
   const DeviceFacts *f = device_facts();
-  static bool ready[kMaxDevices];  // the attribute is per device
-  if (!ready[f->device]) {
-    const cudaError_t e = cudaFuncSetAttribute(add_rmsnorm_rows_kernel<TX, TR, E4M3, KEEP>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-    if (e != cudaSuccess) return e;
-    ready[f->device] = true;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = raise_smem_limit(limit, add_rmsnorm_rows_kernel<TX, TR, E4M3, KEEP>, kRingBytes);
+  if (e != cudaSuccess) return e;
   // blocks per SM: as many as keep two rows each in flight, up to 1536 threads
   int blocks = kRowsSmThreads / threads;
   if (blocks > kRingBytes / (2 * stage)) blocks = kRingBytes / (2 * stage);

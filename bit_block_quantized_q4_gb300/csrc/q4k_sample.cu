@@ -984,14 +984,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
 template <typename T>
 cudaError_t launch_t(const SampleArgs &a, int64_t rows, int ranks, cudaStream_t stream) {
-  static bool ready[kMaxDevices];  // the attribute is per device
-  const int dev = device_facts()->device;
-  if (!ready[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)sizeof(Shared) + kMaxVocab / kMaxCluster * (int)sizeof(T));
-    if (e != cudaSuccess) return e;
-    ready[dev] = true;
-  }
+  static SmemLimit limit;
+  cudaError_t e = raise_smem_limit(limit, sample_kernel<T>, (int)sizeof(Shared) + kMaxVocab / kMaxCluster * (int)sizeof(T));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows, ranks);
   cfg.blockDim = dim3(kThreads);
@@ -1004,7 +999,7 @@ cudaError_t launch_t(const SampleArgs &a, int64_t rows, int ranks, cudaStream_t 
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
+  e = cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -6,7 +6,26 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
+#include "q4k_internal.h"
+
 namespace q4k {
+
+// A kernel's limit of dynamic shared memory, raised once per device, whichever
+// thread comes first; the others wait for it and see its outcome.
+struct SmemLimit {
+  std::once_flag once[kMaxDevices];
+  cudaError_t status[kMaxDevices];
+};
+template <typename Kernel>
+cudaError_t raise_smem_limit(SmemLimit &l, Kernel kernel, int bytes) {
+  const int dev = device_facts()->device;
+  std::call_once(l.once[dev], [&] {
+    l.status[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+  return l.status[dev];
+}
 
 // Around the projections (q4k_kv.cu, q4k_norm.cu, q4k_attn.cu, q4k_sample.cu);
 // arguments as the entry points of the same names.

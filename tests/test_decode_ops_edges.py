@@ -6,14 +6,19 @@ Tolerances count roundings: half a step of a type is eps / 2 relative (bf16 2^-8
 """
 from __future__ import annotations
 
+import glob
 import math
+import os
+import re
+import subprocess
+import sys
 
 import numpy as np
 import pytest
 import torch
 
 from _gpu import DEV
-from test_decode_ops import BAD_PAGE, BF16, E4M3, H16, H32, HB, gen, make_attn, plain_attn, plain_plan, quantize, to_dev
+from test_decode_ops import BAD_PAGE, BF16, E4M3, F32, H16, H32, HB, gen, make_attn, plain_attn, plain_plan, quantize, to_dev
 
 gpu = pytest.mark.gpu
 NULL, SHAPE, ALIGN, MEMORY = 1, 2, 3, 8
@@ -175,3 +180,88 @@ def test_attn_weights_far_below_the_largest(q4k, dim, q_heads, gap):
         assert bool((off <= bo).all()), (length, float((off / bo).max()))
         assert bool(((lse.double() - wl).abs() <= bl).all()), length
     assert q4k.q4k_get_device_error() == 0
+
+
+# ------------------------------------------------------------------------------------------ threads
+
+THREADS = """
+import sys, threading
+import torch
+sys.path.insert(0, sys.argv[1])
+import bit_block_quantized_q4_gb300 as q4k
+BF16, E4M3, F32, I32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
+q4k.lib()
+g = torch.Generator(device="cuda").manual_seed(1)
+rand = lambda *s: torch.randn(s, generator=g, device="cuda")
+lens, table = torch.tensor([90, 3], dtype=I32, device="cuda"), torch.tensor([[0, 1, 2], [3, 0, 0]], dtype=I32, device="cuda")
+x, res, gamma = rand(2000, 5120).to(BF16), rand(2000, 5120).to(BF16), rand(8192)
+wide, logits, u = rand(1400, 8192).to(BF16), rand(4, 50000), torch.rand(4, generator=g, device="cuda")
+caches = {}
+for d in (64, 128, 256):
+    k = [rand(4, 2, 32, d) for _ in range(2)]
+    caches[d] = ([c.to(BF16) for c in k], [c.to(E4M3) for c in k], [torch.rand((4, 2, 32), generator=g, device="cuda") + 0.1 for _ in range(2)])
+
+def calls():
+    for d in (64, 128, 256):
+        plain, small, scales = caches[d]
+        for heads in (4, 32):
+            q = torch.ones((2, heads, d), dtype=BF16, device="cuda")
+            yield lambda: q4k.q4k_paged_attn(q, *plain, table, lens, 0.1)
+            yield lambda: q4k.q4k_paged_attn(q, *small, table, lens, 0.1, *scales)
+    for out in (BF16, E4M3):
+        yield lambda: q4k.q4k_add_rmsnorm(x, res, gamma[:5120], 1e-6, out_dtype=out)
+        yield lambda: q4k.q4k_add_rmsnorm(wide, None, gamma, 1e-6, out_dtype=out)
+    yield lambda: q4k.q4k_sample(logits, u)
+    yield lambda: q4k.q4k_sample(logits.to(BF16), u)
+
+def bits(r):
+    return [t.view(torch.uint8) if t.dtype == E4M3 else t for t in r if t is not None]
+
+torch.cuda.synchronize()
+results, errors, start = [None] * 8, [], threading.Barrier(8)
+
+def work(i):
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            out = []
+            for call in calls():  # every kernel's first call, in all threads at once
+                start.wait(60)
+                out.append(bits(call()))
+            torch.cuda.current_stream().synchronize()
+            results[i] = out
+    except Exception as e:
+        errors.append(repr(e))
+        start.abort()
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert not errors, errors
+want = [bits(call()) for call in calls()]
+torch.cuda.synchronize()
+for r in results:
+    for a, b in zip(r, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+assert q4k.q4k_get_device_error() == 0
+print("threads agree")
+"""
+
+
+@gpu
+def test_first_calls_from_several_threads(q4k):
+    """A fresh process in which eight threads make every kernel's first call at the same time."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", THREADS, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "threads agree" in r.stdout, r.stdout + r.stderr
+
+
+def test_launchers_keep_no_plain_state():
+    """What a launcher does once per device is under std::call_once: a plain static that threads read and
+    write is a data race."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    files = glob.glob(os.path.join(root, "bit_block_quantized_q4_gb300", "csrc", "*.c*"))
+    assert files
+    for f in files:
+        with open(f) as src:
+            found = re.findall(r"^\s+static (?!const|SmemLimit\b|std::once_flag\b|__)[\w:<>]+ \w+(?:\[\w+\])?(?: = [^(]*)?;", src.read(), re.M)
+        assert not found, (os.path.basename(f), found)
