@@ -6,6 +6,7 @@ Tolerances count roundings: half a step of a type is eps / 2 relative (bf16 2^-8
 """
 from __future__ import annotations
 
+import ctypes
 import glob
 import math
 import os
@@ -21,7 +22,7 @@ from _gpu import DEV
 from test_decode_ops import BAD_PAGE, BF16, E4M3, F32, H16, H32, HB, gen, make_attn, plain_attn, plain_plan, quantize, to_dev
 
 gpu = pytest.mark.gpu
-NULL, SHAPE, ALIGN, MEMORY = 1, 2, 3, 8
+OK, NULL, SHAPE, ALIGN, MEMORY = 0, 1, 2, 3, 8
 
 
 @pytest.fixture(scope="module")
@@ -265,3 +266,73 @@ def test_launchers_keep_no_plain_state():
         with open(f) as src:
             found = re.findall(r"^\s+static (?!const|SmemLimit\b|std::once_flag\b|__)[\w:<>]+ \w+(?:\[\w+\])?(?: = [^(]*)?;", src.read(), re.M)
         assert not found, (os.path.basename(f), found)
+
+
+# ------------------------------------------------------------------------------------------ what pointers are refused
+
+
+class Driver:
+    """Allocations straight from the driver, without a caching allocator between."""
+
+    def __init__(self):
+        self.cu = ctypes.CDLL("libcuda.so.1")
+
+    def _ok(self, status):
+        assert status == 0, status
+
+    def device(self, size):
+        p = ctypes.c_uint64()
+        self._ok(self.cu.cuMemAlloc_v2(ctypes.byref(p), ctypes.c_size_t(size)))
+        return p.value
+
+    def pinned(self, size):
+        p = ctypes.c_void_p()
+        self._ok(self.cu.cuMemAllocHost_v2(ctypes.byref(p), ctypes.c_size_t(size)))
+        return p.value
+
+    def managed(self, size):
+        p = ctypes.c_uint64()
+        self._ok(self.cu.cuMemAllocManaged(ctypes.byref(p), ctypes.c_size_t(size), ctypes.c_uint(1)))
+        return p.value
+
+    def free(self, p):
+        self._ok(self.cu.cuMemFree_v2(ctypes.c_uint64(p)))
+
+    def is_device(self, p):
+        """Whether the driver knows the address as device memory."""
+        kind = ctypes.c_uint(0)
+        return self.cu.cuPointerGetAttribute(ctypes.byref(kind), 2, ctypes.c_uint64(p)) == 0 and kind.value == 2
+
+
+@gpu
+def test_every_pointer_of_a_call_is_checked(q4k):
+    """One pointer that is not device memory is refused in any place beside others that are: freed memory and
+    memory past an allocation in the 2 MB that a good pointer lies in too, pinned and managed memory.  (All
+    are refused on the host: nothing is launched.)"""
+    torch.zeros(1, device=DEV)
+    d, L = Driver(), q4k.lib()
+    size = 4096
+    good = [d.device(size) for _ in range(2)]
+    freed = d.device(size)
+    d.free(freed)
+    near = [p for p in (freed, good[0] + (1 << 20), good[0] - (1 << 20), good[0] + (1 << 19)) if p >> 21 == good[0] >> 21 and not d.is_device(p)]
+    assert all(d.is_device(p) for p in good) and near, "no address of the same 2 MB that the driver does not know"
+    pinned, managed = d.pinned(size), d.managed(size)
+    assert L.q4k_dequant(good[0], 1, 256, good[1], 0, None) == OK
+    torch.cuda.synchronize()
+    sample = lambda logits, u, t, token: L.q4k_sample(logits, 0, 1, 64, 64, u, t, None, None, None, token, None, None)  # noqa: E731
+    gemv = lambda w, x, y: L.q4k_gemv(w, 1, 256, x, 1, 256, y, 1, None)  # noqa: E731
+    norm = lambda x, g, y: L.q4k_add_rmsnorm(x, 0, 64, None, 0, 0, g, 1e-6, 1, 64, y, 1, 64, None, 0, None, 0, None)  # noqa: E731
+    plan = lambda state, cu, state_out: L.q4k_kv_plan(None, None, 0, None, 8, 8, 16, None, 64, state, None, cu, None, None, 0, None, state_out, None)  # noqa: E731
+    a, b = good
+    for bad in near + [pinned, managed]:
+        assert not d.is_device(bad) or bad == managed
+        for call, args in ((lambda w, o: L.q4k_dequant(w, 1, 256, o, 0, None), (a, b)), (sample, (a, b, a + 1024, b + 1024)), (gemv, (a, b, a + 1024)),
+                           (norm, (a, b, a + 1024)), (plan, (a, b, a + 1024))):
+            for i in range(len(args)):
+                assert call(*args[:i], bad, *args[i + 1:]) == MEMORY
+    torch.cuda.synchronize()
+    assert q4k.q4k_get_device_error() == 0
+    d._ok(d.cu.cuMemFreeHost(ctypes.c_void_p(pinned)))
+    for p in good + [managed]:
+        d.free(p)
