@@ -544,6 +544,8 @@ def q4k_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if workspace is None:
         size = L.q4k_paged_attn_workspace_size(n, q_heads, heads, dim)
         workspace = _empty(max(size, 16), torch.uint8, q, stream)
+    elif not workspace.is_contiguous():  # its elements would not be bytes of memory
+        _refuse("workspace", workspace)
     _check(L.q4k_paged_attn(
         q.data_ptr(), ldq[0], ldq[1], n, q_heads, heads, dim, k_cache.data_ptr(),
         v_cache.data_ptr(), code, pages, page, strides[0], strides[1], strides[2], ks, vs,

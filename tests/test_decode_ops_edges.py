@@ -336,3 +336,14 @@ def test_every_pointer_of_a_call_is_checked(q4k):
     d._ok(d.cu.cuMemFreeHost(ctypes.c_void_p(pinned)))
     for p in good + [managed]:
         d.free(p)
+
+
+def test_binding_refuses_a_workspace_that_is_not_contiguous(q4k):
+    """An expanded tensor has more elements than memory."""
+    cache = torch.zeros((4, 2, 16, 64), dtype=BF16)
+    lens, table, q = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 3), dtype=torch.int32), torch.zeros((2, 4, 64), dtype=BF16)
+    size = q4k.q4k_paged_attn_workspace_size(2, 4, 2, 64)
+    for workspace in (torch.zeros(1, dtype=torch.uint8).expand(size), torch.zeros(2 * size, dtype=torch.uint8)[::2]):
+        with pytest.raises(q4k.Q4KError) as e:
+            q4k.q4k_paged_attn(q, cache, cache, table, lens, 1.0, workspace=workspace)
+        assert e.value.status == SHAPE
