@@ -264,7 +264,7 @@ struct __align__(16) Shared {
   u64 part[kWarps];
   float partf[kWarps];
   u64 found[4];  // bin, count before, weight before, count in it
-  u64 cut, kept_weight;
+  u64 cut;
   u64 total[kMaxCluster], before[kMaxCluster], inside[kMaxCluster], drawn[kMaxCluster];
   uint64_t full;
   float high;
@@ -423,8 +423,7 @@ struct Ctx {
   // The smallest key kept when a token is kept if the sum of counts (or
   // weights) of those before it is less than `want`; it lies in bins b0 .. b1,
   // which hold `count` tokens, with c0 tokens and weight w0 before them.
-  // s.kept_weight: the weight of the kept ones, if with_weights.
-  __device__ u64 select(bool by_weight, u64 want, bool with_weights, int b0, int b1, u64 c0, u64 w0, u64 count) {
+  __device__ u64 select(bool by_weight, u64 want, int b0, int b1, u64 c0, u64 w0, u64 count) {
     const int tid = threadIdx.x, n = this->n, base = this->base;
     const uint32_t ranks = this->ranks;
     const Scale sc = this->sc;
@@ -436,7 +435,7 @@ struct Ctx {
       const int bits = 64 - __clzll((long long)(hi - lo));
       const int shift = bits > 10 ? bits - 10 : 0;
       sync_cluster();  // the lists or sums that shared this memory are read
-      split_range(lo, hi, shift, with_weights);
+      split_range(lo, hi, shift, by_weight);
       find(by_weight, want, c0, w0);
       const u64 b = s.found[0];
       if (b >= kBins) return 0;  // cannot be: the sum reaches `want` in this range
@@ -447,7 +446,7 @@ struct Ctx {
     }
     // list the tokens: each CTA its own, then all of them everywhere
     sync_cluster();
-    if (tid == 0) s.listed = 0, s.cut = ~0ull, s.kept_weight = 0;
+    if (tid == 0) s.listed = 0, s.cut = ~0ull;
     __syncthreads();
     const uint32_t lo32 = (uint32_t)(lo >> 32), hi32 = (uint32_t)(hi >> 32);
     const auto list = [&](int i, float e) {
@@ -471,7 +470,7 @@ struct Ctx {
       while (p + 1 < ranks && i >= s.counts[p]) i -= s.counts[p++];
       const u64 k = ld_peer64(&s.list.mine[min(i, (uint32_t)kList - 1)], p);
       s.list.all[tid] = k;
-      s.list.weights[tid] = with_weights ? weight(sc, of_key((uint32_t)(k >> 32))) : 0;
+      s.list.weights[tid] = by_weight ? weight(sc, of_key((uint32_t)(k >> 32))) : 0;
     }
     __syncthreads();
     if (tid < at) {
@@ -479,13 +478,8 @@ struct Ctx {
       u64 before = by_weight ? w0 : c0;
       for (int j = 0; j < at; ++j)
         if (s.list.all[j] > k) before += by_weight ? s.list.weights[j] : 1;
-      if (before < want) {
-        atomicMin(&s.cut, k);
-        if (with_weights) atomicAdd(&s.kept_weight, s.list.weights[tid]);
-      }
+      if (before < want) atomicMin(&s.cut, k);
     }
-    __syncthreads();
-    if (tid == 0) s.kept_weight += w0;
     __syncthreads();
     return s.cut;
   }
@@ -742,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     bool have_total = false;
     u64 total_p = 0, less_p = 0;
-    if (count > kShort && use_k && !whole) cut = c.select(false, (u64)k, false, bk, bk, before_k, 0, upto_k - before_k);
+    if (count > kShort && use_k && !whole) cut = c.select(false, (u64)k, bk, bk, before_k, 0, upto_k - before_k);
     if (count > kShort && use_p) {
       // Exact sums: the total of the top-k set, and the weight before bin b0 and
       // up to bin b1, at first for the bins next to where the middles of all
@@ -784,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (whole && upto_p <= kShort) {
         count = upto_p;
       } else {
-        cut = max(cut, c.select(true, want_of(p, total_p), true, b0, b1, before_p, less_p, upto_p - before_p));
+        cut = max(cut, c.select(true, want_of(p, total_p), b0, b1, before_p, less_p, upto_p - before_p));
         have_less = least == 0;
       }
     }
