@@ -58,6 +58,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1024, kList = kThreads, kShort = 2048;
 constexpr float kOrders = 46.f;
 constexpr float kOne = 8796093022208.f;  // weight of the highest logit, 2^43
+constexpr float kLeastTemperature = 3.7615819e-37f;  // 2^-121
 constexpr int kMaxCluster = 8, kMaxVocab = 262144;
 // Tokens per CTA: few rows are spread as thin as kSliceLeast, many rows take as
 // few CTAs as hold them with two CTAs per SM.
@@ -640,12 +641,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     high = 0.f;
     __syncthreads();
   }
-  // c = 2 log2(e) / t as two fp32 numbers (a temperature so small that it is
-  // not finite separates all logits that differ all the same)
+  // c = 2 log2(e) / t as two fp32 numbers.  The least temperature keeps c, and
+  // the bins per difference, finite.
   constexpr float kLh = 2.8853900432586669922f, kLl = 3.851925982e-8f;
-  const float ch = fminf(kLh / t, 3e38f);
-  const float cl = ch > 0.f && ch < 3e38f ? (fmaf(-ch, t, kLh) + kLl) / t : 0.f;
-  c.sc = {high, 0.5f * high, ch, cl, fminf(ch * (kBins / kOrders), 3e38f), s.pow};
+  const float least_t = fmaxf(t, kLeastTemperature), ch = kLh / least_t;
+  const float cl = ch > 0.f ? (fmaf(-ch, least_t, kLh) + kLl) / least_t : 0.f;
+  c.sc = {high, 0.5f * high, ch, cl, ch * (kBins / kOrders), s.pow};
   // min-p: e_i >= min_p, as weights
   const u64 least = mp > 0.f ? max(1ull, (u64)ceilf(fminf(mp, 1.f) * kOne)) : 0;
 

@@ -631,9 +631,10 @@ int q4k_add_rmsnorm(const void *x, int x_dtype, int64_t ldx, const void *residua
  *     0..i exceeds u[r] times the sum over all kept tokens; logp[r] =
  *     ln(e_token / that sum).
  * temperature[r] <= 0 or NaN: the highest logit (the lowest index of equal
- * ones), logp 0.  Logits of -infinity and NaN are never chosen; +infinity
- * shares the whole mass among its tokens.  A row without any other logit gives
- * token -1 and logp -infinity.  u outside [0, 1) is taken as the nearest end.
+ * ones), logp 0; a positive one below 2^-121 counts as 2^-121.  Logits of
+ * -infinity and NaN are never chosen; +infinity shares the whole mass among its
+ * tokens.  A row without any other logit gives token -1 and logp -infinity.  u
+ * outside [0, 1) is taken as the nearest end.
  * Each e_i is held to within about 2^-40 of the largest (sums are 64-bit
  * integers, in any order the same), so that a choice differs from the exact
  * one only where u lies that near to a border; e_i below 2^-44 count as 0.

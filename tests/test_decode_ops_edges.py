@@ -19,7 +19,7 @@ import pytest
 import torch
 
 from _gpu import DEV
-from test_decode_ops import BAD_PAGE, BF16, E4M3, F32, H16, H32, HB, gen, make_attn, plain_attn, plain_plan, quantize, to_dev
+from test_decode_ops import plain_sample, BAD_PAGE, BF16, E4M3, F32, H16, H32, HB, gen, make_attn, plain_attn, plain_plan, quantize, to_dev
 
 gpu = pytest.mark.gpu
 OK, NULL, SHAPE, ALIGN, MEMORY = 0, 1, 2, 3, 8
@@ -347,3 +347,24 @@ def test_binding_refuses_a_workspace_that_is_not_contiguous(q4k):
         with pytest.raises(q4k.Q4KError) as e:
             q4k.q4k_paged_attn(q, cache, cache, table, lens, 1.0, workspace=workspace)
         assert e.value.status == SHAPE
+
+
+# ------------------------------------------------------------------------------------------ the least temperature
+
+
+@gpu
+def test_sample_least_temperature(q4k):
+    """Logits that differ by parts of the least temperature, 2^-121, which all below it count as."""
+    rows, vocab = 24, 5000
+    g = gen(5)
+    x = -torch.rand((rows, vocab), generator=g) * 4e-36
+    u = torch.rand(rows, generator=g)
+    i = torch.arange(rows)
+    t = torch.tensor([1e-40, 2.0 ** -121, 1e-38, 3e-37, 2.0 ** -149, 1e-36])[i % 6]
+    p, k = torch.tensor([0.9, 0.5, 1.0, 0.999])[i % 4], torch.tensor([0, 0, 3000, 40])[(i // 4) % 4]
+    token, logp = (v.cpu() for v in q4k.q4k_sample(x.to(DEV), u.to(DEV), t.to(DEV), k.to(torch.int32).to(DEV), p.to(DEV)))
+    for r in range(rows):
+        want, lp, near = plain_sample(x[r].numpy(), float(u[r]), max(float(t[r]), 2.0 ** -121), int(k[r]), float(p[r]), 0.0)
+        assert int(token[r]) in near, r
+        assert int(token[r]) != want or abs(float(logp[r]) - lp) <= H32 * abs(lp) + 2.0 ** -30, r
+    assert q4k.q4k_get_device_error() == 0
