@@ -19,7 +19,7 @@ import pytest
 import torch
 
 from _gpu import DEV
-from test_decode_ops import plain_sample, BAD_PAGE, BF16, E4M3, F32, H16, H32, HB, gen, make_attn, plain_attn, plain_plan, quantize, to_dev
+from test_decode_ops import plain_sample, BAD_PAGE, BF16, E4M3, F32, H16, H8, H32, HB, gen, make_attn, plain_attn, plain_plan, quantize, to_dev
 
 gpu = pytest.mark.gpu
 OK, NULL, SHAPE, ALIGN, MEMORY = 0, 1, 2, 3, 8
@@ -368,3 +368,153 @@ def test_sample_least_temperature(q4k):
         assert int(token[r]) in near, r
         assert int(token[r]) != want or abs(float(logp[r]) - lp) <= H32 * abs(lp) + 2.0 ** -30, r
     assert q4k.q4k_get_device_error() == 0
+
+
+# ------------------------------------------------------------------------------------------ pipelines in their steady state
+
+
+def sm_count():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def shared_cache(seed, pages, heads, dim, page, kind):
+    """Cache buffers of `pages` pages that many requests may share, on the GPU, with their values in 64 bits."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    caches, scales, values = [], [], []
+    for kv in range(2):
+        x = torch.randn((pages, heads, page, dim), generator=g, device=DEV)
+        if kind == E4M3:
+            x = x * torch.exp2(torch.randint(-6, 7, (pages, heads, page, 1), generator=g, device=DEV).float()) if kv else x
+            b, s = quantize(x)
+            caches.append(b.view(E4M3)), scales.append(s), values.append(b.view(E4M3).double() * s.double()[..., None])
+        else:
+            caches.append(x.to(BF16)), values.append(caches[-1].double())
+    return caches, scales, values
+
+
+def check_long(q4k, seed, lens, q_heads, heads, dim, page, kind, pages, window=0, absent=0.0):
+    """Attention over tables into a shared cache, against 64 bits, a chunk of requests at a time."""
+    g = torch.Generator(device=DEV).manual_seed(seed + 1)
+    caches, scales, values = shared_cache(seed, pages, heads, dim, page, kind)
+    n, width = len(lens), -(-max(lens) // page) + 3
+    table = torch.randint(0, pages, (n, width), generator=g, device=DEV).to(torch.int32)
+    if absent:
+        out_of_range = torch.tensor([-1, pages, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+        hit = torch.rand((n, width), generator=g, device=DEV) < absent
+        table = torch.where(hit, out_of_range[torch.randint(0, 3, (n, width), generator=g, device=DEV)], table)
+    # entries past a request's pages: of no use to anyone
+    at = torch.arange(width, device=DEV)[None]
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    table = torch.where(at * page < ln[:, None], table, torch.full_like(table, -9)).contiguous()
+    q = torch.randn((n, q_heads, dim), generator=g, device=DEV).to(BF16)
+    out, lse = q4k.q4k_paged_attn(q, *caches, table, ln, dim ** -0.5, *scales, window=window)
+    again = q4k.q4k_paged_attn(q, *caches, table, ln, dim ** -0.5, *scales, window=window)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    seen = (at * page < ln[:, None]) & ((at + 1) * page > (ln[:, None] - window if window else 0))
+    bad = bool((seen & ((table < 0) | (table >= pages))).any())
+    assert q4k.q4k_get_device_error() == (BAD_PAGE if bad else 0) and (bad or not absent)
+    order = torch.argsort(ln, stable=True).tolist()
+    while order:
+        longest = max(lens[r] for r in order[-1:])
+        chunk = order[-max(1, min(len(order), int(2e7) // max(1, longest * q_heads * dim))):]
+        del order[-len(chunk):]
+        if not longest:
+            assert not out[chunk].any() and bool((lse[chunk] == -math.inf).all())
+            continue
+        m = -(-longest // page)
+        ids = table[chunk, :m].long()
+        ok = (ids >= 0) & (ids < pages)
+        k, v = (x[ids.clamp(0, pages - 1)].permute(0, 1, 3, 2, 4).reshape(len(chunk), m * page, heads, dim) for x in values)
+        tok = torch.arange(m * page, device=DEV)[None]
+        keep = (tok < ln[chunk, None]) & ok.repeat_interleave(page, 1)
+        if window:
+            keep &= tok >= ln[chunk, None] - window
+        want, wl, bo, bl = attn_bounds(q[chunk].double(), k, v, dim ** -0.5, kind == E4M3, keep)
+        worst = float(((out[chunk].double() - want).abs() - bo).max())
+        assert worst <= 0, worst
+        got = lse[chunk].double()
+        assert torch.equal(got == -math.inf, wl == -math.inf)
+        fin = wl != -math.inf
+        assert not fin.any() or float(((got - wl).abs() - bl)[fin].max()) <= 0
+
+
+# Warps per SM of a configuration, and tokens per tile: what a run of 32 tiles or more per warp needs.
+WARPS = {(64, BF16): 12, (64, E4M3): 12, (128, BF16): 6, (128, E4M3): 12, (256, BF16): 6, (256, E4M3): 6}
+TILE = {(256, BF16): 16}
+
+
+@gpu
+@pytest.mark.parametrize("window,absent,page", [(0, 0.0, 16), (3001, 0.02, 16), (0, 0.05, 64)])
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("dim,group", [(64, 2), (128, 4), (128, 16), (256, 3)])
+def test_attn_many_tiles_per_warp(q4k, dim, group, kind, window, absent, page):
+    """Few long requests, at least 32 tiles for every warp: each stage is refilled many times, table entries are
+    fetched on the way, and pieces begin and end inside of items."""
+    heads, tile = 4, TILE.get((dim, kind), 32)
+    tokens = 32 * sm_count() * WARPS[dim, kind] * tile // heads
+    n = 24
+    per = tokens // n
+    if window:  # a window's tiles only
+        n = -(-tokens // (window - tile))
+        per = 2 * window
+    lens = [per + (i * 7919) % 97 * (per // 200 + 1) for i in range(n)] + [0, 1, 17, per // 3, 0, tile + 1]
+    total = sum(-(-v // tile) - (max(0, v - window) if window else 0) // tile for v in lens) * heads
+    assert total >= 32 * sm_count() * WARPS[dim, kind]
+    check_long(q4k, 41 + dim, lens, heads * group, heads, dim, page, kind, 512, window, absent)
+
+
+@gpu
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("dim,group,page,absent", [(64, 1, 16, 0.0), (64, 16, 32, 0.03), (128, 8, 16, 0.03), (128, 12, 256, 0.0), (256, 8, 32, 0.03), (256, 12, 16, 0.0)])
+def test_attn_many_requests_per_warp(q4k, dim, group, kind, page, absent):
+    """Many short requests: a warp goes through several items and requests, refills across their borders, and
+    stages whose value rows were zeroed are filled again."""
+    heads, tile = 8, TILE.get((dim, kind), 32)
+    groups = -(-group // (8 if dim == 256 or group <= 8 else 16))
+    n = 32 * sm_count() * WARPS[dim, kind] // (heads * groups * (-(-95 // tile)))
+    lens = [(i * 37) % 190 for i in range(n + n // 8)]
+    assert sum(-(-v // tile) for v in lens) * heads * groups >= 32 * sm_count() * WARPS[dim, kind]
+    check_long(q4k, 43 + dim + group, lens, heads * group, heads, dim, page, kind, 1000, 0, absent)
+
+
+@gpu
+@pytest.mark.parametrize("out", [BF16, E4M3])
+@pytest.mark.parametrize("h,src,res,per_sm", [(4104, BF16, None, 5), (5120, BF16, BF16, 4), (5120, F32, BF16, 3), (8200, BF16, BF16, 3), (8200, F32, F32, 1), (12288, BF16, BF16, 2), (17408, BF16, None, 2),
+                                              (12800, F32, F32, 1)])
+def test_norm_rows_in_the_ring(q4k, h, src, res, per_sm, out):
+    """At least 16 rows for every block, so that each stage of its ring (4 at most) is filled again three times;
+    with the residual's new value in a tensor of its own and in place."""
+    m = 16 * per_sm * sm_count() + 37
+    g = torch.Generator(device=DEV).manual_seed(h)
+    x = torch.randn((m, h), generator=g, device=DEV).mul_(2).to(src)
+    r = None if res is None else torch.randn((m, h), generator=g, device=DEV).mul_(3).to(res)
+    gamma = torch.rand(h, generator=g, device=DEV) + 0.5
+    got = q4k.q4k_add_rmsnorm(x, r, gamma, 1e-6, out_dtype=out)
+    if r is not None:
+        kept = r.clone()
+        same = q4k.q4k_add_rmsnorm(x, kept, gamma, 1e-6, out_dtype=out, residual_out=kept)
+        assert torch.equal(kept, got[1]) and torch.equal(same[0].view(torch.uint8), got[0].view(torch.uint8))
+        assert out == BF16 or torch.equal(same[2], got[2])
+    assert q4k.q4k_get_device_error() == 0
+    # h: one fp32 rounding; the sum of squares: h / 32 + 24 additions at most in a row, halved by the square
+    # root; rsqrt, the division by h, two products
+    rel = (h / 32 + 24) * H32 + 8 * H32
+    for part in torch.arange(m, device=DEV).split(1024):
+        xx = x[part].double()
+        rr = 0.0 if r is None else r[part].double()
+        hh = xx + rr
+        norm = torch.sqrt((hh * hh).mean(-1, keepdim=True) + 1e-6)
+        y = hh / norm * gamma.double()
+        size = xx.abs() + (0.0 if r is None else rr.abs())
+        if r is not None:
+            assert float(((got[1][part].double() - hh).abs() - (HB if res == BF16 else 0.0) * hh.abs() * 1.001 - 2 * H32 * size).max()) <= 0
+        slip = rel * y.abs() + H32 * size / norm * gamma.double()
+        if out == BF16:
+            assert float(((got[0][part].double() - y).abs() - HB * y.abs() - 1.01 * slip).max()) <= 0
+            continue
+        s = got[2][part].double()
+        wide = s.repeat_interleave(128, 1)[:, :h]
+        # a value: half a step of e4m3 (of its smallest, 2^-9, where it is subnormal)
+        assert float(((got[0][part].double() * wide - y).abs() - H8 * y.abs() * 1.001 - 2.0 ** -10 * wide - 1.2 * slip).max()) <= 0
+        blocks = torch.nn.functional.pad(torch.stack([y.abs(), slip]), (0, -h % 128)).unflatten(2, (-1, 128)).amax(-1) / 448
+        assert float(((s - blocks[0]).abs() - 4 * H32 * blocks[0] - 1.01 * blocks[1]).max()) <= 0
