@@ -143,9 +143,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
 // it keeps in registers between the sum of squares and y; with KEEP = 0 it takes
 // any number and reads them again.  One barrier per row: behind it every thread
 // has its part of the sum, and every thread has left the row before, whose stage
-// is then refilled.  (8191 x 5120 to e4m3: 47.3 us kept, 49.3 read again; 2000 x
-// 17408: 31.6 us read again, 35.6 with 8 kept, whose registers leave room for one
-// block per SM only.)
+// is then refilled.  (8191 x 5120 to e4m3: 47.3 us kept, 49.3 read again in the
+// same run, 47.9 in others; 2000 x 17408: 31.6 us read again, 35.6 with 8 kept,
+// whose registers leave room for one block per SM only.)
 template <typename TX, typename TR, bool E4M3, int KEEP>
 __global__ void __launch_bounds__(512) add_rmsnorm_rows_kernel(const NormArgs a, int stages) {
   extern __shared__ __align__(16) uint8_t ring[];

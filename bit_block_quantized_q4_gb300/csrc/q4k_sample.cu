@@ -28,7 +28,7 @@
 //     are sent to the cluster's first CTA, which compares all pairs of them (up to
 //     kThreads) or sorts them, and does the rest on the list.  Top-p without top-k needs the exact total of all weights too.
 //   - Else each filter's smallest key is found by histograms over ever smaller
-//     ranges of c_i, counts and exact weights, until at most kList tokens are
+//     ranges of c_i, of counts or of exact weights, until at most kList tokens are
 //     left, which are compared in pairs (whatever the ties); the draw then goes
 //     over all tokens.  After top-p it takes the weights before the border's bins
 //     from the pass that summed them: 256 rows of 131072 with top-p 0.9 alone

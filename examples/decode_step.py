@@ -1,8 +1,7 @@
 """A decode step around the quantized projections, on random weights.
 
 Every step appends one token to each request, from the random numbers that it is
-given, with nothing but this library's calls between the embedding and the next
-token:
+given, with this library's calls between the embedding and the next token:
 
     plan      block tables and slot maps of the step        q4k_kv_plan
     per layer norm (with the residual's addition)           q4k_add_rmsnorm
@@ -12,10 +11,13 @@ token:
               output projection, norm, gate/up, down        q4k_gemv, q4k_add_rmsnorm, q4k_gemv_glu, q4k_gemv
     the end   norm, vocabulary projection, sampling         q4k_add_rmsnorm, q4k_gemv, q4k_sample
 
+Beside them a layer has two torch casts, because projections give fp32 and
+attention and projections take bf16.  The model has no position encoding, and the
+library no call that rotates q and k: where one is wanted, rotate them between
+the projection and the cache write, by the positions that q4k_kv_plan gives.
+
 Run it on the GPU:  python examples/decode_step.py [--steps N] [--cache e4m3]
-It prints the time of a step launched call by call and as a CUDA graph.  (The
-model has no position encoding: rotate q and k between the projection and the
-cache write where one is wanted; q4k_kv_plan gives the positions.)
+It prints the time of a step launched call by call and as a CUDA graph.
 """
 from __future__ import annotations
 

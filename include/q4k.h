@@ -567,6 +567,9 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
  * weights enter the products as two bf16 terms (16 significant bits), for an
  * e4m3 cache as one fp16 term of the weight times the row's scale: 11 bits down
  * to 2^-29 of the largest such term, an error of at most 2^-40 of it below.
+ * q is exact for a bf16 cache; for an e4m3 cache it enters as fp16 times a power
+ * of two per head: exact down to 2^-31 of the head's largest value, to within
+ * 2^-39 of it below.
  * Values that are not finite in rows that take part show in the result; an
  * infinite value of V may do so as NaN.
  *   q       device, bf16, element (r, i, d) at r * ldq + i * ldq_head + d;
@@ -601,7 +604,8 @@ int q4k_paged_attn(const void *q, int64_t ldq, int64_t ldq_head, int32_t n, int3
  *     y = h * gamma / sqrt((1/H) sum_i h_i^2 + eps)
  * in fp32 from the unrounded h, each output rounded once.  y is bf16, or e4m3
  * with one fp32 scale per 128 values: scales[t][b] = max(max |y|, 2^-100) /
- * 448, values e4m3(y * (448 / max)).
+ * 448, values e4m3(y * (448 / max)).  (The projections here take bf16; e4m3 is
+ * for 8-bit products of the caller's own.)
  *   x             device, m x hidden fp32 or bf16, row stride ldx
  *   residual      device, m x hidden fp32 or bf16, or NULL (then residual_out is
  *                 not used)
