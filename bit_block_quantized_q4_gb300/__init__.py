@@ -33,6 +33,7 @@ EXPORTS = ("q4k_abi_version", "q4k_status_str", "q4k_dequant", "q4k_gemv", "q4k_
            "q4k_moe_gemv_ex", "q4k_moe_gemv_noalloc", "q4k_moe_prefill",
            "q4k_moe_prefill_workspace_size",
            "q4k_kv_plan", "q4k_kv_write", "q4k_paged_attn", "q4k_paged_attn_workspace_size",
+           "q4k_paged_attn_chunk", "q4k_paged_attn_chunk_workspace_size",
            "q4k_add_rmsnorm", "q4k_sample",
            "q4k_get_device_error", "q4k_selftest_wait_timeout")
 Q4K_DTYPE_FP32, Q4K_DTYPE_BF16, Q4K_DTYPE_E4M3 = 0, 1, 2
@@ -116,6 +117,12 @@ def lib() -> ctypes.CDLL:
         L.q4k_kv_write.restype = ctypes.c_int
         L.q4k_kv_write.argtypes = [P, P, ctypes.c_int, I64, I64, P, I64, I32, I32, P, P, ctypes.c_int,
                                    I64, I32, I64, I64, I64, P, P, P]
+        L.q4k_paged_attn_chunk_workspace_size.restype = SZ
+        L.q4k_paged_attn_chunk_workspace_size.argtypes = [I64, I32, I32, I32]
+        L.q4k_paged_attn_chunk.restype = ctypes.c_int
+        L.q4k_paged_attn_chunk.argtypes = [P, I64, I64, I64, P, I32, I32, I32, I32, P, P, ctypes.c_int,
+                                           I64, I32, I64, I64, I64, P, P, P, I64, I32, P, F32, I32, P,
+                                           I64, P, P, SZ, P]
         L.q4k_paged_attn_workspace_size.restype = SZ
         L.q4k_paged_attn_workspace_size.argtypes = [I32, I32, I32, I32]
         L.q4k_paged_attn.restype = ctypes.c_int
@@ -552,6 +559,55 @@ def q4k_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         table.data_ptr(), ldt, width, _vec("lens", lens, n, _I32), softmax_scale, window,
         out.data_ptr(), ldo, lse.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _call_stream(stream, q)), "q4k_paged_attn")
+    return out, lse
+
+
+def q4k_paged_attn_chunk_workspace_size(tokens: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    return int(lib().q4k_paged_attn_chunk_workspace_size(tokens, q_heads, kv_heads, dim))
+
+
+def q4k_paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
+                         softmax_scale: float, k_scale=None, v_scale=None, window: int = 0, out=None,
+                         lse=None, workspace=None, stream=None):
+    """Attention of each request's new tokens, the rows cu[r] .. cu[r + 1] - 1 of q [tokens, q_heads,
+    dim] bf16 and the last of its lens[r] cached tokens, over the paged caches [pages, kv_heads, page
+    size, dim] (bf16, or e4m3 with scales) by table [n, max_pages] and lens [n] int32, cu [n + 1]
+    int64.  Each sees the tokens up to its own (with a window, the last `window` of them).  Returns
+    (out [tokens, q_heads, dim] bf16, lse [tokens, q_heads] fp32), rows past cu[n] as they were."""
+    shape, strides, code, ks, vs = _caches(k_cache, v_cache, k_scale, v_scale)
+    pages, heads, page, dim = shape
+    L = _lib or lib()
+    if q.dtype is not _BF16 or len(q.shape) != 3 or q.shape[2] != dim:
+        _refuse("q", q)
+    tokens, q_heads, n = q.shape[0], q.shape[1], lens.numel()
+    ldq = _outer_strides(q)
+    width = table.shape[-1]
+    ldt = _rows("table", table, n, width, _I32)
+    if out is None:
+        out = _empty((tokens, q_heads, dim), _BF16, q, stream)
+        ldo = q_heads * dim
+    else:
+        if out.dtype is not _BF16 or out.shape != q.shape:
+            _refuse("out", out)
+        ldo, inner = _outer_strides(out)
+        if inner != dim:
+            raise Q4KError(2, f"out has head stride {inner}, not {dim}")
+    if lse is None:
+        lse = _empty((tokens, q_heads), _F32, q, stream)
+    elif lse.dtype is not _F32 or lse.shape != (tokens, q_heads) or not lse.is_contiguous():
+        _refuse("lse", lse)
+    if workspace is None:
+        size = L.q4k_paged_attn_chunk_workspace_size(tokens, q_heads, heads, dim)
+        workspace = _empty(max(size, 16), torch.uint8, q, stream)
+    elif not workspace.is_contiguous():  # its elements would not be bytes of memory
+        _refuse("workspace", workspace)
+    _check(L.q4k_paged_attn_chunk(
+        q.data_ptr(), ldq[0], ldq[1], tokens, _vec("cu", cu, n + 1, _I64), n, q_heads, heads, dim,
+        k_cache.data_ptr(), v_cache.data_ptr(), code, pages, page, strides[0], strides[1], strides[2],
+        ks, vs, table.data_ptr(), ldt, width, _vec("lens", lens, n, _I32), softmax_scale, window,
+        out.data_ptr(), ldo, lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _call_stream(stream, q)), "q4k_paged_attn_chunk")
     return out, lse
 
 

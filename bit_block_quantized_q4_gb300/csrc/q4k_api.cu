@@ -718,6 +718,58 @@ int q4k_paged_attn(const void *q, int64_t ldq, int64_t ldq_head, int32_t n, int3
   return map_launch(launch_paged_attn(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t q4k_paged_attn_chunk_workspace_size(int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                           int32_t dim) {
+  if (tokens < 0 || q_heads <= 0 || kv_heads <= 0 || dim <= 0 || tokens > INT32_MAX / q_heads) return 0;
+  return paged_attn_chunk_workspace_size(tokens, q_heads, kv_heads, dim);
+}
+
+int q4k_paged_attn_chunk(const void *q, int64_t ldq, int64_t ldq_head, int64_t tokens,
+                         const int64_t *cu, int32_t n, int32_t q_heads, int32_t kv_heads,
+                         int32_t dim, const void *k_cache, const void *v_cache, int cache_dtype,
+                         int64_t n_pages, int32_t page_size, int64_t page_stride,
+                         int64_t head_stride, int64_t token_stride, const float *k_scale,
+                         const float *v_scale, const int32_t *table, int64_t ldt,
+                         int32_t max_pages, const int32_t *lens, float softmax_scale,
+                         int32_t window, void *out, int64_t ldo, float *lse, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+  int st = check_cache(kv_heads, dim, cache_dtype, n_pages, page_size, page_stride, head_stride,
+                       token_stride);
+  if (st != Q4K_OK) return st;
+  if (n < 0 || n > 65536 || q_heads <= 0 || q_heads > 1024 || q_heads % kv_heads || tokens < 0 ||
+      tokens > INT32_MAX / q_heads)
+    return Q4K_ERR_SHAPE;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return Q4K_ERR_SHAPE;
+  if (max_pages <= 0 || max_pages > (1 << 30) / page_size || ldt < max_pages || window < 0)
+    return Q4K_ERR_SHAPE;
+  if (!(softmax_scale - softmax_scale == 0.f)) return Q4K_ERR_SHAPE;  // NaN or infinite
+  if (ldq_head < dim || ldq < 0 || ldo < (int64_t)q_heads * dim) return Q4K_ERR_SHAPE;
+  if (n == 0 || tokens == 0) return Q4K_OK;
+  const bool e4m3 = cache_dtype == Q4K_DTYPE_E4M3;
+  if (!q || !cu || !k_cache || !v_cache || !table || !lens || !out || (e4m3 && (!k_scale || !v_scale)))
+    return Q4K_ERR_NULL;
+  if (!workspace || workspace_bytes < paged_attn_chunk_workspace_size(tokens, q_heads, kv_heads, dim))
+    return Q4K_ERR_WORKSPACE;
+  if (!aligned(q, 16) || !aligned(cu, 8) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
+      !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) || ldq % 8 || ldq_head % 8 || ldo % 8)
+    return Q4K_ERR_ALIGN;
+  st = check_device();
+  if (st != Q4K_OK) return st;
+  st = check_device_memory({q, cu, k_cache, v_cache, table, lens, out, lse, workspace,
+                            e4m3 ? k_scale : nullptr, e4m3 ? v_scale : nullptr});
+  if (st != Q4K_OK) return st;
+  AttnArgs a = {};
+  a.q = q, a.cache[0] = k_cache, a.cache[1] = v_cache, a.scale[0] = k_scale, a.scale[1] = v_scale;
+  a.table = table, a.lens = lens, a.out = out, a.lse = lse, a.workspace = workspace;
+  a.ldq = ldq, a.ldq_head = ldq_head, a.ldo = ldo, a.ldt = ldt, a.n_pages = n_pages;
+  a.page_stride = page_stride, a.head_stride = head_stride, a.token_stride = token_stride;
+  a.n = n, a.q_heads = q_heads, a.kv_heads = kv_heads, a.dim = dim, a.page = page_size;
+  a.max_pages = max_pages, a.window = window, a.softmax_scale = softmax_scale;
+  a.cache_dtype = cache_dtype, a.err = device_error_word();
+  return map_launch(launch_paged_attn_chunk(a, tokens, cu, static_cast<cudaStream_t>(stream)));
+}
+
 int q4k_add_rmsnorm(const void *x, int x_dtype, int64_t ldx, const void *residual, int res_dtype,
                     int64_t ldr, const float *gamma, float eps, int64_t m, int64_t hidden, void *y,
                     int y_dtype, int64_t ldy, void *residual_out, int64_t ldro, float *scales,

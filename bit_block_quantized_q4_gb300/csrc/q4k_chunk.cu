@@ -1,0 +1,1022 @@
+// q4k_chunk.cu -- attention of each request's new tokens, one or many, over the
+// paged cache (q4k_paged_attn_chunk).
+//
+// "spec: specialized model runtimes", section "Architecture": attention is an
+// op of kernel tier T0.
+//
+// Mathematics.  Token i of a request's m new ones stands at position p = len - m
+// + i and sees the tokens max(0, p + 1 - window) .. p.  One pass over the keys
+// with a running reference M and sum l, in base 2 (scores carry log2 e):
+//   w_j = 2^(z_j - M),  l += w_j,  o += w_j v_j,  out = o / l.
+// M is the running maximum, but it follows only when the maximum has grown by
+// more than 2^kLazy; then l and o are multiplied by 2^(M - M').  A sum of
+// powers is the same whatever its reference, so this costs nothing but kLazy of
+// fp32's exponent, and o, which lives in tensor memory, is rarely touched.
+//
+// Rows.  The query heads of one key head share its keys, so the rows of a
+// product are (token, head) pairs: row = token * group + head.  128 of them are a
+// query tile; a decode step's single tokens fill a part of one, a prompt all.
+//
+// Products, both by tcgen05.mma with fp32 accumulators in tensor memory:
+//   S[128 rows, TILE keys] = Q K^T    (Q, K from shared memory)
+//   O[128 rows, D]        += P V      (P in tensor memory over S, V from shared memory)
+//
+// Roles of a CTA's 16 warps, connected by mbarriers:
+//   0..3, 4..7  softmax of query tile 0 and 1: a thread owns a row of S
+//   8           issues the products
+//   9           finds the work and issues the copies of K and V (TMA, a page each)
+//   10, 11      fetch Q
+//   12..15      prepare what was copied: rows of V that no query sees become zeros
+//               (their weights are 0, but 0 times a NaN is not); an e4m3 cache is
+//               converted to fp16 in place
+//
+// Work split.  An item is (request, key head, block of rows), its cost its key
+// tiles and kItemCost; every CTA of a persistent grid takes an equal run of the
+// list of all items' tiles.  The lengths are on the device, so each CTA sums them
+// itself.  A CTA has at most two pieces of items that it shares with others; they
+// go to the workspace and a second launch joins them.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/q4k.h"
+#include "q4k_device.cuh"
+#include "q4k_internal.h"
+#include "q4k_step.cuh"
+#include "q4k_step.h"
+
+namespace q4k {
+namespace {
+
+constexpr int kMaxSms = 160;     // CTAs that the workspace is sized for
+constexpr int kThreads = 512;
+constexpr int kItemCost = 1;     // of an item's start and end, in tiles
+constexpr float kLazy = 8.f;     // binary orders that a maximum may grow before M follows
+constexpr float kUpBits = 7.f;   // e4m3: weights are stored times 2^7 (see softmax_tile)
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr int kRing = 4;         // items on their way
+
+template <int D, bool E4M3>
+struct Cfg {
+  static constexpr int kNq = D == 256 ? 1 : 2;        // query tiles per block
+  static constexpr int kSb = D == 256 ? 2 : 1;        // score buffers per query tile
+  static constexpr int kTile = D == 256 ? 64 : 128;   // tokens per key tile
+  static constexpr int kParts = D / 64;               // 128-byte parts of a row
+  static constexpr int kSide = kTile * D * 2;         // bytes of a tile of K or V
+  static constexpr int kStages = D == 64 ? 4 : 2;     // of K, and of V
+  static constexpr int kQ = 128 * D * 2;              // bytes of a query tile
+  static constexpr int kRows = 128 * kNq;             // rows of a block
+  static constexpr int kSCols = kSb * kTile;          // tensor memory columns of a tile's S
+  static constexpr int kOCol = kNq * kSCols;          // first column of O
+  static constexpr int kCols = 512;
+  static constexpr int kEs = E4M3 ? 1 : 2;
+  static constexpr int kRaw = kTile * D;              // bytes of an e4m3 tile
+  // Q | K stages | V stages | e4m3: per V stage the K scales, log2 and reciprocal of the V scales
+  static constexpr int kKAt = kNq * kQ, kVAt = kKAt + kStages * kSide;
+  static constexpr int kScaleAt = kVAt + kStages * kSide;
+  static constexpr int kSmem = kScaleAt + (E4M3 ? kStages * 3 * kTile * 4 : 0) + 1024;
+  static_assert(kOCol + kNq * D <= kCols, "S and O fit tensor memory");
+};
+
+struct Params {
+  AttnArgs a;
+  int64_t tokens;     // of q and out
+  const int64_t *cu;
+  int group;          // query heads per key head
+  FastDiv by_group;
+  int box_rows, box_shift, page_shift;
+  int slot_rows;      // rows of a workspace slot, a multiple of 32
+  int4 *desc;         // per CTA: the item that it starts and does not end
+  float *slots;
+};
+
+// ------------------------------------------------------------------ work list
+
+// A request's geometry.
+struct Req {
+  int tok0, m, pos0, rows;  // first token of the step, their number, position of the first, rows per key head
+};
+__device__ __forceinline__ Req request(const Params &p, int r, bool &bad) {
+  const int64_t c0 = p.cu[r], c1 = p.cu[r + 1];
+  const bool ok = c0 >= 0 && c1 >= c0 && c1 <= p.tokens;
+  const int told = max(p.a.lens[r], 0);
+  Req q;
+  q.tok0 = ok ? (int)c0 : 0;
+  q.m = ok ? (int)(c1 - c0) : 0;
+  q.pos0 = told - q.m;
+  q.rows = q.m * p.group;
+  bad |= !ok || (q.m > 0 && told > p.a.max_pages * p.a.page);
+  return q;
+}
+// First token that a position sees; what follows its last one.  Tokens past the
+// table are absent.
+__device__ __forceinline__ int first_seen(const AttnArgs &a, int pos) {
+  return a.window > 0 && pos >= a.window ? pos + 1 - a.window : 0;
+}
+__device__ __forceinline__ int end_seen(const AttnArgs &a, int pos) {
+  return min(max(pos + 1, 0), a.max_pages * a.page);
+}
+// The key tiles [t0, t1) of rows [row0, row0 + rows) of a request.
+template <int TILE>
+__device__ __forceinline__ void tiles_of(const Params &p, const Req &q, int row0, int rows, int &t0, int &t1) {
+  const int lo = first_seen(p.a, q.pos0 + (int)p.by_group.div(row0));
+  const int hi = end_seen(p.a, q.pos0 + (int)p.by_group.div(row0 + rows - 1));
+  t0 = lo / TILE;
+  t1 = hi > lo ? (hi + TILE - 1) / TILE : t0;
+}
+template <int TILE, int ROWS>
+__device__ __forceinline__ int block_cost(const Params &p, const Req &q, int b) {
+  int t0, t1;
+  tiles_of<TILE>(p, q, b * ROWS, min(ROWS, q.rows - b * ROWS), t0, t1);
+  return t1 - t0 + kItemCost;
+}
+
+// What all roles know of an item.
+struct Item {
+  int r, head, row0, rows;  // rows < 0: there are no more items
+  int tok0, pos0;
+  int t0, n;                // its first key tile here, and their number
+  int lo, hi;               // tokens that any of its rows sees
+  int full_lo, full_hi;     // tokens in between are seen by all rows
+  int kind;                 // 0: whole, 1: starts the item (slot 1), 2: does not (slot 0)
+};
+
+// ---------------------------------------------------------------- PTX wrappers
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+#define Q4K_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define Q4K_V8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// 32 lanes x 32 bits, 32 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld_x32(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : Q4K_R8(r, 0), Q4K_R8(r, 8), Q4K_R8(r, 16), Q4K_R8(r, 24)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(addr),
+      Q4K_V8(r, 0), Q4K_V8(r, 8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+// mbar_wait without a call: a call in here would cost every role its registers.
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, unsigned *err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitLimitNs) break;
+  }
+  set_device_error(err, kDevErrTimeout);
+  return false;
+}
+// A wait by a whole warp: true if it was for all lanes, so that they stay together.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
+  return __all_sync(0xffffffffu, wait_on(bar, parity, err));
+}
+// A barrier of the 128 threads of a warpgroup; true if `ok` was true for all.
+// (Every warp passes it whatever happened to it, so that none is left behind.)
+__device__ __forceinline__ bool group_and(int id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "r"(id)
+      : "memory");
+  return all != 0;
+}
+// Descriptor of V as the second operand: [token][64 values] rows of 128 bytes,
+// swizzled, 8 tokens per 1024 bytes; the next 64 values of D `part` bytes on.
+__device__ __forceinline__ uint64_t sdesc_v(uint32_t addr, uint32_t part) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((part >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024u >> 4) << 32 |
+         (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+// Instruction descriptor: fp32 accumulators, operands bf16 or fp16, the second
+// one with its rows along N (K-major) or along K (transposed).
+__host__ __device__ constexpr uint32_t idesc_of(bool bf16, bool transposed, int n) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (transposed ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Four e4m3 values to two fp16 pairs, exact.
+__device__ __forceinline__ uint2 e4m3x4_f16(uint32_t w) {
+  uint2 d;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(d.x), "=r"(d.y) : "r"(w));
+  return d;
+}
+
+// ------------------------------------------------------------------- the kernel
+
+struct Bars {
+  uint64_t item_full[kRing], item_empty[kRing];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
+  uint64_t s_full[2][2], p_full[2][2], o_done[2];
+};
+// Of a stage of V: 16-token pieces that are absent, tokens whose values are not
+// finite; e4m3: the least and the largest exponent field of the V scales.
+struct VInfo {
+  uint32_t absent, bad[4], e_min, e_max;
+};
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D, E4M3>;
+  constexpr int TILE = C::kTile, ROWS = C::kRows, ST = C::kStages, NQ = C::kNq, SB = C::kSb;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) Bars bars;
+  __shared__ VInfo vinfo[4];
+  __shared__ Item items[kRing];
+  __shared__ float q_scale[2][256];  // e4m3: what the rows' scores are multiplied by (this item's, the next one's)
+  __shared__ int64_t sums[kThreads], wsum[kThreads / 32];
+  __shared__ uint32_t tmem_slot;
+  const AttnArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  grid_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(&bars.item_full[i], 1), mbar_init(&bars.item_empty[i], 1 + 2 + 4 * NQ + 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.q_full[i], 2), mbar_init(&bars.q_empty[i], 1), mbar_init(&bars.o_done[i], 1);
+      for (int j = 0; j < 2; ++j) mbar_init(&bars.s_full[i][j], 1), mbar_init(&bars.p_full[i][j], 4);
+    }
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&bars.k_full[i], 1), mbar_init(&bars.k_ready[i], 4), mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_full[i], 1), mbar_init(&bars.v_ready[i], 4), mbar_init(&bars.v_empty[i], 1);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&kmap), prefetch_tmap(&vmap);
+  }
+  if (warp == 8) {
+    tmem_alloc(&tmem_slot, C::kCols);
+    tmem_relinquish();
+  }
+
+  // Sum the costs of all requests: thread i takes requests [i * per, (i + 1) * per).
+  const int per = (a.n + kThreads - 1) / kThreads, r_lo = min(tid * per, a.n), r_hi = min(r_lo + per, a.n);
+  bool bad = false;
+  int64_t mine = 0;
+  const auto cost_of = [&](int r) {
+    const Req q = request(p, r, bad);
+    int64_t c = 0;
+    for (int b = 0; b * ROWS < q.rows; ++b) c += block_cost<TILE, ROWS>(p, q, b);
+    return c * a.kv_heads;
+  };
+  for (int r = r_lo; r < r_hi; ++r) mine += cost_of(r);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) incl += wsum[w];
+    total += wsum[w];
+  }
+  sums[tid] = incl;
+  if (blockIdx.x == 0 && bad) set_device_error(a.err, kDevErrBadPage);
+  __syncthreads();
+  const uint32_t tmem = tmem_slot;
+  const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)1);
+  const int64_t u0 = min((int64_t)blockIdx.x * run, total), u1 = min(u0 + run, total);
+  bool ok = true;
+
+  // The ring of items, as every role but the copying one reads it.
+  int it = 0;
+  const auto take_item = [&](Item &x, bool waited) {  // false: there are no more, or the wait ran out
+    ok = waited;
+    if (ok) x = items[it % kRing];
+    return ok && x.rows >= 0;
+  };
+  const auto next_item = [&](Item &x) {  // by a warp
+    return take_item(x, warp_wait(&bars.item_full[it % kRing], (uint32_t)(it / kRing) & 1u, a.err));
+  };
+  const auto free_item = [&]() {  // by one lane of the warp
+    mbar_arrive(&bars.item_empty[it % kRing]);
+  };
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n");
+    // ---------------------------------------------------------------- softmax
+    const int t = warp >> 2, row_in = 32 * (warp & 3) + lane, row_t = 128 * t + row_in;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s_at = tmem + lanes + t * C::kSCols, o_at = tmem + lanes + C::kOCol + t * D;
+    // scores are multiplied by -1 or 0 first where the scale is not positive
+    const float scale = (a.softmax_scale == 0.f ? 1.f : fabsf(a.softmax_scale)) * kLog2e;
+    const float sign = a.softmax_scale < 0.f ? -1.f : 0.f;
+    const bool positive = a.softmax_scale > 0.f;
+    int tiles = 0, mine_t = 0, taken = 0;  // key tiles of this CTA so far, those of query tile t, and its items
+    Item x;
+    while (t < NQ && ok && next_item(x)) {
+      const bool active = x.rows > 128 * t, used = x.rows > 128 * t + 32 * (warp & 3), live = row_t < x.rows;
+      // this row's token, its head in the group, and the tokens that it sees
+      const int row = x.row0 + row_t, tok = (int)p.by_group.div(row), pos = x.pos0 + tok;
+      const int seen_lo = live ? first_seen(a, pos) : x.lo, seen_hi = live ? end_seen(a, pos) : x.hi;
+      float m = -INFINITY, l = 0.f;
+      bool poisoned = false;
+      float sc = scale;
+      uint32_t e_max = 0;
+      for (int j = 0; active && j < x.n && ok; ++j) {
+        const int g = mine_t + j, buf = SB == 2 ? g & 1 : 0;
+        const int vs = (tiles + j) % ST;
+        ok = warp_wait(&bars.s_full[t][buf], (uint32_t)(SB == 2 ? g >> 1 : g) & 1u, a.err) &&
+             warp_wait(&bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (used) {
+          if (E4M3 && j == 0) sc = scale * q_scale[taken & 1][row_t];
+          const uint32_t at = s_at + buf * TILE;
+          uint32_t s[TILE];
+#pragma unroll
+          for (int c = 0; c < TILE; c += 32) tmem_ld_x32(at + c, s + c);
+          tmem_ld_wait();
+          if (!positive) {
+#pragma unroll
+            for (int c = 0; c < TILE; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * sign);
+          }
+          const float *ks = reinterpret_cast<const float *>(smem + C::kScaleAt) + vs * 3 * TILE, *lv = ks + TILE, *rv = lv + TILE;
+          if (E4M3) {
+#pragma unroll
+            for (int c = 0; c < TILE; c += 4) {
+              const float4 k4 = *reinterpret_cast<const float4 *>(ks + c), l4 = *reinterpret_cast<const float4 *>(lv + c);
+              const float2 sc2 = make_float2(sc, sc);
+              const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), __fmul2_rn(make_float2(k4.x, k4.y), sc2), make_float2(l4.x, l4.y));
+              const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), __fmul2_rn(make_float2(k4.z, k4.w), sc2), make_float2(l4.z, l4.w));
+              s[c] = __float_as_uint(z0.x), s[c + 1] = __float_as_uint(z0.y), s[c + 2] = __float_as_uint(z1.x), s[c + 3] = __float_as_uint(z1.y);
+            }
+          }
+          const uint32_t absent = vinfo[vs].absent;
+          const int lo = seen_lo - (x.t0 + j) * TILE, hi = seen_hi - (x.t0 + j) * TILE;
+          if (__any_sync(0xffffffffu, lo > 0 || hi < TILE || absent)) {
+#pragma unroll
+            for (int c = 0; c < TILE; ++c)
+              if (c < lo || c >= hi || (absent >> (c / 16) & 1u)) s[c] = 0xff800000u;
+#pragma unroll
+            for (int w = 0; w < TILE / 32; ++w) {
+              const uint32_t b = vinfo[vs].bad[w];
+              if (b) {
+                const int lo_w = min(max(lo - 32 * w, 0), 32), hi_w = min(max(hi - 32 * w, 0), 32);
+                const uint32_t below = hi_w == 32 ? 0xffffffffu : (1u << hi_w) - 1u, from = lo_w == 32 ? 0u : 0xffffffffu << lo_w;
+                poisoned |= (b & below & from) != 0;
+              }
+            }
+          }
+          float top = __uint_as_float(s[0]);
+#pragma unroll
+          for (int c = 1; c < TILE; ++c) top = fmaxf(top, __uint_as_float(s[c]));
+          // scores are S here, to be multiplied by sc, or (e4m3) in base 2 already
+          const float unit = E4M3 ? 1.f : sc;
+          const bool grew = m != -INFINITY && (top - m) * unit > kLazy;
+          if (m == -INFINITY) m = top;
+          if (__any_sync(0xffffffffu, grew)) {
+            const float f = grew ? ex2((m - top) * unit) : 1.f;
+            if (grew) m = top;
+            l *= f;
+            ok = warp_wait(&bars.o_done[t], (uint32_t)(g - 1) & 1u, a.err);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld_x16(o_at + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_x16(o_at + c, o);
+            }
+            tmem_st_wait();
+          }
+          const float ref = m == -INFINITY ? 0.f : -m * unit + (E4M3 ? kUpBits : 0.f);
+          const float2 unit2 = make_float2(unit, unit), ref2 = make_float2(ref, ref);
+          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < TILE; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float2 z0 = make_float2(__uint_as_float(s[c + i]), __uint_as_float(s[c + i + 1])), z1 = make_float2(__uint_as_float(s[c + i + 2]), __uint_as_float(s[c + i + 3]));
+              const float2 y0 = E4M3 ? __fadd2_rn(z0, ref2) : __ffma2_rn(z0, unit2, ref2), y1 = E4M3 ? __fadd2_rn(z1, ref2) : __ffma2_rn(z1, unit2, ref2);
+              const float2 e0 = make_float2(ex2(y0.x), ex2(y0.y)), e1 = make_float2(ex2(y1.x), ex2(y1.y));
+              if (E4M3) {
+                const float4 r4 = *reinterpret_cast<const float4 *>(rv + c + i);
+                l2[0] = __ffma2_rn(e0, make_float2(r4.x, r4.y), l2[0]);
+                l2[1] = __ffma2_rn(e1, make_float2(r4.z, r4.w), l2[1]);
+                w[i / 2] = pack_f16(e0.x, e0.y), w[i / 2 + 1] = pack_f16(e1.x, e1.y);
+              } else {
+                l2[0] = __fadd2_rn(l2[0], e0), l2[1] = __fadd2_rn(l2[1], e1);
+                w[i / 2] = pack_bf16(e0.x, e0.y), w[i / 2 + 1] = pack_bf16(e1.x, e1.y);
+              }
+            }
+            tmem_st_x16(at + c / 2, w);
+          }
+          float more = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+          if (E4M3) {
+            // A weight times its scale that underflows has no part in the product, but
+            // where the scales lie more than 2^100 apart its weight may be large: such
+            // tiles' sums are taken from the weights themselves.
+            e_max = max(e_max, vinfo[vs].e_max);
+            if (e_max > vinfo[vs].e_min + 100u) {
+              more = 0.f;
+#pragma unroll
+              for (int c = 0; c < TILE; ++c) more += ex2(__uint_as_float(s[c]) + ref - lv[c]);
+            }
+          }
+          l += more;
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[t][buf]);
+      }
+      // ---- the piece ends: O is complete once its last product is
+      if (active && x.n > 0 && ok) {
+        const int g = mine_t + x.n - 1;
+        ok = (x.n == 1 || warp_wait(&bars.o_done[t], (uint32_t)(g - 1) & 1u, a.err)) &&
+             warp_wait(&bars.o_done[t], (uint32_t)g & 1u, a.err);
+        tc_fence_after();
+      }
+      if (used && ok) {
+        const float big = m == -INFINITY ? -INFINITY : E4M3 ? m : m * sc;
+        const int i = tok, head = x.head * p.group + (row - tok * p.group);
+        const int64_t token = (int64_t)x.tok0 + i;
+        float *slot = p.slots + (2 * (int64_t)blockIdx.x + (x.kind == 1)) * (int64_t)(D + 2) * p.slot_rows + row_t;
+        const float f = poisoned ? __int_as_float(0x7fc00000) : x.kind ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.ldo + (int64_t)head * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (x.n > 0) {
+            tmem_ld_x32(o_at + c, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+          if (live && x.kind) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) slot[(int64_t)(c + k) * p.slot_rows] = __uint_as_float(o[k]) * f;
+          } else if (live) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[k + e]) * f;
+              store8(out + c + k, v);
+            }
+          }
+          __syncwarp();
+        }
+        if (live && x.kind) {
+          slot[(int64_t)D * p.slot_rows] = big;
+          slot[(int64_t)(D + 1) * p.slot_rows] = l;
+        } else if (live && a.lse) {
+          a.lse[token * a.q_heads + head] = l == 0.f ? -INFINITY : (big + log2f(l) - (E4M3 ? kUpBits : 0.f)) * kLn2;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) free_item();
+      tiles += x.n;
+      if (active && x.n > 0) mine_t += x.n, ++taken;
+      ++it;
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    if (warp == 8) {
+      // ------------------------------------------------------------- products
+      if (lane == 0) {
+        constexpr uint32_t id_qk = idesc_of(!E4M3, false, TILE), id_pv = idesc_of(!E4M3, true, D);
+        const uint32_t base = smem_u32(smem);
+        int tiles = 0, count[2] = {0, 0}, seen_q[2] = {0, 0};  // key tiles, products of a query tile, Q tiles consumed
+        uint64_t *k_ready = E4M3 ? bars.k_ready : bars.k_full;
+        // S of query tile t with key tile `kt` (of all), the g-th of this query tile
+        const auto qk = [&](int t, int kt, int g, bool first, bool last, bool last_q) {
+          const int s = kt % ST, buf = SB == 2 ? g & 1 : 0;
+          if (first && !wait_on(&k_ready[s], (uint32_t)(kt / ST) & 1u, a.err)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t qd = sdesc_sw128(base + t * C::kQ + (k / 4) * 128 * 128 + (k % 4) * 32, 1024);
+            const uint64_t kd = sdesc_sw128(base + C::kKAt + s * C::kSide + (k / 4) * TILE * 128 + (k % 4) * 32, 1024);
+            tc_mma_f16(tmem + t * C::kSCols + buf * TILE, qd, kd, id_qk, k != 0);
+          }
+          tc_commit(&bars.s_full[t][buf]);
+          if (last) tc_commit(&bars.k_empty[s]);
+          if (last_q) tc_commit(&bars.q_empty[t]);
+          return true;
+        };
+        const auto pv = [&](int t, int kt, int g, bool first, bool last, bool fresh) {
+          const int s = kt % ST, buf = SB == 2 ? g & 1 : 0;
+          if (first && !wait_on(&bars.v_ready[s], (uint32_t)(kt / ST) & 1u, a.err)) return false;
+          if (!wait_on(&bars.p_full[t][buf], (uint32_t)(SB == 2 ? g >> 1 : g) & 1u, a.err)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < TILE / 16; ++k) {
+            const uint64_t vd = sdesc_v(base + C::kVAt + s * C::kSide + k * 16 * 128, TILE * 128);
+            tc_mma_ts(tmem + C::kOCol + t * D, tmem + t * C::kSCols + buf * TILE + k * 8, vd, id_pv, !fresh || k != 0);
+          }
+          tc_commit(&bars.o_done[t]);
+          if (last) tc_commit(&bars.v_empty[s]);
+          return true;
+        };
+        const auto start = [&](const Item &x, int kt) {  // the item's first scores
+          const int act = x.rows > 128 ? 2 : 1;
+          for (int t = 0; t < act; ++t) {
+            if (!wait_on(&bars.q_full[t], (uint32_t)seen_q[t]++ & 1u, a.err)) return false;
+            if (!qk(t, kt, count[t], t == 0, t == act - 1, x.n == 1)) return false;
+          }
+          return true;
+        };
+        Item x, y;
+        const auto next_work = [&](Item &z) {  // the next item that has tiles
+          while (take_item(z, wait_on(&bars.item_full[it % kRing], (uint32_t)(it / kRing) & 1u, a.err))) {
+            if (z.n > 0) return true;
+            free_item();
+            ++it;
+          }
+          return false;
+        };
+        bool more = next_work(x);
+        if (more) ok = start(x, tiles);
+        while (more && ok) {
+          const int act = x.rows > 128 ? 2 : 1;
+          for (int j = 0; j < x.n && ok; ++j) {
+            // with two score buffers the next scores come before this tile's values
+            if (SB == 2 && j + 1 < x.n) ok = qk(0, tiles + j + 1, count[0] + j + 1, true, true, j + 2 == x.n);
+            for (int t = 0; t < act && ok; ++t) {
+              ok = pv(t, tiles + j, count[t] + j, t == 0, t == act - 1, j == 0);
+              if (SB == 1 && ok && j + 1 < x.n)
+                ok = qk(t, tiles + j + 1, count[t] + j + 1, t == 0, t == act - 1, j + 2 == x.n);
+            }
+          }
+          if (!ok) break;
+          for (int t = 0; t < act; ++t) count[t] += x.n;
+          tiles += x.n;
+          free_item();
+          ++it;
+          more = next_work(y);
+          if (more) ok = start(y, tiles);
+          x = y;
+        }
+      }
+    } else if (warp == 9) {
+      // ----------------------------------------------- work list, copies of K and V
+      int tiles = 0, made = 0;
+      const auto put = [&](const Item &x) {
+        if (!warp_wait(&bars.item_empty[made % kRing], ((uint32_t)(made / kRing) & 1u) ^ 1u, a.err)) return false;
+        if (lane == 0) {
+          items[made % kRing] = x;
+          mbar_arrive(&bars.item_full[made % kRing]);
+        }
+        __syncwarp();
+        ++made;
+        return true;
+      };
+      int4 open = make_int4(-1, 0, 0, 0);  // the item that this CTA starts and does not end
+      int open_rows = 0;
+      if (u0 < u1) {
+        // the request and the place in it of unit u0
+        int lo = 0, hi = kThreads - 1;  // the first thread whose inclusive sum exceeds u0
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (sums[mid] > u0) hi = mid;
+          else lo = mid + 1;
+        }
+        int64_t at = lo ? sums[lo - 1] : 0;  // units before the request
+        bool ignore = false;
+        for (int r = lo * per; r < a.n && at < u1 && ok; ++r) {
+          const Req q = request(p, r, ignore);
+          const int blocks = (q.rows + ROWS - 1) / ROWS;
+          if (!blocks) continue;
+          // units of a key head: lanes take blocks in turn
+          int64_t unit = 0;
+          for (int b = lane; b < blocks; b += 32) unit += block_cost<TILE, ROWS>(p, q, b);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) unit += __shfl_xor_sync(0xffffffffu, unit, o);
+          if (at + unit * a.kv_heads <= u0) {
+            at += unit * a.kv_heads;
+            continue;
+          }
+          int head = at < u0 ? (int)((u0 - at) / unit) : 0;
+          int64_t u = at + head * unit;  // units before the key head
+          for (; head < a.kv_heads && u < u1 && ok; ++head) {
+            for (int b0 = 0; b0 < blocks && u < u1 && ok; b0 += 32) {
+              // the costs of 32 blocks, and the units before each
+              const int cost = b0 + lane < blocks ? block_cost<TILE, ROWS>(p, q, b0 + lane) : 0;
+              int64_t upto = cost;
+#pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+              }
+              const int64_t before = u + upto - cost;
+              unsigned todo = __ballot_sync(0xffffffffu, cost && before + cost > u0 && before < u1);
+              while (todo && ok) {
+                const int src = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const int64_t ub = __shfl_sync(0xffffffffu, before, src);
+                Item x;
+                x.r = r, x.head = head, x.row0 = (b0 + src) * ROWS, x.rows = min(ROWS, q.rows - x.row0);
+                x.tok0 = q.tok0, x.pos0 = q.pos0;
+                int t0, t1;
+                tiles_of<TILE>(p, q, x.row0, x.rows, t0, t1);
+                const int nt = t1 - t0;
+                // tile k of the item is unit ub + kItemCost + k
+                const int ta = (int)min(max(u0 - ub - kItemCost, (int64_t)0), (int64_t)nt), tb = (int)min(max(u1 - ub - kItemCost, (int64_t)0), (int64_t)nt);
+                if (nt == 0 ? ub < u0 : ta == tb) continue;  // another CTA's
+                const int first = q.pos0 + (int)p.by_group.div(x.row0), last = q.pos0 + (int)p.by_group.div(x.row0 + x.rows - 1);
+                x.lo = first_seen(a, first), x.hi = end_seen(a, last);
+                x.full_lo = first_seen(a, last), x.full_hi = end_seen(a, first);
+                x.t0 = t0 + ta, x.n = tb - ta;
+                x.kind = x.n == nt ? 0 : ta == 0 ? 1 : 2;
+                if (x.kind == 1) {
+                  open = make_int4(r, head, x.row0, (int)((ub + kItemCost + nt - 1) / run));
+                  open_rows = x.rows;
+                }
+                if (!(ok = put(x))) break;
+                // ---- its tiles.  Lanes hold 32 table entries from page tb0 on, and the 32 after them.
+                const int boxes = TILE >> p.box_shift;
+                int tb0 = (x.t0 * TILE) >> p.page_shift;
+                const auto table_at = [&](int i) { return i < a.max_pages ? a.table[r * a.ldt + i] : -1; };
+                int entry = table_at(tb0 + lane), entry2 = table_at(tb0 + 32 + lane);
+                for (int j = 0; j < x.n; ++j, ++tiles) {
+                  const int s = tiles % ST;
+                  const uint32_t ph = ((uint32_t)(tiles / ST) & 1u) ^ 1u;
+                  const int pos = (x.t0 + j) * TILE;
+                  while (((pos + TILE - 1) >> p.page_shift) - tb0 >= 64) {
+                    tb0 += 32;
+                    entry = entry2;
+                    entry2 = table_at(tb0 + 32 + lane);
+                  }
+                  // box `lane % boxes` of the tile, its page; the lanes after the first `boxes` take the other parts
+                  const int b = lane & (boxes - 1), box_pos = pos + (b << p.box_shift), i = (box_pos >> p.page_shift) - tb0;
+                  const int e1 = __shfl_sync(0xffffffffu, entry, i & 31), e2 = __shfl_sync(0xffffffffu, entry2, i & 31);
+                  const int page = i < 32 ? e1 : e2;
+                  const bool wanted = box_pos < x.hi && box_pos + p.box_rows > x.lo;
+                  const bool there = wanted && page >= 0 && page < a.n_pages;
+                  const unsigned need = __ballot_sync(0xffffffffu, wanted && lane < boxes), have = __ballot_sync(0xffffffffu, there && lane < boxes);
+                  if (need != have && lane == 0) set_device_error(a.err, kDevErrBadPage);
+                  const uint32_t box_bytes = (uint32_t)p.box_rows * D * C::kEs, loaded = __popc(have) * box_bytes;
+                  const int in_page = box_pos & (a.page - 1);
+                  if (!(ok = warp_wait(&bars.k_empty[s], ph, a.err))) break;
+                  if (lane == 0) mbar_arrive_expect_tx(&bars.k_full[s], loaded);
+                  __syncwarp();
+                  uint8_t *k = smem + C::kKAt + s * C::kSide, *v = smem + C::kVAt + s * C::kSide;
+                  if (E4M3) k += C::kSide - C::kRaw, v += C::kSide - C::kRaw;
+                  const auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar) {
+                    if (E4M3) {
+                      if (there && lane < boxes) tma_load_5d(dst + (b << p.box_shift) * D, map, bar, 0, in_page, 0, x.head, page);
+                    } else {
+                      for (int part = lane / boxes; part < C::kParts; part += 32 / boxes)
+                        if (there) tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * 128, map, bar, 0, in_page, part, x.head, page);
+                    }
+                  };
+                  copy(k, &kmap, &bars.k_full[s]);
+                  if (!(ok = warp_wait(&bars.v_empty[s], ph, a.err))) break;
+                  if (lane == 0) {
+                    // 16-token pieces that are absent
+                    uint32_t gone = 0;
+                    for (unsigned w = need & ~have; w; w &= w - 1) {
+                      const int at16 = (__ffs(w) - 1) << (p.box_shift - 4);
+                      gone |= ((p.box_rows >> 4 == 32 ? 0u : 1u << (p.box_rows >> 4)) - 1u) << at16;
+                    }
+                    vinfo[s].absent = gone;
+                    mbar_arrive_expect_tx(&bars.v_full[s], loaded + (E4M3 ? __popc(have) * p.box_rows * 8 : 0));
+                  }
+                  __syncwarp();
+                  copy(v, &vmap, &bars.v_full[s]);
+                  if (E4M3 && there && lane < boxes) {
+                    float *ks = reinterpret_cast<float *>(smem + C::kScaleAt) + s * 3 * TILE + (b << p.box_shift);
+                    const int64_t from = ((int64_t)page * a.kv_heads + x.head) * a.page + in_page;
+                    bulk_load(ks, a.scale[0] + from, p.box_rows * 4, &bars.v_full[s]);
+                    bulk_load(ks + TILE, a.scale[1] + from, p.box_rows * 4, &bars.v_full[s]);
+                  }
+                  __syncwarp();
+                }
+              }
+              u += __shfl_sync(0xffffffffu, upto, 31);
+            }
+          }
+          at += unit * a.kv_heads;
+        }
+      }
+      if (lane == 0) {
+        p.desc[2 * blockIdx.x] = open;
+        p.desc[2 * blockIdx.x + 1] = make_int4(open_rows, 0, 0, 0);
+      }
+      if (ok) {
+        Item end;
+        end.rows = -1;
+        ok = put(end);
+      }
+      // copies in flight land before the CTA may end
+      const int left = min(tiles, ST);
+      for (int j = tiles - left; !ok && j < tiles; ++j) {
+        wait_on(&bars.k_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
+        wait_on(&bars.v_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
+      }
+    } else {
+      // ------------------------------------------------------------------- Q
+      // Each of the two warps takes 64 rows of a query tile.
+      int count[2] = {0, 0};
+      Item x;
+      while (ok && next_item(x)) {
+        for (int t = 0; t < NQ && x.n > 0 && x.rows > 128 * t && ok; ++t) {
+          const int c = count[t]++;
+          if (!(ok = warp_wait(&bars.q_empty[t], ((uint32_t)c & 1u) ^ 1u, a.err))) break;
+          uint8_t *dst = smem + t * C::kQ;
+          constexpr int CH = D / 8;  // 16-byte pieces of a row
+          const int first = 64 * (warp - 10);
+#pragma unroll 4
+          for (int i = lane; i < 64 * CH; i += 32) {
+            const int row = first + i / CH, ch = i % CH, rr = 128 * t + row;
+            const bool in = rr < x.rows;
+            const int rw = x.row0 + (in ? rr : 0), tok = (int)p.by_group.div(rw);
+            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)x.tok0 + tok) * a.ldq +
+                                       (int64_t)(x.head * p.group + (rw - tok * p.group)) * a.ldq_head + ch * 8;
+            cp_async16(dst + (ch / 8) * 128 * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src, in ? 16 : 0);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          if (E4M3) {
+            // rows to fp16, times a power of two that brings their largest value to 2^14..2^15
+            __syncwarp();
+            for (int row = first + lane; row < first + 64; row += 32) {
+              uint8_t *r0 = dst + row * 128;
+              uint32_t top = 0;
+              for (int ch = 0; ch < CH; ++ch) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(r0 + (ch / 8) * 128 * 128 + (((ch & 7) ^ (row & 7)) << 4));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max(w[e] >> 16 & 0x7fffu, w[e] & 0x7fffu));
+              }
+              const int ex = (int)(top >> 7) - 127;         // of the largest value
+              const int up = min(max(14 - ex, -113), 126);  // factor 2^up
+              const float f = __int_as_float((up + 127) << 23);
+              for (int ch = 0; ch < CH; ++ch) {
+                uint4 *at = reinterpret_cast<uint4 *>(r0 + (ch / 8) * 128 * 128 + (((ch & 7) ^ (row & 7)) << 4));
+                const uint4 v = *at;
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+              q_scale[c & 1][128 * t + row] = __int_as_float((127 - up) << 23);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.q_full[t]);
+        }
+        if (lane == 0) free_item();
+        ++it;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    // ---------------------------------------------------------------- prepare
+    const int th = tid - 384;  // 0..127
+    int tiles = 0;
+    Item x;
+    for (;;) {
+      const bool more = next_item(x);
+      if (!group_and(1, ok) || !more) break;
+      for (int j = 0; j < x.n; ++j, ++tiles) {
+        const int s = tiles % ST;
+        const uint32_t ph = (uint32_t)(tiles / ST) & 1u;
+        constexpr int RC = D / 16, PER = C::kRaw / 16 / 128;  // e4m3: 16-byte pieces of a row, and of a thread
+        // 16 e4m3 values of a token to 16 fp16 values at their swizzled place
+        const auto place = [&](uint8_t *side, int row, int ch, const uint4 &v) {
+          const uint2 a0 = e4m3x4_f16(v.x), a1 = e4m3x4_f16(v.y), a2 = e4m3x4_f16(v.z), a3 = e4m3x4_f16(v.w);
+          uint8_t *to = side + (ch / 4) * TILE * 128 + row * 128;
+          const uint4 w0 = make_uint4(a0.x, a0.y, a1.x, a1.y), w1 = make_uint4(a2.x, a2.y, a3.x, a3.y);
+          // pieces 0..3 of a row and 4..7 lie in the same banks: the latter write their second half first
+          const int sw = (ch >> 2) & 1, c0 = 2 * (ch & 3);
+          *reinterpret_cast<uint4 *>(to + (((c0 + sw) ^ (row & 7)) << 4)) = sw ? w1 : w0;
+          *reinterpret_cast<uint4 *>(to + (((c0 + 1 - sw) ^ (row & 7)) << 4)) = sw ? w0 : w1;
+        };
+        if (E4M3) {
+          ok = warp_wait(&bars.k_full[s], ph, a.err);
+          uint8_t *k = smem + C::kKAt + s * C::kSide;
+          uint4 raw[PER];
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) raw[i] = *reinterpret_cast<const uint4 *>(k + C::kSide - C::kRaw + (th + 128 * i) * 16);
+          }
+          if (!(ok = group_and(1, ok))) break;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) place(k, (th + 128 * i) / RC, (th + 128 * i) % RC, raw[i]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.k_ready[s]);
+        }
+        ok = warp_wait(&bars.v_full[s], ph, a.err);
+        uint8_t *v = smem + C::kVAt + s * C::kSide;
+        const int pos = (x.t0 + j) * TILE;
+        const uint32_t absent = vinfo[s].absent;
+        // tokens that some row does not see, beside those that all rows see
+        const bool partial = pos < x.full_lo || pos + TILE > x.full_hi || absent;
+        const auto dead = [&](int row) { return pos + row < x.lo || pos + row >= x.hi || (absent >> (row / 16) & 1u); };
+        uint4 raw[E4M3 ? PER : 1];
+        if (E4M3 && ok) {
+#pragma unroll
+          for (int i = 0; i < PER; ++i) raw[i] = *reinterpret_cast<const uint4 *>(v + C::kSide - C::kRaw + (th + 128 * i) * 16);
+        }
+        if (th < 4) vinfo[s].bad[th] = 0;
+        if (E4M3 && th == 4) vinfo[s].e_min = 255, vinfo[s].e_max = 0;
+        if (!(ok = group_and(1, ok))) break;
+        if (E4M3) {
+          if (th < TILE) {
+            float *ks = reinterpret_cast<float *>(smem + C::kScaleAt) + s * 3 * TILE + th;
+            float sv = fmaxf(ks[TILE], 1.2621774483536189e-29f);  // 2^-96
+            if (partial) {
+              const bool gone = dead(th), odd = !(ks[0] - ks[0] == 0.f) || !(ks[TILE] - ks[TILE] == 0.f);
+              if (!gone && odd) atomicOr(&vinfo[s].bad[th >> 5], 1u << (th & 31));
+              if (gone || odd) ks[0] = 1.f, sv = 0.f;
+            }
+            const uint32_t e = __float_as_uint(sv) >> 23, e_hi = __reduce_max_sync(0xffffffffu, e), e_lo = __reduce_min_sync(0xffffffffu, e ? e : 255u);
+            if (lane == 0) atomicMax(&vinfo[s].e_max, e_hi), atomicMin(&vinfo[s].e_min, e_lo);
+            if (e == 0) sv = 1.f;
+            ks[TILE] = log2f(sv);
+            ks[2 * TILE] = 1.f / sv;
+          }
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int row = (th + 128 * i) / RC, ch = (th + 128 * i) % RC;
+            if (partial) {
+              const uint4 w = raw[i];
+              const auto nan4 = [](uint32_t y) { return __vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu); };
+              const bool gone = dead(row);
+              const bool odd = (nan4(w.x) | nan4(w.y) | nan4(w.z) | nan4(w.w)) != 0;
+              if (!gone && odd) atomicOr(&vinfo[s].bad[row >> 5], 1u << (row & 31));
+              if (gone || odd) raw[i] = make_uint4(0, 0, 0, 0);
+            }
+            place(v, row, ch, raw[i]);
+          }
+          fence_proxy_async_smem();
+        } else if (partial) {
+          constexpr int CH = D / 8;
+          for (int i = th; i < TILE * CH; i += 128) {
+            const int row = i / CH, ch = i % CH;
+            uint4 *at = reinterpret_cast<uint4 *>(v + (ch / 8) * TILE * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            const uint4 w = *at;
+            const auto odd2 = [](uint32_t y) { return (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u; };
+            const bool gone = dead(row), odd = odd2(w.x) || odd2(w.y) || odd2(w.z) || odd2(w.w);
+            if (!gone && odd) atomicOr(&vinfo[s].bad[row >> 5], 1u << (row & 31));
+            if (gone || odd) *at = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.v_ready[s]);
+      }
+      if (!ok) break;
+      if (lane == 0) free_item();
+      ++it;
+    }
+  }
+
+  // Every warp comes here, whatever happened to it.
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// Joins the pieces of the items that several CTAs share: that of the CTA that
+// starts the item (slot 1) and of all after it up to the last (slot 0).  A lane
+// owns a row, a warp 8 of its values, so all loads are of 128 contiguous bytes.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(D / 8 * 32) chunk_join_kernel(const __grid_constant__ Params p) {
+  const AttnArgs &a = p.a;
+  const int lane = threadIdx.x & 31, c0 = threadIdx.x / 32 * 8, cta = blockIdx.x;
+  grid_dependency_wait();
+  const int4 d = p.desc[2 * cta];
+  const int rows = p.desc[2 * cta + 1].x;
+  const int row_t = blockIdx.y * 32 + lane;
+  if (d.x < 0 || (int)blockIdx.y * 32 >= rows) return;
+  float m = -INFINITY, l = 0.f, o[8] = {};
+  const int64_t size = (int64_t)(D + 2) * p.slot_rows;
+  for (int c = cta; c <= d.w; ++c) {
+    const float *slot = p.slots + (2 * (int64_t)c + (c == cta)) * size + row_t;
+    const float pm = slot[(int64_t)D * p.slot_rows], pl = slot[(int64_t)(D + 1) * p.slot_rows];
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = slot[(int64_t)(c0 + i) * p.slot_rows];
+    const float mn = fmaxf(m, pm), f = m == mn ? 1.f : ex2(m - mn), g = pm == mn ? 1.f : ex2(pm - mn);
+    m = mn;
+    l = l * f + pl * g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * f + v[i] * g;
+  }
+  if (row_t >= rows) return;
+  bool ignore = false;
+  const Req q = request(p, d.x, ignore);
+  const int row = d.z + row_t, tok = (int)p.by_group.div(row), head = d.y * p.group + (row - tok * p.group);
+  const int64_t token = (int64_t)q.tok0 + tok;
+  const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = l == 0.f && o[i] == o[i] ? 0.f : o[i] * f;
+  store8(static_cast<__nv_bfloat16 *>(a.out) + token * a.ldo + (int64_t)head * D + c0, o);
+  if (c0 == 0 && a.lse)
+    a.lse[token * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l) - (E4M3 ? kUpBits : 0.f)) * kLn2;
+}
+
+int slot_rows(int64_t tokens, int group, int dim) {
+  const int64_t rows = (tokens * group + 31) / 32 * 32, most = dim == 256 ? 128 : 256;
+  return (int)(rows < most ? rows : most);
+}
+size_t desc_bytes() { return (size_t)kMaxSms * 2 * sizeof(int4); }
+
+template <int D, bool E4M3>
+cudaError_t launch_cfg(Params &p, cudaStream_t stream) {
+  using C = Cfg<D, E4M3>;
+  const AttnArgs &a = p.a;
+  static SmemLimit limit;
+  cudaError_t e = raise_smem_limit(limit, chunk_kernel<D, E4M3>, C::kSmem);
+  if (e != cudaSuccess) return e;
+  p.box_rows = a.page < C::kTile ? a.page : C::kTile;
+  p.box_shift = 31 - __builtin_clz((unsigned)p.box_rows);
+  p.page_shift = 31 - __builtin_clz((unsigned)a.page);
+  // (values of a part of a row, token, part, head, page): a bf16 row in 128-byte
+  // parts, swizzled; an e4m3 row in one
+  const int inner = E4M3 ? D : 64, parts = E4M3 ? 1 : C::kParts;
+  const uint64_t dims[5] = {(uint64_t)inner, (uint64_t)a.page, (uint64_t)parts, (uint64_t)a.kv_heads, (uint64_t)a.n_pages};
+  const uint64_t strides[4] = {(uint64_t)a.token_stride * C::kEs, (uint64_t)inner * C::kEs, (uint64_t)a.head_stride * C::kEs,
+                               (uint64_t)a.page_stride * C::kEs};
+  const uint32_t box[5] = {(uint32_t)inner, (uint32_t)p.box_rows, 1, 1, 1};
+  CUtensorMap maps[2];
+  for (int i = 0; i < 2; ++i)
+    if (encode_tiled(&maps[i], E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                     const_cast<void *>(a.cache[i]), dims, strides, box,
+                     E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  const int sms = device_facts()->sm_count, grid = sms < kMaxSms ? sms : kMaxSms;
+  chunk_kernel<D, E4M3><<<grid, kThreads, C::kSmem, stream>>>(p, maps[0], maps[1]);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.slot_rows / 32));
+  cfg.blockDim = dim3(D / 8 * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, E4M3>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+size_t paged_attn_chunk_workspace_size(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t dim) {
+  const int group = q_heads / (kv_heads < q_heads ? kv_heads : q_heads);
+  return desc_bytes() + (size_t)kMaxSms * 2 * (dim + 2) * slot_rows(tokens, group, dim) * 4;
+}
+
+cudaError_t launch_paged_attn_chunk(const AttnArgs &a, int64_t tokens, const int64_t *cu, cudaStream_t s) {
+  const int group = a.q_heads / a.kv_heads;
+  Params p = {a, tokens, cu, group, FastDiv(group), 0, 0, 0, slot_rows(tokens, group, a.dim), static_cast<int4 *>(a.workspace),
+              reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + desc_bytes())};
+  const bool e = a.cache_dtype == Q4K_DTYPE_E4M3;
+  if (a.dim == 64) return e ? launch_cfg<64, true>(p, s) : launch_cfg<64, false>(p, s);
+  if (a.dim == 128) return e ? launch_cfg<128, true>(p, s) : launch_cfg<128, false>(p, s);
+  return e ? launch_cfg<256, true>(p, s) : launch_cfg<256, false>(p, s);
+}
+
+}  // namespace q4k

@@ -63,6 +63,10 @@ struct AttnArgs {
 };
 size_t paged_attn_workspace_size(int32_t n, int32_t q_heads, int32_t kv_heads, int32_t dim);
 cudaError_t launch_paged_attn(const AttnArgs &a, cudaStream_t stream);
+// Chunks: q, out and lse of `tokens` tokens, request r's are cu[r] .. cu[r + 1] - 1.
+size_t paged_attn_chunk_workspace_size(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t dim);
+cudaError_t launch_paged_attn_chunk(const AttnArgs &a, int64_t tokens, const int64_t *cu,
+                                    cudaStream_t stream);
 cudaError_t launch_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
                           const float *u, const float *temperature, const int32_t *top_k,
                           const float *top_p, const float *min_p, int32_t *token, float *logp,

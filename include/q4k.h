@@ -599,6 +599,60 @@ int q4k_paged_attn(const void *q, int64_t ldq, int64_t ldq_head, int32_t n, int3
                    float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * q4k_paged_attn_chunk -- attention of each request's new tokens, one or many,
+ * over the cache.
+ * Request r's m = cu[r+1] - cu[r] >= 0 new tokens are tokens cu[r] .. cu[r+1] - 1
+ * of q and out, and the last m of the lens[r] tokens that the cache holds of it
+ * (their keys and values have been written before; lens and cu are as
+ * q4k_kv_plan gives them).  Its token i stands at position p = lens[r] - m + i
+ * and sees the tokens max(0, p + 1 - window) <= j <= p (window 0: 0 <= j <= p).
+ * For each of them and query head h, with key head h / (q_heads / kv_heads):
+ *     z_j = softmax_scale * q . k_j,  lse = ln sum_j e^z_j,
+ *     out = sum_j e^(z_j - lse) v_j                    (bf16, rounded once)
+ * A token that sees none (p < 0, as where the plan served no pages and lens is
+ * what it was before) gets zeros and lse = -infinity.  Rows of out and lse past
+ * cu[n] are left as they are.  cu has to rise from a value >= 0 to one <= tokens;
+ * a request for which it does not has no tokens and sets Q4K_DEVERR_BAD_PAGE.
+ * What a token does not see does not touch its result, whatever it holds (NaN
+ * and infinities included): neither rows that no request's tokens refer to nor
+ * the request's own later tokens.  A page outside [0, n_pages) counts as
+ * absent, and so do tokens past max_pages * page_size; both set
+ * Q4K_DEVERR_BAD_PAGE.
+ * Scores, softmax statistics and sums are fp32.  For a bf16 cache the softmax
+ * weights enter the products as one bf16 term (8 significant bits, as the
+ * result has), for an e4m3 cache as one fp16 term of the weight times the row's
+ * scale: 11 bits down to 2^-21 of the largest such term, an error of at most
+ * 2^-32 of it below.  q is exact for a bf16 cache; for an e4m3 cache it enters
+ * as fp16 times a power of two per row: exact down to 2^-31 of the row's largest
+ * value, to within 2^-39 of it below.
+ * Values that are not finite in a row that a token sees show in the token's
+ * result; one of V may do so as NaN in all of it.
+ *   q       device, bf16, element (t, h, d) at t * ldq + h * ldq_head + d;
+ *           16-byte aligned, strides multiples of 8
+ *   tokens  rows of q and out
+ *   cu      device, n + 1 int64
+ *   caches, scales, table, lens  as q4k_paged_attn
+ *   out     device, bf16, row stride ldo >= q_heads * dim, heads contiguous;
+ *           16-byte aligned, ldo a multiple of 8; may not overlap q
+ *   lse     device, tokens x q_heads fp32, or NULL
+ *   workspace  device, >= q4k_paged_attn_chunk_workspace_size(...) bytes,
+ *           16-byte aligned; nothing in it is kept between calls
+ * Limits: as q4k_paged_attn, and tokens * q_heads < 2^31.
+ * Errors: NULL, SHAPE, ALIGN, WORKSPACE, DEVICE, MEMORY, CUDA.
+ */
+size_t q4k_paged_attn_chunk_workspace_size(int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                           int32_t dim);
+int q4k_paged_attn_chunk(const void *q, int64_t ldq, int64_t ldq_head, int64_t tokens,
+                         const int64_t *cu, int32_t n, int32_t q_heads, int32_t kv_heads,
+                         int32_t dim, const void *k_cache, const void *v_cache, int cache_dtype,
+                         int64_t n_pages, int32_t page_size, int64_t page_stride,
+                         int64_t head_stride, int64_t token_stride, const float *k_scale,
+                         const float *v_scale, const int32_t *table, int64_t ldt,
+                         int32_t max_pages, const int32_t *lens, float softmax_scale,
+                         int32_t window, void *out, int64_t ldo, float *lse, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
  * q4k_add_rmsnorm -- residual addition and root-mean-square norm.
  *     h = x + residual;  residual_out = h;
  *     y = h * gamma / sqrt((1/H) sum_i h_i^2 + eps)
