@@ -33,8 +33,9 @@ EXPORTS = ("q4k_abi_version", "q4k_status_str", "q4k_dequant", "q4k_gemv", "q4k_
            "q4k_moe_gemv_ex", "q4k_moe_gemv_noalloc", "q4k_moe_prefill",
            "q4k_moe_prefill_workspace_size",
            "q4k_kv_plan", "q4k_kv_write", "q4k_paged_attn", "q4k_paged_attn_workspace_size",
+           "q4k_rope_steps", "q4k_rope", "q4k_rope_kv_write",
            "q4k_paged_attn_chunk", "q4k_paged_attn_chunk_workspace_size",
-           "q4k_add_rmsnorm", "q4k_sample",
+           "q4k_add_rmsnorm", "q4k_sample", "q4k_logprobs",
            "q4k_get_device_error", "q4k_selftest_wait_timeout")
 Q4K_DTYPE_FP32, Q4K_DTYPE_BF16, Q4K_DTYPE_E4M3 = 0, 1, 2
 Q4K_KV_OK, Q4K_KV_NO_PAGES, Q4K_KV_BAD_LENGTH, Q4K_KV_NO_SLOTS = 0, 1, 2, 3
@@ -117,6 +118,18 @@ def lib() -> ctypes.CDLL:
         L.q4k_kv_write.restype = ctypes.c_int
         L.q4k_kv_write.argtypes = [P, P, ctypes.c_int, I64, I64, P, I64, I32, I32, P, P, ctypes.c_int,
                                    I64, I32, I64, I64, I64, P, P, P]
+        F64 = ctypes.c_double
+        L.q4k_rope_steps.restype = ctypes.c_int
+        L.q4k_rope_steps.argtypes = [I32, F64, F64, I64, F64, F64, P, P, ctypes.POINTER(F32)]
+        L.q4k_rope.restype = ctypes.c_int
+        L.q4k_rope.argtypes = [P, ctypes.c_int, I64, I64, I64, I32, I32, P, F32, P, P, I32, ctypes.c_int, F32,
+                               P, ctypes.c_int, I64, I64, P]
+        L.q4k_rope_kv_write.restype = ctypes.c_int
+        L.q4k_rope_kv_write.argtypes = [P, I64, I64, P, P, I64, I64, ctypes.c_int, I64, I32, I32, I32, P, P, F32,
+                                        P, P, P, I32, ctypes.c_int, F32, P, I64, I64, P, P, ctypes.c_int,
+                                        I64, I32, I64, I64, I64, P, P, P]
+        L.q4k_logprobs.restype = ctypes.c_int
+        L.q4k_logprobs.argtypes = [P, ctypes.c_int, I64, I64, I64, P, I32, P, P, P, P, P, P]
         L.q4k_paged_attn_chunk_workspace_size.restype = SZ
         L.q4k_paged_attn_chunk_workspace_size.argtypes = [I64, I32, I32, I32]
         L.q4k_paged_attn_chunk.restype = ctypes.c_int
@@ -516,6 +529,103 @@ def q4k_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache:
         _call_stream(stream, k)), "q4k_kv_write")
 
 
+def q4k_rope_steps(rot_dim: int, base: float, factor: float = 1.0, original: int = 0,
+                   beta_fast: float = 32.0, beta_slow: float = 1.0, factors=None):
+    """(steps, amplitude): the table of frequencies of q4k_rope and q4k_rope_kv_write, an int64 tensor
+    [rot_dim / 2] on the host (turns per position in units of 2^-64; move it to the device once), and
+    the amplitude to give them.  Positions are scaled by `factor`, with `original` > 0 only those of
+    slow pairs; factors [rot_dim / 2] fp32 (host) divide the frequencies one by one."""
+    steps = torch.empty(max(rot_dim, 0) // 2, dtype=_I64)
+    if factors is not None and (factors.is_cuda or factors.dtype is not _F32 or factors.shape != steps.shape):
+        _refuse("factors", factors)
+    factors = None if factors is None else factors.contiguous()
+    amplitude = ctypes.c_float()
+    _check((_lib or lib()).q4k_rope_steps(
+        rot_dim, base, factor, original, beta_fast, beta_slow, _ptr(factors),
+        steps.data_ptr() or ctypes.addressof(amplitude), ctypes.byref(amplitude)), "q4k_rope_steps")
+    return steps, amplitude.value
+
+
+def _heads3(what: str, t: torch.Tensor, tokens: int, dim: int):
+    if len(t.shape) != 3 or t.shape[0] != tokens or t.shape[2] != dim:
+        _refuse(what, t)
+    return _outer_strides(t)
+
+
+def q4k_rope(x: torch.Tensor, pos: torch.Tensor, steps: torch.Tensor, gamma=None, eps: float = 1e-6,
+             interleaved: bool = False, amplitude: float = 1.0, out=None, out_dtype=torch.bfloat16,
+             stream=None) -> torch.Tensor:
+    """Norm of each head (where gamma [dim] fp32 is given) and rotation of its first 2 * len(steps)
+    values by the positions pos [tokens] int32; x [tokens, heads, dim] fp32 or bf16, steps as
+    q4k_rope_steps gives them, on the device.  Returns out, bf16 or fp32 (out may be x itself); tokens
+    with a negative position are left alone."""
+    dtype = x.dtype
+    if len(x.shape) != 3 or (dtype is not _F32 and dtype is not _BF16):
+        _refuse("x", x)
+    tokens, heads, dim = x.shape
+    ld = _outer_strides(x)
+    if out is None:
+        if out_dtype is not _BF16 and out_dtype is not _F32:
+            raise Q4KError(2, f"out_dtype is {out_dtype}")
+        out, ldo = _empty((tokens, heads, dim), out_dtype, x, stream), (heads * dim, dim)
+    else:
+        out_dtype = out.dtype
+        if out.shape != x.shape or (out_dtype is not _F32 and out_dtype is not _BF16):
+            _refuse("out", out)
+        ldo = _outer_strides(out)
+    half = steps.numel()
+    if 2 * half > dim:
+        _refuse("steps", steps)
+    _check((_lib or lib()).q4k_rope(
+        x.data_ptr(), 1 if dtype is _BF16 else 0, ld[0], ld[1], tokens, heads, dim,
+        None if gamma is None else _vec("gamma", gamma, dim, _F32), eps, _vec("pos", pos, tokens, _I32),
+        _vec("steps", steps, half, _I64), 2 * half, 1 if interleaved else 0, amplitude, out.data_ptr(),
+        1 if out_dtype is _BF16 else 0, ldo[0], ldo[1], _call_stream(stream, x)), "q4k_rope")
+    return out
+
+
+def q4k_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                      slots: torch.Tensor, steps: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, k_scale=None, v_scale=None, q_gamma=None, k_gamma=None,
+                      eps: float = 1e-6, interleaved: bool = False, amplitude: float = 1.0, out=None,
+                      stream=None) -> torch.Tensor:
+    """q4k_rope of q [tokens, q_heads, dim] and of k [tokens, kv_heads, dim], and q4k_kv_write of these
+    keys and of v to the slots [tokens] int32 of the paged caches [pages, kv_heads, page size, dim]
+    (bf16, or e4m3 with scales), in one launch.  Returns the rotated queries [tokens, q_heads, dim]
+    bf16 (out may be q itself)."""
+    shape, strides, code, ks, vs = _caches(k_cache, v_cache, k_scale, v_scale)
+    pages, heads, page, dim = shape
+    dtype, tokens = q.dtype, slots.numel()
+    if dtype is not _F32 and dtype is not _BF16:
+        _refuse("q", q)
+    ldq = _heads3("q", q, tokens, dim)
+    if k.dtype is not dtype or k.shape[1:2] != (heads,):
+        _refuse("k", k)
+    ld = _heads3("k", k, tokens, dim)
+    if v.dtype is not dtype or v.shape != k.shape:
+        _refuse("v", v)
+    if v.stride() != k.stride() and ld != _outer_strides(v):
+        raise Q4KError(2, "k and v have different strides")
+    q_heads, half = q.shape[1], steps.numel()
+    if out is None:
+        out, ldo = _empty((tokens, q_heads, dim), _BF16, q, stream), (q_heads * dim, dim)
+    else:
+        if out.shape != q.shape or out.dtype is not _BF16:
+            _refuse("out", out)
+        ldo = _outer_strides(out)
+    if 2 * half > dim:
+        _refuse("steps", steps)
+    _check((_lib or lib()).q4k_rope_kv_write(
+        q.data_ptr(), ldq[0], ldq[1], k.data_ptr(), v.data_ptr(), ld[0], ld[1], 1 if dtype is _BF16 else 0,
+        tokens, q_heads, heads, dim, None if q_gamma is None else _vec("q_gamma", q_gamma, dim, _F32),
+        None if k_gamma is None else _vec("k_gamma", k_gamma, dim, _F32), eps, _vec("pos", pos, tokens, _I32),
+        _vec("slots", slots, tokens, _I32), _vec("steps", steps, half, _I64), 2 * half,
+        1 if interleaved else 0, amplitude, out.data_ptr(), ldo[0], ldo[1], k_cache.data_ptr(),
+        v_cache.data_ptr(), code, pages, page, strides[0], strides[1], strides[2], ks, vs,
+        _call_stream(stream, q)), "q4k_rope_kv_write")
+    return out
+
+
 def q4k_paged_attn_workspace_size(n: int, q_heads: int, kv_heads: int, dim: int) -> int:
     return int(lib().q4k_paged_attn_workspace_size(n, q_heads, kv_heads, dim))
 
@@ -683,6 +793,37 @@ def q4k_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=No
         p, mp, _vec("out", out, rows, _I32), _vec("logp", logp, rows, _F32),
         _call_stream(stream, logits)), "q4k_sample")
     return out, logp
+
+
+def q4k_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, logp=None, rank=None,
+                 entropy=None, top_tokens=None, top_logp=None, stream=None):
+    """Log-probability and rank of one token per row of logits [rows, vocab] (fp32 or bf16), the rows'
+    entropy and their `top` most likely tokens; tokens [rows] int32 (-1: none).  Returns (logp [rows]
+    fp32, rank [rows] int32, entropy [rows] fp32, top_tokens [rows, top] int32, top_logp [rows, top]
+    fp32)."""
+    dtype = logits.dtype
+    if len(logits.shape) != 2 or (dtype is not _F32 and dtype is not _BF16):
+        _refuse("logits", logits)
+    if not 0 <= top <= 32:
+        raise Q4KError(2, f"top is {top}")
+    rows, vocab = logits.shape
+    ld = _rows("logits", logits, rows, vocab, dtype)
+
+    def given(what, t, shape, kind):
+        if t is None:
+            return _empty(shape, kind, logits, stream)
+        if t.dtype is not kind or t.shape != shape or not t.is_contiguous():
+            _refuse(what, t)
+        return t
+
+    logp, entropy = given("logp", logp, (rows,), _F32), given("entropy", entropy, (rows,), _F32)
+    rank = given("rank", rank, (rows,), _I32)
+    top_tokens, top_logp = given("top_tokens", top_tokens, (rows, top), _I32), given("top_logp", top_logp, (rows, top), _F32)
+    _check((_lib or lib()).q4k_logprobs(
+        logits.data_ptr(), 1 if dtype is _BF16 else 0, rows, vocab, ld, _vec("tokens", tokens, rows, _I32),
+        top, logp.data_ptr(), rank.data_ptr(), entropy.data_ptr(), top_tokens.data_ptr(),
+        top_logp.data_ptr(), _call_stream(stream, logits)), "q4k_logprobs")
+    return logp, rank, entropy, top_tokens, top_logp
 
 
 def q4k_get_device_error(stream=None) -> int:

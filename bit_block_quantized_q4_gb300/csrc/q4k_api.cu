@@ -671,6 +671,113 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
                                     static_cast<cudaStream_t>(stream)));
 }
 
+int q4k_rope_steps(int32_t rot_dim, double base, double factor, int64_t original, double beta_fast,
+                   double beta_slow, const float *factors, uint64_t *steps, float *amplitude) {
+  if (rot_dim < 0 || rot_dim > 256 || rot_dim % 2) return Q4K_ERR_SHAPE;
+  const auto finite = [](double v) { return v > 0 && v - v == 0.0; };
+  if (!finite(base) || !finite(factor) || original < 0) return Q4K_ERR_SHAPE;
+  if (original > 0 && (base == 1.0 || !finite(beta_fast) || !finite(beta_slow))) return Q4K_ERR_SHAPE;
+  if (!steps || !amplitude) return Q4K_ERR_NULL;
+  for (int i = 0; factors && i < rot_dim / 2; ++i)
+    if (!finite(factors[i])) return Q4K_ERR_SHAPE;
+  return rope_steps(rot_dim, base, factor, original, beta_fast, beta_slow, factors, steps, amplitude)
+             ? Q4K_OK
+             : Q4K_ERR_SHAPE;
+}
+
+namespace {
+// What q4k_rope and q4k_rope_kv_write share.
+int check_rope(int dtype, int64_t tokens, int32_t dim, const float *gamma, const float *gamma2, float eps,
+               int32_t rot_dim, float amplitude) {
+  if (dtype != Q4K_DTYPE_FP32 && dtype != Q4K_DTYPE_BF16) return Q4K_ERR_SHAPE;
+  if (tokens < 0 || tokens > INT32_MAX || dim <= 0 || dim > 256 || dim % 8) return Q4K_ERR_SHAPE;
+  if (rot_dim < 0 || rot_dim > dim || rot_dim % 2) return Q4K_ERR_SHAPE;
+  if ((gamma || gamma2) && (!(eps >= 0.f) || !(eps - eps == 0.f))) return Q4K_ERR_SHAPE;
+  if (!(amplitude - amplitude == 0.f)) return Q4K_ERR_SHAPE;
+  return Q4K_OK;
+}
+}  // namespace
+
+int q4k_rope(const void *x, int x_dtype, int64_t ld_token, int64_t ld_head, int64_t tokens,
+             int32_t heads, int32_t dim, const float *gamma, float eps, const int32_t *pos,
+             const uint64_t *steps, int32_t rot_dim, int interleaved, float amplitude, void *y,
+             int y_dtype, int64_t ldy_token, int64_t ldy_head, void *stream) {
+  int st = check_rope(x_dtype, tokens, dim, gamma, nullptr, eps, rot_dim, amplitude);
+  if (st != Q4K_OK) return st;
+  if ((y_dtype != Q4K_DTYPE_FP32 && y_dtype != Q4K_DTYPE_BF16) || heads <= 0 || heads > 1024 ||
+      (interleaved != 0 && interleaved != 1))
+    return Q4K_ERR_SHAPE;
+  if (ld_head < dim || ld_token < 0 || ldy_head < dim || ldy_token < 0) return Q4K_ERR_SHAPE;
+  // rows of y may not overlap: one of its strides steps over the other
+  if (tokens > 1 && ldy_token / ldy_head < heads && (ldy_token < dim || ldy_head / ldy_token < tokens))
+    return Q4K_ERR_SHAPE;
+  if (tokens == 0) return Q4K_OK;
+  if (!x || !pos || !y || (rot_dim > 0 && !steps)) return Q4K_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(gamma, 16) || !aligned(pos, 4) || !aligned(steps, 8) ||
+      ld_token % 8 || ld_head % 8 || ldy_token % 8 || ldy_head % 8)
+    return Q4K_ERR_ALIGN;
+  st = check_device();
+  if (st != Q4K_OK) return st;
+  st = check_device_memory({x, gamma, pos, rot_dim ? steps : nullptr, y});
+  if (st != Q4K_OK) return st;
+  RopeArgs r = {};
+  r.in[0] = x, r.ld_token[0] = ld_token, r.ld_head[0] = ld_head, r.tokens = tokens, r.heads[0] = heads;
+  r.dim = dim, r.rot = rot_dim, r.gamma[0] = gamma, r.eps = eps, r.amplitude = amplitude;
+  r.pos = pos, r.steps = steps, r.out = y, r.ldo_token = ldy_token, r.ldo_head = ldy_head, r.out_dtype = y_dtype;
+  r.err = device_error_word();
+  return map_launch(launch_rope(r, x_dtype, interleaved != 0, static_cast<cudaStream_t>(stream)));
+}
+
+int q4k_rope_kv_write(const void *q, int64_t ldq_token, int64_t ldq_head, const void *k, const void *v,
+                      int64_t ld_token, int64_t ld_head, int dtype, int64_t tokens, int32_t q_heads,
+                      int32_t kv_heads, int32_t dim, const float *q_gamma, const float *k_gamma,
+                      float eps, const int32_t *pos, const int32_t *slots, const uint64_t *steps,
+                      int32_t rot_dim, int interleaved, float amplitude, void *q_out,
+                      int64_t ldo_token, int64_t ldo_head, void *k_cache, void *v_cache,
+                      int cache_dtype, int64_t n_pages, int32_t page_size, int64_t page_stride,
+                      int64_t head_stride, int64_t token_stride, float *k_scale, float *v_scale,
+                      void *stream) {
+  int st = check_cache(kv_heads, dim, cache_dtype, n_pages, page_size, page_stride, head_stride,
+                       token_stride);
+  if (st != Q4K_OK) return st;
+  st = check_rope(dtype, tokens, dim, q_gamma, k_gamma, eps, rot_dim, amplitude);
+  if (st != Q4K_OK) return st;
+  if (q_heads <= 0 || q_heads > 1024 || (interleaved != 0 && interleaved != 1)) return Q4K_ERR_SHAPE;
+  if (ldq_head < dim || ldq_token < 0 || ld_head < dim || ld_token < 0 || ldo_head < dim || ldo_token < 0)
+    return Q4K_ERR_SHAPE;
+  if (tokens > 1 && ldo_token / ldo_head < q_heads && (ldo_token < dim || ldo_head / ldo_token < tokens))
+    return Q4K_ERR_SHAPE;
+  if (tokens == 0) return Q4K_OK;
+  const bool e4m3 = cache_dtype == Q4K_DTYPE_E4M3;
+  if (!q || !k || !v || !pos || !slots || (rot_dim > 0 && !steps) || !q_out || !k_cache || !v_cache ||
+      (e4m3 && (!k_scale || !v_scale)))
+    return Q4K_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_gamma, 16) ||
+      !aligned(k_gamma, 16) || !aligned(pos, 4) || !aligned(slots, 4) || !aligned(steps, 8) ||
+      !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || ldq_token % 8 || ldq_head % 8 || ld_token % 8 || ld_head % 8 ||
+      ldo_token % 8 || ldo_head % 8)
+    return Q4K_ERR_ALIGN;
+  st = check_device();
+  if (st != Q4K_OK) return st;
+  st = check_device_memory({q, k, v, q_gamma, k_gamma, pos, slots, rot_dim ? steps : nullptr, q_out, k_cache,
+                            v_cache, e4m3 ? k_scale : nullptr, e4m3 ? v_scale : nullptr});
+  if (st != Q4K_OK) return st;
+  RopeArgs r = {};
+  r.in[0] = q, r.in[1] = k, r.in[2] = v;
+  r.ld_token[0] = ldq_token, r.ld_head[0] = ldq_head;
+  r.ld_token[1] = r.ld_token[2] = ld_token, r.ld_head[1] = r.ld_head[2] = ld_head;
+  r.tokens = tokens, r.heads[0] = q_heads, r.heads[1] = kv_heads, r.dim = dim, r.rot = rot_dim;
+  r.gamma[0] = q_gamma, r.gamma[1] = k_gamma, r.eps = eps, r.amplitude = amplitude;
+  r.pos = pos, r.slots = slots, r.steps = steps;
+  r.out = q_out, r.ldo_token = ldo_token, r.ldo_head = ldo_head, r.out_dtype = Q4K_DTYPE_BF16;
+  r.cache[0] = k_cache, r.cache[1] = v_cache, r.scale[0] = k_scale, r.scale[1] = v_scale;
+  r.cache_dtype = cache_dtype, r.n_slots = (uint32_t)(n_pages * page_size), r.page = page_size;
+  r.page_stride = page_stride, r.head_stride = head_stride, r.token_stride = token_stride;
+  r.err = device_error_word();
+  return map_launch(launch_rope(r, dtype, interleaved != 0, static_cast<cudaStream_t>(stream)));
+}
+
 size_t q4k_paged_attn_workspace_size(int32_t n, int32_t q_heads, int32_t kv_heads, int32_t dim) {
   if (n < 0 || q_heads <= 0 || kv_heads <= 0 || dim <= 0) return 0;
   return paged_attn_workspace_size(n, q_heads, kv_heads, dim);
@@ -817,6 +924,26 @@ int q4k_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, int64
   if (st != Q4K_OK) return st;
   return map_launch(launch_sample(logits, dtype, rows, vocab, ld, u, temperature, top_k, top_p, min_p,
                                   token, logp, static_cast<cudaStream_t>(stream)));
+}
+
+int q4k_logprobs(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                 const int32_t *tokens, int32_t top, float *logp, int32_t *rank, float *entropy,
+                 int32_t *top_tokens, float *top_logp, void *stream) {
+  if (dtype != Q4K_DTYPE_FP32 && dtype != Q4K_DTYPE_BF16) return Q4K_ERR_SHAPE;
+  if (rows < 0 || rows > (1 << 24) || vocab <= 0 || vocab > (1 << 24) || ld < vocab || top < 0 || top > 32)
+    return Q4K_ERR_SHAPE;
+  if (rows == 0) return Q4K_OK;
+  if (!logits || !tokens || !logp || (top > 0 && (!top_tokens || !top_logp))) return Q4K_ERR_NULL;
+  if (!aligned(logits, dtype == Q4K_DTYPE_FP32 ? 4 : 2) || !aligned(tokens, 4) || !aligned(logp, 4) ||
+      !aligned(rank, 4) || !aligned(entropy, 4) || !aligned(top_tokens, 4) || !aligned(top_logp, 4))
+    return Q4K_ERR_ALIGN;
+  int st = check_device();
+  if (st != Q4K_OK) return st;
+  st = check_device_memory({logits, tokens, logp, rank, entropy, top ? top_tokens : nullptr,
+                            top ? top_logp : nullptr});
+  if (st != Q4K_OK) return st;
+  return map_launch(launch_logprobs(logits, dtype, rows, vocab, ld, tokens, top, logp, rank, entropy,
+                                    top_tokens, top_logp, static_cast<cudaStream_t>(stream)));
 }
 
 int q4k_selftest_wait_timeout(void *stream) {

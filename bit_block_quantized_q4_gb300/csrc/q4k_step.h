@@ -67,6 +67,37 @@ cudaError_t launch_paged_attn(const AttnArgs &a, cudaStream_t stream);
 size_t paged_attn_chunk_workspace_size(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t dim);
 cudaError_t launch_paged_attn_chunk(const AttnArgs &a, int64_t tokens, const int64_t *cu,
                                     cudaStream_t stream);
+// Norm of heads, rotation, and with caches the write of keys and values
+// (q4k_rope.cu): [0] queries, [1] keys, [2] values.
+struct RopeArgs {
+  const void *in[3];
+  int64_t ld_token[3], ld_head[3];
+  int64_t tokens;
+  int heads[2];             // queries; keys and values
+  int dim, rot;
+  const float *gamma[2];    // queries, keys; or nullptr
+  float eps, amplitude;
+  const int32_t *pos, *slots;
+  const uint64_t *steps;    // [rot / 2] turns per position, in units of 2^-64
+  void *out;                // queries, bf16 or fp32
+  int64_t ldo_token, ldo_head;
+  int out_dtype;
+  void *cache[2];           // nullptr: queries alone
+  float *scale[2];
+  int cache_dtype;
+  uint32_t n_slots;
+  int page;
+  int64_t page_stride, head_stride, token_stride;
+  unsigned *err;
+};
+// The table of frequencies, on the host; false: one is not finite.
+bool rope_steps(int rot, double base, double factor, int64_t original, double beta_fast,
+                double beta_slow, const float *factors, uint64_t *steps, float *amplitude);
+cudaError_t launch_rope(const RopeArgs &r, int dtype, bool interleaved, cudaStream_t stream);
+cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                            const int32_t *tokens, int top, float *logp, int32_t *rank,
+                            float *entropy, int32_t *top_tokens, float *top_logp,
+                            cudaStream_t stream);
 cudaError_t launch_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
                           const float *u, const float *temperature, const int32_t *top_k,
                           const float *top_p, const float *min_p, int32_t *token, float *logp,

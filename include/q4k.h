@@ -553,6 +553,93 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
                  float *v_scale, void *stream);
 
 /*
+ * q4k_rope_steps -- the table of frequencies that q4k_rope and
+ * q4k_rope_kv_write take.  On the host: it touches no device.
+ * Pair i < rot_dim / 2 turns by f_i radians per position:
+ *     g_i = base^(-2 i / rot_dim) / factors[i]      (factors NULL: 1)
+ *     original == 0:  f_i = g_i / factor            (factor 1: g_i)
+ *     original > 0:   f_i = (1 - k_i) g_i / factor + k_i g_i  with a ramp
+ *         k_i = 1 - min(1, max(0, (i - low) / max(0.001, high - low))),
+ *         low = max(0, floor(c(beta_fast))),  high = min(rot_dim - 1, ceil(c(beta_slow))),
+ *         c(turns) = rot_dim ln(original / (2 pi turns)) / (2 ln base):
+ *         pairs that turn more than beta_fast times over the `original` positions
+ *         keep their frequency, those that turn less than beta_slow times are
+ *         slowed by factor.
+ *   steps      host, rot_dim / 2 values: f_i / 2 pi, modulo 1, in units of 2^-64;
+ *              the caller copies them to the device
+ *   amplitude  host, one value: what the caller gives the calls as amplitude, 1 or
+ *              (original > 0) 1 + 0.1 ln factor
+ *   factors    host, rot_dim / 2 positive finite values, or NULL
+ * rot_dim even, 0 .. 256; base and factor positive and finite (and with original
+ * > 0 base not 1, the betas positive and finite).
+ * Errors: NULL, SHAPE.
+ */
+int q4k_rope_steps(int32_t rot_dim, double base, double factor, int64_t original, double beta_fast,
+                   double beta_slow, const float *factors, uint64_t *steps, float *amplitude);
+
+/*
+ * q4k_rope -- norm of each head, and rotation by position.
+ * For token t and head h, with x the row of dim values:
+ *     gamma given:  x = x * gamma / sqrt((1/dim) sum_i x_i^2 + eps)
+ *     of the first rot_dim values, the pairs (a, b), a turning by the angle
+ *     pos[t] f_i:  (a cos - b sin, b cos + a sin) * amplitude
+ * in fp32, each value rounded once.  Pair i is (i, i + rot_dim / 2), or with
+ * interleaved (2 i, 2 i + 1).  Angles are exact to 2^-32 of a turn at any
+ * position.  The other dim - rot_dim values are only normed.  (A part of a head
+ * that does not begin it is a call on that part: x and y point at its first value,
+ * dim is its length.)  A token with a negative position is left alone: its row of
+ * y is not written.
+ *   x      device, fp32 or bf16, element (t, h, i) at t * ld_token + h * ld_head +
+ *          i; 16-byte aligned, strides multiples of 8
+ *   gamma  device, dim fp32, 16-byte aligned, or NULL
+ *   pos    device, tokens int32
+ *   steps  device, rot_dim / 2 values as q4k_rope_steps gives them (not used with
+ *          rot_dim 0)
+ *   y      device, fp32 or bf16, as x with strides of its own, of which one steps
+ *          over the other; may be x (same type, same strides), but not overlap it
+ *          otherwise
+ * dim a multiple of 8, at most 256; rot_dim even, 0 .. dim; heads <= 1024.
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, MEMORY, CUDA.
+ */
+int q4k_rope(const void *x, int x_dtype, int64_t ld_token, int64_t ld_head, int64_t tokens,
+             int32_t heads, int32_t dim, const float *gamma, float eps, const int32_t *pos,
+             const uint64_t *steps, int32_t rot_dim, int interleaved, float amplitude, void *y,
+             int y_dtype, int64_t ldy_token, int64_t ldy_head, void *stream);
+
+/*
+ * q4k_rope_kv_write -- what lies between a step's q, k, v projection and its
+ * attention: q4k_rope of queries and of keys, and q4k_kv_write of these keys
+ * and of the values, in one launch.
+ * Query rows go to q_out (bf16); key rows, normed and rotated in fp32, and value
+ * rows go to slot slots[t] of the caches, each rounded once as q4k_kv_write does
+ * it.  A token with a negative position is left alone.  Slot -1 skips a token's
+ * keys and values (its queries are written); any other slot outside the cache
+ * does too, and sets Q4K_DEVERR_BAD_PAGE.  Tokens of one call that share a slot
+ * leave one of their rows there, unspecified which.
+ *   q         device, dtype (fp32 or bf16), element (t, h, i) at t * ldq_token +
+ *             h * ldq_head + i
+ *   k, v      device, the same type, with strides ld_token and ld_head (q, k and v
+ *             may be parts of one projection's rows)
+ *   q_gamma, k_gamma  device, dim fp32, or NULL (no norm); each by itself
+ *   slots     device, tokens int32
+ *   q_out     device, bf16, strides as y of q4k_rope; may be q (bf16, same strides)
+ *   caches, scales  as q4k_kv_write
+ *   dim       64, 128 or 256
+ * Pointers 16-byte aligned (pos, slots and scales 4, steps 8), strides multiples
+ * of 8.
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, MEMORY, CUDA.
+ */
+int q4k_rope_kv_write(const void *q, int64_t ldq_token, int64_t ldq_head, const void *k, const void *v,
+                      int64_t ld_token, int64_t ld_head, int dtype, int64_t tokens, int32_t q_heads,
+                      int32_t kv_heads, int32_t dim, const float *q_gamma, const float *k_gamma,
+                      float eps, const int32_t *pos, const int32_t *slots, const uint64_t *steps,
+                      int32_t rot_dim, int interleaved, float amplitude, void *q_out,
+                      int64_t ldo_token, int64_t ldo_head, void *k_cache, void *v_cache,
+                      int cache_dtype, int64_t n_pages, int32_t page_size, int64_t page_stride,
+                      int64_t head_stride, int64_t token_stride, float *k_scale, float *v_scale,
+                      void *stream);
+
+/*
  * q4k_paged_attn -- attention of one new token per request over the cache.
  * For request r, query head i and key head i / (q_heads / kv_heads), with the
  * tokens max(0, lens[r] - window) <= j < lens[r] (window 0: all of them):
@@ -707,6 +794,34 @@ int q4k_add_rmsnorm(const void *x, int x_dtype, int64_t ldx, const void *residua
 int q4k_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
                const float *u, const float *temperature, const int32_t *top_k, const float *top_p,
                const float *min_p, int32_t *token, float *logp, void *stream);
+
+/*
+ * q4k_logprobs -- log-probability and rank of given tokens, entropy, and the
+ * most likely tokens.
+ * Row r, with p_i = e^x_i / sum_j e^x_j over the whole vocabulary:
+ *     logp[r] = ln p_token,  entropy[r] = - sum_i p_i ln p_i,
+ *     rank[r] = the number of tokens before this one, where tokens are ordered by
+ *     logit, highest first, equal ones by index (so 0 is the most likely one);
+ *     top_tokens[r], top_logp[r]: the first `top` tokens of that order and their
+ *     logarithms.
+ * A token outside [0, vocab) (as -1, for none) gives logp -infinity and rank -1;
+ * the rest of its row is as for any other.  Logits of NaN count as -infinity,
+ * tokens of -infinity are not listed (-1 and -infinity fill what is left);
+ * +infinity shares the whole mass among its tokens.  A row without any other
+ * logit than -infinity has entropy 0.
+ * Sums are fp32; ranks and top_tokens are exact.
+ *   logits  device, rows x vocab fp32 or bf16 (dtype), row stride ld
+ *   tokens  device, rows int32
+ *   logp    device, rows fp32
+ *   rank    device, rows int32, or NULL;  entropy  device, rows fp32, or NULL
+ *   top_tokens, top_logp  device, rows x top int32 / fp32, contiguous; not used
+ *           with top 0
+ * Limits: top <= 32, vocab <= 2^24.
+ * Errors: NULL, SHAPE, ALIGN (element size), DEVICE, MEMORY, CUDA.
+ */
+int q4k_logprobs(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                 const int32_t *tokens, int32_t top, float *logp, int32_t *rank, float *entropy,
+                 int32_t *top_tokens, float *top_logp, void *stream);
 
 /*
  * q4k_get_device_error -- synchronize `stream`, return the device error word
