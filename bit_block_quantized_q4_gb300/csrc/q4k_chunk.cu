@@ -158,6 +158,12 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
 #define Q4K_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define Q4K_V8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
 // 32 lanes x 32 bits, 32 consecutive columns per thread.
@@ -234,7 +240,7 @@ struct Bars {
   uint64_t item_full[kRing], item_empty[kRing];
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
-  uint64_t s_full[2][2], p_full[2][2], o_done[2];
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // of a query tile; by score buffer
 };
 // Of a stage of V: 16-token pieces that are absent, tokens whose values are not
 // finite; e4m3: the least and the largest exponent field of the V scales.
@@ -262,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) mbar_init(&bars.item_full[i], 1), mbar_init(&bars.item_empty[i], 1 + 2 + 4 * NQ + 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.q_full[i], 2), mbar_init(&bars.q_empty[i], 1), mbar_init(&bars.o_done[i], 1);
-      for (int j = 0; j < 2; ++j) mbar_init(&bars.s_full[i][j], 1), mbar_init(&bars.p_full[i][j], 4);
+      mbar_init(&bars.q_full[i], 2), mbar_init(&bars.q_empty[i], 1);
+      for (int j = 0; j < 2; ++j) mbar_init(&bars.s_full[i][j], 1), mbar_init(&bars.p_full[i][j], 4), mbar_init(&bars.o_done[i][j], 1);
     }
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.k_full[i], 1), mbar_init(&bars.k_ready[i], 4), mbar_init(&bars.k_empty[i], 1);
@@ -338,6 +344,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sign = a.softmax_scale < 0.f ? -1.f : 0.f;
     const bool positive = a.softmax_scale > 0.f;
     int tiles = 0, mine_t = 0, taken = 0;  // key tiles of this CTA so far, those of query tile t, and its items
+    // The g-th product P V of this query tile is complete.  A wait tells phases apart
+    // by their parity alone, so it must not come when the one before may be missing
+    // or the one after be there: g - 1 (one score buffer), or g - 2 (two, a barrier
+    // each), was complete before the scores that this warp has seen, and the next one
+    // waits for weights that it has not written.
+    const auto values_done = [&](int g) {
+      return warp_wait(&bars.o_done[t][SB == 2 ? g & 1 : 0], (uint32_t)(SB == 2 ? g >> 1 : g) & 1u, a.err);
+    };
     Item x;
     while (t < NQ && ok && next_item(x)) {
       const bool active = x.rows > 128 * t, used = x.rows > 128 * t + 32 * (warp & 3), live = row_t < x.rows;
@@ -393,9 +407,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          float top = __uint_as_float(s[0]);
+          float tops[4];
 #pragma unroll
-          for (int c = 1; c < TILE; ++c) top = fmaxf(top, __uint_as_float(s[c]));
+          for (int c = 0; c < 4; ++c) tops[c] = fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 4]));
+#pragma unroll
+          for (int c = 8; c < TILE; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], fmaxf(__uint_as_float(s[c + k]), __uint_as_float(s[c + k + 4])));
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
           // scores are S here, to be multiplied by sc, or (e4m3) in base 2 already
           const float unit = E4M3 ? 1.f : sc;
           const bool grew = m != -INFINITY && (top - m) * unit > kLazy;
@@ -404,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = grew ? ex2((m - top) * unit) : 1.f;
             if (grew) m = top;
             l *= f;
-            ok = warp_wait(&bars.o_done[t], (uint32_t)(g - 1) & 1u, a.err);
+            ok = values_done(g - 1);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -462,8 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the piece ends: O is complete once its last product is
       if (active && x.n > 0 && ok) {
         const int g = mine_t + x.n - 1;
-        ok = (x.n == 1 || warp_wait(&bars.o_done[t], (uint32_t)(g - 1) & 1u, a.err)) &&
-             warp_wait(&bars.o_done[t], (uint32_t)g & 1u, a.err);
+        ok = values_done(g);
         tc_fence_after();
       }
       if (used && ok) {
@@ -515,80 +533,104 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
     if (warp == 8) {
       // ------------------------------------------------------------- products
-      if (lane == 0) {
-        constexpr uint32_t id_qk = idesc_of(!E4M3, false, TILE), id_pv = idesc_of(!E4M3, true, D);
-        const uint32_t base = smem_u32(smem);
-        int tiles = 0, count[2] = {0, 0}, seen_q[2] = {0, 0};  // key tiles, products of a query tile, Q tiles consumed
-        uint64_t *k_ready = E4M3 ? bars.k_ready : bars.k_full;
-        // S of query tile t with key tile `kt` (of all), the g-th of this query tile
-        const auto qk = [&](int t, int kt, int g, bool first, bool last, bool last_q) {
-          const int s = kt % ST, buf = SB == 2 ? g & 1 : 0;
-          if (first && !wait_on(&k_ready[s], (uint32_t)(kt / ST) & 1u, a.err)) return false;
-          tc_fence_after();
+      // The whole warp runs this, so that descriptors are uniform values; one lane
+      // issues.  (With one lane alone in here 8 products took 700 to 800 cycles to
+      // issue, and 512 to run.)
+      const bool leader = elect_one();
+      constexpr uint32_t id_qk = idesc_of(!E4M3, false, TILE), id_pv = idesc_of(!E4M3, true, D);
+      const uint32_t base = smem_u32(smem);
+      const uint64_t q_desc = sdesc_sw128(base, 1024), k_desc = sdesc_sw128(base + C::kKAt, 1024), v_desc = sdesc_v(base + C::kVAt, TILE * 128);
+      uint64_t *k_ready = E4M3 ? bars.k_ready : bars.k_full;
+      int ks = 0, vs = 0;                       // next stages of K and V, and their phases
+      uint32_t kph = 0, vph = 0;
+      uint32_t count0 = 0, count1 = 0, q_seen0 = 0, q_seen1 = 0;  // products P V, and Q tiles, of query tiles 0 and 1
+      // S of query tile t with the key tile in stage ks; g: the how manieth of this query tile
+      const auto qk = [&](int t, uint32_t g, bool last_key, bool last_q) {
+        const uint32_t buf = SB == 2 ? g & 1u : 0u;
+        if (leader) {
+          const uint64_t qd = q_desc + (uint64_t)((uint32_t)t * (C::kQ >> 4)), kd = k_desc + (uint64_t)((uint32_t)ks * (C::kSide >> 4));
+          const uint32_t d = tmem + t * C::kSCols + buf * TILE;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t qd = sdesc_sw128(base + t * C::kQ + (k / 4) * 128 * 128 + (k % 4) * 32, 1024);
-            const uint64_t kd = sdesc_sw128(base + C::kKAt + s * C::kSide + (k / 4) * TILE * 128 + (k % 4) * 32, 1024);
-            tc_mma_f16(tmem + t * C::kSCols + buf * TILE, qd, kd, id_qk, k != 0);
-          }
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma_f16(d, qd + (uint64_t)((k / 4) * (128 * 128 >> 4) + (k % 4) * 2), kd + (uint64_t)((k / 4) * (TILE * 128 >> 4) + (k % 4) * 2), id_qk, k != 0);
           tc_commit(&bars.s_full[t][buf]);
-          if (last) tc_commit(&bars.k_empty[s]);
+          if (last_key) tc_commit(&bars.k_empty[ks]);
           if (last_q) tc_commit(&bars.q_empty[t]);
-          return true;
-        };
-        const auto pv = [&](int t, int kt, int g, bool first, bool last, bool fresh) {
-          const int s = kt % ST, buf = SB == 2 ? g & 1 : 0;
-          if (first && !wait_on(&bars.v_ready[s], (uint32_t)(kt / ST) & 1u, a.err)) return false;
-          if (!wait_on(&bars.p_full[t][buf], (uint32_t)(SB == 2 ? g >> 1 : g) & 1u, a.err)) return false;
-          tc_fence_after();
+        }
+        __syncwarp();
+        if (last_key && ++ks == ST) ks = 0, kph ^= 1u;
+      };
+      const auto pv = [&](int t, uint32_t g, bool fresh, bool last_value) {
+        const uint32_t buf = SB == 2 ? g & 1u : 0u;
+        if (!warp_wait(&bars.p_full[t][buf], (SB == 2 ? g >> 1 : g) & 1u, a.err)) return false;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t vd = v_desc + (uint64_t)((uint32_t)vs * (C::kSide >> 4));
+          const uint32_t d = tmem + C::kOCol + t * D, pa = tmem + t * C::kSCols + buf * TILE;
 #pragma unroll
-          for (int k = 0; k < TILE / 16; ++k) {
-            const uint64_t vd = sdesc_v(base + C::kVAt + s * C::kSide + k * 16 * 128, TILE * 128);
-            tc_mma_ts(tmem + C::kOCol + t * D, tmem + t * C::kSCols + buf * TILE + k * 8, vd, id_pv, !fresh || k != 0);
-          }
-          tc_commit(&bars.o_done[t]);
-          if (last) tc_commit(&bars.v_empty[s]);
-          return true;
-        };
-        const auto start = [&](const Item &x, int kt) {  // the item's first scores
-          const int act = x.rows > 128 ? 2 : 1;
-          for (int t = 0; t < act; ++t) {
-            if (!wait_on(&bars.q_full[t], (uint32_t)seen_q[t]++ & 1u, a.err)) return false;
-            if (!qk(t, kt, count[t], t == 0, t == act - 1, x.n == 1)) return false;
-          }
-          return true;
-        };
-        Item x, y;
-        const auto next_work = [&](Item &z) {  // the next item that has tiles
-          while (take_item(z, wait_on(&bars.item_full[it % kRing], (uint32_t)(it / kRing) & 1u, a.err))) {
-            if (z.n > 0) return true;
-            free_item();
-            ++it;
-          }
-          return false;
-        };
-        bool more = next_work(x);
-        if (more) ok = start(x, tiles);
-        while (more && ok) {
-          const int act = x.rows > 128 ? 2 : 1;
-          for (int j = 0; j < x.n && ok; ++j) {
+          for (int k = 0; k < TILE / 16; ++k) tc_mma_ts(d, pa + k * 8, vd + (uint64_t)(k * (16 * 128 >> 4)), id_pv, k != 0 || !fresh);
+          tc_commit(&bars.o_done[t][buf]);
+          if (last_value) tc_commit(&bars.v_empty[vs]);
+        }
+        __syncwarp();
+        if (last_value && ++vs == ST) vs = 0, vph ^= 1u;
+        return true;
+      };
+      const auto key_tile = [&]() {
+        if (!warp_wait(&k_ready[ks], kph, a.err)) return false;
+        tc_fence_after();
+        return true;
+      };
+      Item x;
+      int n = 0, act = 0;
+      const auto start = [&]() {  // the next item that has tiles, its first scores
+        n = 0;
+        while (next_item(x)) {
+          n = __shfl_sync(0xffffffffu, x.n, 0);
+          act = NQ == 1 || __shfl_sync(0xffffffffu, x.rows, 0) <= 128 ? 1 : 2;
+          if (n > 0) break;
+          if (leader) free_item();
+          ++it;
+        }
+        if (!ok || n <= 0) return false;
+        if (!warp_wait(&bars.q_full[0], q_seen0++ & 1u, a.err) || !key_tile()) return ok = false;
+        qk(0, count0, act == 1, n == 1);
+        if (act == 2) {
+          if (!warp_wait(&bars.q_full[1], q_seen1++ & 1u, a.err)) return ok = false;
+          tc_fence_after();
+          qk(1, count1, true, n == 1);
+        }
+        return true;
+      };
+      bool more = start();
+      while (more) {
+        for (int j = 0; j < n && ok; ++j) {
+          const bool next = j + 1 < n, last_q = j + 2 == n;
+          if (SB == 2) {
             // with two score buffers the next scores come before this tile's values
-            if (SB == 2 && j + 1 < x.n) ok = qk(0, tiles + j + 1, count[0] + j + 1, true, true, j + 2 == x.n);
-            for (int t = 0; t < act && ok; ++t) {
-              ok = pv(t, tiles + j, count[t] + j, t == 0, t == act - 1, j == 0);
-              if (SB == 1 && ok && j + 1 < x.n)
-                ok = qk(t, tiles + j + 1, count[t] + j + 1, t == 0, t == act - 1, j + 2 == x.n);
+            if (next) {
+              if (!(ok = key_tile())) break;
+              qk(0, count0 + j + 1, true, last_q);
+            }
+            ok = warp_wait(&bars.v_ready[vs], vph, a.err) && pv(0, count0 + j, j == 0, true);
+          } else {
+            ok = warp_wait(&bars.v_ready[vs], vph, a.err) && pv(0, count0 + j, j == 0, act == 1);
+            if (next && ok) {
+              if (!(ok = key_tile())) break;
+              qk(0, count0 + j + 1, act == 1, last_q);
+            }
+            if (act == 2 && ok) {
+              ok = pv(1, count1 + j, j == 0, true);
+              if (next && ok) qk(1, count1 + j + 1, true, last_q);
             }
           }
-          if (!ok) break;
-          for (int t = 0; t < act; ++t) count[t] += x.n;
-          tiles += x.n;
-          free_item();
-          ++it;
-          more = next_work(y);
-          if (more) ok = start(y, tiles);
-          x = y;
         }
+        if (!ok) break;
+        count0 += n;
+        if (act == 2) count1 += n;
+        if (leader) free_item();
+        ++it;
+        more = start();
       }
     } else if (warp == 9) {
       // ----------------------------------------------- work list, copies of K and V
@@ -605,130 +647,160 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int4 open = make_int4(-1, 0, 0, 0);  // the item that this CTA starts and does not end
       int open_rows = 0;
+      // Where the search stands: request r (its key heads take `unit` units each),
+      // key head, the first of 32 blocks, the units before each lane's block, and
+      // which of these blocks are still to come.
+      int r = 0, head = 0, b0 = 0, blocks = 0;
+      int64_t at = 0, unit = 0, u = 0, before = 0, upto = 0;
+      unsigned todo = 0;
+      Req q = {};
+      bool ignore = false, fresh = true;
       if (u0 < u1) {
-        // the request and the place in it of unit u0
         int lo = 0, hi = kThreads - 1;  // the first thread whose inclusive sum exceeds u0
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
           if (sums[mid] > u0) hi = mid;
           else lo = mid + 1;
         }
-        int64_t at = lo ? sums[lo - 1] : 0;  // units before the request
-        bool ignore = false;
-        for (int r = lo * per; r < a.n && at < u1 && ok; ++r) {
-          const Req q = request(p, r, ignore);
-          const int blocks = (q.rows + ROWS - 1) / ROWS;
-          if (!blocks) continue;
-          // units of a key head: lanes take blocks in turn
-          int64_t unit = 0;
-          for (int b = lane; b < blocks; b += 32) unit += block_cost<TILE, ROWS>(p, q, b);
+        at = lo ? sums[lo - 1] : 0;  // units before the request
+        r = lo * per;
+      } else {
+        r = a.n;
+      }
+      const auto blocks_at = [&]() {  // the costs of 32 blocks, and the units before each
+        const int cost = b0 + lane < blocks ? block_cost<TILE, ROWS>(p, q, b0 + lane) : 0;
+        upto = cost;
 #pragma unroll
-          for (int o = 16; o; o >>= 1) unit += __shfl_xor_sync(0xffffffffu, unit, o);
-          if (at + unit * a.kv_heads <= u0) {
-            at += unit * a.kv_heads;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        before = u + upto - cost;
+        todo = __ballot_sync(0xffffffffu, cost && before + cost > u0 && before < u1);
+      };
+      const auto find = [&](Item &x) {  // this CTA's next piece; false: there is none
+        for (;;) {
+          while (todo) {
+            const int src = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int64_t ub = __shfl_sync(0xffffffffu, before, src);
+            x.r = r, x.head = head, x.row0 = (b0 + src) * ROWS, x.rows = min(ROWS, q.rows - x.row0);
+            x.tok0 = q.tok0, x.pos0 = q.pos0;
+            int t0, t1;
+            tiles_of<TILE>(p, q, x.row0, x.rows, t0, t1);
+            const int nt = t1 - t0;
+            // tile k of the item is unit ub + kItemCost + k
+            const int ta = (int)min(max(u0 - ub - kItemCost, (int64_t)0), (int64_t)nt), tb = (int)min(max(u1 - ub - kItemCost, (int64_t)0), (int64_t)nt);
+            if (nt == 0 ? ub < u0 : ta == tb) continue;  // another CTA's
+            const int first = q.pos0 + (int)p.by_group.div(x.row0), last = q.pos0 + (int)p.by_group.div(x.row0 + x.rows - 1);
+            x.lo = first_seen(a, first), x.hi = end_seen(a, last);
+            x.full_lo = first_seen(a, last), x.full_hi = end_seen(a, first);
+            x.t0 = t0 + ta, x.n = tb - ta;
+            x.kind = x.n == nt ? 0 : ta == 0 ? 1 : 2;
+            if (x.kind == 1) {
+              open = make_int4(r, head, x.row0, (int)((ub + kItemCost + nt - 1) / run));
+              open_rows = x.rows;
+            }
+            return true;
+          }
+          if (fresh) {  // a request
+            if (r >= a.n || at >= u1) return false;
+            q = request(p, r, ignore);
+            blocks = (q.rows + ROWS - 1) / ROWS;
+            unit = 0;  // of a key head: lanes take blocks in turn
+            for (int b = lane; b < blocks; b += 32) unit += block_cost<TILE, ROWS>(p, q, b);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) unit += __shfl_xor_sync(0xffffffffu, unit, o);
+            if (!blocks || at + unit * a.kv_heads <= u0) {
+              at += unit * a.kv_heads;
+              ++r;
+              continue;
+            }
+            head = at < u0 ? (int)((u0 - at) / unit) : 0;
+            u = at + head * unit;  // units before the key head, then before block b0
+            b0 = 0, fresh = false;
+            blocks_at();
             continue;
           }
-          int head = at < u0 ? (int)((u0 - at) / unit) : 0;
-          int64_t u = at + head * unit;  // units before the key head
-          for (; head < a.kv_heads && u < u1 && ok; ++head) {
-            for (int b0 = 0; b0 < blocks && u < u1 && ok; b0 += 32) {
-              // the costs of 32 blocks, and the units before each
-              const int cost = b0 + lane < blocks ? block_cost<TILE, ROWS>(p, q, b0 + lane) : 0;
-              int64_t upto = cost;
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-              }
-              const int64_t before = u + upto - cost;
-              unsigned todo = __ballot_sync(0xffffffffu, cost && before + cost > u0 && before < u1);
-              while (todo && ok) {
-                const int src = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int64_t ub = __shfl_sync(0xffffffffu, before, src);
-                Item x;
-                x.r = r, x.head = head, x.row0 = (b0 + src) * ROWS, x.rows = min(ROWS, q.rows - x.row0);
-                x.tok0 = q.tok0, x.pos0 = q.pos0;
-                int t0, t1;
-                tiles_of<TILE>(p, q, x.row0, x.rows, t0, t1);
-                const int nt = t1 - t0;
-                // tile k of the item is unit ub + kItemCost + k
-                const int ta = (int)min(max(u0 - ub - kItemCost, (int64_t)0), (int64_t)nt), tb = (int)min(max(u1 - ub - kItemCost, (int64_t)0), (int64_t)nt);
-                if (nt == 0 ? ub < u0 : ta == tb) continue;  // another CTA's
-                const int first = q.pos0 + (int)p.by_group.div(x.row0), last = q.pos0 + (int)p.by_group.div(x.row0 + x.rows - 1);
-                x.lo = first_seen(a, first), x.hi = end_seen(a, last);
-                x.full_lo = first_seen(a, last), x.full_hi = end_seen(a, first);
-                x.t0 = t0 + ta, x.n = tb - ta;
-                x.kind = x.n == nt ? 0 : ta == 0 ? 1 : 2;
-                if (x.kind == 1) {
-                  open = make_int4(r, head, x.row0, (int)((ub + kItemCost + nt - 1) / run));
-                  open_rows = x.rows;
-                }
-                if (!(ok = put(x))) break;
-                // ---- its tiles.  Lanes hold 32 table entries from page tb0 on, and the 32 after them.
-                const int boxes = TILE >> p.box_shift;
-                int tb0 = (x.t0 * TILE) >> p.page_shift;
-                const auto table_at = [&](int i) { return i < a.max_pages ? a.table[r * a.ldt + i] : -1; };
-                int entry = table_at(tb0 + lane), entry2 = table_at(tb0 + 32 + lane);
-                for (int j = 0; j < x.n; ++j, ++tiles) {
-                  const int s = tiles % ST;
-                  const uint32_t ph = ((uint32_t)(tiles / ST) & 1u) ^ 1u;
-                  const int pos = (x.t0 + j) * TILE;
-                  while (((pos + TILE - 1) >> p.page_shift) - tb0 >= 64) {
-                    tb0 += 32;
-                    entry = entry2;
-                    entry2 = table_at(tb0 + 32 + lane);
-                  }
-                  // box `lane % boxes` of the tile, its page; the lanes after the first `boxes` take the other parts
-                  const int b = lane & (boxes - 1), box_pos = pos + (b << p.box_shift), i = (box_pos >> p.page_shift) - tb0;
-                  const int e1 = __shfl_sync(0xffffffffu, entry, i & 31), e2 = __shfl_sync(0xffffffffu, entry2, i & 31);
-                  const int page = i < 32 ? e1 : e2;
-                  const bool wanted = box_pos < x.hi && box_pos + p.box_rows > x.lo;
-                  const bool there = wanted && page >= 0 && page < a.n_pages;
-                  const unsigned need = __ballot_sync(0xffffffffu, wanted && lane < boxes), have = __ballot_sync(0xffffffffu, there && lane < boxes);
-                  if (need != have && lane == 0) set_device_error(a.err, kDevErrBadPage);
-                  const uint32_t box_bytes = (uint32_t)p.box_rows * D * C::kEs, loaded = __popc(have) * box_bytes;
-                  const int in_page = box_pos & (a.page - 1);
-                  if (!(ok = warp_wait(&bars.k_empty[s], ph, a.err))) break;
-                  if (lane == 0) mbar_arrive_expect_tx(&bars.k_full[s], loaded);
-                  __syncwarp();
-                  uint8_t *k = smem + C::kKAt + s * C::kSide, *v = smem + C::kVAt + s * C::kSide;
-                  if (E4M3) k += C::kSide - C::kRaw, v += C::kSide - C::kRaw;
-                  const auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar) {
-                    if (E4M3) {
-                      if (there && lane < boxes) tma_load_5d(dst + (b << p.box_shift) * D, map, bar, 0, in_page, 0, x.head, page);
-                    } else {
-                      for (int part = lane / boxes; part < C::kParts; part += 32 / boxes)
-                        if (there) tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * 128, map, bar, 0, in_page, part, x.head, page);
-                    }
-                  };
-                  copy(k, &kmap, &bars.k_full[s]);
-                  if (!(ok = warp_wait(&bars.v_empty[s], ph, a.err))) break;
-                  if (lane == 0) {
-                    // 16-token pieces that are absent
-                    uint32_t gone = 0;
-                    for (unsigned w = need & ~have; w; w &= w - 1) {
-                      const int at16 = (__ffs(w) - 1) << (p.box_shift - 4);
-                      gone |= ((p.box_rows >> 4 == 32 ? 0u : 1u << (p.box_rows >> 4)) - 1u) << at16;
-                    }
-                    vinfo[s].absent = gone;
-                    mbar_arrive_expect_tx(&bars.v_full[s], loaded + (E4M3 ? __popc(have) * p.box_rows * 8 : 0));
-                  }
-                  __syncwarp();
-                  copy(v, &vmap, &bars.v_full[s]);
-                  if (E4M3 && there && lane < boxes) {
-                    float *ks = reinterpret_cast<float *>(smem + C::kScaleAt) + s * 3 * TILE + (b << p.box_shift);
-                    const int64_t from = ((int64_t)page * a.kv_heads + x.head) * a.page + in_page;
-                    bulk_load(ks, a.scale[0] + from, p.box_rows * 4, &bars.v_full[s]);
-                    bulk_load(ks + TILE, a.scale[1] + from, p.box_rows * 4, &bars.v_full[s]);
-                  }
-                  __syncwarp();
-                }
-              }
-              u += __shfl_sync(0xffffffffu, upto, 31);
+          u += __shfl_sync(0xffffffffu, upto, 31);
+          b0 += 32;
+          if (b0 >= blocks) {
+            b0 = 0;
+            if (++head == a.kv_heads || u >= u1) {
+              fresh = true;
+              at += unit * a.kv_heads;
+              ++r;
+              continue;
             }
           }
-          at += unit * a.kv_heads;
+          blocks_at();
+        }
+      };
+      Item x, y;
+      bool more = find(y);
+      if (more) ok = put(y);
+      while (more && ok) {
+        x = y;
+        more = find(y);  // the others know of an item before the copies of the one before it
+        if (more && !(ok = put(y))) break;
+        // ---- its tiles.  Lanes hold 32 table entries from page tb0 on, and the 32 after them.
+        const int boxes = TILE >> p.box_shift;
+        int tb0 = (x.t0 * TILE) >> p.page_shift;
+        const auto table_at = [&](int i) { return i < a.max_pages ? a.table[x.r * a.ldt + i] : -1; };
+        int entry = table_at(tb0 + lane), entry2 = table_at(tb0 + 32 + lane);
+        for (int j = 0; j < x.n; ++j, ++tiles) {
+          const int s = tiles % ST;
+          const uint32_t ph = ((uint32_t)(tiles / ST) & 1u) ^ 1u;
+          const int pos = (x.t0 + j) * TILE;
+          while (((pos + TILE - 1) >> p.page_shift) - tb0 >= 64) {
+            tb0 += 32;
+            entry = entry2;
+            entry2 = table_at(tb0 + 32 + lane);
+          }
+          // box `lane % boxes` of the tile, its page; the lanes after the first `boxes` take the other parts
+          const int b = lane & (boxes - 1), box_pos = pos + (b << p.box_shift), i = (box_pos >> p.page_shift) - tb0;
+          const int e1 = __shfl_sync(0xffffffffu, entry, i & 31), e2 = __shfl_sync(0xffffffffu, entry2, i & 31);
+          const int page = i < 32 ? e1 : e2;
+          const bool wanted = box_pos < x.hi && box_pos + p.box_rows > x.lo;
+          const bool there = wanted && page >= 0 && page < a.n_pages;
+          const unsigned need = __ballot_sync(0xffffffffu, wanted && lane < boxes), have = __ballot_sync(0xffffffffu, there && lane < boxes);
+          if (need != have && lane == 0) set_device_error(a.err, kDevErrBadPage);
+          const uint32_t box_bytes = (uint32_t)p.box_rows * D * C::kEs, loaded = __popc(have) * box_bytes;
+          const int in_page = box_pos & (a.page - 1);
+          if (!(ok = warp_wait(&bars.k_empty[s], ph, a.err))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bars.k_full[s], loaded);
+          __syncwarp();
+          uint8_t *k = smem + C::kKAt + s * C::kSide, *v = smem + C::kVAt + s * C::kSide;
+          if (E4M3) k += C::kSide - C::kRaw, v += C::kSide - C::kRaw;
+          const auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar) {
+            if (E4M3) {
+              if (there && lane < boxes) tma_load_5d(dst + (b << p.box_shift) * D, map, bar, 0, in_page, 0, x.head, page);
+            } else {
+              for (int part = lane / boxes; part < C::kParts; part += 32 / boxes)
+                if (there) tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * 128, map, bar, 0, in_page, part, x.head, page);
+            }
+          };
+          copy(k, &kmap, &bars.k_full[s]);
+          if (!(ok = warp_wait(&bars.v_empty[s], ph, a.err))) break;
+          if (lane == 0) {
+            // 16-token pieces that are absent
+            uint32_t gone = 0;
+            for (unsigned w = need & ~have; w; w &= w - 1) {
+              const int at16 = (__ffs(w) - 1) << (p.box_shift - 4);
+              gone |= ((p.box_rows >> 4 == 32 ? 0u : 1u << (p.box_rows >> 4)) - 1u) << at16;
+            }
+            vinfo[s].absent = gone;
+            mbar_arrive_expect_tx(&bars.v_full[s], loaded + (E4M3 ? __popc(have) * p.box_rows * 8 : 0));
+          }
+          __syncwarp();
+          copy(v, &vmap, &bars.v_full[s]);
+          if (E4M3 && there && lane < boxes) {
+            float *ks = reinterpret_cast<float *>(smem + C::kScaleAt) + s * 3 * TILE + (b << p.box_shift);
+            const int64_t from = ((int64_t)page * a.kv_heads + x.head) * a.page + in_page;
+            bulk_load(ks, a.scale[0] + from, p.box_rows * 4, &bars.v_full[s]);
+            bulk_load(ks + TILE, a.scale[1] + from, p.box_rows * 4, &bars.v_full[s]);
+          }
+          __syncwarp();
         }
       }
       if (lane == 0) {
@@ -754,19 +826,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && next_item(x)) {
         for (int t = 0; t < NQ && x.n > 0 && x.rows > 128 * t && ok; ++t) {
           const int c = count[t]++;
-          if (!(ok = warp_wait(&bars.q_empty[t], ((uint32_t)c & 1u) ^ 1u, a.err))) break;
           uint8_t *dst = smem + t * C::kQ;
           constexpr int CH = D / 8;  // 16-byte pieces of a row
           const int first = 64 * (warp - 10);
-#pragma unroll 4
-          for (int i = lane; i < 64 * CH; i += 32) {
-            const int row = first + i / CH, ch = i % CH, rr = 128 * t + row;
-            const bool in = rr < x.rows;
-            const int rw = x.row0 + (in ? rr : 0), tok = (int)p.by_group.div(rw);
-            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)x.tok0 + tok) * a.ldq +
-                                       (int64_t)(x.head * p.group + (rw - tok * p.group)) * a.ldq_head + ch * 8;
-            cp_async16(dst + (ch / 8) * 128 * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src, in ? 16 : 0);
+          // a lane knows where two rows lie; -1: not of this item, zeros
+          int64_t where[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int rr = 128 * t + first + 32 * h + lane, rw = x.row0 + rr, tok = (int)p.by_group.div(rw);
+            where[h] = rr < x.rows ? ((int64_t)x.tok0 + tok) * a.ldq + (int64_t)(x.head * p.group + (rw - tok * p.group)) * a.ldq_head : -1;
           }
+          if (!(ok = warp_wait(&bars.q_empty[t], ((uint32_t)c & 1u) ^ 1u, a.err))) break;
+          constexpr int RPI = 32 / CH ? 32 / CH : 1;  // rows of an iteration (CH = 32: one, else more)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll 4
+            for (int i = 0; i < 32 / RPI; ++i) {
+              const int rr = i * RPI + lane / CH, row = first + 32 * h + rr, ch = lane % CH;
+              const int64_t from = __shfl_sync(0xffffffffu, where[h], rr);
+              cp_async16(dst + (ch / 8) * 128 * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), static_cast<const __nv_bfloat16 *>(a.q) + max(from, (int64_t)0) + ch * 8, from >= 0 ? 16 : 0);
+            }
           cp_async_commit();
           cp_async_wait<0>();
           if (E4M3) {
