@@ -61,15 +61,18 @@ constexpr int kRing = 4;         // items on their way
 template <int D, bool E4M3>
 struct Cfg {
   static constexpr int kNq = D == 256 ? 1 : 2;        // query tiles per block
-  static constexpr int kSb = D == 256 ? 2 : 1;        // score buffers per query tile
+  // Buffers in tensor memory: O of each query tile; scores, of each query tile (dim
+  // 64), of both in turn (128), or of a key tile and the next (256); weights, of
+  // each query tile, or of a key tile and the next (256).
+  static constexpr int kSBufs = D == 128 ? 1 : 2, kPBufs = 2;
   static constexpr int kTile = D == 256 ? 64 : 128;   // tokens per key tile
   static constexpr int kParts = D / 64;               // 128-byte parts of a row
   static constexpr int kSide = kTile * D * 2;         // bytes of a tile of K or V
   static constexpr int kStages = D == 64 ? 4 : 2;     // of K, and of V
   static constexpr int kQ = 128 * D * 2;              // bytes of a query tile
   static constexpr int kRows = 128 * kNq;             // rows of a block
-  static constexpr int kSCols = kSb * kTile;          // tensor memory columns of a tile's S
-  static constexpr int kOCol = kNq * kSCols;          // first column of O
+  static constexpr int kSCol = kNq * D;               // first columns of scores, of weights
+  static constexpr int kPCol = kSCol + kSBufs * kTile;
   static constexpr int kCols = 512;
   static constexpr int kEs = E4M3 ? 1 : 2;
   static constexpr int kRaw = kTile * D;              // bytes of an e4m3 tile
@@ -77,7 +80,7 @@ struct Cfg {
   static constexpr int kKAt = kNq * kQ, kVAt = kKAt + kStages * kSide;
   static constexpr int kScaleAt = kVAt + kStages * kSide;
   static constexpr int kSmem = kScaleAt + (E4M3 ? kStages * 3 * kTile * 4 : 0) + 1024;
-  static_assert(kOCol + kNq * D <= kCols, "S and O fit tensor memory");
+  static_assert(kPCol + kPBufs * kTile / 2 <= kCols, "O, S and P fit tensor memory");
 };
 
 struct Params {
@@ -182,22 +185,22 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t *r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-// mbar_wait without a call: a call in here would cost every role its registers.
-__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, unsigned *err) {
-  if (mbar_try_wait(bar, parity)) return true;
+// A wait by a whole warp, whose lanes stay together; false after the time limit.
+// (Without a call, which would cost every role its registers.)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (global_ns() - t0 > kWaitLimitNs) break;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) break;
   }
   set_device_error(err, kDevErrTimeout);
   return false;
 }
-// A wait by a whole warp: true if it was for all lanes, so that they stay together.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
-  return __all_sync(0xffffffffu, wait_on(bar, parity, err));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // A barrier of the 128 threads of a warpgroup; true if `ok` was true for all.
 // (Every warp passes it whatever happened to it, so that none is left behind.)
@@ -240,7 +243,8 @@ struct Bars {
   uint64_t item_full[kRing], item_empty[kRing];
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
-  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // of a query tile; by score buffer
+  uint64_t s_full[2], s_free[2];  // scores: of a query tile (dim 256: of a buffer); buffers
+  uint64_t p_full[2], o_done[2];  // weights and their products, by buffer of weights
 };
 // Of a stage of V: 16-token pieces that are absent, tokens whose values are not
 // finite; e4m3: the least and the largest exponent field of the V scales.
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, E4M3>;
-  constexpr int TILE = C::kTile, ROWS = C::kRows, ST = C::kStages, NQ = C::kNq, SB = C::kSb;
+  constexpr int TILE = C::kTile, ROWS = C::kRows, ST = C::kStages, NQ = C::kNq;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars bars;
   __shared__ VInfo vinfo[4];
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kRing; ++i) mbar_init(&bars.item_full[i], 1), mbar_init(&bars.item_empty[i], 1 + 2 + 4 * NQ + 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 2), mbar_init(&bars.q_empty[i], 1);
-      for (int j = 0; j < 2; ++j) mbar_init(&bars.s_full[i][j], 1), mbar_init(&bars.p_full[i][j], 4), mbar_init(&bars.o_done[i][j], 1);
+      mbar_init(&bars.s_full[i], 1), mbar_init(&bars.s_free[i], 4), mbar_init(&bars.p_full[i], 4), mbar_init(&bars.o_done[i], 1);
     }
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.k_full[i], 1), mbar_init(&bars.k_ready[i], 4), mbar_init(&bars.k_empty[i], 1);
@@ -321,13 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // The ring of items, as every role but the copying one reads it.
   int it = 0;
-  const auto take_item = [&](Item &x, bool waited) {  // false: there are no more, or the wait ran out
-    ok = waited;
+  const auto next_item = [&](Item &x) {  // false: there are no more, or the wait ran out
+    ok = warp_wait(&bars.item_full[it % kRing], (uint32_t)(it / kRing) & 1u, a.err);
     if (ok) x = items[it % kRing];
     return ok && x.rows >= 0;
-  };
-  const auto next_item = [&](Item &x) {  // by a warp
-    return take_item(x, warp_wait(&bars.item_full[it % kRing], (uint32_t)(it / kRing) & 1u, a.err));
   };
   const auto free_item = [&]() {  // by one lane of the warp
     mbar_arrive(&bars.item_empty[it % kRing]);
@@ -338,20 +339,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- softmax
     const int t = warp >> 2, row_in = 32 * (warp & 3) + lane, row_t = 128 * t + row_in;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_at = tmem + lanes + t * C::kSCols, o_at = tmem + lanes + C::kOCol + t * D;
+    const uint32_t o_at = tmem + lanes + t * D, s_col = tmem + lanes + C::kSCol, p_col = tmem + lanes + C::kPCol;
     // scores are multiplied by -1 or 0 first where the scale is not positive
     const float scale = (a.softmax_scale == 0.f ? 1.f : fabsf(a.softmax_scale)) * kLog2e;
     const float sign = a.softmax_scale < 0.f ? -1.f : 0.f;
     const bool positive = a.softmax_scale > 0.f;
     int tiles = 0, mine_t = 0, taken = 0;  // key tiles of this CTA so far, those of query tile t, and its items
     // The g-th product P V of this query tile is complete.  A wait tells phases apart
-    // by their parity alone, so it must not come when the one before may be missing
-    // or the one after be there: g - 1 (one score buffer), or g - 2 (two, a barrier
-    // each), was complete before the scores that this warp has seen, and the next one
-    // waits for weights that it has not written.
+    // by their parity alone, so it must not come when the phase before may be missing
+    // or the one after be there.  Each tile waits for the product that used its buffer
+    // of weights last; and the next one in that buffer waits for weights that this
+    // warp has not written yet.
     const auto values_done = [&](int g) {
-      return warp_wait(&bars.o_done[t][SB == 2 ? g & 1 : 0], (uint32_t)(SB == 2 ? g >> 1 : g) & 1u, a.err);
+      return warp_wait(&bars.o_done[NQ == 1 ? g & 1 : t], (uint32_t)(NQ == 1 ? g >> 1 : g) & 1u, a.err);
     };
+    const auto weights_free = [&](int g) { return g < (NQ == 1 ? 2 : 1) || values_done(g - (NQ == 1 ? 2 : 1)); };
     Item x;
     while (t < NQ && ok && next_item(x)) {
       const bool active = x.rows > 128 * t, used = x.rows > 128 * t + 32 * (warp & 3), live = row_t < x.rows;
@@ -363,19 +365,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sc = scale;
       uint32_t e_max = 0;
       for (int j = 0; active && j < x.n && ok; ++j) {
-        const int g = mine_t + j, buf = SB == 2 ? g & 1 : 0;
+        const int g = mine_t + j, buf = NQ == 1 ? g & 1 : t;
         const int vs = (tiles + j) % ST;
-        ok = warp_wait(&bars.s_full[t][buf], (uint32_t)(SB == 2 ? g >> 1 : g) & 1u, a.err) &&
-             warp_wait(&bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err);
-        if (!ok) break;
+        if (!(ok = warp_wait(&bars.s_full[buf], (uint32_t)(NQ == 1 ? g >> 1 : g) & 1u, a.err))) break;
         tc_fence_after();
+        uint32_t s[TILE];
+        if (used) {
+#pragma unroll
+          for (int c = 0; c < TILE; c += 32) tmem_ld_x32(s_col + (C::kSBufs == 1 ? 0 : buf) * TILE + c, s + c);
+          tmem_ld_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.s_free[C::kSBufs == 1 ? 0 : buf]);
+        if (!(ok = warp_wait(&bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err))) break;
         if (used) {
           if (E4M3 && j == 0) sc = scale * q_scale[taken & 1][row_t];
-          const uint32_t at = s_at + buf * TILE;
-          uint32_t s[TILE];
-#pragma unroll
-          for (int c = 0; c < TILE; c += 32) tmem_ld_x32(at + c, s + c);
-          tmem_ld_wait();
+          const uint32_t at = p_col + buf * (TILE / 2);
           if (!positive) {
 #pragma unroll
             for (int c = 0; c < TILE; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * sign);
@@ -407,23 +413,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          float tops[4];
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tops[c] = fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 4]));
+          for (int c = 0; c < TILE; c += 8)
 #pragma unroll
-          for (int c = 8; c < TILE; c += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], fmaxf(__uint_as_float(s[c + k]), __uint_as_float(s[c + k + 4])));
-          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            for (int k = 0; k < 4; ++k) tops[k] = max3(tops[k], __uint_as_float(s[c + k]), __uint_as_float(s[c + k + 4]));
+          const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
           // scores are S here, to be multiplied by sc, or (e4m3) in base 2 already
           const float unit = E4M3 ? 1.f : sc;
           const bool grew = m != -INFINITY && (top - m) * unit > kLazy;
           if (m == -INFINITY) m = top;
+          // the buffer of weights is free, and (g - 1: the last product, else in order) O
+          // may be touched, once these are done
+          if (!(ok = weights_free(g))) break;
           if (__any_sync(0xffffffffu, grew)) {
             const float f = grew ? ex2((m - top) * unit) : 1.f;
             if (grew) m = top;
             l *= f;
-            ok = values_done(g - 1);
+            if (NQ == 1 && !(ok = values_done(g - 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -473,10 +480,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l += more;
           tmem_st_wait();
+        } else if (!(ok = weights_free(g))) {  // a warp without rows must not run ahead of the others
+          break;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[t][buf]);
+        if (lane == 0) mbar_arrive(&bars.p_full[buf]);
       }
       // ---- the piece ends: O is complete once its last product is
       if (active && x.n > 0 && ok) {
@@ -541,96 +550,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t base = smem_u32(smem);
       const uint64_t q_desc = sdesc_sw128(base, 1024), k_desc = sdesc_sw128(base + C::kKAt, 1024), v_desc = sdesc_v(base + C::kVAt, TILE * 128);
       uint64_t *k_ready = E4M3 ? bars.k_ready : bars.k_full;
-      int ks = 0, vs = 0;                       // next stages of K and V, and their phases
-      uint32_t kph = 0, vph = 0;
-      uint32_t count0 = 0, count1 = 0, q_seen0 = 0, q_seen1 = 0;  // products P V, and Q tiles, of query tiles 0 and 1
-      // S of query tile t with the key tile in stage ks; g: the how manieth of this query tile
+      int ks = 0, vs = 0;                       // next stages of K and V
+      uint32_t kph = 0;
+      uint32_t count0 = 0, count1 = 0, q_seen0 = 0, q_seen1 = 0;  // key tiles, and Q tiles, of query tiles 0 and 1
+      uint32_t used = 0;                        // times that the one score buffer was used (dim 128)
+      // Scores of query tile t with the key tile in stage ks, the g-th of this query tile
       const auto qk = [&](int t, uint32_t g, bool last_key, bool last_q) {
-        const uint32_t buf = SB == 2 ? g & 1u : 0u;
+        const uint32_t buf = NQ == 1 ? g & 1u : t, sb = C::kSBufs == 1 ? 0u : buf;
+        const uint32_t use = C::kSBufs == 1 ? used++ : NQ == 1 ? g >> 1 : g;
+        if (!warp_wait(&bars.s_free[sb], (use & 1u) ^ 1u, a.err)) return false;  // what was there has been read
+        tc_fence_after();
         if (leader) {
           const uint64_t qd = q_desc + (uint64_t)((uint32_t)t * (C::kQ >> 4)), kd = k_desc + (uint64_t)((uint32_t)ks * (C::kSide >> 4));
-          const uint32_t d = tmem + t * C::kSCols + buf * TILE;
+          const uint32_t d = tmem + C::kSCol + sb * TILE;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             tc_mma_f16(d, qd + (uint64_t)((k / 4) * (128 * 128 >> 4) + (k % 4) * 2), kd + (uint64_t)((k / 4) * (TILE * 128 >> 4) + (k % 4) * 2), id_qk, k != 0);
-          tc_commit(&bars.s_full[t][buf]);
+          tc_commit(&bars.s_full[buf]);
           if (last_key) tc_commit(&bars.k_empty[ks]);
           if (last_q) tc_commit(&bars.q_empty[t]);
         }
         __syncwarp();
         if (last_key && ++ks == ST) ks = 0, kph ^= 1u;
+        return true;
       };
+      // its weights times the values in stage vs.  (Whoever wrote the weights has seen that V is ready.)
       const auto pv = [&](int t, uint32_t g, bool fresh, bool last_value) {
-        const uint32_t buf = SB == 2 ? g & 1u : 0u;
-        if (!warp_wait(&bars.p_full[t][buf], (SB == 2 ? g >> 1 : g) & 1u, a.err)) return false;
+        const uint32_t buf = NQ == 1 ? g & 1u : t;
+        if (!warp_wait(&bars.p_full[buf], (NQ == 1 ? g >> 1 : g) & 1u, a.err)) return false;
         tc_fence_after();
         if (leader) {
           const uint64_t vd = v_desc + (uint64_t)((uint32_t)vs * (C::kSide >> 4));
-          const uint32_t d = tmem + C::kOCol + t * D, pa = tmem + t * C::kSCols + buf * TILE;
+          const uint32_t d = tmem + t * D, pa = tmem + C::kPCol + buf * (TILE / 2);
 #pragma unroll
           for (int k = 0; k < TILE / 16; ++k) tc_mma_ts(d, pa + k * 8, vd + (uint64_t)(k * (16 * 128 >> 4)), id_pv, k != 0 || !fresh);
-          tc_commit(&bars.o_done[t][buf]);
+          tc_commit(&bars.o_done[buf]);
           if (last_value) tc_commit(&bars.v_empty[vs]);
         }
         __syncwarp();
-        if (last_value && ++vs == ST) vs = 0, vph ^= 1u;
-        return true;
-      };
-      const auto key_tile = [&]() {
-        if (!warp_wait(&k_ready[ks], kph, a.err)) return false;
-        tc_fence_after();
+        if (last_value && ++vs == ST) vs = 0;
         return true;
       };
       Item x;
-      int n = 0, act = 0;
-      const auto start = [&]() {  // the next item that has tiles, its first scores
-        n = 0;
-        while (next_item(x)) {
-          n = __shfl_sync(0xffffffffu, x.n, 0);
-          act = NQ == 1 || __shfl_sync(0xffffffffu, x.rows, 0) <= 128 ? 1 : 2;
-          if (n > 0) break;
-          if (leader) free_item();
-          ++it;
-        }
-        if (!ok || n <= 0) return false;
-        if (!warp_wait(&bars.q_full[0], q_seen0++ & 1u, a.err) || !key_tile()) return ok = false;
-        qk(0, count0, act == 1, n == 1);
-        if (act == 2) {
-          if (!warp_wait(&bars.q_full[1], q_seen1++ & 1u, a.err)) return ok = false;
-          tc_fence_after();
-          qk(1, count1, true, n == 1);
-        }
-        return true;
-      };
-      bool more = start();
-      while (more) {
-        for (int j = 0; j < n && ok; ++j) {
-          const bool next = j + 1 < n, last_q = j + 2 == n;
-          if (SB == 2) {
-            // with two score buffers the next scores come before this tile's values
-            if (next) {
-              if (!(ok = key_tile())) break;
-              qk(0, count0 + j + 1, true, last_q);
-            }
-            ok = warp_wait(&bars.v_ready[vs], vph, a.err) && pv(0, count0 + j, j == 0, true);
-          } else {
-            ok = warp_wait(&bars.v_ready[vs], vph, a.err) && pv(0, count0 + j, j == 0, act == 1);
-            if (next && ok) {
-              if (!(ok = key_tile())) break;
-              qk(0, count0 + j + 1, act == 1, last_q);
-            }
-            if (act == 2 && ok) {
-              ok = pv(1, count1 + j, j == 0, true);
-              if (next && ok) qk(1, count1 + j + 1, true, last_q);
-            }
-          }
+      while (ok && next_item(x)) {
+        const int n = __shfl_sync(0xffffffffu, x.n, 0), act = NQ == 1 || __shfl_sync(0xffffffffu, x.rows, 0) <= 128 ? 1 : 2;
+        // The scores of the next key tile come before the products with this one's
+        // values, so that the softmax of one overlaps both products of the other.
+        for (int j = 0; n > 0 && j <= n; ++j) {
+          if (j == 0 && !(ok = warp_wait(&bars.q_full[0], q_seen0++ & 1u, a.err))) break;
+          if (j < n && !(ok = warp_wait(&k_ready[ks], kph, a.err) && qk(0, count0 + j, act == 1, j + 1 == n))) break;
+          if (j > 0 && !(ok = pv(0, count0 + j - 1, j == 1, act == 1))) break;
+          if (act == 1) continue;
+          if (j == 0 && !(ok = warp_wait(&bars.q_full[1], q_seen1++ & 1u, a.err))) break;
+          if (j < n && !(ok = qk(1, count1 + j, true, j + 1 == n))) break;
+          if (j > 0 && !(ok = pv(1, count1 + j - 1, j == 1, true))) break;
         }
         if (!ok) break;
         count0 += n;
         if (act == 2) count1 += n;
+        __syncwarp();
         if (leader) free_item();
         ++it;
-        more = start();
       }
     } else if (warp == 9) {
       // ----------------------------------------------- work list, copies of K and V
@@ -815,8 +795,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // copies in flight land before the CTA may end
       const int left = min(tiles, ST);
       for (int j = tiles - left; !ok && j < tiles; ++j) {
-        wait_on(&bars.k_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
-        wait_on(&bars.v_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
+        warp_wait(&bars.k_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
+        warp_wait(&bars.v_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
       }
     } else {
       // ------------------------------------------------------------------- Q
@@ -878,6 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.q_full[t]);
         }
+        __syncwarp();
         if (lane == 0) free_item();
         ++it;
       }
