@@ -23,12 +23,12 @@
 //
 // Roles of a CTA's 16 warps, connected by mbarriers:
 //   0..3, 4..7  softmax of query tile 0 and 1: a thread owns a row of S
-//   8           issues the products
+//   8, 10       issue the products, Q K^T and P V.  (Issuing and the waits before it
+//               take one warp about as long as the tensor cores take for both.)
 //   9           finds the work and issues the copies of K and V (TMA, a page each)
-//   10, 11      fetch Q
-//   12..15      prepare what was copied: rows of V that no query sees become zeros
-//               (their weights are 0, but 0 times a NaN is not); an e4m3 cache is
-//               converted to fp16 in place
+//   12..15      fetch Q and prepare what was copied: rows of V that no query sees
+//               become zeros (their weights are 0, but 0 times a NaN is not); an e4m3
+//               cache is converted to fp16 in place
 //
 // Work split.  An item is (request, key head, block of rows), its cost its key
 // tiles and kItemCost; every CTA of a persistent grid takes an equal run of the
@@ -153,19 +153,37 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D[tmem] (+)= A[smem desc or tmem] * B[smem desc], kind::f16, issued by the lanes
+// whose `lead` is not 0.  (A predicate and not a branch, so that the descriptors
+// stay uniform values: 8 products with both operands in shared memory issue in 126
+// cycles, in a branch of one lane in 365; with one in tensor memory 60 and 244.
+// They run for 512.)
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+// tc_commit by the lanes whose `lead` is not 0.
+__device__ __forceinline__ void tc_commit_if(uint64_t *bar, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)), "r"(lead)
       : "memory");
 }
 // One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
-  return p != 0;
+  return p;
 }
 #define Q4K_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define Q4K_V8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
@@ -190,12 +208,18 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = global_ns();
-  for (;;) {
+#pragma unroll 1
+  do {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) break;
-  }
+  } while (!__any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs));
   set_device_error(err, kDevErrTimeout);
   return false;
+}
+// Two waits, whose first polls go out together.
+__device__ __forceinline__ bool warp_wait2(uint64_t *bar, uint32_t parity, uint64_t *bar2, uint32_t parity2, unsigned *err) {
+  const bool x = mbar_try_wait(bar, parity), y = mbar_try_wait(bar2, parity2);
+  if (__all_sync(0xffffffffu, x && y)) return true;
+  return warp_wait(bar, parity, err) && warp_wait(bar2, parity2, err);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -270,9 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   grid_launch_dependents();
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) mbar_init(&bars.item_full[i], 1), mbar_init(&bars.item_empty[i], 1 + 2 + 4 * NQ + 4);
+    for (int i = 0; i < kRing; ++i) mbar_init(&bars.item_full[i], 1), mbar_init(&bars.item_empty[i], 2 + 4 * NQ + 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.q_full[i], 2), mbar_init(&bars.q_empty[i], 1);
+      mbar_init(&bars.q_full[i], 4), mbar_init(&bars.q_empty[i], 1);
       mbar_init(&bars.s_full[i], 1), mbar_init(&bars.s_free[i], 4), mbar_init(&bars.p_full[i], 4), mbar_init(&bars.o_done[i], 1);
     }
     for (int i = 0; i < ST; ++i) {
@@ -335,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
     // ---------------------------------------------------------------- softmax
     const int t = warp >> 2, row_in = 32 * (warp & 3) + lane, row_t = 128 * t + row_in;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -539,78 +563,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++it;
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-    if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    if (warp == 8 || warp == 10) {
       // ------------------------------------------------------------- products
-      // The whole warp runs this, so that descriptors are uniform values; one lane
-      // issues.  (With one lane alone in here 8 products took 700 to 800 cycles to
-      // issue, and 512 to run.)
-      const bool leader = elect_one();
-      constexpr uint32_t id_qk = idesc_of(!E4M3, false, TILE), id_pv = idesc_of(!E4M3, true, D);
+      // A whole warp runs each half, so that descriptors are uniform values; one lane issues.
+      const uint32_t leader = elect_one();
       const uint32_t base = smem_u32(smem);
-      const uint64_t q_desc = sdesc_sw128(base, 1024), k_desc = sdesc_sw128(base + C::kKAt, 1024), v_desc = sdesc_v(base + C::kVAt, TILE * 128);
-      uint64_t *k_ready = E4M3 ? bars.k_ready : bars.k_full;
-      int ks = 0, vs = 0;                       // next stages of K and V
-      uint32_t kph = 0;
-      uint32_t count0 = 0, count1 = 0, q_seen0 = 0, q_seen1 = 0;  // key tiles, and Q tiles, of query tiles 0 and 1
-      uint32_t used = 0;                        // times that the one score buffer was used (dim 128)
-      // Scores of query tile t with the key tile in stage ks, the g-th of this query tile
-      const auto qk = [&](int t, uint32_t g, bool last_key, bool last_q) {
-        const uint32_t buf = NQ == 1 ? g & 1u : t, sb = C::kSBufs == 1 ? 0u : buf;
-        const uint32_t use = C::kSBufs == 1 ? used++ : NQ == 1 ? g >> 1 : g;
-        if (!warp_wait(&bars.s_free[sb], (use & 1u) ^ 1u, a.err)) return false;  // what was there has been read
-        tc_fence_after();
-        if (leader) {
+      uint32_t count0 = 0, count1 = 0;  // key tiles of query tiles 0 and 1
+      Item x;
+      if (warp == 8) {
+        constexpr uint32_t id_qk = idesc_of(!E4M3, false, TILE);
+        const uint64_t q_desc = sdesc_sw128(base, 1024), k_desc = sdesc_sw128(base + C::kKAt, 1024);
+        uint64_t *k_ready = E4M3 ? bars.k_ready : bars.k_full;
+        int ks = 0;         // next stage of K
+        uint32_t kph = 0, q_seen0 = 0, q_seen1 = 0;
+        uint32_t used = 0;  // times that the one score buffer was used (dim 128)
+        // Scores of query tile t with the key tile in stage ks, the g-th of this query tile
+        const auto qk = [&](int t, uint32_t g, bool first_key, bool last_key, bool last_q) {
+          const uint32_t buf = NQ == 1 ? g & 1u : t, sb = C::kSBufs == 1 ? 0u : buf;
+          const uint32_t use = C::kSBufs == 1 ? used++ : NQ == 1 ? g >> 1 : g;
+          // the key tile is there, and the scores that were in this buffer have been read
+          const uint32_t sp = (use & 1u) ^ 1u;
+          if (!(first_key ? warp_wait2(&k_ready[ks], kph, &bars.s_free[sb], sp, a.err) : warp_wait(&bars.s_free[sb], sp, a.err))) return false;
+          tc_fence_after();
           const uint64_t qd = q_desc + (uint64_t)((uint32_t)t * (C::kQ >> 4)), kd = k_desc + (uint64_t)((uint32_t)ks * (C::kSide >> 4));
           const uint32_t d = tmem + C::kSCol + sb * TILE;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            tc_mma_f16(d, qd + (uint64_t)((k / 4) * (128 * 128 >> 4) + (k % 4) * 2), kd + (uint64_t)((k / 4) * (TILE * 128 >> 4) + (k % 4) * 2), id_qk, k != 0);
-          tc_commit(&bars.s_full[buf]);
-          if (last_key) tc_commit(&bars.k_empty[ks]);
-          if (last_q) tc_commit(&bars.q_empty[t]);
+            tc_mma_ss(d, qd + (uint64_t)((k / 4) * (128 * 128 >> 4) + (k % 4) * 2), kd + (uint64_t)((k / 4) * (TILE * 128 >> 4) + (k % 4) * 2), id_qk, k != 0, leader);
+          tc_commit_if(&bars.s_full[buf], leader);
+          tc_commit_if(&bars.k_empty[ks], last_key ? leader : 0u);
+          tc_commit_if(&bars.q_empty[t], last_q ? leader : 0u);
+          if (last_key && ++ks == ST) ks = 0, kph ^= 1u;
+          return true;
+        };
+        while (ok && next_item(x)) {
+          const int n = __shfl_sync(0xffffffffu, x.n, 0), act = NQ == 1 || __shfl_sync(0xffffffffu, x.rows, 0) <= 128 ? 1 : 2;
+          for (int j = 0; j < n; ++j) {
+            if (j == 0 && !(ok = warp_wait(&bars.q_full[0], q_seen0++ & 1u, a.err))) break;
+            if (!(ok = qk(0, count0 + j, true, act == 1, j + 1 == n))) break;
+            if (act == 1) continue;
+            if (j == 0 && !(ok = warp_wait(&bars.q_full[1], q_seen1++ & 1u, a.err))) break;
+            if (!(ok = qk(1, count1 + j, false, true, j + 1 == n))) break;
+          }
+          if (!ok) break;
+          count0 += n;
+          if (act == 2) count1 += n;
+          __syncwarp();
+          if (leader) free_item();
+          ++it;
         }
-        __syncwarp();
-        if (last_key && ++ks == ST) ks = 0, kph ^= 1u;
-        return true;
-      };
-      // its weights times the values in stage vs.  (Whoever wrote the weights has seen that V is ready.)
-      const auto pv = [&](int t, uint32_t g, bool fresh, bool last_value) {
-        const uint32_t buf = NQ == 1 ? g & 1u : t;
-        if (!warp_wait(&bars.p_full[buf], (NQ == 1 ? g >> 1 : g) & 1u, a.err)) return false;
-        tc_fence_after();
-        if (leader) {
+      } else {
+        constexpr uint32_t id_pv = idesc_of(!E4M3, true, D);
+        const uint64_t v_desc = sdesc_v(base + C::kVAt, TILE * 128);
+        int vs = 0;  // next stage of V
+        // The weights of query tile t times the values in stage vs.  (Whoever wrote the
+        // weights has seen that V is ready.)
+        const auto pv = [&](int t, uint32_t g, bool fresh, bool last_value) {
+          const uint32_t buf = NQ == 1 ? g & 1u : t;
+          if (!warp_wait(&bars.p_full[buf], (NQ == 1 ? g >> 1 : g) & 1u, a.err)) return false;
+          tc_fence_after();
           const uint64_t vd = v_desc + (uint64_t)((uint32_t)vs * (C::kSide >> 4));
           const uint32_t d = tmem + t * D, pa = tmem + C::kPCol + buf * (TILE / 2);
 #pragma unroll
-          for (int k = 0; k < TILE / 16; ++k) tc_mma_ts(d, pa + k * 8, vd + (uint64_t)(k * (16 * 128 >> 4)), id_pv, k != 0 || !fresh);
-          tc_commit(&bars.o_done[buf]);
-          if (last_value) tc_commit(&bars.v_empty[vs]);
+          for (int k = 0; k < TILE / 16; ++k) tc_mma_ts(d, pa + k * 8, vd + (uint64_t)(k * (16 * 128 >> 4)), id_pv, k != 0 || !fresh, leader);
+          tc_commit_if(&bars.o_done[buf], leader);
+          tc_commit_if(&bars.v_empty[vs], last_value ? leader : 0u);
+          if (last_value && ++vs == ST) vs = 0;
+          return true;
+        };
+        while (ok && next_item(x)) {
+          const int n = __shfl_sync(0xffffffffu, x.n, 0), act = NQ == 1 || __shfl_sync(0xffffffffu, x.rows, 0) <= 128 ? 1 : 2;
+          for (int j = 0; j < n; ++j) {
+            if (!(ok = pv(0, count0 + j, j == 0, act == 1))) break;
+            if (act == 2 && !(ok = pv(1, count1 + j, j == 0, true))) break;
+          }
+          if (!ok) break;
+          count0 += n;
+          if (act == 2) count1 += n;
+          __syncwarp();
+          if (leader) free_item();
+          ++it;
         }
-        __syncwarp();
-        if (last_value && ++vs == ST) vs = 0;
-        return true;
-      };
-      Item x;
-      while (ok && next_item(x)) {
-        const int n = __shfl_sync(0xffffffffu, x.n, 0), act = NQ == 1 || __shfl_sync(0xffffffffu, x.rows, 0) <= 128 ? 1 : 2;
-        // The scores of the next key tile come before the products with this one's
-        // values, so that the softmax of one overlaps both products of the other.
-        for (int j = 0; n > 0 && j <= n; ++j) {
-          if (j == 0 && !(ok = warp_wait(&bars.q_full[0], q_seen0++ & 1u, a.err))) break;
-          if (j < n && !(ok = warp_wait(&k_ready[ks], kph, a.err) && qk(0, count0 + j, act == 1, j + 1 == n))) break;
-          if (j > 0 && !(ok = pv(0, count0 + j - 1, j == 1, act == 1))) break;
-          if (act == 1) continue;
-          if (j == 0 && !(ok = warp_wait(&bars.q_full[1], q_seen1++ & 1u, a.err))) break;
-          if (j < n && !(ok = qk(1, count1 + j, true, j + 1 == n))) break;
-          if (j > 0 && !(ok = pv(1, count1 + j - 1, j == 1, true))) break;
-        }
-        if (!ok) break;
-        count0 += n;
-        if (act == 2) count1 += n;
-        __syncwarp();
-        if (leader) free_item();
-        ++it;
       }
     } else if (warp == 9) {
       // ----------------------------------------------- work list, copies of K and V
@@ -716,14 +750,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           blocks_at();
         }
       };
-      Item x, y;
-      bool more = find(y);
-      if (more) ok = put(y);
-      while (more && ok) {
-        x = y;
-        more = find(y);  // the others know of an item before the copies of the one before it
+      Item x = {}, y = {};  // (no tiles yet)
+      for (bool more = true; more && ok; x = y) {
+        // the others know of an item before the copies of the one before it
+        more = find(y);
         if (more && !(ok = put(y))) break;
         // ---- its tiles.  Lanes hold 32 table entries from page tb0 on, and the 32 after them.
+        if (x.n == 0) continue;
         const int boxes = TILE >> p.box_shift;
         int tb0 = (x.t0 * TILE) >> p.page_shift;
         const auto table_at = [&](int i) { return i < a.max_pages ? a.table[x.r * a.ldt + i] : -1; };
@@ -798,80 +831,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_wait(&bars.k_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
         warp_wait(&bars.v_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
       }
-    } else {
-      // ------------------------------------------------------------------- Q
-      // Each of the two warps takes 64 rows of a query tile.
-      int count[2] = {0, 0};
-      Item x;
-      while (ok && next_item(x)) {
-        for (int t = 0; t < NQ && x.n > 0 && x.rows > 128 * t && ok; ++t) {
-          const int c = count[t]++;
-          uint8_t *dst = smem + t * C::kQ;
-          constexpr int CH = D / 8;  // 16-byte pieces of a row
-          const int first = 64 * (warp - 10);
-          // a lane knows where two rows lie; -1: not of this item, zeros
-          int64_t where[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int rr = 128 * t + first + 32 * h + lane, rw = x.row0 + rr, tok = (int)p.by_group.div(rw);
-            where[h] = rr < x.rows ? ((int64_t)x.tok0 + tok) * a.ldq + (int64_t)(x.head * p.group + (rw - tok * p.group)) * a.ldq_head : -1;
-          }
-          if (!(ok = warp_wait(&bars.q_empty[t], ((uint32_t)c & 1u) ^ 1u, a.err))) break;
-          constexpr int RPI = 32 / CH ? 32 / CH : 1;  // rows of an iteration (CH = 32: one, else more)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll 4
-            for (int i = 0; i < 32 / RPI; ++i) {
-              const int rr = i * RPI + lane / CH, row = first + 32 * h + rr, ch = lane % CH;
-              const int64_t from = __shfl_sync(0xffffffffu, where[h], rr);
-              cp_async16(dst + (ch / 8) * 128 * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), static_cast<const __nv_bfloat16 *>(a.q) + max(from, (int64_t)0) + ch * 8, from >= 0 ? 16 : 0);
-            }
-          cp_async_commit();
-          cp_async_wait<0>();
-          if (E4M3) {
-            // rows to fp16, times a power of two that brings their largest value to 2^14..2^15
-            __syncwarp();
-            for (int row = first + lane; row < first + 64; row += 32) {
-              uint8_t *r0 = dst + row * 128;
-              uint32_t top = 0;
-              for (int ch = 0; ch < CH; ++ch) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(r0 + (ch / 8) * 128 * 128 + (((ch & 7) ^ (row & 7)) << 4));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max(w[e] >> 16 & 0x7fffu, w[e] & 0x7fffu));
-              }
-              const int ex = (int)(top >> 7) - 127;         // of the largest value
-              const int up = min(max(14 - ex, -113), 126);  // factor 2^up
-              const float f = __int_as_float((up + 127) << 23);
-              for (int ch = 0; ch < CH; ++ch) {
-                uint4 *at = reinterpret_cast<uint4 *>(r0 + (ch / 8) * 128 * 128 + (((ch & 7) ^ (row & 7)) << 4));
-                const uint4 v = *at;
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-                *at = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-              q_scale[c & 1][128 * t + row] = __int_as_float((127 - up) << 23);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.q_full[t]);
-        }
-        __syncwarp();
-        if (lane == 0) free_item();
-        ++it;
-      }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     // ---------------------------------------------------------------- prepare
     const int th = tid - 384;  // 0..127
-    int tiles = 0;
+    int tiles = 0, count[2] = {0, 0};
     Item x;
     for (;;) {
       const bool more = next_item(x);
       if (!group_and(1, ok) || !more) break;
+      // ---- Q: a warp takes 32 rows of a query tile, a lane knows where one lies (-1: not of this item, zeros)
+      for (int t = 0; t < NQ && x.n > 0 && x.rows > 128 * t; ++t) {
+        const int c = count[t]++, first = 32 * (warp - 12), rr = 128 * t + first + lane, rw = x.row0 + rr, tok = (int)p.by_group.div(rw);
+        const int64_t where = rr < x.rows ? ((int64_t)x.tok0 + tok) * a.ldq + (int64_t)(x.head * p.group + (rw - tok * p.group)) * a.ldq_head : -1;
+        uint8_t *dst = smem + t * C::kQ;
+        constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows of an iteration
+        if (!(ok = warp_wait(&bars.q_empty[t], ((uint32_t)c & 1u) ^ 1u, a.err))) break;
+#pragma unroll 4
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int r = i * RPI + lane / CH, row = first + r, ch = lane % CH;
+          const int64_t from = __shfl_sync(0xffffffffu, where, r);
+          cp_async16(dst + (ch / 8) * 128 * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), static_cast<const __nv_bfloat16 *>(a.q) + max(from, (int64_t)0) + ch * 8, from >= 0 ? 16 : 0);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        if (E4M3) {
+          // rows to fp16, times a power of two that brings their largest value to 2^14..2^15
+          __syncwarp();
+          const int row = first + lane;
+          uint8_t *r0 = dst + row * 128;
+          uint32_t top = 0;
+          for (int ch = 0; ch < CH; ++ch) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(r0 + (ch / 8) * 128 * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] >> 16 & 0x7fffu, w[e] & 0x7fffu));
+          }
+          const int ex = (int)(top >> 7) - 127;         // of the largest value
+          const int up = min(max(14 - ex, -113), 126);  // factor 2^up
+          const float f = __int_as_float((up + 127) << 23);
+          for (int ch = 0; ch < CH; ++ch) {
+            uint4 *at = reinterpret_cast<uint4 *>(r0 + (ch / 8) * 128 * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            const uint4 v = *at;
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          q_scale[c & 1][128 * t + row] = __int_as_float((127 - up) << 23);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.q_full[t]);
+      }
+      if (!group_and(1, ok)) break;
       for (int j = 0; j < x.n; ++j, ++tiles) {
         const int s = tiles % ST;
         const uint32_t ph = (uint32_t)(tiles / ST) & 1u;
