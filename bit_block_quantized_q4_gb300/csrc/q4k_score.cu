@@ -4,20 +4,24 @@
 // "spec: specialized model runtimes", section "Architecture": what is read off
 // the logits belongs to tier T1, with the sampler.
 //
-// Mathematics.  With M a reference near the row's maximum, in one pass
-//   l = sum e^(x_i - M),   w = sum e^(x_i - M) (x_i - M),
-//   logp(t) = x_t - M - ln l,   entropy = ln l - w / l,
-// two parts with references M, M' are joined by l' e^(M' - M) and
-// (w' + (M' - M) l') e^(M' - M).  Differences below -128 count as -128, whose
-// e is 0 in fp32: so a logit of -infinity, or the lowest number of its type,
-// adds 0 and not 0 times infinity.
+// Mathematics.  In base 2: z_i = x_i log2 e - c with c a reference near the row's
+// maximum, one multiply-add with one rounding, and in one pass
+//   l = sum 2^z_i,   w = sum 2^z_i z_i,
+//   logp(t) = (z_t - log2 l) ln 2,   entropy = (log2 l - w / l) ln 2;
+// two parts with references c, c' are joined by l' 2^(c' - c) and
+// (w' + (c' - c) l') 2^(c' - c).  Logits below -10^30 count as -10^30 beside any
+// that are not: their weight is 0, and 0 times their z is 0 and not 0 times infinity.
+// That one rounding of c leaves a residue of |c| 2^-24 in every z, which is the same
+// for all and for z_t: of no account while |c| is small.  Rows whose maximum is beyond
+// 2^22 either way (all masked with the lowest number, say) are done again by
+// differences, x_i - max.
 //
 // Order.  Tokens are ordered by logit, highest first, equal ones by index: the
 // descending order of the distinct integers key_i = (monotone image of x_i) <<
 // 32 | ~i.
 //
 // Alternatives.  Every thread keeps the first of its highest logits.  The n-th
-// highest of the 32 maxima of half warps is a bound that at least n tokens
+// highest of the maxima of 32 groups of threads is a bound that at least n tokens
 // reach; a few dozen do in all, found again among the tokens of the threads whose
 // own maximum reaches it.  Should more reach it than the list holds, they are
 // taken one after the other instead.
@@ -40,10 +44,11 @@ namespace q4k {
 namespace {
 
 using u64 = unsigned long long;
-constexpr int kThreads = 512, kWarps = kThreads / 32, kGroups = 2 * kWarps;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kGroups = 4 * kWarps, kGroup = kThreads / kGroups;
+static_assert(kGroups == 32 && kGroup == 8, "one warp looks at the maxima of all groups, eight lanes each");
 constexpr int kTop = 32, kList = 1024, kMaxCluster = 8;
-constexpr float kLow = -128.f;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLow = -1e30f, kPlain = 4194304.f;  // what counts as masked; maxima up to here need no second pass
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Args {
   const void *logits;
@@ -78,22 +83,78 @@ __device__ __forceinline__ float one(const T *p) {
 
 // What a thread, a warp, a CTA knows of the tokens that it has seen.
 struct Sums {
-  float m, l, w;
+  float c, l, w;
 };
+constexpr float kNoRef = -3.0e38f;
 __device__ __forceinline__ void join(Sums &a, const Sums &b) {
-  const float m = fmaxf(a.m, b.m);
-  // without a token l is 0, and its reference says nothing
-  const float da = a.l == 0.f ? 0.f : fmaxf(a.m - m, kLow), db = b.l == 0.f ? 0.f : fmaxf(b.m - m, kLow);
-  const float fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);
+  const float c = fmaxf(a.c, b.c);
+  // without a token l is 0, and its reference says nothing; beyond 2^-200 a part counts for nothing
+  const float da = a.l == 0.f ? 0.f : fmaxf(a.c - c, -200.f), db = b.l == 0.f ? 0.f : fmaxf(b.c - c, -200.f);
+  const float fa = ex2(da), fb = ex2(db);
   a.w = fa * fmaf(da, a.l, a.w) + fb * fmaf(db, b.l, b.w);
   a.l = fa * a.l + fb * b.l;
-  a.m = m;
+  a.c = c;
 }
+// Eight logits as fp32, none below kLow and none NaN, and their maximum; with `raw`
+// their maximum as they are (NaN only if all are).
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  static __device__ __forceinline__ float raw_top(const Raw8<float> &r) {
+    return fmaxf(fmaxf(fmaxf(r.a.x, r.a.y), fmaxf(r.a.z, r.a.w)), fmaxf(fmaxf(r.b.x, r.b.y), fmaxf(r.b.z, r.b.w)));
+  }
+  static __device__ __forceinline__ float below(float x) {  // the next number below a finite one
+    const int b = __float_as_int(x + 0.f);
+    return b == 0 ? -1.4e-45f : __int_as_float(b > 0 ? b - 1 : b + 1);
+  }
+  static __device__ __forceinline__ float above(const Raw8<float> &r, float bar) {  // how many lie above
+    float v[8];
+    r.to(v);
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) n += v[j] > bar;
+    return (float)n;
+  }
+  static __device__ __forceinline__ void clamped(const Raw8<float> &r, float (&v)[8]) {
+    r.to(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fmaxf(v[j], kLow);
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
+  static __device__ __forceinline__ float raw_top(const Raw8<__nv_bfloat16> &r) {
+    const __nv_bfloat162 t = __hmax2(__hmax2(pair(r.a.x), pair(r.a.y)), __hmax2(pair(r.a.z), pair(r.a.w)));
+    return fmaxf(__low2float(t), __high2float(t));
+  }
+  static __device__ __forceinline__ float below(float x) {
+    const int b = __float_as_int(x + 0.f) >> 16;
+    return b == 0 ? __int_as_float(0x80010000) : __int_as_float((b > 0 ? b - 1 : b + 1) << 16);
+  }
+  static __device__ __forceinline__ float above(const Raw8<__nv_bfloat16> &r, float bar) {
+    const __nv_bfloat162 t = __float2bfloat162_rn(bar);  // (a bf16 value)
+    const __nv_bfloat162 n = __hadd2(__hadd2(__hgt2(pair(r.a.x), t), __hgt2(pair(r.a.y), t)), __hadd2(__hgt2(pair(r.a.z), t), __hgt2(pair(r.a.w), t)));
+    return __low2float(n) + __high2float(n);
+  }
+  static __device__ __forceinline__ void clamped(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
+    const __nv_bfloat162 low = __float2bfloat162_rn(kLow);
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 p = __hmax2(pair(w[j]), low);
+      const uint32_t u = *reinterpret_cast<const uint32_t *>(&p);
+      v[2 * j] = __uint_as_float(u << 16), v[2 * j + 1] = __uint_as_float(u & 0xffff0000u);
+    }
+  }
+};
 
 struct Shared {
   Sums sums[kWarps];
   int count[kWarps], infinite[kWarps];
-  u64 group[kGroups];       // highest key of each half warp
+  float top[kWarps];        // highest logit
+  u64 group[kGroups];       // highest key of each group
   u64 list[kList];
   u64 chosen[kTop];
   u64 bound;
@@ -101,6 +162,7 @@ struct Shared {
   // of all CTAs of the cluster, in the first one
   Sums all_sums[kMaxCluster];
   int all_count[kMaxCluster], all_infinite[kMaxCluster];
+  float all_top[kMaxCluster];
   u64 all_keys[kMaxCluster * kTop];
 };
 
@@ -131,9 +193,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   constexpr int kV = 8;
   const int head = min(hi - lo, (int)((16 - ((uintptr_t)(x + lo) & 15)) & 15) / (int)sizeof(T));
   const int v0 = lo + head, vectors = (hi - v0) / kV, tail = v0 + vectors * kV;
-  Sums s = {-3.4028235e38f, 0.f, 0.f};
+  Sums s = {kNoRef, 0.f, 0.f};
   float best = -INFINITY;  // highest logit, and where it was first seen (its vector's first token)
   int best_at = -1, count = 0, infinite = 0;
+  float above = 0.f;                           // tokens above the given one (whole numbers below 2^24)
+  const bool plain_xt = fabsf(xt) < INFINITY;  // has a next number below
+  const float under = plain_xt ? Eight<T>::below(xt) : xt;
+  float2 l2 = make_float2(0.f, 0.f), w2 = l2;  // s.l and s.w of the vectors
 
   const auto ahead = [&](float v, int i) {  // NaN counts as -infinity
     const float c = v > -INFINITY ? v : -INFINITY;
@@ -141,61 +207,82 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   };
   const auto single = [&](int i) {
     const float v = one(x + i);
-    if (v > best) best = v, best_at = i;
+    if (v > best || (v == best && i < best_at)) best = v, best_at = i;
     count += ahead(v, i);
-    if (v == INFINITY) ++infinite;
-    const Sums t = {v > -INFINITY ? v : s.m, v > -INFINITY ? 1.f : 0.f, 0.f};
-    join(s, t);
+    infinite += v == INFINITY;
+    if (fabsf(v) <= kPlain) {
+      const float c = v * kLog2e;
+      const Sums t = {c, 1.f, fmaf(v, kLog2e, -c)};
+      join(s, t);
+    }
   };
-  if (tid < head) single(lo + tid);
-  const auto eight = [&](const float (&v)[8], int i) {
-    float top = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+  const auto eight = [&](const Raw8<T> &raw, int i) {
+    const float top = Eight<T>::raw_top(raw);
     if (top > best) best = top, best_at = i;
     if (!(top < xt)) {
+      // before the token equal logits count, after it they do not
+      if (i + 8 <= token ? plain_xt : i >= token) {
+        above += Eight<T>::above(raw, i >= token ? xt : under);
+      } else {
+        float v[8];
+        raw.to(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) count += ahead(v[j], i + j);
-    }
-    if (top > s.m + 8.f) {
-      if (s.l != 0.f) {
-        const float d = fmaxf(s.m - top, kLow), f = ex2(d * kLog2e);
-        s.w = f * fmaf(d, s.l, s.w);
-        s.l *= f;
+        for (int j = 0; j < 8; ++j) count += ahead(v[j], i + j);
       }
-      s.m = top;
     }
-    if (s.m == INFINITY) {
+    if (!(top > 0.1f * kLow)) return;  // nothing but what is masked
+    const float ct = top * kLog2e;
+    if (ct > s.c + 12.f) {  // the reference follows when it lies 2^12 and more below
+      if (top == INFINITY) {
+        float v[8];
+        raw.to(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) infinite += v[j] == INFINITY;
-      return;
+        for (int j = 0; j < 8; ++j) infinite += v[j] == INFINITY;
+      } else {
+        // (l is 0 while there is no reference)
+        const float d = fmaxf(s.c - ct, -200.f), f = ex2(d);
+        const float2 f2 = make_float2(f, f);
+        w2 = __fmul2_rn(f2, __ffma2_rn(make_float2(d, d), l2, w2));
+        l2 = __fmul2_rn(f2, l2);
+        s.c = ct;
+      }
     }
-    const float2 m2 = make_float2(-s.m, -s.m);
-    float2 l2 = make_float2(0.f, 0.f), w2 = make_float2(0.f, 0.f);
+    float v[8];
+    Eight<T>::clamped(raw, v);
+    const float2 c2 = make_float2(-s.c, -s.c), log2e2 = make_float2(kLog2e, kLog2e);
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      float2 d = __fadd2_rn(make_float2(v[j], v[j + 1]), m2);
-      d = make_float2(fmaxf(d.x, kLow), fmaxf(d.y, kLow));  // (NaN too)
-      const float2 z = __fmul2_rn(d, make_float2(kLog2e, kLog2e)), e = make_float2(ex2(z.x), ex2(z.y));
+      const float2 z = __ffma2_rn(make_float2(v[j], v[j + 1]), log2e2, c2), e = make_float2(ex2(z.x), ex2(z.y));
       l2 = __fadd2_rn(l2, e);
-      w2 = __ffma2_rn(e, d, w2);
+      w2 = __ffma2_rn(e, z, w2);
     }
-    s.l += l2.x + l2.y;
-    s.w += w2.x + w2.y;
   };
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;  // vectors on their way
+  // the next vectors are on their way while these are worked on
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;
+  Raw8<T> next[U];
+  const T *from = x + v0;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (tid + u * kThreads < vectors) next[u].load(from + (tid + u * kThreads) * kV);
   for (int k0 = tid; k0 < vectors; k0 += U * kThreads) {
     Raw8<T> raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (k0 + u * kThreads < vectors) raw[u].load(x + v0 + (k0 + u * kThreads) * kV);
+    for (int u = 0; u < U; ++u) raw[u] = next[u];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (k0 + u * kThreads < vectors) {
-        float v[8];
-        raw[u].to(v);
-        eight(v, v0 + (k0 + u * kThreads) * kV);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + (U + u) * kThreads;
+      if (k < vectors) next[u].load(from + k * kV);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kThreads;
+      if (k < vectors) eight(raw[u], v0 + k * kV);
+    }
   }
+  s.l = l2.x + l2.y, s.w = w2.x + w2.y;
+  if (tid < head) single(lo + tid);
   if (tid < hi - tail) single(tail + tid);
+  count += (int)above;
 
   // the key of this thread's best
   u64 key = 0;
@@ -209,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     Sums t;
-    t.m = __shfl_xor_sync(0xffffffffu, s.m, o), t.l = __shfl_xor_sync(0xffffffffu, s.l, o), t.w = __shfl_xor_sync(0xffffffffu, s.w, o);
+    t.c = __shfl_xor_sync(0xffffffffu, s.c, o), t.l = __shfl_xor_sync(0xffffffffu, s.l, o), t.w = __shfl_xor_sync(0xffffffffu, s.w, o);
     // the lower lane's part first, on both sides: the same sums in every lane
     if (lane & o) {
       join(t, s);
@@ -220,12 +307,15 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   }
   count = __reduce_add_sync(0xffffffffu, count);
   infinite = __reduce_add_sync(0xffffffffu, infinite);
-  if (lane == 0) sh.sums[warp] = s, sh.count[warp] = count, sh.infinite[warp] = infinite;
+  float top = best;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) sh.sums[warp] = s, sh.count[warp] = count, sh.infinite[warp] = infinite, sh.top[warp] = top;
   if (a.top) {
     u64 g = key;
 #pragma unroll
-    for (int o = 8; o; o >>= 1) g = max64(g, shfl64(g, lane ^ o));
-    if ((lane & 15) == 0) sh.group[2 * warp + lane / 16] = g;
+    for (int o = kGroup / 2; o; o >>= 1) g = max64(g, shfl64(g, lane ^ o));
+    if (lane % kGroup == 0) sh.group[(32 / kGroup) * warp + lane / kGroup] = g;
   }
   __syncthreads();
 
@@ -311,7 +401,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
   if (warp == 0) {
     s = sh.sums[0];
-    for (int i = 1; i < kWarps; ++i) join(s, sh.sums[i]);
+    top = sh.top[0];
+    for (int i = 1; i < kWarps; ++i) join(s, sh.sums[i]), top = fmaxf(top, sh.top[i]);
     count = lane < kWarps ? sh.count[lane] : 0, infinite = lane < kWarps ? sh.infinite[lane] : 0;
     count = __reduce_add_sync(0xffffffffu, count);
     infinite = __reduce_add_sync(0xffffffffu, infinite);
@@ -321,24 +412,45 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
       asm("mapa.u64 %0, %1, 0;\n" : "=l"(p) : "l"((uint64_t)&sh));
       first = reinterpret_cast<Shared *>(p);
     }
-    if (lane == 0) first->all_sums[rank] = s, first->all_count[rank] = count, first->all_infinite[rank] = infinite;
+    if (lane == 0) first->all_sums[rank] = s, first->all_count[rank] = count, first->all_infinite[rank] = infinite, first->all_top[rank] = top;
     if (lane < n) first->all_keys[rank * kTop + lane] = sh.chosen[lane];
   }
   if (ranks > 1) cluster_sync();
   else __syncthreads();
   if (rank) return;
-  s = sh.all_sums[0], count = sh.all_count[0], infinite = sh.all_infinite[0];
-  for (int i = 1; i < ranks; ++i) join(s, sh.all_sums[i]), count += sh.all_count[i], infinite += sh.all_infinite[i];
+  s = sh.all_sums[0], count = sh.all_count[0], infinite = sh.all_infinite[0], top = sh.all_top[0];
+  for (int i = 1; i < ranks; ++i) {
+    join(s, sh.all_sums[i]);
+    count += sh.all_count[i], infinite += sh.all_infinite[i], top = fmaxf(top, sh.all_top[i]);
+  }
+  // a finite maximum beyond what one rounding of the reference allows: again by differences
+  const bool again = fabsf(top) > kPlain && fabsf(top) < INFINITY;
+  if (again) {
+    s = {0.f, 0.f, 0.f};
+    for (int i = tid; i < a.vocab; i += kThreads) {
+      const float z = fmaxf((one(x + i) - top) * kLog2e, -200.f), e = ex2(z);  // (NaN too)
+      s.l += e;
+      s.w = fmaf(e, z, s.w);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s.l += __shfl_xor_sync(0xffffffffu, s.l, o), s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+    if (lane == 0) sh.sums[warp] = s;
+    __syncthreads();
+    s = sh.sums[0];
+    for (int i = 1; i < kWarps; ++i) s.l += sh.sums[i].l, s.w += sh.sums[i].w;
+  }
   // logits of +infinity share all the mass
-  const float ln = infinite ? logf((float)infinite) : logf(s.l);
+  const float lg = log2f(infinite ? (float)infinite : s.l);
   const auto logp_of = [&](float v) {
     if (!(v > -INFINITY)) return -INFINITY;
-    return infinite ? (v == INFINITY ? -ln : -INFINITY) : (v - s.m) - ln;
+    if (infinite) return v == INFINITY ? -lg * kLn2 : -INFINITY;
+    if (again) return (v - top) - lg * kLn2;
+    return fabsf(v) > kPlain ? v - (s.c + lg) * kLn2 : (fmaf(v, kLog2e, -s.c) - lg) * kLn2;
   };
   if (tid == 0) {
     a.logp[row] = real ? logp_of(xt) : -INFINITY;
     if (a.rank) a.rank[row] = real ? count : -1;
-    if (a.entropy) a.entropy[row] = infinite ? ln : s.l == 0.f ? 0.f : ln - s.w / s.l;
+    if (a.entropy) a.entropy[row] = (infinite ? lg : s.l == 0.f ? 0.f : lg - s.w / s.l) * kLn2;
   }
   // the n highest of all: of ranks x n keys, those with fewer than n above
   if (tid < ranks * n) {
