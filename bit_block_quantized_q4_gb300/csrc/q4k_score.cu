@@ -259,13 +259,12 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   };
   // the next vectors are on their way while these are worked on
   constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  Raw8<T> next[U];
+  Raw8<T> next[U], raw[U];
   const T *from = x + v0;
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (tid + u * kThreads < vectors) next[u].load(from + (tid + u * kThreads) * kV);
   for (int k0 = tid; k0 < vectors; k0 += U * kThreads) {
-    Raw8<T> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) raw[u] = next[u];
 #pragma unroll
@@ -288,28 +287,30 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   u64 key = 0;
   if (a.top && best > -INFINITY) {
     int at = best_at;
-    while (one(x + at) != best) ++at;  // within its vector
+    if (at >= v0 && at < tail) {  // the first of its vector that is as high
+      float v[8];
+      load8(x + at, v);
+      int j = 7;
+#pragma unroll
+      for (int e = 6; e >= 0; --e) j = v[e] == best ? e : j;
+      at += j;
+    }
     key = key_at(best, at);
   }
 
-  // ---- sums of the CTA
+  // ---- sums of the CTA: to the highest reference of the warp, then of the CTA
+  const auto onto = [&](float c) {
+    const float d = s.l == 0.f ? 0.f : fmaxf(s.c - c, -200.f), f = ex2(d);
+    s.w = f * fmaf(d, s.l, s.w);
+    s.l *= f;
+    s.c = c;
+  };
+  onto(of_key(__reduce_max_sync(0xffffffffu, key_of(s.c))));
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Sums t;
-    t.c = __shfl_xor_sync(0xffffffffu, s.c, o), t.l = __shfl_xor_sync(0xffffffffu, s.l, o), t.w = __shfl_xor_sync(0xffffffffu, s.w, o);
-    // the lower lane's part first, on both sides: the same sums in every lane
-    if (lane & o) {
-      join(t, s);
-      s = t;
-    } else {
-      join(s, t);
-    }
-  }
+  for (int o = 16; o; o >>= 1) s.l += __shfl_xor_sync(0xffffffffu, s.l, o), s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
   count = __reduce_add_sync(0xffffffffu, count);
   infinite = __reduce_add_sync(0xffffffffu, infinite);
-  float top = best;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float top = of_key(__reduce_max_sync(0xffffffffu, key_of(best)));
   if (lane == 0) sh.sums[warp] = s, sh.count[warp] = count, sh.infinite[warp] = infinite, sh.top[warp] = top;
   if (a.top) {
     u64 g = key;
@@ -321,7 +322,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
 
   // ---- this CTA's `top` highest keys, in order, in chosen[]
   const int n = a.top;
-  if (n) {
+  if (n == 1) {
+    if (warp == 0) {
+      u64 g = sh.group[lane];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) g = max64(g, shfl64(g, lane ^ o));
+      if (lane == 0) sh.chosen[0] = g;
+    }
+  } else if (n) {
     if (warp == 0) {
       const u64 g = sh.group[lane];
       int above = 0;
@@ -333,23 +341,43 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
     }
     __syncthreads();
     const u64 bound = sh.bound;
+    const float bar = bound > 1 ? of_key((uint32_t)(bound >> 32)) : -INFINITY;
     const auto offer = [&](u64 k) {
       if (k >= bound) {
         const int i = atomicAdd(&sh.listed, 1);
         if (i < kList) sh.list[i] = k;
       }
     };
-    // the threads whose best reaches the bound: a warp goes through the tokens of one at a time
-    unsigned todo = __ballot_sync(0xffffffffu, key >= bound);
+    // the threads whose best reaches the bound: they still hold all of their vectors, or
+    // a warp goes through the tokens of one at a time
+    const bool held = vectors <= U * kThreads;
+    if (held && key >= bound) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (tid + u * kThreads < vectors && Eight<T>::raw_top(raw[u]) >= bar) {
+          const int i = v0 + (tid + u * kThreads) * kV;
+          float v[8];
+          raw[u].to(v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) offer(key_at(v[j], i + j));
+        }
+      if (tid < head) offer(key_at(one(x + lo + tid), lo + tid));
+      if (tid < hi - tail) offer(key_at(one(x + tail + tid), tail + tid));
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, !held && key >= bound);
     while (todo) {
       const int src = __ffs(todo) - 1, th = warp * 32 + src;
       todo &= todo - 1;
       for (int k = th + lane * kThreads; k < vectors; k += 32 * kThreads) {
-        float v[8];
+        Raw8<T> r;
         const int i = v0 + k * kV;
-        load8(x + i, v);
+        r.load(x + i);
+        if (Eight<T>::raw_top(r) >= bar) {
+          float v[8];
+          r.to(v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) offer(key_at(v[j], i + j));
+          for (int j = 0; j < 8; ++j) offer(key_at(v[j], i + j));
+        }
       }
       if (lane == 0 && th < head) offer(key_at(one(x + lo + th), lo + th));
       if (lane == 1 && th < hi - tail) offer(key_at(one(x + tail + th), tail + th));
@@ -400,12 +428,15 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   // ---- to the cluster's first CTA
   if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
   if (warp == 0) {
-    s = sh.sums[0];
-    top = sh.top[0];
-    for (int i = 1; i < kWarps; ++i) join(s, sh.sums[i]), top = fmaxf(top, sh.top[i]);
-    count = lane < kWarps ? sh.count[lane] : 0, infinite = lane < kWarps ? sh.infinite[lane] : 0;
-    count = __reduce_add_sync(0xffffffffu, count);
-    infinite = __reduce_add_sync(0xffffffffu, infinite);
+    const bool in = lane < kWarps;
+    s = {in ? sh.sums[lane].c : kNoRef, in ? sh.sums[lane].l : 0.f, in ? sh.sums[lane].w : 0.f};
+    count = __reduce_add_sync(0xffffffffu, in ? sh.count[lane] : 0);
+    infinite = __reduce_add_sync(0xffffffffu, in ? sh.infinite[lane] : 0);
+    top = of_key(__reduce_max_sync(0xffffffffu, key_of(in ? sh.top[lane] : -INFINITY)));
+    onto(of_key(__reduce_max_sync(0xffffffffu, key_of(s.c))));
+#pragma unroll
+    for (int o = kWarps / 2; o; o >>= 1) s.l += __shfl_xor_sync(0xffffffffu, s.l, o), s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+    __syncwarp();  // chosen[0]
     Shared *first = &sh;
     if (ranks > 1) {
       uint64_t p;
@@ -454,12 +485,21 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   }
   // the n highest of all: of ranks x n keys, those with fewer than n above
   if (tid < ranks * n) {
-    const u64 k = sh.all_keys[tid / n * kTop + tid % n];
-    int above = 0;
+    // each CTA's are in order: its own place, and by halving those above in the others
+    // (only keys of no token, 0, are equal: there the earlier CTA's come first)
+    const int mine = tid / n;
+    const u64 k = sh.all_keys[mine * kTop + tid % n];
+    int above = tid % n;
     for (int i = 0; i < ranks; ++i)
-      for (int j = 0; j < n; ++j) {
-        const u64 o = sh.all_keys[i * kTop + j];
-        above += o > k || (o == k && i * n + j < tid);  // (only those of no token, 0, are equal)
+      if (i != mine) {
+        int lo_n = 0, hi_n = n;
+        while (lo_n < hi_n) {
+          const int mid = (lo_n + hi_n) >> 1;
+          const u64 o = sh.all_keys[i * kTop + mid];
+          if (o > k || (o == k && i < mine)) lo_n = mid + 1;
+          else hi_n = mid;
+        }
+        above += lo_n;
       }
     if (above < n) {
       a.top_tokens[row * n + above] = k ? (int32_t)~(uint32_t)k : -1;
@@ -475,9 +515,9 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t
                             float *entropy, int32_t *top_tokens, float *top_logp,
                             cudaStream_t stream) {
   const int64_t sms = device_facts()->sm_count;
-  // A cluster per row while rows do not fill the GPU, of slices of 4096 tokens or more.
+  // A cluster per row while rows do not fill the GPU, of slices of 2048 tokens or more.
   int ranks = 1;
-  while (ranks < kMaxCluster && rows * ranks * 2 <= 2 * sms && vocab >= (int64_t)ranks * 2 * 4096) ranks *= 2;
+  while (ranks < kMaxCluster && rows * ranks * 2 <= 2 * sms && vocab >= (int64_t)ranks * 2 * 2048) ranks *= 2;
   const int slice = (int)(((vocab + ranks - 1) / ranks + 63) / 64 * 64);
   for (int64_t r0 = 0; r0 < rows; r0 += 65535) {  // rows are the grid's y
     const int64_t n = rows - r0 < 65535 ? rows - r0 : 65535;
