@@ -16,10 +16,14 @@
 // that the table's rounding leaves times the position.  Its upper 32 bits, signed,
 // are the angle in (-1/2, 1/2] turns.
 //
-// What bounds it: bytes, each read and written once.  A block takes a few tokens,
-// whose angles' cosines and sines it computes once, into shared memory (they are
-// the same for all heads), while its first rows are on their way; then groups of
-// D / 8 lanes take a row each.
+// What bounds it: bytes, each read and written once; so rows stay in registers, all
+// loads of a thread go out at its start, and no thread waits for another.  D / 8
+// lanes take a row; they take up to R heads of the same token, for which each lane
+// computes the cosines and sines of its four pairs once.
+//
+// Cosine and sine of q quarter turns and x more, |x| <= 1/2: Taylor's series of sin
+// and cos of x pi / 2 to the terms x^9 and x^10, beyond which there are 2 10^-9, and
+// the quadrant's signs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -35,19 +39,45 @@ namespace q4k {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFew = 1, kMany = 4;  // heads of a thread
 
 enum Pairs { kHalf = 0, kAdjacent = 1, kAny = 2 };  // kAny: (i, i + R / 2) where R / 2 is no multiple of 4
 
 struct Args {
   RopeArgs r;
-  // [0]: queries, [1]: keys and values.  A block takes some tokens and a group of the
-  // heads of one kind; the grid runs over those of queries, of keys, of values.
-  uint32_t blocks[2];
-  int tokens_per_block[2], heads_per_block[2];
-  FastDiv groups[2]{FastDiv{1}, FastDiv{1}};
-  FastDiv half{1};     // of the rotated values
-  FastDiv page{1};
+  FastDiv per_token[2];  // groups of lanes that share a token: of a block of queries, of keys and values
+  int tokens[2];         // tokens of such a block
+  int rows[2];           // rows of a thread there, at most R
+  uint32_t blocks[2];    // such blocks: head groups of the first tokens, of the next
+  FastDiv groups[2];
+  FastDiv page;
 };
+
+// (cos, sin) of two angles, of turn / 2^32 turns each.
+__device__ __forceinline__ void cos_sin2(uint32_t turn0, uint32_t turn1, float2 &co, float2 &si) {
+  const uint32_t q0 = (turn0 + 0x20000000u) >> 30, q1 = (turn1 + 0x20000000u) >> 30;
+  const float2 x = make_float2((float)(int32_t)(turn0 - (q0 << 30)) * 9.313225746154785e-10f,  // 2^-30
+                               (float)(int32_t)(turn1 - (q1 << 30)) * 9.313225746154785e-10f);
+  const float2 z = __fmul2_rn(x, x);
+  const auto both = [](float v) { return make_float2(v, v); };
+  float2 s = __ffma2_rn(z, both(1.60441184e-4f), both(-4.68175413e-3f));
+  s = __ffma2_rn(z, s, both(7.96926262e-2f));
+  s = __ffma2_rn(z, s, both(-6.45964097e-1f));
+  s = __ffma2_rn(z, s, both(1.57079633f));
+  s = __fmul2_rn(s, x);
+  float2 c = __ffma2_rn(z, both(-2.52020424e-5f), both(9.19260274e-4f));
+  c = __ffma2_rn(z, c, both(-2.08634807e-2f));
+  c = __ffma2_rn(z, c, both(2.53669508e-1f));
+  c = __ffma2_rn(z, c, both(-1.23370055f));
+  c = __ffma2_rn(z, c, both(1.f));
+  const auto sign = [](float v, uint32_t bit) { return __int_as_float(__float_as_int(v) ^ (int)((bit & 2u) << 30)); };
+  co = make_float2(sign(q0 & 1u ? s.x : c.x, q0 + 1u), sign(q1 & 1u ? s.y : c.y, q1 + 1u));
+  si = make_float2(sign(q0 & 1u ? c.x : s.x, q0), sign(q1 & 1u ? c.y : s.y, q1));
+}
+// The upper half of pos * step modulo 2^64: the fraction of a turn.
+__device__ __forceinline__ uint32_t turn_of(uint32_t pos, uint64_t step) {
+  return __umulhi(pos, (uint32_t)step) + pos * (uint32_t)(step >> 32);
+}
 
 // A lane's 8 values of a row, as two times four: where pairs lie half a rotated
 // part apart, 4 values of its first half and their partners in the second, so that
@@ -101,103 +131,88 @@ __device__ __forceinline__ void store_fours(__nv_bfloat16 *p, int oa, int ob, co
   }
 }
 
-template <int LPR, typename T, typename TO, int PAIRS, bool CACHE, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const Args a) {
-  extern __shared__ __align__(16) float table[];
+template <int LPR, typename T, int PAIRS, bool CACHE, int R>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
   const RopeArgs &r = a.r;
-  constexpr int SLOTS = kThreads / LPR, U = 2;  // rows at a time, of the block and of a thread
+  constexpr int SLOTS = kThreads / LPR;  // rows at a time
   const int c = threadIdx.x % LPR, slot_in = threadIdx.x / LPR, lane = threadIdx.x & 31;
-  // the block's kind of heads (0: queries, 1: keys, 2: values), which of them, and its tokens
-  const uint32_t x0 = blockIdx.x;
-  const int kind = !CACHE || x0 < a.blocks[0] ? 0 : x0 < a.blocks[0] + a.blocks[1] ? 1 : 2, kv = kind ? 1 : 0;
-  const uint32_t xk = kind == 0 ? x0 : kind == 1 ? x0 - a.blocks[0] : x0 - a.blocks[0] - a.blocks[1];
-  const uint32_t part = a.groups[kv].div(xk);
-  const int head0 = (int)(xk - part * a.groups[kv].d) * a.heads_per_block[kv], heads = min(a.heads_per_block[kv], r.heads[kv] - head0);
-  const int tpb = a.tokens_per_block[kv], tok0 = (int)part * tpb, toks = min(tpb, (int)(r.tokens - tok0));
-  const int half = r.rot / 2, stride = (half + 3) & ~3;
-  float *cs = table, *sn = table + tpb * stride;
+  // Blocks of queries first, then of keys and values (heads 0 .. of keys, then of values).
+  const int kv = CACHE && blockIdx.x >= a.blocks[0];
+  const uint32_t x = blockIdx.x - (kv ? a.blocks[0] : 0u), part = a.groups[kv].div(x);
+  const int all = kv ? 2 * r.heads[1] : r.heads[0], per_token = (int)a.per_token[kv].d, rows = a.rows[kv];
+  // this group's token, and its heads s, s + per_token, ...
+  const int tt = (int)a.per_token[kv].div(slot_in), s = slot_in - tt * per_token + (int)(x - part * a.groups[kv].d) * per_token * rows;
+  const int64_t tok = (int64_t)part * a.tokens[kv] + tt;
+  const bool there = tt < a.tokens[kv] && tok < r.tokens;
+  const int half = r.rot / 2;
   const unsigned mask = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (lane / LPR * LPR);
   const bool mine = c * 8 < r.dim;  // lanes past the row's end only take part in sums
   // this lane's values oa .. oa + 3 and ob .. ob + 3; whether they turn, by the angles 4 c ..
   int oa = 8 * c, ob = oa + 4;
-  bool turns = oa < r.rot && kind != 2;
-  if (PAIRS == kHalf && 4 * c < half) oa = 4 * c, ob = half + 4 * c;
-  if (PAIRS == kHalf) turns = 4 * c < half && kind != 2;
+  bool turns = oa < r.rot;
+  if (PAIRS == kHalf) {
+    turns = 4 * c < half;
+    if (turns) oa = 4 * c, ob = half + 4 * c;
+  }
+  const int pos = there ? r.pos[tok] : -1;
+  const int slot = kv && there ? r.slots[tok] : -1;
 
-  // Rows (token, head) of the block in a list, heads first; a thread takes every SLOTS-th.
-  const int step_t = SLOTS / heads, step_h = SLOTS - step_t * heads, rows = toks * heads;
-  const int64_t ld_t = r.ld_token[kind], ld_h = r.ld_head[kind];
-  int t = slot_in / heads, h = slot_in - t * heads;
-  const T *from = static_cast<const T *>(r.in[kind]) + (int64_t)(tok0 + t) * ld_t + (int64_t)(head0 + h) * ld_h;
-  const int64_t step = step_t * ld_t + step_h * ld_h, carry = ld_t - heads * ld_h;
-  struct Row {
-    int t, h;
-    bool on;
-    const T *from;
-    Fours<T> raw;
-  } row[U];
-  int next = slot_in;  // its place in the list
-  const auto fetch = [&](Row &x) {
-    x.t = t, x.h = h, x.on = next < rows, x.from = from;
-    if (x.on && mine) x.raw.load(from, oa, ob);
-    next += SLOTS;
-    t += step_t, h += step_h, from += step;
-    if (h >= heads) h -= heads, ++t, from += carry;
-  };
+  // ---- all rows of this thread
+  const T *from = static_cast<const T *>(r.in[kv]) + tok * r.ld_token[kv] + s * r.ld_head[kv];
+  const int64_t step = per_token * r.ld_head[kv];
+  // values lie so far from keys, and their heads begin again
+  const int64_t to_v = kv ? (static_cast<const T *>(r.in[2]) - static_cast<const T *>(r.in[1])) - r.heads[1] * r.ld_head[1] : 0;
+  Fours<T> raw[R];
 #pragma unroll
-  for (int u = 0; u < U; ++u) row[u].raw = Fours<T>(), fetch(row[u]);
+  for (int k = 0; k < R; ++k) {
+    raw[k] = Fours<T>();
+    const int h = s + k * per_token;
+    if (k < rows && there && h < all && mine) raw[k].load(from + k * step + (kv && h >= r.heads[1] ? to_v : 0), oa, ob);
+  }
 
-  const float *gamma = kind == 2 ? nullptr : r.gamma[kind];
+  // ---- its angles, and its pairs (p, q): p' = p pc + q qs, q' = q qc + p ps, with
+  // gamma in them; values that do not turn keep their size
+  const float *gamma = r.gamma[kv];
   float g[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) g[j] = 1.f;
   if (mine && gamma) {
-    const float4 x = *reinterpret_cast<const float4 *>(gamma + oa), z = *reinterpret_cast<const float4 *>(gamma + ob);
-    g[0] = x.x, g[1] = x.y, g[2] = x.z, g[3] = x.w, g[4] = z.x, g[5] = z.y, g[6] = z.z, g[7] = z.w;
+    const float4 y = *reinterpret_cast<const float4 *>(gamma + oa), z = *reinterpret_cast<const float4 *>(gamma + ob);
+    g[0] = y.x, g[1] = y.y, g[2] = y.z, g[3] = y.w, g[4] = z.x, g[5] = z.y, g[6] = z.z, g[7] = z.w;
   }
-  if (kind != 2) {
-    for (int i = threadIdx.x; i < toks * half; i += kThreads) {
-      const int tt = (int)a.half.div(i), f = i - tt * half;
-      const uint64_t turn = (uint64_t)(int64_t)r.pos[tok0 + tt] * r.steps[f];
-      float si, co;
-      sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &si, &co);  // in units of 2^-31 half turns
-      cs[tt * stride + f] = co * r.amplitude, sn[tt * stride + f] = si * r.amplitude;
-    }
-    __syncthreads();
-  }
-
-  const float inv_dim = 1.f / (float)r.dim;
-  int pos = -1, slot = -1, at = -1;  // of token `at`
-  // of the lane's pairs (p, q): p' = p pc - q qs, q' = q qc + p ps, with gamma in them
+  // kHalf: p in values 0..3, q in 4..7; kAdjacent: p, q in turn
+  constexpr int P0[2] = {0, PAIRS == kHalf ? 2 : 4}, S1 = PAIRS == kHalf ? 1 : 2, Q = PAIRS == kHalf ? 4 : 1;
   float2 pc[2], qs[2], qc[2], ps[2];
-  const auto work = [&](const Row &x) {
-    if (x.t != at) {
-      at = x.t;
-      pos = x.on ? r.pos[tok0 + x.t] : -1;
-      slot = CACHE && kind && x.on ? r.slots[tok0 + x.t] : -1;
-      if (PAIRS != kAny) {
-        float co[4], si[4];
+  if (PAIRS != kAny) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool in = turns && x.on && (PAIRS == kHalf || 4 * c + j < half);
-          co[j] = in ? cs[x.t * stride + 4 * c + j] : 1.f, si[j] = in ? sn[x.t * stride + 4 * c + j] : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          // kHalf: p in g[0..3], q in g[4..7]; kAdjacent: p, q in turn
-          const int p0 = PAIRS == kHalf ? 2 * j : 4 * j, p1 = PAIRS == kHalf ? 2 * j + 1 : 4 * j + 2, q0 = PAIRS == kHalf ? p0 + 4 : p0 + 1, q1 = PAIRS == kHalf ? p1 + 4 : p1 + 1;
-          pc[j] = make_float2(g[p0] * co[2 * j], g[p1] * co[2 * j + 1]), qs[j] = make_float2(-g[q0] * si[2 * j], -g[q1] * si[2 * j + 1]);
-          qc[j] = make_float2(g[q0] * co[2 * j], g[q1] * co[2 * j + 1]), ps[j] = make_float2(g[p0] * si[2 * j], g[p1] * si[2 * j + 1]);
-        }
-      }
+    for (int j = 0; j < 2; ++j) {
+      const int f = 4 * c + 2 * j;
+      const bool in0 = turns && f < half, in1 = turns && f + 1 < half;
+      float2 co, si;
+      cos_sin2(in0 && pos >= 0 ? turn_of((uint32_t)pos, r.steps[f]) : 0u, in1 && pos >= 0 ? turn_of((uint32_t)pos, r.steps[f + 1]) : 0u, co, si);
+      co = make_float2(in0 ? co.x * r.amplitude : 1.f, in1 ? co.y * r.amplitude : 1.f);
+      si = make_float2(in0 ? si.x * r.amplitude : 0.f, in1 ? si.y * r.amplitude : 0.f);
+      const float2 gp = make_float2(g[P0[j]], g[P0[j] + S1]), gq = make_float2(g[P0[j] + Q], g[P0[j] + S1 + Q]);
+      pc[j] = __fmul2_rn(gp, co), qc[j] = __fmul2_rn(gq, co), ps[j] = __fmul2_rn(gp, si);
+      qs[j] = __fmul2_rn(gq, make_float2(-si.x, -si.y));
     }
+  }
+  const float inv_dim = 1.f / (float)r.dim;
+  uint32_t page = 0, off = 0;
+  if (kv && (uint32_t)slot < r.n_slots) page = a.page.div(slot), off = slot - page * a.page.d;
+
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (k >= rows) break;
+    const int h = s + k * per_token;
+    const bool on = there && h < all, value = kv && h >= r.heads[1];
     float v[8], partner[8];
-    x.raw.to(v);
-    if (PAIRS == kAny && x.on && mine && kind != 2) {
+    raw[k].to(v);
+    if (PAIRS == kAny && on && mine && !value) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int e = c * 8 + j;
-        partner[j] = e < r.rot ? (float)x.from[e < half ? e + half : e - half] : 0.f;
+        partner[j] = e < r.rot ? (float)from[k * step + (e < half ? e + half : e - half)] : 0.f;
       }
     }
     // ---- the norm's factor
@@ -214,43 +229,49 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const Args a) {
     }
     // ---- norm and rotation
     if (PAIRS != kAny) {
-      if (kind != 2) {
+      if (!value) {
         const float2 i2 = make_float2(inv, inv);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int p0 = PAIRS == kHalf ? 2 * j : 4 * j, p1 = PAIRS == kHalf ? 2 * j + 1 : 4 * j + 2, q0 = PAIRS == kHalf ? p0 + 4 : p0 + 1, q1 = PAIRS == kHalf ? p1 + 4 : p1 + 1;
-          const float2 p = __fmul2_rn(make_float2(v[p0], v[p1]), i2), q = __fmul2_rn(make_float2(v[q0], v[q1]), i2);
+          const float2 p = __fmul2_rn(make_float2(v[P0[j]], v[P0[j] + S1]), i2), q = __fmul2_rn(make_float2(v[P0[j] + Q], v[P0[j] + S1 + Q]), i2);
           const float2 n = __ffma2_rn(p, pc[j], __fmul2_rn(q, qs[j])), m = __ffma2_rn(q, qc[j], __fmul2_rn(p, ps[j]));
-          v[p0] = n.x, v[p1] = n.y, v[q0] = m.x, v[q1] = m.y;
+          v[P0[j]] = n.x, v[P0[j] + S1] = n.y, v[P0[j] + Q] = m.x, v[P0[j] + S1 + Q] = m.y;
         }
       }
     } else {
-      if (x.on && mine && kind != 2) {
+      if (on && mine && !value) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 8; j += 2) {  // (r.rot is even, so both turn or none)
           const int e = c * 8 + j;
-          v[j] = v[j] * inv * g[j];
+          v[j] = v[j] * inv * g[j], v[j + 1] = v[j + 1] * inv * g[j + 1];
           if (e < r.rot) {
-            const int f = x.t * stride + (e < half ? e : e - half);
-            const float w = partner[j] * inv * (gamma ? gamma[e < half ? e + half : e - half] : 1.f);
-            v[j] = e < half ? v[j] * cs[f] - w * sn[f] : v[j] * cs[f] + w * sn[f];
+            const bool lo0 = e < half, lo1 = e + 1 < half;
+            const int o0 = lo0 ? e + half : e - half, o1 = lo1 ? e + 1 + half : e + 1 - half;  // partners
+            float2 co, si;
+            cos_sin2(turn_of((uint32_t)max(pos, 0), r.steps[min(e, o0)]), turn_of((uint32_t)max(pos, 0), r.steps[min(e + 1, o1)]), co, si);
+            const float w0 = partner[j] * inv * (gamma ? gamma[o0] : 1.f), w1 = partner[j + 1] * inv * (gamma ? gamma[o1] : 1.f);
+            v[j] = (v[j] * co.x + (lo0 ? -w0 : w0) * si.x) * r.amplitude;
+            v[j + 1] = (v[j + 1] * co.y + (lo1 ? -w1 : w1) * si.y) * r.amplitude;
           }
         }
       }
       __syncwarp();  // partners are read before a row is written in place
     }
     // ---- out
-    if (!x.on || pos < 0) return;
-    const int tok = tok0 + x.t, head = head0 + x.h;
-    if (!CACHE || kind == 0) {
-      if (mine) store_fours(static_cast<TO *>(r.out) + tok * r.ldo_token + head * r.ldo_head, oa, ob, v);
+    if (!on || pos < 0) continue;
+    if (!kv) {
+      const int64_t to = tok * r.ldo_token + h * r.ldo_head;
+      if (!mine) continue;
+      if (CACHE || r.out_dtype == Q4K_DTYPE_BF16) store_fours(static_cast<__nv_bfloat16 *>(r.out) + to, oa, ob, v);
+      else store_fours(static_cast<float *>(r.out) + to, oa, ob, v);
     } else if ((uint32_t)slot >= r.n_slots) {
       if (slot != -1 && c == 0) set_device_error(r.err, kDevErrBadPage);
     } else {
-      const uint32_t page = a.page.div(slot), off = slot - page * a.page.d;
+      const int head = value ? h - r.heads[1] : h;
       const int64_t to = page * r.page_stride + head * r.head_stride + off * r.token_stride;
-      if (!E4M3) {
-        store_fours(static_cast<__nv_bfloat16 *>(r.cache[kind - 1]) + to, oa, ob, v);
+      void *cache = value ? r.cache[1] : r.cache[0];
+      if (r.cache_dtype == Q4K_DTYPE_BF16) {
+        store_fours(static_cast<__nv_bfloat16 *>(cache) + to, oa, ob, v);
       } else {
         float amax = 0.f;
 #pragma unroll
@@ -261,50 +282,48 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const Args a) {
         float factor;
         const float up = block_factor(amax, c, mask, factor);
         const uint2 w = to_e4m3x8(v, up);
-        uint8_t *p = static_cast<uint8_t *>(r.cache[kind - 1]) + to;
+        uint8_t *p = static_cast<uint8_t *>(cache) + to;
         *reinterpret_cast<uint32_t *>(p + oa) = w.x;
         *reinterpret_cast<uint32_t *>(p + ob) = w.y;
-        if (c == 0) r.scale[kind - 1][((int64_t)page * r.heads[1] + head) * a.page.d + off] = factor;
+        if (c == 0) (value ? r.scale[1] : r.scale[0])[((int64_t)page * r.heads[1] + head) * a.page.d + off] = factor;
       }
     }
-  };
-  for (int i = 0; i < rows; i += U * SLOTS) {
-    Row now[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) now[u] = row[u];
-    // the next rows are on their way while these are worked on
-#pragma unroll
-    for (int u = 0; u < U; ++u) fetch(row[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u) work(now[u]);
   }
 }
 
-template <int LPR, typename T, typename TO, int PAIRS, bool CACHE, bool E4M3>
-cudaError_t go(const Args &a, dim3 grid, size_t smem, cudaStream_t s) {
-  rope_kernel<LPR, T, TO, PAIRS, CACHE, E4M3><<<grid, kThreads, smem, s>>>(a);
+template <int LPR, typename T, int PAIRS, bool CACHE>
+cudaError_t go(const RopeArgs &r, cudaStream_t s) {
+  constexpr int SLOTS = kThreads / LPR;
+  // Heads of a thread: one while that leaves SMs without work; else kMany, for which
+  // its angles are computed once, of as many tokens as a block has room for.
+  const bool many = r.tokens * (r.heads[0] + (CACHE ? 2 * r.heads[1] : 0)) > (int64_t)device_facts()->sm_count * 8 * SLOTS;
+  Args a = {r, {FastDiv(1), FastDiv(1)}, {}, {}, {}, {FastDiv(1), FastDiv(1)}, FastDiv(CACHE ? r.page : 1)};
+  for (int i = 0; i < (CACHE ? 2 : 1); ++i) {
+    const int heads = i ? 2 * r.heads[1] : r.heads[0], most = many ? kMany : kFew, least = (heads + most - 1) / most;
+    const int per_token = least < SLOTS ? least : SLOTS, each = (heads + per_token - 1) / per_token;
+    const int groups = (each + most - 1) / most;
+    a.per_token[i] = FastDiv(per_token), a.tokens[i] = SLOTS / per_token, a.rows[i] = (each + groups - 1) / groups, a.groups[i] = FastDiv(groups);
+    a.blocks[i] = (uint32_t)((r.tokens + a.tokens[i] - 1) / a.tokens[i] * groups);
+  }
+  if (many) rope_kernel<LPR, T, PAIRS, CACHE, kMany><<<a.blocks[0] + a.blocks[1], kThreads, 0, s>>>(a);
+  else rope_kernel<LPR, T, PAIRS, CACHE, kFew><<<a.blocks[0] + a.blocks[1], kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
-template <int LPR, typename T, typename TO, bool CACHE, bool E4M3>
-cudaError_t go_pairs(int pairs, const Args &a, dim3 grid, size_t smem, cudaStream_t s) {
-  if (pairs == kHalf) return go<LPR, T, TO, kHalf, CACHE, E4M3>(a, grid, smem, s);
-  if (pairs == kAdjacent) return go<LPR, T, TO, kAdjacent, CACHE, E4M3>(a, grid, smem, s);
-  return go<LPR, T, TO, kAny, CACHE, E4M3>(a, grid, smem, s);
+template <int LPR, typename T, int PAIRS>
+cudaError_t go_kind(const RopeArgs &r, cudaStream_t s) {
+  return r.cache[0] ? go<LPR, T, PAIRS, true>(r, s) : go<LPR, T, PAIRS, false>(r, s);
 }
 template <int LPR, typename T>
-cudaError_t go_kind(int pairs, const Args &a, dim3 grid, size_t smem, cudaStream_t s) {
-  using B = __nv_bfloat16;
-  if (!a.r.cache[0])
-    return a.r.out_dtype == Q4K_DTYPE_BF16 ? go_pairs<LPR, T, B, false, false>(pairs, a, grid, smem, s)
-                                           : go_pairs<LPR, T, float, false, false>(pairs, a, grid, smem, s);
-  return a.r.cache_dtype == Q4K_DTYPE_BF16 ? go_pairs<LPR, T, B, true, false>(pairs, a, grid, smem, s)
-                                           : go_pairs<LPR, T, B, true, true>(pairs, a, grid, smem, s);
+cudaError_t go_pairs(int pairs, const RopeArgs &r, cudaStream_t s) {
+  if (pairs == kHalf) return go_kind<LPR, T, kHalf>(r, s);
+  if (pairs == kAdjacent) return go_kind<LPR, T, kAdjacent>(r, s);
+  return go_kind<LPR, T, kAny>(r, s);
 }
 template <typename T>
-cudaError_t go_lanes(int lanes, int pairs, const Args &a, dim3 grid, size_t smem, cudaStream_t s) {
-  if (lanes <= 8) return go_kind<8, T>(pairs, a, grid, smem, s);
-  if (lanes <= 16) return go_kind<16, T>(pairs, a, grid, smem, s);
-  return go_kind<32, T>(pairs, a, grid, smem, s);
+cudaError_t go_lanes(int pairs, const RopeArgs &r, cudaStream_t s) {
+  if (r.dim <= 64) return go_pairs<8, T>(pairs, r, s);
+  if (r.dim <= 128) return go_pairs<16, T>(pairs, r, s);
+  return go_pairs<32, T>(pairs, r, s);
 }
 
 }  // namespace
@@ -335,30 +354,8 @@ bool rope_steps(int rot, double base, double factor, int64_t original, double be
 }
 
 cudaError_t launch_rope(const RopeArgs &r, int dtype, bool interleaved, cudaStream_t stream) {
-  const int lanes = (r.dim + 7) / 8, lpr = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32, slots = kThreads / lpr;
-  const int heads = r.heads[0] + (r.cache[0] ? 2 * r.heads[1] : 0), half = r.rot / 2;
-  const int pairs = interleaved ? kAdjacent : half % 4 ? kAny : kHalf;
-  // Rows per block: one per group of lanes while there are few, so that all SMs
-  // take part; of many, 8 or more, of as many tokens as give every thread an angle.
-  Args a = {};
-  a.r = r, a.half = FastDiv(half > 0 ? half : 1), a.page = FastDiv(r.cache[0] ? r.page : 1);
-  const int64_t sms = device_facts()->sm_count;
-  const bool few = r.tokens * heads <= sms * 16 * slots;
-  int most = 1;
-  for (int i = 0; i < (r.cache[0] ? 2 : 1); ++i) {
-    int toks = 1, hpb = r.heads[i];
-    if (few) hpb = hpb < slots ? hpb : slots;
-    else
-      while (toks * half < kThreads && toks * hpb < 8 * slots) ++toks;
-    const int groups = (r.heads[i] + hpb - 1) / hpb;
-    a.tokens_per_block[i] = toks, a.heads_per_block[i] = hpb, a.groups[i] = FastDiv(groups);
-    a.blocks[i] = (uint32_t)((r.tokens + toks - 1) / toks * groups);
-    most = toks > most ? toks : most;
-  }
-  const dim3 grid(a.blocks[0] + 2 * a.blocks[1]);
-  const size_t smem = (size_t)2 * most * ((half + 3) & ~3) * 4;
-  return dtype == Q4K_DTYPE_BF16 ? go_lanes<__nv_bfloat16>(lanes, pairs, a, grid, smem, stream)
-                                 : go_lanes<float>(lanes, pairs, a, grid, smem, stream);
+  const int pairs = interleaved ? kAdjacent : (r.rot / 2) % 4 ? kAny : kHalf;
+  return dtype == Q4K_DTYPE_BF16 ? go_lanes<__nv_bfloat16>(pairs, r, stream) : go_lanes<float>(pairs, r, stream);
 }
 
 }  // namespace q4k
