@@ -16,10 +16,11 @@
 // that the table's rounding leaves times the position.  Its upper 32 bits, signed,
 // are the angle in (-1/2, 1/2] turns.
 //
-// What bounds it: bytes, each read and written once; so rows stay in registers, all
-// loads of a thread go out at its start, and no thread waits for another.  D / 8
-// lanes take a row; they take up to R heads of the same token, for which each lane
-// computes the cosines and sines of its four pairs once.
+// What bounds it: bytes, each read and written once; so rows stay in registers, and
+// all loads of a thread go out at its start.  D / 8 lanes take a row, and up to R
+// heads of the same token.  While the rows are on their way the block computes the
+// cosines and sines of its tokens, which are the same for all heads, into shared
+// memory: a thread one or a few.
 //
 // Cosine and sine of q quarter turns and x more, |x| <= 1/2: Taylor's series of sin
 // and cos of x pi / 2 to the terms x^9 and x^10, beyond which there are 2 10^-9, and
@@ -50,29 +51,25 @@ struct Args {
   int rows[2];           // rows of a thread there, at most R
   uint32_t blocks[2];    // such blocks: head groups of the first tokens, of the next
   FastDiv groups[2];
-  FastDiv page;
+  FastDiv half, page;
 };
 
-// (cos, sin) of two angles, of turn / 2^32 turns each.
-__device__ __forceinline__ void cos_sin2(uint32_t turn0, uint32_t turn1, float2 &co, float2 &si) {
-  const uint32_t q0 = (turn0 + 0x20000000u) >> 30, q1 = (turn1 + 0x20000000u) >> 30;
-  const float2 x = make_float2((float)(int32_t)(turn0 - (q0 << 30)) * 9.313225746154785e-10f,  // 2^-30
-                               (float)(int32_t)(turn1 - (q1 << 30)) * 9.313225746154785e-10f);
-  const float2 z = __fmul2_rn(x, x);
-  const auto both = [](float v) { return make_float2(v, v); };
-  float2 s = __ffma2_rn(z, both(1.60441184e-4f), both(-4.68175413e-3f));
-  s = __ffma2_rn(z, s, both(7.96926262e-2f));
-  s = __ffma2_rn(z, s, both(-6.45964097e-1f));
-  s = __ffma2_rn(z, s, both(1.57079633f));
-  s = __fmul2_rn(s, x);
-  float2 c = __ffma2_rn(z, both(-2.52020424e-5f), both(9.19260274e-4f));
-  c = __ffma2_rn(z, c, both(-2.08634807e-2f));
-  c = __ffma2_rn(z, c, both(2.53669508e-1f));
-  c = __ffma2_rn(z, c, both(-1.23370055f));
-  c = __ffma2_rn(z, c, both(1.f));
+// Cosine and sine of turn / 2^32 turns.
+__device__ __forceinline__ void cos_sin(uint32_t turn, float &co, float &si) {
+  const uint32_t q = (turn + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(turn - (q << 30)) * 9.313225746154785e-10f, z = x * x;  // 2^-30
+  float s = fmaf(z, 1.60441184e-4f, -4.68175413e-3f);
+  s = fmaf(z, s, 7.96926262e-2f);
+  s = fmaf(z, s, -6.45964097e-1f);
+  s = fmaf(z, s, 1.57079633f) * x;
+  float c = fmaf(z, -2.52020424e-5f, 9.19260274e-4f);
+  c = fmaf(z, c, -2.08634807e-2f);
+  c = fmaf(z, c, 2.53669508e-1f);
+  c = fmaf(z, c, -1.23370055f);
+  c = fmaf(z, c, 1.f);
   const auto sign = [](float v, uint32_t bit) { return __int_as_float(__float_as_int(v) ^ (int)((bit & 2u) << 30)); };
-  co = make_float2(sign(q0 & 1u ? s.x : c.x, q0 + 1u), sign(q1 & 1u ? s.y : c.y, q1 + 1u));
-  si = make_float2(sign(q0 & 1u ? c.x : s.x, q0), sign(q1 & 1u ? c.y : s.y, q1));
+  co = sign(q & 1u ? s : c, q + 1u);
+  si = sign(q & 1u ? c : s, q);
 }
 // The upper half of pos * step modulo 2^64: the fraction of a turn.
 __device__ __forceinline__ uint32_t turn_of(uint32_t pos, uint64_t step) {
@@ -133,8 +130,10 @@ __device__ __forceinline__ void store_fours(__nv_bfloat16 *p, int oa, int ob, co
 
 template <int LPR, typename T, int PAIRS, bool CACHE, int R>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
-  const RopeArgs &r = a.r;
+  // cosines and sines of the block's tokens, [token][R / 2] each
   constexpr int SLOTS = kThreads / LPR;  // rows at a time
+  __shared__ __align__(16) float cs[SLOTS * LPR * 4], sn[SLOTS * LPR * 4];
+  const RopeArgs &r = a.r;
   const int c = threadIdx.x % LPR, slot_in = threadIdx.x / LPR, lane = threadIdx.x & 31;
   // Blocks of queries first, then of keys and values (heads 0 .. of keys, then of values).
   const int kv = CACHE && blockIdx.x >= a.blocks[0];
@@ -144,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
   const int tt = (int)a.per_token[kv].div(slot_in), s = slot_in - tt * per_token + (int)(x - part * a.groups[kv].d) * per_token * rows;
   const int64_t tok = (int64_t)part * a.tokens[kv] + tt;
   const bool there = tt < a.tokens[kv] && tok < r.tokens;
-  const int half = r.rot / 2;
+  const int half = r.rot / 2, stride = (half + 3) & ~3;
   const unsigned mask = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (lane / LPR * LPR);
   const bool mine = c * 8 < r.dim;  // lanes past the row's end only take part in sums
   // this lane's values oa .. oa + 3 and ob .. ob + 3; whether they turn, by the angles 4 c ..
@@ -170,7 +169,18 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
     if (k < rows && there && h < all && mine) raw[k].load(from + k * step + (kv && h >= r.heads[1] ? to_v : 0), oa, ob);
   }
 
-  // ---- its angles, and its pairs (p, q): p' = p pc + q qs, q' = q qc + p ps, with
+  // ---- the block's angles
+  const int64_t tok0 = (int64_t)part * a.tokens[kv];
+  const int toks = (int)min((int64_t)a.tokens[kv], r.tokens - tok0);
+  for (int i = threadIdx.x; i < toks * half; i += kThreads) {
+    const int ti = (int)a.half.div(i), f = i - ti * half;
+    float co, si;
+    cos_sin(turn_of((uint32_t)max(r.pos[tok0 + ti], 0), r.steps[f]), co, si);
+    cs[ti * stride + f] = co * r.amplitude, sn[ti * stride + f] = si * r.amplitude;
+  }
+  __syncthreads();
+
+  // ---- its pairs (p, q): p' = p pc + q qs, q' = q qc + p ps, with
   // gamma in them; values that do not turn keep their size
   const float *gamma = r.gamma[kv];
   float g[8];
@@ -184,14 +194,17 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
   constexpr int P0[2] = {0, PAIRS == kHalf ? 2 : 4}, S1 = PAIRS == kHalf ? 1 : 2, Q = PAIRS == kHalf ? 4 : 1;
   float2 pc[2], qs[2], qc[2], ps[2];
   if (PAIRS != kAny) {
+    float4 co4 = make_float4(1.f, 1.f, 1.f, 1.f), si4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (turns && tt < a.tokens[kv]) {
+      const float4 y = *reinterpret_cast<const float4 *>(cs + tt * stride + 4 * c), z = *reinterpret_cast<const float4 *>(sn + tt * stride + 4 * c);
+      co4.x = y.x, si4.x = z.x;
+      if (PAIRS == kHalf || 4 * c + 1 < half) co4.y = y.y, si4.y = z.y;
+      if (PAIRS == kHalf || 4 * c + 2 < half) co4.z = y.z, si4.z = z.z;
+      if (PAIRS == kHalf || 4 * c + 3 < half) co4.w = y.w, si4.w = z.w;
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int f = 4 * c + 2 * j;
-      const bool in0 = turns && f < half, in1 = turns && f + 1 < half;
-      float2 co, si;
-      cos_sin2(in0 && pos >= 0 ? turn_of((uint32_t)pos, r.steps[f]) : 0u, in1 && pos >= 0 ? turn_of((uint32_t)pos, r.steps[f + 1]) : 0u, co, si);
-      co = make_float2(in0 ? co.x * r.amplitude : 1.f, in1 ? co.y * r.amplitude : 1.f);
-      si = make_float2(in0 ? si.x * r.amplitude : 0.f, in1 ? si.y * r.amplitude : 0.f);
+      const float2 co = j ? make_float2(co4.z, co4.w) : make_float2(co4.x, co4.y), si = j ? make_float2(si4.z, si4.w) : make_float2(si4.x, si4.y);
       const float2 gp = make_float2(g[P0[j]], g[P0[j] + S1]), gq = make_float2(g[P0[j] + Q], g[P0[j] + S1 + Q]);
       pc[j] = __fmul2_rn(gp, co), qc[j] = __fmul2_rn(gq, co), ps[j] = __fmul2_rn(gp, si);
       qs[j] = __fmul2_rn(gq, make_float2(-si.x, -si.y));
@@ -247,11 +260,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
           if (e < r.rot) {
             const bool lo0 = e < half, lo1 = e + 1 < half;
             const int o0 = lo0 ? e + half : e - half, o1 = lo1 ? e + 1 + half : e + 1 - half;  // partners
-            float2 co, si;
-            cos_sin2(turn_of((uint32_t)max(pos, 0), r.steps[min(e, o0)]), turn_of((uint32_t)max(pos, 0), r.steps[min(e + 1, o1)]), co, si);
+            const int f0 = tt * stride + min(e, o0), f1 = tt * stride + min(e + 1, o1);
             const float w0 = partner[j] * inv * (gamma ? gamma[o0] : 1.f), w1 = partner[j + 1] * inv * (gamma ? gamma[o1] : 1.f);
-            v[j] = (v[j] * co.x + (lo0 ? -w0 : w0) * si.x) * r.amplitude;
-            v[j + 1] = (v[j + 1] * co.y + (lo1 ? -w1 : w1) * si.y) * r.amplitude;
+            v[j] = v[j] * cs[f0] + (lo0 ? -w0 : w0) * sn[f0];
+            v[j + 1] = v[j + 1] * cs[f1] + (lo1 ? -w1 : w1) * sn[f1];
           }
         }
       }
@@ -297,7 +309,7 @@ cudaError_t go(const RopeArgs &r, cudaStream_t s) {
   // Heads of a thread: one while that leaves SMs without work; else kMany, for which
   // its angles are computed once, of as many tokens as a block has room for.
   const bool many = r.tokens * (r.heads[0] + (CACHE ? 2 * r.heads[1] : 0)) > (int64_t)device_facts()->sm_count * 8 * SLOTS;
-  Args a = {r, {FastDiv(1), FastDiv(1)}, {}, {}, {}, {FastDiv(1), FastDiv(1)}, FastDiv(CACHE ? r.page : 1)};
+  Args a = {r, {FastDiv(1), FastDiv(1)}, {}, {}, {}, {FastDiv(1), FastDiv(1)}, FastDiv(r.rot > 0 ? r.rot / 2 : 1), FastDiv(CACHE ? r.page : 1)};
   for (int i = 0; i < (CACHE ? 2 : 1); ++i) {
     const int heads = i ? 2 * r.heads[1] : r.heads[0], most = many ? kMany : kFew, least = (heads + most - 1) / most;
     const int per_token = least < SLOTS ? least : SLOTS, each = (heads + per_token - 1) / per_token;
