@@ -40,7 +40,12 @@ namespace q4k {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFew = 1, kMany = 4;  // heads of a thread
+// Heads of a thread: where rows are few, and where they are many.  A prompt block of
+// 8191 x 80 x 128 bf16 to e4m3 took 127, 84 and 80 us with 2, 4 and 8; fp32 rows take
+// twice the registers.
+constexpr int kFew = 1;
+template <typename T>
+constexpr int kMany = sizeof(T) == 2 ? 8 : 4;
 
 enum Pairs { kHalf = 0, kAdjacent = 1, kAny = 2 };  // kAny: (i, i + R / 2) where R / 2 is no multiple of 4
 
@@ -129,7 +134,7 @@ __device__ __forceinline__ void store_fours(__nv_bfloat16 *p, int oa, int ob, co
 }
 
 template <int LPR, typename T, int PAIRS, bool CACHE, int R>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const Args a) {
   // cosines and sines of the block's tokens, [token][R / 2] each
   constexpr int SLOTS = kThreads / LPR;  // rows at a time
   __shared__ __align__(16) float cs[SLOTS * LPR * 4], sn[SLOTS * LPR * 4];
@@ -211,8 +216,29 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
     }
   }
   const float inv_dim = 1.f / (float)r.dim;
-  uint32_t page = 0, off = 0;
-  if (kv && (uint32_t)slot < r.n_slots) page = a.page.div(slot), off = slot - page * a.page.d;
+  // ---- where the first row goes, in bytes; the next ones lie steps further, values elsewhere
+  const bool e4m3 = CACHE && r.cache_dtype != Q4K_DTYPE_BF16, wide = !CACHE && r.out_dtype == Q4K_DTYPE_FP32;
+  const bool valid = !kv || (uint32_t)slot < r.n_slots;
+  uint8_t *to = nullptr;
+  int64_t to_step = 0, to_value = 0;
+  float *scale = nullptr;
+  int64_t scale_value = 0;
+  if (!kv) {
+    const int shift = wide ? 2 : 1;
+    to = static_cast<uint8_t *>(r.out) + ((tok * r.ldo_token + s * r.ldo_head) << shift);
+    to_step = (per_token * r.ldo_head) << shift;
+  } else if (valid) {
+    const int shift = e4m3 ? 0 : 1;
+    const uint32_t page = a.page.div(slot), off = slot - page * a.page.d;
+    to = static_cast<uint8_t *>(r.cache[0]) + ((page * r.page_stride + s * r.head_stride + off * r.token_stride) << shift);
+    to_step = (per_token * r.head_stride) << shift;
+    to_value = (static_cast<uint8_t *>(r.cache[1]) - static_cast<uint8_t *>(r.cache[0])) - ((r.heads[1] * r.head_stride) << shift);
+    if (e4m3) {
+      scale = r.scale[0] + ((int64_t)page * r.heads[1] + s) * a.page.d + off;
+      scale_value = (r.scale[1] - r.scale[0]) - (int64_t)r.heads[1] * a.page.d;
+    }
+  }
+  if (kv && !valid && slot != -1 && pos >= 0 && c == 0) set_device_error(r.err, kDevErrBadPage);
 
 #pragma unroll
   for (int k = 0; k < R; ++k) {
@@ -270,36 +296,25 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
       __syncwarp();  // partners are read before a row is written in place
     }
     // ---- out
-    if (!on || pos < 0) continue;
-    if (!kv) {
-      const int64_t to = tok * r.ldo_token + h * r.ldo_head;
+    if (!on || pos < 0 || !valid) continue;
+    uint8_t *p = to + k * to_step + (value ? to_value : 0);
+    if (!kv || !e4m3) {
       if (!mine) continue;
-      if (CACHE || r.out_dtype == Q4K_DTYPE_BF16) store_fours(static_cast<__nv_bfloat16 *>(r.out) + to, oa, ob, v);
-      else store_fours(static_cast<float *>(r.out) + to, oa, ob, v);
-    } else if ((uint32_t)slot >= r.n_slots) {
-      if (slot != -1 && c == 0) set_device_error(r.err, kDevErrBadPage);
-    } else {
-      const int head = value ? h - r.heads[1] : h;
-      const int64_t to = page * r.page_stride + head * r.head_stride + off * r.token_stride;
-      void *cache = value ? r.cache[1] : r.cache[0];
-      if (r.cache_dtype == Q4K_DTYPE_BF16) {
-        store_fours(static_cast<__nv_bfloat16 *>(cache) + to, oa, ob, v);
-      } else {
-        float amax = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-#pragma unroll
-        for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
-        amax = fmaxf(amax, kAmaxFloor);
-        float factor;
-        const float up = block_factor(amax, c, mask, factor);
-        const uint2 w = to_e4m3x8(v, up);
-        uint8_t *p = static_cast<uint8_t *>(cache) + to;
-        *reinterpret_cast<uint32_t *>(p + oa) = w.x;
-        *reinterpret_cast<uint32_t *>(p + ob) = w.y;
-        if (c == 0) (value ? r.scale[1] : r.scale[0])[((int64_t)page * r.heads[1] + head) * a.page.d + off] = factor;
-      }
+      if (wide) store_fours(reinterpret_cast<float *>(p), oa, ob, v);
+      else store_fours(reinterpret_cast<__nv_bfloat16 *>(p), oa, ob, v);
+      continue;
     }
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
+    amax = fmaxf(amax, kAmaxFloor);
+    // (a reciprocal and products, each off by half a unit, where q4k_kv_write divides: 60 instructions fewer)
+    const uint2 w = to_e4m3x8(v, 448.f * __frcp_rn(amax));
+    *reinterpret_cast<uint32_t *>(p + oa) = w.x;
+    *reinterpret_cast<uint32_t *>(p + ob) = w.y;
+    if (c == 0) scale[k * per_token * (int)a.page.d + (value ? scale_value : 0)] = amax * (1.f / 448.f);
   }
 }
 
@@ -311,13 +326,13 @@ cudaError_t go(const RopeArgs &r, cudaStream_t s) {
   const bool many = r.tokens * (r.heads[0] + (CACHE ? 2 * r.heads[1] : 0)) > (int64_t)device_facts()->sm_count * 8 * SLOTS;
   Args a = {r, {FastDiv(1), FastDiv(1)}, {}, {}, {}, {FastDiv(1), FastDiv(1)}, FastDiv(r.rot > 0 ? r.rot / 2 : 1), FastDiv(CACHE ? r.page : 1)};
   for (int i = 0; i < (CACHE ? 2 : 1); ++i) {
-    const int heads = i ? 2 * r.heads[1] : r.heads[0], most = many ? kMany : kFew, least = (heads + most - 1) / most;
+    const int heads = i ? 2 * r.heads[1] : r.heads[0], most = many ? kMany<T> : kFew, least = (heads + most - 1) / most;
     const int per_token = least < SLOTS ? least : SLOTS, each = (heads + per_token - 1) / per_token;
     const int groups = (each + most - 1) / most;
     a.per_token[i] = FastDiv(per_token), a.tokens[i] = SLOTS / per_token, a.rows[i] = (each + groups - 1) / groups, a.groups[i] = FastDiv(groups);
     a.blocks[i] = (uint32_t)((r.tokens + a.tokens[i] - 1) / a.tokens[i] * groups);
   }
-  if (many) rope_kernel<LPR, T, PAIRS, CACHE, kMany><<<a.blocks[0] + a.blocks[1], kThreads, 0, s>>>(a);
+  if (many) rope_kernel<LPR, T, PAIRS, CACHE, kMany<T>><<<a.blocks[0] + a.blocks[1], kThreads, 0, s>>>(a);
   else rope_kernel<LPR, T, PAIRS, CACHE, kFew><<<a.blocks[0] + a.blocks[1], kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
