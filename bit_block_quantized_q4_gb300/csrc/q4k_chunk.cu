@@ -54,7 +54,7 @@ constexpr int kMaxSms = 160;     // CTAs that the workspace is sized for
 constexpr int kThreads = 512;
 constexpr int kItemCost = 1;     // of an item's start and end, in tiles
 constexpr float kLazy = 8.f;     // binary orders that a maximum may grow before M follows
-constexpr float kUpBits = 7.f;   // e4m3: weights are stored times 2^7 (see softmax_tile)
+constexpr float kUpBits = 7.f;   // e4m3: weights are stored times 2^7, so that the largest, 2^kLazy more, are below 2^16
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr int kRing = 4;         // items on their way
 
@@ -76,10 +76,10 @@ struct Cfg {
   static constexpr int kCols = 512;
   static constexpr int kEs = E4M3 ? 1 : 2;
   static constexpr int kRaw = kTile * D;              // bytes of an e4m3 tile
-  // Q | K stages | V stages | e4m3: per V stage the K scales, log2 and reciprocal of the V scales
+  // Q | K stages | V stages | e4m3: per stage of V the scales of K and V
   static constexpr int kKAt = kNq * kQ, kVAt = kKAt + kStages * kSide;
   static constexpr int kScaleAt = kVAt + kStages * kSide;
-  static constexpr int kSmem = kScaleAt + (E4M3 ? kStages * 3 * kTile * 4 : 0) + 1024;
+  static constexpr int kSmem = kScaleAt + (E4M3 ? kStages * 2 * kTile * 4 : 0) + 1024;
   static_assert(kPCol + kPBufs * kTile / 2 <= kCols, "O, S and P fit tensor memory");
 };
 
@@ -271,9 +271,10 @@ struct Bars {
   uint64_t p_full[2], o_done[2];  // weights and their products, by buffer of weights
 };
 // Of a stage of V: 16-token pieces that are absent, tokens whose values are not
-// finite; e4m3: the least and the largest exponent field of the V scales.
+// finite; e4m3: the binary logarithm of what the values are multiplied by.
 struct VInfo {
-  uint32_t absent, bad[4], e_min, e_max;
+  uint32_t absent, bad[4];
+  float v_log;
 };
 
 template <int D, bool E4M3>
@@ -285,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars bars;
   __shared__ VInfo vinfo[4];
+  __shared__ uint32_t v_absent[4], e_max[4];  // of a stage of V; largest exponents of its scales by warp
   __shared__ Item items[kRing];
   __shared__ float q_scale[2][256];  // e4m3: what the rows' scores are multiplied by (this item's, the next one's)
   __shared__ int64_t sums[kThreads], wsum[kThreads / 32];
@@ -387,7 +389,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       bool poisoned = false;
       float sc = scale;
-      uint32_t e_max = 0;
       for (int j = 0; active && j < x.n && ok; ++j) {
         const int g = mine_t + j, buf = NQ == 1 ? g & 1 : t;
         const int vs = (tiles + j) % ST;
@@ -410,15 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < TILE; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * sign);
           }
-          const float *ks = reinterpret_cast<const float *>(smem + C::kScaleAt) + vs * 3 * TILE, *lv = ks + TILE, *rv = lv + TILE;
-          if (E4M3) {
+          if (E4M3) {  // the keys' scales: the same for all rows
+            const float4 *ks = reinterpret_cast<const float4 *>(smem + C::kScaleAt + vs * 2 * TILE * 4);
 #pragma unroll
             for (int c = 0; c < TILE; c += 4) {
-              const float4 k4 = *reinterpret_cast<const float4 *>(ks + c), l4 = *reinterpret_cast<const float4 *>(lv + c);
-              const float2 sc2 = make_float2(sc, sc);
-              const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), __fmul2_rn(make_float2(k4.x, k4.y), sc2), make_float2(l4.x, l4.y));
-              const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), __fmul2_rn(make_float2(k4.z, k4.w), sc2), make_float2(l4.z, l4.w));
-              s[c] = __float_as_uint(z0.x), s[c + 1] = __float_as_uint(z0.y), s[c + 2] = __float_as_uint(z1.x), s[c + 3] = __float_as_uint(z1.y);
+              const float4 k4 = ks[c / 4];
+              const float2 x0 = __fmul2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), make_float2(k4.x, k4.y));
+              const float2 x1 = __fmul2_rn(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), make_float2(k4.z, k4.w));
+              s[c] = __float_as_uint(x0.x), s[c + 1] = __float_as_uint(x0.y), s[c + 2] = __float_as_uint(x1.x), s[c + 3] = __float_as_uint(x1.y);
             }
           }
           const uint32_t absent = vinfo[vs].absent;
@@ -443,16 +443,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) tops[k] = max3(tops[k], __uint_as_float(s[c + k]), __uint_as_float(s[c + k + 4]));
           const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
-          // scores are S here, to be multiplied by sc, or (e4m3) in base 2 already
-          const float unit = E4M3 ? 1.f : sc;
-          const bool grew = m != -INFINITY && (top - m) * unit > kLazy;
-          if (m == -INFINITY) m = top;
+          // z = S sc (+ v_log: e4m3 weights carry what the tile's values were divided by).
+          // m is in S for bf16, in z for e4m3.
+          const float unit = E4M3 ? fmaxf(sc, 1e-37f) : sc, v_log = E4M3 ? vinfo[vs].v_log : 0.f;
+          const float top_z = !E4M3 || top == -INFINITY ? top : fmaf(top, unit, v_log), m_unit = E4M3 ? 1.f : sc;
+          const bool grew = m != -INFINITY && (top_z - m) * m_unit > kLazy;
+          if (m == -INFINITY) m = top_z;
           // the buffer of weights is free, and (g - 1: the last product, else in order) O
           // may be touched, once these are done
           if (!(ok = weights_free(g))) break;
           if (__any_sync(0xffffffffu, grew)) {
-            const float f = grew ? ex2((m - top) * unit) : 1.f;
-            if (grew) m = top;
+            const float f = grew ? ex2((m - top_z) * m_unit) : 1.f;
+            if (grew) m = top_z;
             l *= f;
             if (NQ == 1 && !(ok = values_done(g - 1))) break;
             tc_fence_after();
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_wait();
           }
-          const float ref = m == -INFINITY ? 0.f : -m * unit + (E4M3 ? kUpBits : 0.f);
+          const float ref = m == -INFINITY ? 0.f : E4M3 ? (v_log - m) + kUpBits : -m * sc;
           const float2 unit2 = make_float2(unit, unit), ref2 = make_float2(ref, ref);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -476,33 +478,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               const float2 z0 = make_float2(__uint_as_float(s[c + i]), __uint_as_float(s[c + i + 1])), z1 = make_float2(__uint_as_float(s[c + i + 2]), __uint_as_float(s[c + i + 3]));
-              const float2 y0 = E4M3 ? __fadd2_rn(z0, ref2) : __ffma2_rn(z0, unit2, ref2), y1 = E4M3 ? __fadd2_rn(z1, ref2) : __ffma2_rn(z1, unit2, ref2);
+              const float2 y0 = __ffma2_rn(z0, unit2, ref2), y1 = __ffma2_rn(z1, unit2, ref2);
               const float2 e0 = make_float2(ex2(y0.x), ex2(y0.y)), e1 = make_float2(ex2(y1.x), ex2(y1.y));
-              if (E4M3) {
-                const float4 r4 = *reinterpret_cast<const float4 *>(rv + c + i);
-                l2[0] = __ffma2_rn(e0, make_float2(r4.x, r4.y), l2[0]);
-                l2[1] = __ffma2_rn(e1, make_float2(r4.z, r4.w), l2[1]);
-                w[i / 2] = pack_f16(e0.x, e0.y), w[i / 2 + 1] = pack_f16(e1.x, e1.y);
-              } else {
-                l2[0] = __fadd2_rn(l2[0], e0), l2[1] = __fadd2_rn(l2[1], e1);
-                w[i / 2] = pack_bf16(e0.x, e0.y), w[i / 2 + 1] = pack_bf16(e1.x, e1.y);
-              }
+              l2[0] = __fadd2_rn(l2[0], e0), l2[1] = __fadd2_rn(l2[1], e1);
+              w[i / 2] = E4M3 ? pack_f16(e0.x, e0.y) : pack_bf16(e0.x, e0.y);
+              w[i / 2 + 1] = E4M3 ? pack_f16(e1.x, e1.y) : pack_bf16(e1.x, e1.y);
             }
             tmem_st_x16(at + c / 2, w);
           }
-          float more = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
-          if (E4M3) {
-            // A weight times its scale that underflows has no part in the product, but
-            // where the scales lie more than 2^100 apart its weight may be large: such
-            // tiles' sums are taken from the weights themselves.
-            e_max = max(e_max, vinfo[vs].e_max);
-            if (e_max > vinfo[vs].e_min + 100u) {
-              more = 0.f;
-#pragma unroll
-              for (int c = 0; c < TILE; ++c) more += ex2(__uint_as_float(s[c]) + ref - lv[c]);
-            }
-          }
-          l += more;
+          const float more = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+          l += E4M3 ? more * ex2(-v_log) : more;
           tmem_st_wait();
         } else if (!(ok = weights_free(g))) {  // a warp without rows must not run ahead of the others
           break;
@@ -802,13 +787,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int at16 = (__ffs(w) - 1) << (p.box_shift - 4);
               gone |= ((p.box_rows >> 4 == 32 ? 0u : 1u << (p.box_rows >> 4)) - 1u) << at16;
             }
-            vinfo[s].absent = gone;
+            v_absent[s] = gone;
             mbar_arrive_expect_tx(&bars.v_full[s], loaded + (E4M3 ? __popc(have) * p.box_rows * 8 : 0));
           }
           __syncwarp();
           copy(v, &vmap, &bars.v_full[s]);
           if (E4M3 && there && lane < boxes) {
-            float *ks = reinterpret_cast<float *>(smem + C::kScaleAt) + s * 3 * TILE + (b << p.box_shift);
+            float *ks = reinterpret_cast<float *>(smem + C::kScaleAt) + s * 2 * TILE + (b << p.box_shift);
             const int64_t from = ((int64_t)page * a.kv_heads + x.head) * a.page + in_page;
             bulk_load(ks, a.scale[0] + from, p.box_rows * 4, &bars.v_full[s]);
             bulk_load(ks + TILE, a.scale[1] + from, p.box_rows * 4, &bars.v_full[s]);
@@ -886,20 +871,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bars.q_full[t]);
       }
       if (!group_and(1, ok)) break;
+      int v_run = -1000;  // largest unit of this item's values so far
       for (int j = 0; j < x.n; ++j, ++tiles) {
         const int s = tiles % ST;
         const uint32_t ph = (uint32_t)(tiles / ST) & 1u;
         constexpr int RC = D / 16, PER = C::kRaw / 16 / 128;  // e4m3: 16-byte pieces of a row, and of a thread
-        // 16 e4m3 values of a token to 16 fp16 values at their swizzled place
-        const auto place = [&](uint8_t *side, int row, int ch, const uint4 &v) {
-          const uint2 a0 = e4m3x4_f16(v.x), a1 = e4m3x4_f16(v.y), a2 = e4m3x4_f16(v.z), a3 = e4m3x4_f16(v.w);
+        // 16 e4m3 values of a token, times f where they have a scale, to 16 fp16 values at their swizzled place
+        const auto place = [&](uint8_t *side, int row, int ch, const uint4 &v, bool scaled, float f) {
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          uint32_t out[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint2 h = e4m3x4_f16(in[e]);
+            out[2 * e] = h.x, out[2 * e + 1] = h.y;
+            if (scaled) {
+              const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&h.x)), hi = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
+              const float2 x0 = __fmul2_rn(lo, make_float2(f, f)), x1 = __fmul2_rn(hi, make_float2(f, f));
+              out[2 * e] = pack_f16(x0.x, x0.y), out[2 * e + 1] = pack_f16(x1.x, x1.y);
+            }
+          }
           uint8_t *to = side + (ch / 4) * TILE * 128 + row * 128;
-          const uint4 w0 = make_uint4(a0.x, a0.y, a1.x, a1.y), w1 = make_uint4(a2.x, a2.y, a3.x, a3.y);
+          const uint4 w0 = make_uint4(out[0], out[1], out[2], out[3]), w1 = make_uint4(out[4], out[5], out[6], out[7]);
           // pieces 0..3 of a row and 4..7 lie in the same banks: the latter write their second half first
           const int sw = (ch >> 2) & 1, c0 = 2 * (ch & 3);
           *reinterpret_cast<uint4 *>(to + (((c0 + sw) ^ (row & 7)) << 4)) = sw ? w1 : w0;
           *reinterpret_cast<uint4 *>(to + (((c0 + 1 - sw) ^ (row & 7)) << 4)) = sw ? w0 : w1;
         };
+        const int pos = (x.t0 + j) * TILE;
         if (E4M3) {
           ok = warp_wait(&bars.k_full[s], ph, a.err);
           uint8_t *k = smem + C::kKAt + s * C::kSide;
@@ -910,67 +908,77 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!(ok = group_and(1, ok))) break;
 #pragma unroll
-          for (int i = 0; i < PER; ++i) place(k, (th + 128 * i) / RC, (th + 128 * i) % RC, raw[i]);
+          for (int i = 0; i < PER; ++i) place(k, (th + 128 * i) / RC, (th + 128 * i) % RC, raw[i], false, 1.f);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.k_ready[s]);
         }
         ok = warp_wait(&bars.v_full[s], ph, a.err);
         uint8_t *v = smem + C::kVAt + s * C::kSide;
-        const int pos = (x.t0 + j) * TILE;
-        const uint32_t absent = vinfo[s].absent;
+        const uint32_t absent = v_absent[s];
+        const auto dead = [&](int row) { return pos + row < x.lo || pos + row >= x.hi || (absent >> (row / 16) & 1u); };
         // tokens that some row does not see, beside those that all rows see
         const bool partial = pos < x.full_lo || pos + TILE > x.full_hi || absent;
-        const auto dead = [&](int row) { return pos + row < x.lo || pos + row >= x.hi || (absent >> (row / 16) & 1u); };
         uint4 raw[E4M3 ? PER : 1];
-        if (E4M3 && ok) {
+        const float *v_scales = reinterpret_cast<const float *>(smem + C::kScaleAt) + (2 * s + 1) * TILE;
+        float mine = 1.f;
+        if (E4M3) {
+          if (ok) {
 #pragma unroll
-          for (int i = 0; i < PER; ++i) raw[i] = *reinterpret_cast<const uint4 *>(v + C::kSide - C::kRaw + (th + 128 * i) * 16);
+            for (int i = 0; i < PER; ++i) raw[i] = *reinterpret_cast<const uint4 *>(v + C::kSide - C::kRaw + (th + 128 * i) * 16);
+          }
+          mine = th < TILE ? v_scales[th] : 0.f;
+          // the largest exponent of this warp's scales; after the barrier that of all is known
+          const uint32_t e = th < TILE && !dead(th) && mine - mine == 0.f && mine > 0.f ? __float_as_uint(mine) >> 23 : 0u, top = __reduce_max_sync(0xffffffffu, e);
+          if (lane == 0) e_max[warp - 12] = top;
         }
         if (th < 4) vinfo[s].bad[th] = 0;
-        if (E4M3 && th == 4) vinfo[s].e_min = 255, vinfo[s].e_max = 0;
         if (!(ok = group_and(1, ok))) break;
         if (E4M3) {
-          if (th < TILE) {
-            float *ks = reinterpret_cast<float *>(smem + C::kScaleAt) + s * 3 * TILE + th;
-            float sv = fmaxf(ks[TILE], 1.2621774483536189e-29f);  // 2^-96
-            if (partial) {
-              const bool gone = dead(th), odd = !(ks[0] - ks[0] == 0.f) || !(ks[TILE] - ks[TILE] == 0.f);
-              if (!gone && odd) atomicOr(&vinfo[s].bad[th >> 5], 1u << (th & 31));
-              if (gone || odd) ks[0] = 1.f, sv = 0.f;
-            }
-            const uint32_t e = __float_as_uint(sv) >> 23, e_hi = __reduce_max_sync(0xffffffffu, e), e_lo = __reduce_min_sync(0xffffffffu, e ? e : 255u);
-            if (lane == 0) atomicMax(&vinfo[s].e_max, e_hi), atomicMin(&vinfo[s].e_min, e_lo);
-            if (e == 0) sv = 1.f;
-            ks[TILE] = log2f(sv);
-            ks[2 * TILE] = 1.f / sv;
+          // Values enter as fp16 times their scale over 2^v_log, by which the largest scale
+          // becomes 2^6 .. 2^7 (times 448 still fp16).  A tile whose scales are all far below
+          // an earlier one's keeps to 2^-90 of it: a weight that underflows with its
+          // scale would be missing in the sum of weights.
+          const uint32_t e = max(max(e_max[0], e_max[1]), max(e_max[2], e_max[3]));
+          const int here = max((e ? (int)e - 127 : 0) - 6, -120);
+          v_run = max(v_run, here);
+          const int v_log = max(here, v_run - 90);
+          const float down = __int_as_float((127 - v_log) << 23);
+          if (th == 0) vinfo[s].absent = absent, vinfo[s].v_log = (float)v_log;
+          // tokens whose scale is not finite, seen by some rows only
+          if (partial && th < TILE) {
+            const uint32_t odd = __ballot_sync(0xffffffffu, !dead(th) && !(mine - mine == 0.f));
+            if (odd && lane == 0) atomicOr(&vinfo[s].bad[th >> 5], odd);
           }
 #pragma unroll
           for (int i = 0; i < PER; ++i) {
             const int row = (th + 128 * i) / RC, ch = (th + 128 * i) % RC;
+            float f = v_scales[row] * down;
             if (partial) {
               const uint4 w = raw[i];
               const auto nan4 = [](uint32_t y) { return __vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu); };
-              const bool gone = dead(row);
-              const bool odd = (nan4(w.x) | nan4(w.y) | nan4(w.z) | nan4(w.w)) != 0;
-              if (!gone && odd) atomicOr(&vinfo[s].bad[row >> 5], 1u << (row & 31));
-              if (gone || odd) raw[i] = make_uint4(0, 0, 0, 0);
+              const bool gone = dead(row), nan = (nan4(w.x) | nan4(w.y) | nan4(w.z) | nan4(w.w)) != 0, odd = !(f - f == 0.f);
+              if (!gone && nan) atomicOr(&vinfo[s].bad[row >> 5], 1u << (row & 31));
+              if (gone || nan || odd) raw[i] = make_uint4(0, 0, 0, 0), f = 1.f;
             }
-            place(v, row, ch, raw[i]);
+            place(v, row, ch, raw[i], true, f);
           }
           fence_proxy_async_smem();
-        } else if (partial) {
-          constexpr int CH = D / 8;
-          for (int i = th; i < TILE * CH; i += 128) {
-            const int row = i / CH, ch = i % CH;
-            uint4 *at = reinterpret_cast<uint4 *>(v + (ch / 8) * TILE * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-            const uint4 w = *at;
-            const auto odd2 = [](uint32_t y) { return (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u; };
-            const bool gone = dead(row), odd = odd2(w.x) || odd2(w.y) || odd2(w.z) || odd2(w.w);
-            if (!gone && odd) atomicOr(&vinfo[s].bad[row >> 5], 1u << (row & 31));
-            if (gone || odd) *at = make_uint4(0, 0, 0, 0);
+        } else {
+          if (th == 0) vinfo[s].absent = absent;
+          if (partial) {
+            constexpr int CH = D / 8;
+            for (int i = th; i < TILE * CH; i += 128) {
+              const int row = i / CH, ch = i % CH;
+              uint4 *at = reinterpret_cast<uint4 *>(v + (ch / 8) * TILE * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+              const uint4 w = *at;
+              const auto odd2 = [](uint32_t y) { return (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u; };
+              const bool gone = dead(row), odd = odd2(w.x) || odd2(w.y) || odd2(w.z) || odd2(w.w);
+              if (!gone && odd) atomicOr(&vinfo[s].bad[row >> 5], 1u << (row & 31));
+              if (gone || odd) *at = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.v_ready[s]);

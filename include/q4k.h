@@ -707,11 +707,13 @@ int q4k_paged_attn(const void *q, int64_t ldq, int64_t ldq_head, int32_t n, int3
  * Q4K_DEVERR_BAD_PAGE.
  * Scores, softmax statistics and sums are fp32.  For a bf16 cache the softmax
  * weights enter the products as one bf16 term (8 significant bits, as the
- * result has), for an e4m3 cache as one fp16 term of the weight times the row's
- * scale: 11 bits down to 2^-21 of the largest such term, an error of at most
- * 2^-32 of it below.  q is exact for a bf16 cache; for an e4m3 cache it enters
- * as fp16 times a power of two per row: exact down to 2^-31 of the row's largest
- * value, to within 2^-39 of it below.
+ * result has), for an e4m3 cache as one fp16 term: 11 bits down to 2^-21 of the
+ * largest weight times scale, an error of at most 2^-32 of it below.  Keys are
+ * exact, and q for a bf16 cache; for an e4m3 cache q enters as fp16 times a power of
+ * two per row: exact down to 2^-31 of the row's largest value, to within 2^-39 of it
+ * below; and its values times their scales enter as fp16 times a power of two per
+ * 64 or 128 tokens: 11 bits down to 2^-29 of 448 times the largest of these tokens'
+ * scales, an error of at most 2^-40 of that below.
  * Values that are not finite in a row that a token sees show in the token's
  * result; one of V may do so as NaN in all of it.
  *   q       device, bf16, element (t, h, d) at t * ldq + h * ldq_head + d;
