@@ -272,8 +272,8 @@ struct Bars {
 };
 // Of a stage of V: 16-token pieces that are absent, tokens whose values are not
 // finite; e4m3: the binary logarithm of what the values are multiplied by.
-struct VInfo {
-  uint32_t absent, bad[4];
+struct __align__(16) VInfo {
+  uint32_t bad[4], absent;
   float v_log;
 };
 
@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
+    if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
     // ---------------------------------------------------------------- softmax
     const int t = warp >> 2, row_in = 32 * (warp & 3) + lane, row_t = 128 * t + row_in;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -423,13 +424,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t absent = vinfo[vs].absent;
           const int lo = seen_lo - (x.t0 + j) * TILE, hi = seen_hi - (x.t0 + j) * TILE;
-          if (__any_sync(0xffffffffu, lo > 0 || hi < TILE || absent)) {
+          // (bf16: only tiles that some row does not see entirely are looked through)
+          uint4 bad = make_uint4(0, 0, 0, 0);
+          if (E4M3) bad = *reinterpret_cast<const uint4 *>(vinfo[vs].bad);
+          if (__any_sync(0xffffffffu, lo > 0 || hi < TILE || (absent | bad.x | bad.y | bad.z | bad.w))) {
+            if (!E4M3) bad = *reinterpret_cast<const uint4 *>(vinfo[vs].bad);
 #pragma unroll
             for (int c = 0; c < TILE; ++c)
               if (c < lo || c >= hi || (absent >> (c / 16) & 1u)) s[c] = 0xff800000u;
 #pragma unroll
             for (int w = 0; w < TILE / 32; ++w) {
-              const uint32_t b = vinfo[vs].bad[w];
+              const uint32_t b = w == 0 ? bad.x : w == 1 ? bad.y : w == 2 ? bad.z : bad.w;
               if (b) {
                 const int lo_w = min(max(lo - 32 * w, 0), 32), hi_w = min(max(hi - 32 * w, 0), 32);
                 const uint32_t below = hi_w == 32 ? 0xffffffffu : (1u << hi_w) - 1u, from = lo_w == 32 ? 0u : 0xffffffffu << lo_w;
@@ -548,7 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++it;
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (warp == 8 || warp == 10) {
       // ------------------------------------------------------------- products
       // A whole warp runs each half, so that descriptors are uniform values; one lane issues.
@@ -818,7 +824,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     // ---------------------------------------------------------------- prepare
     const int th = tid - 384;  // 0..127
     int tiles = 0, count[2] = {0, 0};
@@ -876,26 +883,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = tiles % ST;
         const uint32_t ph = (uint32_t)(tiles / ST) & 1u;
         constexpr int RC = D / 16, PER = C::kRaw / 16 / 128;  // e4m3: 16-byte pieces of a row, and of a thread
-        // 16 e4m3 values of a token, times f where they have a scale, to 16 fp16 values at their swizzled place
-        const auto place = [&](uint8_t *side, int row, int ch, const uint4 &v, bool scaled, float f) {
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t out[8];
+        // This thread's 16-byte pieces (16 e4m3 values) of a tile lie in rows row0 + i
+        // (128 / RC), a multiple of 8 apart, at place ch of the row; they become two pieces
+        // of fp16 at their swizzled places.  Pieces 0..3 of a row and 4..7 lie in the same
+        // banks: the latter write their second half first.
+        const int row0 = th / RC, ch = th % RC, sw = (ch >> 2) & 1, c0 = 2 * (ch & 3);
+        const uint32_t at0 = (uint32_t)((ch / 4) * TILE * 128 + row0 * 128);
+        const uint32_t first = at0 + (uint32_t)(((c0 + sw) ^ (row0 & 7)) << 4), second = at0 + (uint32_t)(((c0 + 1 - sw) ^ (row0 & 7)) << 4);
+        const auto place = [&](uint8_t *side, int i, const uint4 &v, bool scaled, __half2 f) {
+          uint2 h[4] = {e4m3x4_f16(v.x), e4m3x4_f16(v.y), e4m3x4_f16(v.z), e4m3x4_f16(v.w)};
+          if (scaled) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint2 h = e4m3x4_f16(in[e]);
-            out[2 * e] = h.x, out[2 * e + 1] = h.y;
-            if (scaled) {
-              const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&h.x)), hi = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
-              const float2 x0 = __fmul2_rn(lo, make_float2(f, f)), x1 = __fmul2_rn(hi, make_float2(f, f));
-              out[2 * e] = pack_f16(x0.x, x0.y), out[2 * e + 1] = pack_f16(x1.x, x1.y);
+            for (int e = 0; e < 4; ++e) {
+              const __half2 lo = __hmul2(*reinterpret_cast<const __half2 *>(&h[e].x), f), hi = __hmul2(*reinterpret_cast<const __half2 *>(&h[e].y), f);
+              h[e] = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
             }
           }
-          uint8_t *to = side + (ch / 4) * TILE * 128 + row * 128;
-          const uint4 w0 = make_uint4(out[0], out[1], out[2], out[3]), w1 = make_uint4(out[4], out[5], out[6], out[7]);
-          // pieces 0..3 of a row and 4..7 lie in the same banks: the latter write their second half first
-          const int sw = (ch >> 2) & 1, c0 = 2 * (ch & 3);
-          *reinterpret_cast<uint4 *>(to + (((c0 + sw) ^ (row & 7)) << 4)) = sw ? w1 : w0;
-          *reinterpret_cast<uint4 *>(to + (((c0 + 1 - sw) ^ (row & 7)) << 4)) = sw ? w0 : w1;
+          const uint4 w0 = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y), w1 = make_uint4(h[2].x, h[2].y, h[3].x, h[3].y);
+          *reinterpret_cast<uint4 *>(side + first + i * (128 / RC) * 128) = sw ? w1 : w0;
+          *reinterpret_cast<uint4 *>(side + second + i * (128 / RC) * 128) = sw ? w0 : w1;
         };
         const int pos = (x.t0 + j) * TILE;
         if (E4M3) {
@@ -908,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!(ok = group_and(1, ok))) break;
 #pragma unroll
-          for (int i = 0; i < PER; ++i) place(k, (th + 128 * i) / RC, (th + 128 * i) % RC, raw[i], false, 1.f);
+          for (int i = 0; i < PER; ++i) place(k, i, raw[i], false, __half2());
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.k_ready[s]);
@@ -945,23 +951,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int v_log = max(here, v_run - 90);
           const float down = __int_as_float((127 - v_log) << 23);
           if (th == 0) vinfo[s].absent = absent, vinfo[s].v_log = (float)v_log;
-          // tokens whose scale is not finite, seen by some rows only
-          if (partial && th < TILE) {
+          // tokens whose scale is not finite
+          if (th < TILE) {
             const uint32_t odd = __ballot_sync(0xffffffffu, !dead(th) && !(mine - mine == 0.f));
             if (odd && lane == 0) atomicOr(&vinfo[s].bad[th >> 5], odd);
           }
+          if (partial) {
 #pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int row = (th + 128 * i) / RC, ch = (th + 128 * i) % RC;
-            float f = v_scales[row] * down;
-            if (partial) {
+            for (int i = 0; i < PER; ++i) {
+              const int row = row0 + i * (128 / RC);
               const uint4 w = raw[i];
               const auto nan4 = [](uint32_t y) { return __vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu); };
-              const bool gone = dead(row), nan = (nan4(w.x) | nan4(w.y) | nan4(w.z) | nan4(w.w)) != 0, odd = !(f - f == 0.f);
+              const bool gone = dead(row), nan = (nan4(w.x) | nan4(w.y) | nan4(w.z) | nan4(w.w)) != 0;
               if (!gone && nan) atomicOr(&vinfo[s].bad[row >> 5], 1u << (row & 31));
-              if (gone || nan || odd) raw[i] = make_uint4(0, 0, 0, 0), f = 1.f;
+              if (gone || nan) raw[i] = make_uint4(0, 0, 0, 0);
             }
-            place(v, row, ch, raw[i], true, f);
+          }
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const float f = v_scales[row0 + i * (128 / RC)] * down;
+            place(v, i, raw[i], true, __float2half2_rn(fabsf(f) <= 128.f ? f : 0.f));
           }
           fence_proxy_async_smem();
         } else {
