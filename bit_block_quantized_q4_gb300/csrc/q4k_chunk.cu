@@ -9,9 +9,10 @@
 // with a running reference M and sum l, in base 2 (scores carry log2 e):
 //   w_j = 2^(z_j - M),  l += w_j,  o += w_j v_j,  out = o / l.
 // M is the running maximum, but it follows only when the maximum has grown by
-// more than 2^kLazy; then l and o are multiplied by 2^(M - M').  A sum of
-// powers is the same whatever its reference, so this costs nothing but kLazy of
-// fp32's exponent, and o, which lives in tensor memory, is rarely touched.
+// more than 2^kLazy, and it is a whole number; then l and o are multiplied by the
+// power of two 2^(M - M').  A sum of powers is the same whatever its reference, so
+// this costs nothing but kLazy of fp32's exponent, and o, which lives in tensor
+// memory, is rarely touched.
 //
 // Rows.  The query heads of one key head share its keys, so the rows of a
 // product are (token, head) pairs: row = token * group + head.  128 of them are a
@@ -66,6 +67,8 @@ struct Cfg {
   // each query tile, or of a key tile and the next (256).
   static constexpr int kSBufs = D == 128 ? 1 : 2, kPBufs = 2;
   static constexpr int kTile = D == 256 ? 64 : 128;   // tokens per key tile
+  // Registers of a softmax thread; the others have 256 less these.
+  static constexpr int kMoreRegs = D == 256 ? 152 : E4M3 ? 176 : 184;
   static constexpr int kParts = D / 64;               // 128-byte parts of a row
   static constexpr int kSide = kTile * D * 2;         // bytes of a tile of K or V
   static constexpr int kStages = D == 64 ? 4 : 2;     // of K, and of V
@@ -361,8 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 8) {
-    if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kMoreRegs));
     // ---------------------------------------------------------------- softmax
     const int t = warp >> 2, row_in = 32 * (warp & 3) + lane, row_t = 128 * t + row_in;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -395,19 +397,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int vs = (tiles + j) % ST;
         if (!(ok = warp_wait(&bars.s_full[buf], (uint32_t)(NQ == 1 ? g >> 1 : g) & 1u, a.err))) break;
         tc_fence_after();
+        const uint32_t s_at = s_col + (C::kSBufs == 1 ? 0 : buf) * TILE, at = p_col + buf * (TILE / 2);
         uint32_t s[TILE];
         if (used) {
 #pragma unroll
-          for (int c = 0; c < TILE; c += 32) tmem_ld_x32(s_col + (C::kSBufs == 1 ? 0 : buf) * TILE + c, s + c);
+          for (int c = 0; c < TILE; c += 32) tmem_ld_x32(s_at + c, s + c);
           tmem_ld_wait();
           tc_fence_before();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.s_free[C::kSBufs == 1 ? 0 : buf]);
-        if (!(ok = warp_wait(&bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err))) break;
+        // V is ready, so that the product waits for the weights alone; and the buffer of
+        // weights is free, and O complete but for this tile
+        if (!(ok = warp_wait(&bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err) && weights_free(g))) break;
         if (used) {
           if (E4M3 && j == 0) sc = scale * q_scale[taken & 1][row_t];
-          const uint32_t at = p_col + buf * (TILE / 2);
           if (!positive) {
 #pragma unroll
             for (int c = 0; c < TILE; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * sign);
@@ -425,21 +429,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t absent = vinfo[vs].absent;
           const int lo = seen_lo - (x.t0 + j) * TILE, hi = seen_hi - (x.t0 + j) * TILE;
           // (bf16: only tiles that some row does not see entirely are looked through)
-          uint4 bad = make_uint4(0, 0, 0, 0);
-          if (E4M3) bad = *reinterpret_cast<const uint4 *>(vinfo[vs].bad);
-          if (__any_sync(0xffffffffu, lo > 0 || hi < TILE || (absent | bad.x | bad.y | bad.z | bad.w))) {
-            if (!E4M3) bad = *reinterpret_cast<const uint4 *>(vinfo[vs].bad);
+          const uint32_t *bad_words = vinfo[vs].bad;
+          uint32_t some = absent;
+          if (E4M3) {
 #pragma unroll
-            for (int c = 0; c < TILE; ++c)
-              if (c < lo || c >= hi || (absent >> (c / 16) & 1u)) s[c] = 0xff800000u;
+            for (int w = 0; w < TILE / 32; ++w) some |= bad_words[w];
+          }
+          if (__any_sync(0xffffffffu, lo > 0 || hi < TILE || some)) {
 #pragma unroll
-            for (int w = 0; w < TILE / 32; ++w) {
-              const uint32_t b = w == 0 ? bad.x : w == 1 ? bad.y : w == 2 ? bad.z : bad.w;
-              if (b) {
-                const int lo_w = min(max(lo - 32 * w, 0), 32), hi_w = min(max(hi - 32 * w, 0), 32);
-                const uint32_t below = hi_w == 32 ? 0xffffffffu : (1u << hi_w) - 1u, from = lo_w == 32 ? 0u : 0xffffffffu << lo_w;
-                poisoned |= (b & below & from) != 0;
-              }
+            for (int w = 0; w < TILE / 32; ++w) {  // the tokens that this row sees, as bits
+              const int lo_w = min(max(lo - 32 * w, 0), 32), hi_w = min(max(hi - 32 * w, 0), 32);
+              uint32_t sees = (hi_w == 32 ? 0xffffffffu : (1u << hi_w) - 1u) & (lo_w == 32 ? 0u : 0xffffffffu << lo_w);
+              if (absent >> 2 * w & 1u) sees &= 0xffff0000u;
+              if (absent >> (2 * w + 1) & 1u) sees &= 0x0000ffffu;
+              poisoned |= (bad_words[w] & sees) != 0;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(sees >> c & 1u)) s[32 * w + c] = 0xff800000u;
             }
           }
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -449,19 +455,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) tops[k] = max3(tops[k], __uint_as_float(s[c + k]), __uint_as_float(s[c + k + 4]));
           const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
           // z = S sc (+ v_log: e4m3 weights carry what the tile's values were divided by).
-          // m is in S for bf16, in z for e4m3.
-          const float unit = E4M3 ? fmaxf(sc, 1e-37f) : sc, v_log = E4M3 ? vinfo[vs].v_log : 0.f;
-          const float top_z = !E4M3 || top == -INFINITY ? top : fmaf(top, unit, v_log), m_unit = E4M3 ? 1.f : sc;
-          const bool grew = m != -INFINITY && (top_z - m) * m_unit > kLazy;
-          if (m == -INFINITY) m = top_z;
-          // the buffer of weights is free, and (g - 1: the last product, else in order) O
-          // may be touched, once these are done
-          if (!(ok = weights_free(g))) break;
+          // m is a whole number, so that a change of it multiplies by a power of two.
+          const float unit = fmaxf(sc, 1e-37f), v_log = E4M3 ? vinfo[vs].v_log : 0.f;
+          const float top_z = top == -INFINITY ? top : fmaf(top, unit, v_log);
+          const bool grew = m != -INFINITY && top_z > m + kLazy;
+          if (m == -INFINITY) m = ceilf(top_z);
           if (__any_sync(0xffffffffu, grew)) {
-            const float f = grew ? ex2((m - top_z) * m_unit) : 1.f;
-            if (grew) m = top_z;
+            const float up = ceilf(top_z), d = grew ? m - up : 0.f, f = d > -126.f ? __int_as_float((127 + (int)d) << 23) : 0.f;
+            if (grew) m = up;
             l *= f;
-            if (NQ == 1 && !(ok = values_done(g - 1))) break;
+            if (NQ == 1 && !(ok = g == 0 || values_done(g - 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_wait();
           }
-          const float ref = m == -INFINITY ? 0.f : E4M3 ? (v_log - m) + kUpBits : -m * sc;
+          const float ref = m == -INFINITY ? 0.f : (v_log - m) + (E4M3 ? kUpBits : 0.f);
           const float2 unit2 = make_float2(unit, unit), ref2 = make_float2(ref, ref);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -494,8 +497,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float more = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
           l += E4M3 ? more * ex2(-v_log) : more;
           tmem_st_wait();
-        } else if (!(ok = weights_free(g))) {  // a warp without rows must not run ahead of the others
-          break;
         }
         tc_fence_before();
         __syncwarp();
@@ -508,7 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       if (used && ok) {
-        const float big = m == -INFINITY ? -INFINITY : E4M3 ? m : m * sc;
         const int i = tok, head = x.head * p.group + (row - tok * p.group);
         const int64_t token = (int64_t)x.tok0 + i;
         float *slot = p.slots + (2 * (int64_t)blockIdx.x + (x.kind == 1)) * (int64_t)(D + 2) * p.slot_rows + row_t;
@@ -539,10 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (live && x.kind) {
-          slot[(int64_t)D * p.slot_rows] = big;
+          slot[(int64_t)D * p.slot_rows] = m;
           slot[(int64_t)(D + 1) * p.slot_rows] = l;
         } else if (live && a.lse) {
-          a.lse[token * a.q_heads + head] = l == 0.f ? -INFINITY : (big + log2f(l) - (E4M3 ? kUpBits : 0.f)) * kLn2;
+          a.lse[token * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l) - (E4M3 ? kUpBits : 0.f)) * kLn2;
         }
       }
       tc_fence_before();
@@ -553,8 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++it;
     }
   } else if (warp < 12) {
-    if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(256 - C::kMoreRegs));
     if (warp == 8 || warp == 10) {
       // ------------------------------------------------------------- products
       // A whole warp runs each half, so that descriptors are uniform values; one lane issues.
@@ -824,8 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(256 - C::kMoreRegs));
     // ---------------------------------------------------------------- prepare
     const int th = tid - 384;  // 0..127
     int tiles = 0, count[2] = {0, 0};
