@@ -32,7 +32,7 @@
 //               cache is converted to fp16 in place
 //
 // Work split.  An item is (request, key head, block of rows), its cost its key
-// tiles and kItemCost; every CTA of a persistent grid takes an equal run of the
+// tiles and a fixed cost; every CTA of a persistent grid takes an equal run of the
 // list of all items' tiles.  The lengths are on the device, so each CTA sums them
 // itself.  A CTA has at most two pieces of items that it shares with others; they
 // go to the workspace and a second launch joins them.
@@ -53,7 +53,6 @@ namespace {
 
 constexpr int kMaxSms = 160;     // CTAs that the workspace is sized for
 constexpr int kThreads = 512;
-constexpr int kItemCost = 1;     // of an item's start and end, in tiles
 constexpr float kLazy = 8.f;     // binary orders that a maximum may grow before M follows
 constexpr float kUpBits = 7.f;   // e4m3: weights are stored times 2^7, so that the largest, 2^kLazy more, are below 2^16
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
@@ -69,6 +68,10 @@ struct Cfg {
   static constexpr int kTile = D == 256 ? 64 : 128;   // tokens per key tile
   // Registers of a softmax thread; the others have 256 less these.
   static constexpr int kMoreRegs = D == 256 ? 152 : E4M3 ? 176 : 184;
+  // Cost of an item's start and end, in key tiles, for the shares of the CTAs.  Measured
+  // on an 8191-token prompt, bf16, head size 128: 1: 972 us, 2: 916, 4: 813, 6: 807, 8: 835;
+  // on 24 requests of e4m3, whose tiles cost more: 1: 1184, 4: 1208, 6: 1227.
+  static constexpr int kItemCost = E4M3 ? 1 : 5;
   static constexpr int kParts = D / 64;               // 128-byte parts of a row
   static constexpr int kSide = kTile * D * 2;         // bytes of a tile of K or V
   static constexpr int kStages = D == 64 ? 4 : 2;     // of K, and of V
@@ -132,11 +135,11 @@ __device__ __forceinline__ void tiles_of(const Params &p, const Req &q, int row0
   t0 = lo / TILE;
   t1 = hi > lo ? (hi + TILE - 1) / TILE : t0;
 }
-template <int TILE, int ROWS>
+template <int TILE, int ROWS, int ITEM_COST>
 __device__ __forceinline__ int block_cost(const Params &p, const Req &q, int b) {
   int t0, t1;
   tiles_of<TILE>(p, q, b * ROWS, min(ROWS, q.rows - b * ROWS), t0, t1);
-  return t1 - t0 + kItemCost;
+  return t1 - t0 + ITEM_COST;
 }
 
 // What all roles know of an item.
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto cost_of = [&](int r) {
     const Req q = request(p, r, bad);
     int64_t c = 0;
-    for (int b = 0; b * ROWS < q.rows; ++b) c += block_cost<TILE, ROWS>(p, q, b);
+    for (int b = 0; b * ROWS < q.rows; ++b) c += block_cost<TILE, ROWS, C::kItemCost>(p, q, b);
     return c * a.kv_heads;
   };
   for (int r = r_lo; r < r_hi; ++r) mine += cost_of(r);
@@ -672,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         r = a.n;
       }
       const auto blocks_at = [&]() {  // the costs of 32 blocks, and the units before each
-        const int cost = b0 + lane < blocks ? block_cost<TILE, ROWS>(p, q, b0 + lane) : 0;
+        const int cost = b0 + lane < blocks ? block_cost<TILE, ROWS, C::kItemCost>(p, q, b0 + lane) : 0;
         upto = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -693,8 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int t0, t1;
             tiles_of<TILE>(p, q, x.row0, x.rows, t0, t1);
             const int nt = t1 - t0;
-            // tile k of the item is unit ub + kItemCost + k
-            const int ta = (int)min(max(u0 - ub - kItemCost, (int64_t)0), (int64_t)nt), tb = (int)min(max(u1 - ub - kItemCost, (int64_t)0), (int64_t)nt);
+            // tile k of the item is unit ub + item cost + k
+            const int ta = (int)min(max(u0 - ub - C::kItemCost, (int64_t)0), (int64_t)nt), tb = (int)min(max(u1 - ub - C::kItemCost, (int64_t)0), (int64_t)nt);
             if (nt == 0 ? ub < u0 : ta == tb) continue;  // another CTA's
             const int first = q.pos0 + (int)p.by_group.div(x.row0), last = q.pos0 + (int)p.by_group.div(x.row0 + x.rows - 1);
             x.lo = first_seen(a, first), x.hi = end_seen(a, last);
@@ -702,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.t0 = t0 + ta, x.n = tb - ta;
             x.kind = x.n == nt ? 0 : ta == 0 ? 1 : 2;
             if (x.kind == 1) {
-              open = make_int4(r, head, x.row0, (int)((ub + kItemCost + nt - 1) / run));
+              open = make_int4(r, head, x.row0, (int)((ub + C::kItemCost + nt - 1) / run));
               open_rows = x.rows;
             }
             return true;
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             q = request(p, r, ignore);
             blocks = (q.rows + ROWS - 1) / ROWS;
             unit = 0;  // of a key head: lanes take blocks in turn
-            for (int b = lane; b < blocks; b += 32) unit += block_cost<TILE, ROWS>(p, q, b);
+            for (int b = lane; b < blocks; b += 32) unit += block_cost<TILE, ROWS, C::kItemCost>(p, q, b);
 #pragma unroll
             for (int o = 16; o; o >>= 1) unit += __shfl_xor_sync(0xffffffffu, unit, o);
             if (!blocks || at + unit * a.kv_heads <= u0) {
