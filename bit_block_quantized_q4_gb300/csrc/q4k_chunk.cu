@@ -68,10 +68,10 @@ struct Cfg {
   static constexpr int kTile = D == 256 ? 64 : 128;   // tokens per key tile
   // Registers of a softmax thread; the others have 256 less these.
   static constexpr int kMoreRegs = D == 256 ? 152 : E4M3 ? 176 : 184;
-  // Cost of an item's start and end, in key tiles, for the shares of the CTAs.  Measured
-  // on an 8191-token prompt, bf16, head size 128: 1: 972 us, 2: 916, 4: 813, 6: 807, 8: 835;
-  // on 24 requests of e4m3, whose tiles cost more: 1: 1184, 4: 1208, 6: 1227.
-  static constexpr int kItemCost = E4M3 ? 1 : 5;
+  // Cost of an item's start and end, in key tiles, for the shares of the CTAs.  Measured on
+  // an 8191-token prompt, bf16, head size 128: 1: 972 us, 2: 916, 4: 813, 5: 786, 6: 807,
+  // 8: 835; on 60 requests of e4m3, whose tiles cost more: 1: 929, 2: 926, 3: 922.
+  static constexpr int kItemCost = E4M3 ? 3 : 5;
   static constexpr int kParts = D / 64;               // 128-byte parts of a row
   static constexpr int kSide = kTile * D * 2;         // bytes of a tile of K or V
   static constexpr int kStages = D == 64 ? 4 : 2;     // of K, and of V
@@ -907,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Head size 128: a row's values lie where the second half of the same row goes, and a
         // row belongs to one warp, so that rows are converted one after the other by a short
         // loop.  (Unrolled, these warps wait for their instructions, which the others' push
-        // out: 24 requests and three chunks 1183 us, unrolled by 4 1072, by 2 945, not 927.)
+        // out: 60 requests, three of them chunks, 1183 us, unrolled by 4 1072, by 2 945, not 927.)
         constexpr bool kRowwise = D == 128;
         const int pos = (x.t0 + j) * TILE;
         if (E4M3) {
