@@ -9,10 +9,9 @@
 // with a running reference M and sum l, in base 2 (scores carry log2 e):
 //   w_j = 2^(z_j - M),  l += w_j,  o += w_j v_j,  out = o / l.
 // M is the running maximum, but it follows only when the maximum has grown by
-// more than 2^kLazy, and it is a whole number; then l and o are multiplied by the
-// power of two 2^(M - M').  A sum of powers is the same whatever its reference, so
-// this costs nothing but kLazy of fp32's exponent, and o, which lives in tensor
-// memory, is rarely touched.
+// more than 2^kLazy; then l and o are multiplied by 2^(M - M').  A sum of powers is
+// the same whatever its reference, so this costs nothing but kLazy of fp32's
+// exponent, and o, which lives in tensor memory, is rarely touched.
 //
 // Rows.  The query heads of one key head share its keys, so the rows of a
 // product are (token, head) pairs: row = token * group + head.  128 of them are a
@@ -458,14 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) tops[k] = max3(tops[k], __uint_as_float(s[c + k]), __uint_as_float(s[c + k + 4]));
           const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
           // z = S sc (+ v_log: e4m3 weights carry what the tile's values were divided by).
-          // m is a whole number, so that a change of it multiplies by a power of two.
+          // m starts as the maximum itself: the weight of a row's only token is 1, exactly.
           const float unit = fmaxf(sc, 1e-37f), v_log = E4M3 ? vinfo[vs].v_log : 0.f;
           const float top_z = top == -INFINITY ? top : fmaf(top, unit, v_log);
           const bool grew = m != -INFINITY && top_z > m + kLazy;
-          if (m == -INFINITY) m = ceilf(top_z);
+          if (m == -INFINITY) m = top_z;
           if (__any_sync(0xffffffffu, grew)) {
-            const float up = ceilf(top_z), d = grew ? m - up : 0.f, f = d > -126.f ? __int_as_float((127 + (int)d) << 23) : 0.f;
-            if (grew) m = up;
+            const float f = grew ? ex2(m - top_z) : 1.f;
+            if (grew) m = top_z;
             l *= f;
             if (NQ == 1 && !(ok = g == 0 || values_done(g - 1))) break;
             tc_fence_after();
