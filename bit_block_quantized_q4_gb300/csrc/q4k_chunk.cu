@@ -291,9 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars bars;
   __shared__ VInfo vinfo[4];
-  __shared__ uint32_t v_absent[4], e_max[4];  // of a stage of V; largest exponents of its scales by warp
+  __shared__ uint32_t v_absent[4], e_max[2][4];  // of a stage of V; largest exponents of a tile's scales by warp, two tiles in turn
   __shared__ Item items[kRing];
-  __shared__ float q_scale[2][256];  // e4m3: what the rows' scores are multiplied by (this item's, the next one's)
+  __shared__ float q_scale[kRing][ROWS];  // e4m3: what the rows' scores are multiplied by, of the items on their way
   __shared__ int64_t sums[kThreads], wsum[kThreads / 32];
   __shared__ uint32_t tmem_slot;
   const AttnArgs &a = p.a;
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // weights is free, and O complete but for this tile
         if (!(ok = warp_wait(&bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err) && weights_free(g))) break;
         if (used) {
-          if (E4M3 && j == 0) sc = scale * q_scale[taken & 1][row_t];
+          if (E4M3 && j == 0) sc = scale * q_scale[taken % kRing][row_t];
           if (!positive) {
 #pragma unroll
             for (int c = 0; c < TILE; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * sign);
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) w[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
             *at = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          q_scale[c & 1][128 * t + row] = __int_as_float((127 - up) << 23);
+          q_scale[c % kRing][128 * t + row] = __int_as_float((127 - up) << 23);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -913,9 +913,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&bars.k_full[s], ph, a.err);
           uint8_t *k = smem + C::kKAt + s * C::kSide;
           if (kRowwise) {
-            if (!ok) break;
 #pragma unroll 1
-            for (int i = 0; i < PER; ++i) {
+            for (int i = 0; ok && i < PER; ++i) {
               const uint4 raw = *reinterpret_cast<const uint4 *>(k + C::kSide - C::kRaw + (th + 128 * i) * 16);
               __syncwarp();
               place(k, i, raw, false, __half2());
@@ -934,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.k_ready[s]);
         }
-        ok = warp_wait(&bars.v_full[s], ph, a.err);
+        ok = warp_wait(&bars.v_full[s], ph, a.err) && ok;  // (the group leaves as one, below)
         uint8_t *v = smem + C::kVAt + s * C::kSide;
         const uint32_t absent = v_absent[s];
         const auto dead = [&](int row) { return pos + row < x.lo || pos + row >= x.hi || (absent >> (row / 16) & 1u); };
@@ -951,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mine = th < TILE ? v_scales[th] : 0.f;
           // the largest exponent of this warp's scales; after the barrier that of all is known
           const uint32_t e = th < TILE && !dead(th) && mine - mine == 0.f && mine > 0.f ? __float_as_uint(mine) >> 23 : 0u, top = __reduce_max_sync(0xffffffffu, e);
-          if (lane == 0) e_max[warp - 12] = top;
+          if (lane == 0) e_max[tiles & 1][warp - 12] = top;
         }
         if (th < 4) vinfo[s].bad[th] = 0;
         if (!(ok = group_and(1, ok))) break;
@@ -960,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // becomes 2^6 .. 2^7 (times 448 still fp16).  A tile whose scales are all far below
           // an earlier one's keeps to 2^-90 of it: a weight that underflows with its
           // scale would be missing in the sum of weights.
-          const uint32_t e = max(max(e_max[0], e_max[1]), max(e_max[2], e_max[3]));
+          const uint32_t *tops = e_max[tiles & 1], e = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
           const int here = max((e ? (int)e - 127 : 0) - 6, -120);
           v_run = max(v_run, here);
           const int v_log = max(here, v_run - 90);
