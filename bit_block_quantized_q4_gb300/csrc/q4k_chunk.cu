@@ -81,6 +81,7 @@ struct Cfg {
   static constexpr int kCols = 512;
   static constexpr int kEs = E4M3 ? 1 : 2;
   static constexpr int kRaw = kTile * D;              // bytes of an e4m3 tile
+  static constexpr int kRawParts = D == 256 ? 2 : 1;  // in which its rows are copied
   // Q | K stages | V stages | e4m3: per stage of V the scales of K and V
   static constexpr int kKAt = kNq * kQ, kVAt = kKAt + kStages * kSide;
   static constexpr int kScaleAt = kVAt + kStages * kSide;
@@ -779,7 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (E4M3) k += C::kSide - C::kRaw, v += C::kSide - C::kRaw;
           const auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar) {
             if (E4M3) {
-              if (there && lane < boxes) tma_load_5d(dst + (b << p.box_shift) * D, map, bar, 0, in_page, 0, x.head, page);
+              for (int part = lane / boxes; part < C::kRawParts; part += 32 / boxes)
+                if (there) tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * (D / C::kRawParts), map, bar, 0, in_page, part, x.head, page);
             } else {
               for (int part = lane / boxes; part < C::kParts; part += 32 / boxes)
                 if (there) tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * 128, map, bar, 0, in_page, part, x.head, page);
@@ -903,32 +905,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4 *>(side + first + i * (128 / RC) * 128) = sw ? w1 : w0;
           *reinterpret_cast<uint4 *>(side + second + i * (128 / RC) * 128) = sw ? w0 : w1;
         };
-        // Head size 128: a row's values lie where the second half of the same row goes, and a
-        // row belongs to one warp, so that rows are converted one after the other by a short
-        // loop.  (Unrolled, these warps wait for their instructions, which the others' push
-        // out: 60 requests, three of them chunks, 1183 us, unrolled by 4 1072, by 2 945, not 927.)
-        constexpr bool kRowwise = D == 128;
+        // Rows are converted one after the other by a short loop.  (Unrolled, these warps
+        // wait for their instructions, which the others' push out: 60 requests, three of
+        // them chunks, head size 128, 1183 us, unrolled by 4 1072, by 2 945, not 927.)
+        // Head sizes 128 and 256: 128 values of a row lie where their later half goes, and a
+        // row belongs to one warp.  Size 64: row r goes where rows 2 r - 128 and 2 r - 127 lay,
+        // so that all warps have read up to r before one of them writes.
+        const uint32_t raw_at = (uint32_t)(C::kSide - C::kRaw + (D == 256 ? (ch / 8) * TILE * 128 + row0 * 128 + (ch & 7) * 16 : th * 16));
+        const auto convert = [&](uint8_t *side, const auto &put) {
+#pragma unroll 1
+          for (int i = 0; i < PER; ++i) {
+            const uint4 raw = *reinterpret_cast<const uint4 *>(side + raw_at + i * (128 / RC) * (D == 64 ? 64 : 128));
+            if (D == 64) ok = group_and(1, ok);
+            else __syncwarp();
+            put(i, raw);
+          }
+        };
         const int pos = (x.t0 + j) * TILE;
         if (E4M3) {
           ok = warp_wait(&bars.k_full[s], ph, a.err);
           uint8_t *k = smem + C::kKAt + s * C::kSide;
-          if (kRowwise) {
-#pragma unroll 1
-            for (int i = 0; ok && i < PER; ++i) {
-              const uint4 raw = *reinterpret_cast<const uint4 *>(k + C::kSide - C::kRaw + (th + 128 * i) * 16);
-              __syncwarp();
-              place(k, i, raw, false, __half2());
-            }
-          } else {
-            uint4 raw[PER];
-            if (ok) {
-#pragma unroll
-              for (int i = 0; i < PER; ++i) raw[i] = *reinterpret_cast<const uint4 *>(k + C::kSide - C::kRaw + (th + 128 * i) * 16);
-            }
-            if (!(ok = group_and(1, ok))) break;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) place(k, i, raw[i], false, __half2());
-          }
+          convert(k, [&](int i, const uint4 &w) { place(k, i, w, false, __half2()); });
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.k_ready[s]);
@@ -939,14 +936,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto dead = [&](int row) { return pos + row < x.lo || pos + row >= x.hi || (absent >> (row / 16) & 1u); };
         // tokens that some row does not see, beside those that all rows see
         const bool partial = pos < x.full_lo || pos + TILE > x.full_hi || absent;
-        uint4 raw[E4M3 && !kRowwise ? PER : 1];
         const float *v_scales = reinterpret_cast<const float *>(smem + C::kScaleAt) + (2 * s + 1) * TILE;
         float mine = 1.f;
         if (E4M3) {
-          if (ok && !kRowwise) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) raw[i] = *reinterpret_cast<const uint4 *>(v + C::kSide - C::kRaw + (th + 128 * i) * 16);
-          }
           mine = th < TILE ? v_scales[th] : 0.f;
           // the largest exponent of this warp's scales; after the barrier that of all is known
           const uint32_t e = th < TILE && !dead(th) && mine - mine == 0.f && mine > 0.f ? __float_as_uint(mine) >> 23 : 0u, top = __reduce_max_sync(0xffffffffu, e);
@@ -970,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t odd = __ballot_sync(0xffffffffu, !dead(th) && !(mine - mine == 0.f));
             if (odd && lane == 0) atomicOr(&vinfo[s].bad[th >> 5], odd);
           }
-          const auto piece = [&](int i, uint4 w) {
+          convert(v, [&](int i, uint4 w) {
             const int row = row0 + i * (128 / RC);
             if (partial) {
               const auto nan4 = [](uint32_t y) { return __vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu); };
@@ -980,18 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float f = v_scales[row] * down;
             place(v, i, w, true, __float2half2_rn(fabsf(f) <= 128.f ? f : 0.f));
-          };
-          if (kRowwise) {
-#pragma unroll 1
-            for (int i = 0; i < PER; ++i) {
-              const uint4 w = *reinterpret_cast<const uint4 *>(v + C::kSide - C::kRaw + (th + 128 * i) * 16);
-              __syncwarp();
-              piece(i, w);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) piece(i, raw[i]);
-          }
+          });
           fence_proxy_async_smem();
         } else {
           if (th == 0) vinfo[s].absent = absent;
@@ -1084,8 +1065,8 @@ cudaError_t launch_cfg(Params &p, cudaStream_t stream) {
   p.box_shift = 31 - __builtin_clz((unsigned)p.box_rows);
   p.page_shift = 31 - __builtin_clz((unsigned)a.page);
   // (values of a part of a row, token, part, head, page): a bf16 row in 128-byte
-  // parts, swizzled; an e4m3 row in one
-  const int inner = E4M3 ? D : 64, parts = E4M3 ? 1 : C::kParts;
+  // parts, swizzled; an e4m3 row in parts of 64 or 128 bytes
+  const int parts = E4M3 ? C::kRawParts : C::kParts, inner = D / parts;
   const uint64_t dims[5] = {(uint64_t)inner, (uint64_t)a.page, (uint64_t)parts, (uint64_t)a.kv_heads, (uint64_t)a.n_pages};
   const uint64_t strides[4] = {(uint64_t)a.token_stride * C::kEs, (uint64_t)inner * C::kEs, (uint64_t)a.head_stride * C::kEs,
                                (uint64_t)a.page_stride * C::kEs};
