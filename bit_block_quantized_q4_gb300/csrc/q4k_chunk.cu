@@ -35,6 +35,20 @@
 // list of all items' tiles.  The lengths are on the device, so each CTA sums them
 // itself.  A CTA has at most two pieces of items that it shares with others; they
 // go to the workspace and a second launch joins them.
+//
+// What bounds it, measured.  A prompt of 8191 tokens, 64 / 8 heads x 128, bf16: 787 us,
+// 1396 TFLOP/s, 71% of the library product's rate; the tensor pipe is busy half of the
+// time, and the softmax warps take longer for a tile than the products do.  4 chunks
+// of 2049 with a window of 4096, 24 / 4 x 256: 781 us, 49%, the tensor pipe busy 41% of the
+// time with tiles of 64 keys, the most that fit beside Q.  8 requests of up to 60000 tokens, 5
+// new ones each: 267 us, 76% of the copy rate.  e4m3, 60 requests of up to 16001 tokens,
+// three of them with 700 new ones: 943 us; the conversion's warps share the softmax's
+// instruction caches and pipes.  45 tokens behind 700: 24 us, a chain of lengths, table,
+// tile, products and the join.
+// Tried: scores in halves of 64 columns (prompt 1157 us, not 1036: the shared score buffer
+// is free later); four more warps for e4m3 that convert V beside K (1375 us, not 1184);
+// two groups of softmax warps for the one query tile of head size 256, its key tiles in turn
+// (822 us, not 784).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -65,7 +79,9 @@ struct Cfg {
   // each query tile, or of a key tile and the next (256).
   static constexpr int kSBufs = D == 128 ? 1 : 2, kPBufs = 2;
   static constexpr int kTile = D == 256 ? 64 : 128;   // tokens per key tile
-  // Registers of a softmax thread; the others have 256 less these.
+  // Registers of a softmax thread; the others have 256 less these.  Measured: dim 128, bf16, 184
+  // or 176: prompt 976 or 1040 us; e4m3, 176, 184 or 168: mixed step 929, 935, 949; dim 256, 152
+  // or 176: 797 or 808.
   static constexpr int kMoreRegs = D == 256 ? 152 : E4M3 ? 176 : 184;
   // Cost of an item's start and end, in key tiles, for the shares of the CTAs.  Measured on
   // an 8191-token prompt, bf16, head size 128: 1: 972 us, 2: 916, 4: 813, 5: 786, 6: 807,
