@@ -611,8 +611,9 @@ int q4k_rope(const void *x, int x_dtype, int64_t ld_token, int64_t ld_head, int6
  * attention: q4k_rope of queries and of keys, and q4k_kv_write of these keys
  * and of the values, in one launch.
  * Query rows go to q_out (bf16); key rows, normed and rotated in fp32, and value
- * rows go to slot slots[t] of the caches, each rounded once as q4k_kv_write does
- * it.  A token with a negative position is left alone.  Slot -1 skips a token's
+ * rows go to slot slots[t] of the caches, each rounded once, in q4k_kv_write's
+ * layout (e4m3: times a factor 448 / max that is off by half a unit in its last
+ * place before that).  A token with a negative position is left alone.  Slot -1 skips a token's
  * keys and values (its queries are written); any other slot outside the cache
  * does too, and sets Q4K_DEVERR_BAD_PAGE.  Tokens of one call that share a slot
  * leave one of their rows there, unspecified which.
