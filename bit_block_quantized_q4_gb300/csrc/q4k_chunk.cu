@@ -447,13 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t absent = vinfo[vs].absent;
           const int lo = seen_lo - (x.t0 + j) * TILE, hi = seen_hi - (x.t0 + j) * TILE;
-          // (bf16: only tiles that some row does not see entirely are looked through)
           const uint32_t *bad_words = vinfo[vs].bad;
           uint32_t some = absent;
-          if (E4M3) {
 #pragma unroll
-            for (int w = 0; w < TILE / 32; ++w) some |= bad_words[w];
-          }
+          for (int w = 0; w < TILE / 32; ++w) some |= bad_words[w];
           if (__any_sync(0xffffffffu, lo > 0 || hi < TILE || some)) {
 #pragma unroll
             for (int w = 0; w < TILE / 32; ++w) {  // the tokens that this row sees, as bits

@@ -118,3 +118,24 @@ def test_pages_beyond_4_gb(q4k, cache):  # noqa: F811
     part = 2.0 ** -8 * 4 + 2.0 ** -8 * 12 if cache == BF16 else (2.0 ** -8 + 2.0 ** -4) * 3
     assert float((got[0][1][-1].double().cpu() - want).norm() / want.norm()) <= part
     assert q4k.q4k_get_device_error() == 0
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("dim,heads,kv_heads,window", [(128, 8, 2, 200), (64, 8, 2, 200), (256, 8, 2, 200), (128, 32, 1, 0), (128, 64, 1, 0), (64, 32, 1, 130)])
+def test_values_that_are_not_finite_show_in_every_token_that_sees_them(q4k, cache, dim, heads, kv_heads, window):  # noqa: F811
+    """Also in those that see the whole tile of keys beside others that do not."""
+    s = Step(37, [(400, 300), (257, 1)], heads, kv_heads, dim, 16, cache)
+    clean = [x.clone() for x in s.run(q4k, 0.1, window)]
+    for token in (5, 127, 128, 255, 399):
+        s2 = Step(37, [(400, 300), (257, 1)], heads, kv_heads, dim, 16, cache)
+        raw = s2.v.view(torch.uint8) if cache == E4M3 else s2.v
+        raw[s2.table[0, token // 16].long(), 0, token % 16, dim // 2] = 0x7F if cache == E4M3 else math.nan
+        out, lse = s2.run(q4k, 0.1, window)
+        pos = torch.arange(100, 400)
+        sees = (token <= pos) & ((token > pos - window) if window else True)
+        group = heads // kv_heads
+        mine = out[:300, :group]
+        assert bool(torch.isnan(mine[sees.to(DEV)][..., dim // 2]).all()), token
+        assert torch.equal(mine[~sees.to(DEV)], clean[0][:300, :group][~sees.to(DEV)]), token
+        assert torch.equal(out[:, group:], clean[0][:, group:]) and torch.equal(out[300:], clean[0][300:])
+    assert q4k.q4k_get_device_error() == 0
