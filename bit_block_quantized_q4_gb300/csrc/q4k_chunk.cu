@@ -1025,10 +1025,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the pieces of the items that several CTAs share: that of the CTA that
 // starts the item (slot 1) and of all after it up to the last (slot 0).  A lane
 // owns a row, a warp 8 of its values, so all loads are of 128 contiguous bytes.
+// Blocks are small, because most of them find that their CTA starts no such item:
+// with all of a row's values in one block, 745 tokens x 16 heads x 256 took 28.7 us in
+// all and not 22.6, 100000 tokens x 32 heads x 128 93.5 and not 89.2.
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(D / 8 * 32) chunk_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__ Params p) {
   const AttnArgs &a = p.a;
-  const int lane = threadIdx.x & 31, c0 = threadIdx.x / 32 * 8, cta = blockIdx.x;
+  const int lane = threadIdx.x & 31, c0 = blockIdx.z * 32 + threadIdx.x / 32 * 8, cta = blockIdx.x;
   grid_dependency_wait();
   const int4 d = p.desc[2 * cta];
   const int rows = p.desc[2 * cta + 1].x;
@@ -1036,21 +1039,29 @@ __global__ void __launch_bounds__(D / 8 * 32) chunk_join_kernel(const __grid_con
   if (d.x < 0 || (int)blockIdx.y * 32 >= rows) return;
   float m = -INFINITY, l = 0.f, o[8] = {};
   const int64_t size = (int64_t)(D + 2) * p.slot_rows;
-  for (int c = cta; c <= d.w; ++c) {
-    const float *slot = p.slots + (2 * (int64_t)c + (c == cta)) * size + row_t;
-    const float pm = slot[(int64_t)D * p.slot_rows], pl = slot[(int64_t)(D + 1) * p.slot_rows];
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = slot[(int64_t)(c0 + i) * p.slot_rows];
-    const float mn = fmaxf(m, pm), f = m == mn ? 1.f : ex2(m - mn), g = pm == mn ? 1.f : ex2(pm - mn);
-    m = mn;
-    l = l * f + pl * g;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * f + v[i] * g;
-  }
-  if (row_t >= rows) return;
   bool ignore = false;
   const Req q = request(p, d.x, ignore);
+  constexpr int kAtOnce = 4;  // pieces whose loads are on their way together (100000 tokens: with 1 103.9 us, with 4 93.5, with 8 94.5)
+  for (int c = cta; c <= d.w; c += kAtOnce) {
+    float pm[kAtOnce], pl[kAtOnce], v[kAtOnce][8];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const float *slot = p.slots + (2 * (int64_t)(c + u) + (c + u == cta)) * size + row_t;
+      const bool there = c + u <= d.w;
+      pm[u] = there ? slot[(int64_t)D * p.slot_rows] : -INFINITY, pl[u] = there ? slot[(int64_t)(D + 1) * p.slot_rows] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = there ? slot[(int64_t)(c0 + i) * p.slot_rows] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const float mn = fmaxf(m, pm[u]), f = m == mn ? 1.f : ex2(m - mn), g = pm[u] == mn ? 1.f : ex2(pm[u] - mn);
+      m = mn;
+      l = l * f + pl[u] * g;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = o[i] * f + v[u][i] * g;
+    }
+  }
+  if (row_t >= rows) return;
   const int row = d.z + row_t, tok = (int)p.by_group.div(row), head = d.y * p.group + (row - tok * p.group);
   const int64_t token = (int64_t)q.tok0 + tok;
   const float f = l == 0.f ? 0.f : 1.f / l;
@@ -1095,8 +1106,8 @@ cudaError_t launch_cfg(Params &p, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.slot_rows / 32));
-  cfg.blockDim = dim3(D / 8 * 32);
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.slot_rows / 32), D / 32);
+  cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
