@@ -29,7 +29,8 @@
 // What bounds it: the logits are read once.  A row is one CTA's, or while rows
 // are few a cluster's, whose CTAs take equal slices and send sums and lists to
 // the first one.  Measured: 2047 x 131072 bf16 111 us (72% of the copy rate; issue
-// slots 79% busy, the ALU pipe 59%), 1024 x 131072 fp32 87 us (92%), 64 x 131072 17 us,
+// slots 79% busy, the ALU pipe 59%), 1024 x 131072 fp32 87 us (92%; with 5
+// alternatives 99), 64 x 131072 17 us,
 // one row of 32000 11 us, of which the chain launch, load, cluster barrier, list is most.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
