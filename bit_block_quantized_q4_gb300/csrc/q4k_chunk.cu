@@ -763,7 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more && !(ok = put(y))) break;
         // ---- its tiles.  Lanes hold 32 table entries from page tb0 on, and the 32 after them.
         if (x.n == 0) continue;
-        const int boxes = TILE >> p.box_shift;
+        // Boxes of a tile: a lane copies a part of one of them.
+        const int boxes = TILE >> p.box_shift, part = lane >> ((TILE == 64 ? 6 : 7) - p.box_shift);
+        static_assert(TILE / 16 * C::kParts <= 32 && C::kRawParts <= C::kParts);
         int tb0 = (x.t0 * TILE) >> p.page_shift;
         const auto table_at = [&](int i) { return i < a.max_pages ? a.table[x.r * a.ldt + i] : -1; };
         int entry = table_at(tb0 + lane), entry2 = table_at(tb0 + 32 + lane);
@@ -792,13 +794,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t *k = smem + C::kKAt + s * C::kSide, *v = smem + C::kVAt + s * C::kSide;
           if (E4M3) k += C::kSide - C::kRaw, v += C::kSide - C::kRaw;
           const auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar) {
-            if (E4M3) {
-              for (int part = lane / boxes; part < C::kRawParts; part += 32 / boxes)
-                if (there) tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * (D / C::kRawParts), map, bar, 0, in_page, part, x.head, page);
-            } else {
-              for (int part = lane / boxes; part < C::kParts; part += 32 / boxes)
-                if (there) tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * 128, map, bar, 0, in_page, part, x.head, page);
-            }
+            if (!there || part >= (E4M3 ? C::kRawParts : C::kParts)) return;
+            tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * (E4M3 ? D / C::kRawParts : 128), map, bar, 0, in_page, part, x.head, page);
           };
           copy(k, &kmap, &bars.k_full[s]);
           if (!(ok = warp_wait(&bars.v_empty[s], ph, a.err))) break;
