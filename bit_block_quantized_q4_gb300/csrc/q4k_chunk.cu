@@ -25,7 +25,8 @@
 //   0..3, 4..7  softmax of query tile 0 and 1: a thread owns a row of S
 //   8, 10       issue the products, Q K^T and P V.  (Issuing and the waits before it
 //               take one warp about as long as the tensor cores take for both.)
-//   9           finds the work and issues the copies of K and V (TMA, a page each)
+//   9, 11       find the work and issue the copies of K; issue the copies of V (TMA, a
+//               page each)
 //   12..15      fetch Q and prepare what was copied: rows of V that no query sees
 //               become zeros (their weights are 0, but 0 times a NaN is not); an e4m3
 //               cache is converted to fp16 in place
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   grid_launch_dependents();
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) mbar_init(&bars.item_full[i], 1), mbar_init(&bars.item_empty[i], 2 + 4 * NQ + 4);
+    for (int i = 0; i < kRing; ++i) mbar_init(&bars.item_full[i], 1), mbar_init(&bars.item_empty[i], 2 + 4 * NQ + 1 + 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 4), mbar_init(&bars.q_empty[i], 1);
       mbar_init(&bars.s_full[i], 1), mbar_init(&bars.s_free[i], 4), mbar_init(&bars.p_full[i], 4), mbar_init(&bars.o_done[i], 1);
@@ -652,8 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++it;
         }
       }
-    } else if (warp == 9) {
-      // ----------------------------------------------- work list, copies of K and V
+    } else {
+      // --------------------------------- work list, copies of K (warp 9), copies of V (11)
+      const bool values = warp == 11;
       int tiles = 0, made = 0;
       const auto put = [&](const Item &x) {
         if (!warp_wait(&bars.item_empty[made % kRing], ((uint32_t)(made / kRing) & 1u) ^ 1u, a.err)) return false;
@@ -758,17 +760,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Item x = {}, y = {};  // (no tiles yet)
       for (bool more = true; more && ok; x = y) {
-        // the others know of an item before the copies of the one before it
-        more = find(y);
-        if (more && !(ok = put(y))) break;
+        if (values) {
+          if (!next_item(x)) break;
+        } else {
+          // the others know of an item before the copies of the one before it
+          more = find(y);
+          if (more && !(ok = put(y))) break;
+        }
         // ---- its tiles.  Lanes hold 32 table entries from page tb0 on, and the 32 after them.
-        if (x.n == 0) continue;
         // Boxes of a tile: a lane copies a part of one of them.
         const int boxes = TILE >> p.box_shift, part = lane >> ((TILE == 64 ? 6 : 7) - p.box_shift);
         static_assert(TILE / 16 * C::kParts <= 32 && C::kRawParts <= C::kParts);
         int tb0 = (x.t0 * TILE) >> p.page_shift;
         const auto table_at = [&](int i) { return i < a.max_pages ? a.table[x.r * a.ldt + i] : -1; };
-        int entry = table_at(tb0 + lane), entry2 = table_at(tb0 + 32 + lane);
+        int entry = 0, entry2 = 0;
+        if (x.n > 0) entry = table_at(tb0 + lane), entry2 = table_at(tb0 + 32 + lane);
         for (int j = 0; j < x.n; ++j, ++tiles) {
           const int s = tiles % ST;
           const uint32_t ph = ((uint32_t)(tiles / ST) & 1u) ^ 1u;
@@ -785,46 +791,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool wanted = box_pos < x.hi && box_pos + p.box_rows > x.lo;
           const bool there = wanted && page >= 0 && page < a.n_pages;
           const unsigned need = __ballot_sync(0xffffffffu, wanted && lane < boxes), have = __ballot_sync(0xffffffffu, there && lane < boxes);
-          if (need != have && lane == 0) set_device_error(a.err, kDevErrBadPage);
+          if (need != have && !values && lane == 0) set_device_error(a.err, kDevErrBadPage);
           const uint32_t box_bytes = (uint32_t)p.box_rows * D * C::kEs, loaded = __popc(have) * box_bytes;
           const int in_page = box_pos & (a.page - 1);
-          if (!(ok = warp_wait(&bars.k_empty[s], ph, a.err))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bars.k_full[s], loaded);
-          __syncwarp();
-          uint8_t *k = smem + C::kKAt + s * C::kSide, *v = smem + C::kVAt + s * C::kSide;
-          if (E4M3) k += C::kSide - C::kRaw, v += C::kSide - C::kRaw;
-          const auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar) {
-            if (!there || part >= (E4M3 ? C::kRawParts : C::kParts)) return;
-            tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * (E4M3 ? D / C::kRawParts : 128), map, bar, 0, in_page, part, x.head, page);
-          };
-          copy(k, &kmap, &bars.k_full[s]);
-          if (!(ok = warp_wait(&bars.v_empty[s], ph, a.err))) break;
+          uint64_t *full = values ? &bars.v_full[s] : &bars.k_full[s];
+          if (!(ok = warp_wait(values ? &bars.v_empty[s] : &bars.k_empty[s], ph, a.err))) break;
           if (lane == 0) {
-            // 16-token pieces that are absent
-            uint32_t gone = 0;
-            for (unsigned w = need & ~have; w; w &= w - 1) {
-              const int at16 = (__ffs(w) - 1) << (p.box_shift - 4);
-              gone |= ((p.box_rows >> 4 == 32 ? 0u : 1u << (p.box_rows >> 4)) - 1u) << at16;
+            if (values) {  // 16-token pieces that are absent
+              uint32_t gone = 0;
+              for (unsigned w = need & ~have; w; w &= w - 1) {
+                const int at16 = (__ffs(w) - 1) << (p.box_shift - 4);
+                gone |= ((p.box_rows >> 4 == 32 ? 0u : 1u << (p.box_rows >> 4)) - 1u) << at16;
+              }
+              v_absent[s] = gone;
             }
-            v_absent[s] = gone;
-            mbar_arrive_expect_tx(&bars.v_full[s], loaded + (E4M3 ? __popc(have) * p.box_rows * 8 : 0));
+            mbar_arrive_expect_tx(full, loaded + (E4M3 && values ? __popc(have) * p.box_rows * 8 : 0));
           }
           __syncwarp();
-          copy(v, &vmap, &bars.v_full[s]);
-          if (E4M3 && there && lane < boxes) {
+          uint8_t *dst = smem + (values ? C::kVAt : C::kKAt) + s * C::kSide + (E4M3 ? C::kSide - C::kRaw : 0);
+          if (there && part < (E4M3 ? C::kRawParts : C::kParts))
+            tma_load_5d(dst + part * TILE * 128 + (b << p.box_shift) * (E4M3 ? D / C::kRawParts : 128), values ? &vmap : &kmap, full, 0, in_page, part, x.head, page);
+          if (E4M3 && values && there && lane < boxes) {
             float *ks = reinterpret_cast<float *>(smem + C::kScaleAt) + s * 2 * TILE + (b << p.box_shift);
             const int64_t from = ((int64_t)page * a.kv_heads + x.head) * a.page + in_page;
-            bulk_load(ks, a.scale[0] + from, p.box_rows * 4, &bars.v_full[s]);
-            bulk_load(ks + TILE, a.scale[1] + from, p.box_rows * 4, &bars.v_full[s]);
+            bulk_load(ks, a.scale[0] + from, p.box_rows * 4, full);
+            bulk_load(ks + TILE, a.scale[1] + from, p.box_rows * 4, full);
           }
           __syncwarp();
         }
+        if (values) {
+          if (!ok) break;
+          if (lane == 0) free_item();
+          ++it, y = x;
+        }
       }
-      if (lane == 0) {
+      if (!values && lane == 0) {
         p.desc[2 * blockIdx.x] = open;
         p.desc[2 * blockIdx.x + 1] = make_int4(open_rows, 0, 0, 0);
       }
-      if (ok) {
+      if (!values && ok) {
         Item end;
         end.rows = -1;
         ok = put(end);
@@ -832,8 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // copies in flight land before the CTA may end
       const int left = min(tiles, ST);
       for (int j = tiles - left; !ok && j < tiles; ++j) {
-        warp_wait(&bars.k_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
-        warp_wait(&bars.v_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
+        warp_wait(values ? &bars.v_full[j % ST] : &bars.k_full[j % ST], (uint32_t)(j / ST) & 1u, a.err);
       }
     }
   } else {
