@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars bars;
   __shared__ VInfo vinfo[4];
+  __shared__ uint32_t gone[8];  // 16-token pieces that are absent, of the last eight tiles of K
   __shared__ uint32_t v_absent[4], e_max[2][4];  // of a stage of V; largest exponents of a tile's scales by warp, two tiles in turn
   __shared__ Item items[kRing];
   __shared__ float q_scale[kRing][ROWS];  // e4m3: what the rows' scores are multiplied by, of the items on their way
@@ -407,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (t < NQ && ok && next_item(x)) {
       const bool active = x.rows > 128 * t, used = x.rows > 128 * t + 32 * (warp & 3), live = row_t < x.rows;
       // this row's token, its head in the group, and the tokens that it sees
-      const int row = x.row0 + row_t, tok = (int)p.by_group.div(row), pos = x.pos0 + tok;
-      const int seen_lo = live ? first_seen(a, pos) : x.lo, seen_hi = live ? end_seen(a, pos) : x.hi;
+      const int row = x.row0 + row_t, tok = (int)p.by_group.div(row), at_pos = x.pos0 + tok;
+      const int seen_lo = live ? first_seen(a, at_pos) : x.lo, seen_hi = live ? end_seen(a, at_pos) : x.hi;
       float m = -INFINITY, l = 0.f;
       bool poisoned = false;
       float sc = scale;
@@ -427,9 +428,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.s_free[C::kSBufs == 1 ? 0 : buf]);
-        // V is ready, so that the product waits for the weights alone; and the buffer of
-        // weights is free, and O complete but for this tile
-        if (!(ok = warp_wait(&bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err) && weights_free(g))) break;
+        // The buffer of weights is free, and O complete but for this tile; and what VInfo
+        // says of V is there, where it is needed: bf16 tiles that all rows see entirely are
+        // only multiplied.
+        const int pos = (x.t0 + j) * TILE;
+        const bool whole = !E4M3 && pos >= x.full_lo && pos + TILE <= x.full_hi && gone[(tiles + j) & 7] == 0;
+        if (!(ok = weights_free(g) && (whole || warp_wait(&bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err)))) break;
         if (used) {
           if (E4M3 && j == 0) sc = scale * q_scale[taken % kRing][row_t];
           if (!positive) {
@@ -446,13 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               s[c] = __float_as_uint(x0.x), s[c + 1] = __float_as_uint(x0.y), s[c + 2] = __float_as_uint(x1.x), s[c + 3] = __float_as_uint(x1.y);
             }
           }
-          const uint32_t absent = vinfo[vs].absent;
-          const int lo = seen_lo - (x.t0 + j) * TILE, hi = seen_hi - (x.t0 + j) * TILE;
+          const uint32_t absent = whole ? 0u : vinfo[vs].absent;
+          const int lo = seen_lo - pos, hi = seen_hi - pos;
           const uint32_t *bad_words = vinfo[vs].bad;
           uint32_t some = absent;
 #pragma unroll
-          for (int w = 0; w < TILE / 32; ++w) some |= bad_words[w];
-          if (__any_sync(0xffffffffu, lo > 0 || hi < TILE || some)) {
+          for (int w = 0; w < TILE / 32; ++w) some |= whole ? 0u : bad_words[w];
+          if (!whole && __any_sync(0xffffffffu, lo > 0 || hi < TILE || some)) {
 #pragma unroll
             for (int w = 0; w < TILE / 32; ++w) {  // the tokens that this row sees, as bits
               const int lo_w = min(max(lo - 32 * w, 0), 32), hi_w = min(max(hi - 32 * w, 0), 32);
@@ -624,11 +628,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id_pv = idesc_of(!E4M3, true, D);
         const uint64_t v_desc = sdesc_v(base + C::kVAt, TILE * 128);
         int vs = 0;  // next stage of V
-        // The weights of query tile t times the values in stage vs.  (Whoever wrote the
-        // weights has seen that V is ready.)
+        uint32_t vph = 0;
+        // The weights of query tile t times the values in stage vs.
         const auto pv = [&](int t, uint32_t g, bool fresh, bool last_value) {
           const uint32_t buf = NQ == 1 ? g & 1u : t;
-          if (!warp_wait(&bars.p_full[buf], (NQ == 1 ? g >> 1 : g) & 1u, a.err)) return false;
+          const uint32_t pp = (NQ == 1 ? g >> 1 : g) & 1u;
+          if (!(t == 0 ? warp_wait2(&bars.v_ready[vs], vph, &bars.p_full[buf], pp, a.err) : warp_wait(&bars.p_full[buf], pp, a.err))) return false;
           tc_fence_after();
           const uint64_t vd = v_desc + (uint64_t)((uint32_t)vs * (C::kSide >> 4));
           const uint32_t d = tmem + t * D, pa = tmem + C::kPCol + buf * (TILE / 2);
@@ -636,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < TILE / 16; ++k) tc_mma_ts(d, pa + k * 8, vd + (uint64_t)(k * (16 * 128 >> 4)), id_pv, k != 0 || !fresh, leader);
           tc_commit_if(&bars.o_done[buf], leader);
           tc_commit_if(&bars.v_empty[vs], last_value ? leader : 0u);
-          if (last_value && ++vs == ST) vs = 0;
+          if (last_value && ++vs == ST) vs = 0, vph ^= 1u;
           return true;
         };
         while (ok && next_item(x)) {
@@ -797,14 +802,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t *full = values ? &bars.v_full[s] : &bars.k_full[s];
           if (!(ok = warp_wait(values ? &bars.v_empty[s] : &bars.k_empty[s], ph, a.err))) break;
           if (lane == 0) {
-            if (values) {  // 16-token pieces that are absent
-              uint32_t gone = 0;
-              for (unsigned w = need & ~have; w; w &= w - 1) {
-                const int at16 = (__ffs(w) - 1) << (p.box_shift - 4);
-                gone |= ((p.box_rows >> 4 == 32 ? 0u : 1u << (p.box_rows >> 4)) - 1u) << at16;
-              }
-              v_absent[s] = gone;
+            uint32_t pieces = 0;  // 16-token pieces that are absent
+            for (unsigned w = need & ~have; w; w &= w - 1) {
+              const int at16 = (__ffs(w) - 1) << (p.box_shift - 4);
+              pieces |= ((p.box_rows >> 4 == 32 ? 0u : 1u << (p.box_rows >> 4)) - 1u) << at16;
             }
+            if (values) v_absent[s] = pieces;
+            else gone[tiles & 7] = pieces;
             mbar_arrive_expect_tx(full, loaded + (E4M3 && values ? __popc(have) * p.box_rows * 8 : 0));
           }
           __syncwarp();
