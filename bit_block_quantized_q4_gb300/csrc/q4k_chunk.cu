@@ -289,7 +289,7 @@ __device__ __forceinline__ uint2 e4m3x4_f16(uint32_t w) {
 struct Bars {
   uint64_t item_full[kRing], item_empty[kRing];
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
+  uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_known[4], v_ready[4], v_empty[4];
   uint64_t s_full[2], s_free[2];  // scores: of a query tile (dim 256: of a buffer); buffers
   uint64_t p_full[2], o_done[2];  // weights and their products, by buffer of weights
 };
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.k_full[i], 1), mbar_init(&bars.k_ready[i], 4), mbar_init(&bars.k_empty[i], 1);
-      mbar_init(&bars.v_full[i], 1), mbar_init(&bars.v_ready[i], 4), mbar_init(&bars.v_empty[i], 1);
+      mbar_init(&bars.v_full[i], 1), mbar_init(&bars.v_known[i], 4), mbar_init(&bars.v_ready[i], 4), mbar_init(&bars.v_empty[i], 1);
     }
     fence_mbar_init();
     prefetch_tmap(&kmap), prefetch_tmap(&vmap);
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // only multiplied.
         const int pos = (x.t0 + j) * TILE;
         const bool whole = !E4M3 && pos >= x.full_lo && pos + TILE <= x.full_hi && gone[(tiles + j) & 7] == 0;
-        if (!(ok = weights_free(g) && (whole || warp_wait(&bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err)))) break;
+        if (!(ok = weights_free(g) && (whole || warp_wait(E4M3 ? &bars.v_known[vs] : &bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err)))) break;
         if (used) {
           if (E4M3 && j == 0) sc = scale * q_scale[taken % kRing][row_t];
           if (!positive) {
@@ -980,6 +980,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t odd = __ballot_sync(0xffffffffu, !dead(th) && !(mine - mine == 0.f));
             if (odd && lane == 0) atomicOr(&vinfo[s].bad[th >> 5], odd);
           }
+          if (!partial) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.v_known[s]);
+          }
           convert(v, [&](int i, uint4 w) {
             const int row = row0 + i * (128 / RC);
             if (partial) {
@@ -1009,7 +1013,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.v_ready[s]);
+        if (lane == 0) {
+          if (E4M3 && partial) mbar_arrive(&bars.v_known[s]);
+          mbar_arrive(&bars.v_ready[s]);
+        }
       }
       if (!ok) break;
       if (lane == 0) free_item();
