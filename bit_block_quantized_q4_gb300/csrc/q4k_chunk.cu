@@ -37,19 +37,21 @@
 // itself.  A CTA has at most two pieces of items that it shares with others; they
 // go to the workspace and a second launch joins them.
 //
-// What bounds it, measured.  A prompt of 8191 tokens, 64 / 8 heads x 128, bf16: 800 us,
-// 1375 TFLOP/s, 70% of the library product's rate; the tensor pipe is busy half of the
+// What bounds it, measured.  A prompt of 8191 tokens, 64 / 8 heads x 128, bf16: 765 us,
+// 1438 TFLOP/s, 74% of the library product's rate; the tensor pipe is busy half of the
 // time, and the softmax warps take longer for a tile than the products do.  4 chunks
-// of 2049 with a window of 4096, 24 / 4 x 256: 781 us, 49%, the tensor pipe busy 41% of the
+// of 2049 with a window of 4096, 24 / 4 x 256: 618 us, 62%, the tensor pipe busy 53% of the
 // time with tiles of 64 keys, the most that fit beside Q.  8 requests of up to 60000 tokens, 5
-// new ones each: 265 us, 77% of the copy rate.  e4m3, 60 requests of up to 16001 tokens,
-// three of them with 700 new ones: 947 us; the conversion's warps share the softmax's
+// new ones each: 220 us, 92% of the copy rate.  e4m3, 60 requests of up to 16001 tokens,
+// three of them with 700 new ones: 880 us; the conversion's warps share the softmax's
 // instruction caches and pipes.  45 tokens behind 700: 21 to 22.5 us, a chain of lengths, table,
 // tile, products and the join.
 // Tried: scores in halves of 64 columns (prompt 1157 us, not 1036: the shared score buffer
 // is free later); four more warps for e4m3 that convert V beside K (1375 us, not 1184);
 // two groups of softmax warps for the one query tile of head size 256, its key tiles in turn
-// (822 us, not 784).
+// (822 us, not 784).  Kept: K and V copied by a warp each (the last two bf16 cases 233 and
+// 708 us, not 260 and 765); scores of tiles that all rows see entirely do not wait for
+// V (220 and 618).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
