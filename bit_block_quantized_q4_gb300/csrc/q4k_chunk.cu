@@ -49,7 +49,7 @@
 // Tried: scores in halves of 64 columns (prompt 1157 us, not 1036: the shared score buffer
 // is free later); four more warps for e4m3 that convert V beside K (1375 us, not 1184);
 // two groups of softmax warps for the one query tile of head size 256, its key tiles in turn
-// (822 us, not 784).  Kept: K and V copied by a warp each (the 8 requests 233 us, not
+// (625 us, not 622).  Kept: K and V copied by a warp each (the 8 requests 233 us, not
 // 260; the window 708, not 765); scores of tiles that all rows see entirely do not wait
 // for V (220 and 618).
 #include <cuda_bf16.h>
