@@ -71,6 +71,9 @@ constexpr int kMaxSms = 160;     // CTAs that the workspace is sized for
 constexpr int kThreads = 512;
 constexpr float kLazy = 8.f;     // binary orders that a maximum may grow before M follows
 constexpr float kUpBits = 7.f;   // e4m3: weights are stored times 2^7, so that the largest, 2^kLazy more, are below 2^16
+// e4m3: no tile's values are divided by less than 2^kLeastLog (rows of zeros have scales of 2^-109).  The sum of weights
+// is that of stored ones over this power, at most 2^15 2^80 for each of 2^30 tokens: finite.
+constexpr int kLeastLog = -80;
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr int kRing = 4;         // items on their way
 
@@ -484,9 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool grew = m != -INFINITY && top_z > m + kLazy;
           if (m == -INFINITY) m = top_z;
           if (__any_sync(0xffffffffu, grew)) {
-            const float f = grew ? ex2(m - top_z) : 1.f;
+            // (e4m3: m may grow by the 200 orders between two tiles' v_log, of which l, which has none of
+            // them, keeps its part: half of them at a time, none of which underflows)
+            const float half = grew ? ex2(E4M3 ? 0.5f * (m - top_z) : m - top_z) : 1.f, f = E4M3 ? half * half : half;
             if (grew) m = top_z;
-            l *= f;
+            l = E4M3 ? l * half * half : l * f;
             if (NQ == 1 && !(ok = g == 0 || values_done(g - 1))) break;
             tc_fence_after();
 #pragma unroll 1
@@ -968,11 +973,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = group_and(1, ok))) break;
         if (E4M3) {
           // Values enter as fp16 times their scale over 2^v_log, by which the largest scale
-          // becomes 2^6 .. 2^7 (times 448 still fp16).  A tile whose scales are all far below
-          // an earlier one's keeps to 2^-90 of it: a weight that underflows with its
-          // scale would be missing in the sum of weights.
+          // becomes 2^6 .. 2^7 (times 448 still fp16); below 2^(kLeastLog + 6) they are less.  A
+          // tile whose scales are all far below an earlier one's keeps to 2^-90 of it: a weight
+          // that underflows with its scale would be missing in the sum of weights.
           const uint32_t *tops = e_max[tiles & 1], e = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-          const int here = max((e ? (int)e - 127 : 0) - 6, -120);
+          const int here = max((e ? (int)e - 127 : 0) - 6, kLeastLog);
           v_run = max(v_run, here);
           const int v_log = max(here, v_run - 90);
           const float down = __int_as_float((127 - v_log) << 23);
@@ -1068,9 +1073,12 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__
     }
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      const float mn = fmaxf(m, pm[u]), f = m == mn ? 1.f : ex2(m - mn), g = pm[u] == mn ? 1.f : ex2(pm[u] - mn);
+      // (e4m3: the sums' factors half at a time, as where a tile's reference grows)
+      constexpr float kPart = E4M3 ? 0.5f : 1.f;
+      const float mn = fmaxf(m, pm[u]), hf = m == mn ? 1.f : ex2(kPart * (m - mn)), hg = pm[u] == mn ? 1.f : ex2(kPart * (pm[u] - mn));
+      const float f = E4M3 ? hf * hf : hf, g = E4M3 ? hg * hg : hg;
       m = mn;
-      l = l * f + pl[u] * g;
+      l = E4M3 ? l * hf * hf + pl[u] * hg * hg : l * f + pl[u] * g;
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = o[i] * f + v[u][i] * g;
     }
