@@ -73,7 +73,8 @@ constexpr float kLazy = 8.f;     // binary orders that a maximum may grow before
 constexpr float kUpBits = 7.f;   // e4m3: weights are stored times 2^7, so that the largest, 2^kLazy more, are below 2^16
 // e4m3: no tile's values are divided by less than 2^kLeastLog (rows of zeros have scales of 2^-109).  The sum of weights
 // is that of stored ones over this power, at most 2^15 2^80 for each of 2^30 tokens: finite.
-constexpr int kLeastLog = -80;
+// (2^-v_log is a normal number up to 2^kMostLog, where the largest scale becomes 2^6 .. 2^7.)
+constexpr int kLeastLog = -80, kMostLog = 121;
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr int kRing = 4;         // items on their way
 
@@ -86,9 +87,9 @@ struct Cfg {
   static constexpr int kSBufs = D == 128 ? 1 : 2, kPBufs = 2;
   static constexpr int kTile = D == 256 ? 64 : 128;   // tokens per key tile
   // Registers of a softmax thread; the others have 256 less these.  Measured: dim 128, bf16, 184
-  // or 176: prompt 976 or 1040 us; e4m3, 176, 184 or 168: mixed step 929, 935, 949; dim 256, 152
+  // or 176: prompt 976 or 1040 us; e4m3, 176, 184 or 192: mixed step 926, 910, 920; dim 256, 152
   // or 176: 797 or 808.
-  static constexpr int kMoreRegs = D == 256 ? 152 : E4M3 ? 176 : 184;
+  static constexpr int kMoreRegs = D == 256 ? 152 : 184;
   // Cost of an item's start and end, in key tiles, for the shares of the CTAs.  Measured on
   // an 8191-token prompt, bf16, head size 128: 1: 972 us, 2: 916, 4: 813, 5: 786, 6: 807,
   // 8: 835; on 60 requests of e4m3, whose tiles cost more: 1: 929, 2: 926, 3: 922.
@@ -102,6 +103,11 @@ struct Cfg {
   static constexpr int kPCol = kSCol + kSBufs * kTile;
   static constexpr int kCols = 512;
   static constexpr int kEs = E4M3 ? 1 : 2;
+  // Rows of Q that a lane fetches at once, and pieces that it converts (e4m3).  This runs once
+  // per item, and its instructions push out others'.  Prompt, size 64: 4 and all 8: 1260 us, 4
+  // and 2: 1181, 1 and 1: 1095; size 128: 4 and all 16: 1357, 4 and 2: 1261, 1 and 1: 1265; window,
+  // size 256: 4 and 2: 1284, 1 and 1: 1340.
+  static constexpr int kQRows = E4M3 && D == 64 ? 1 : 4, kQPieces = D == 64 ? 1 : 2;
   static constexpr int kRaw = kTile * D;              // bytes of an e4m3 tile
   static constexpr int kRawParts = D == 256 ? 2 : 1;  // in which its rows are copied
   // Q | K stages | V stages | e4m3: per stage of V the scales of K and V
@@ -230,6 +236,12 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t *r) {
       Q4K_V8(r, 0), Q4K_V8(r, 8)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_st_x4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 // A wait by a whole warp, whose lanes stay together; false after the time limit.
 // (Without a call, which would cost every role its registers.)
@@ -299,11 +311,13 @@ struct Bars {
   uint64_t p_full[2], o_done[2];  // weights and their products, by buffer of weights
 };
 // Of a stage of V: 16-token pieces that are absent, tokens whose values are not
-// finite; e4m3: the binary logarithm of what the values are multiplied by.
+// finite; e4m3: the binary logarithm of what the values were divided by (and kOwn in absent where
+// some tokens' were divided by more or less), and the largest one so far of tokens that all rows see.
 struct __align__(16) VInfo {
   uint32_t bad[4], absent;
-  float v_log;
+  float v_log, v_run;
 };
+constexpr uint32_t kOwn = 0x80000000u;
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -316,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ VInfo vinfo[4];
   __shared__ uint32_t gone[8];  // 16-token pieces that are absent, of the last eight tiles of K
   __shared__ uint32_t v_absent[4], e_max[2][4];  // of a stage of V; largest exponents of a tile's scales by warp, two tiles in turn
+  __shared__ __align__(16) int16_t v_own[E4M3 ? 4 : 1][128];  // of a stage of V: orders by which a token's values were divided besides
   __shared__ Item items[kRing];
   __shared__ float q_scale[kRing][ROWS];  // e4m3: what the rows' scores are multiplied by, of the items on their way
   __shared__ int64_t sums[kThreads], wsum[kThreads / 32];
@@ -395,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, row_in = 32 * (warp & 3) + lane, row_t = 128 * t + row_in;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t o_at = tmem + lanes + t * D, s_col = tmem + lanes + C::kSCol, p_col = tmem + lanes + C::kPCol;
-    // scores are multiplied by -1 or 0 first where the scale is not positive
+    // scores are multiplied by -1 or 0 first where the scale is not positive (e4m3: q was)
     const float scale = (a.softmax_scale == 0.f ? 1.f : fabsf(a.softmax_scale)) * kLog2e;
     const float sign = a.softmax_scale < 0.f ? -1.f : 0.f;
     const bool positive = a.softmax_scale > 0.f;
@@ -418,6 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       bool poisoned = false;
       float sc = scale;
+      float v_seen = -1000.f;  // e4m3: the largest v_log of this row's where tokens have ones of their own
+      uint32_t wide = 0u;      // kOwn once that, of a row of this warp, is so large that another tile's may need it
       for (int j = 0; active && j < x.n && ok; ++j) {
         const int g = mine_t + j, buf = NQ == 1 ? g & 1 : t;
         const int vs = (tiles + j) % ST;
@@ -441,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = weights_free(g) && (whole || warp_wait(E4M3 ? &bars.v_known[vs] : &bars.v_ready[vs], (uint32_t)((tiles + j) / ST) & 1u, a.err)))) break;
         if (used) {
           if (E4M3 && j == 0) sc = scale * q_scale[taken % kRing][row_t];
-          if (!positive) {
+          if (!E4M3 && !positive) {
 #pragma unroll
             for (int c = 0; c < TILE; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * sign);
           }
@@ -482,7 +499,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
           // z = S sc (+ v_log: e4m3 weights carry what the tile's values were divided by).
           // m starts as the maximum itself: the weight of a row's only token is 1, exactly.
-          const float unit = fmaxf(sc, 1e-37f), v_log = E4M3 ? vinfo[vs].v_log : 0.f;
+          const float unit = fmaxf(sc, 1e-37f);
+          float v_log = E4M3 ? vinfo[vs].v_log : 0.f;
+          if (E4M3 && (absent | wide) & kOwn) {
+            // Tokens whose values were divided by 2^(v_log + own): the weights carry the largest of
+            // those that this row sees.  (Tiles without such tokens come here once a row has seen
+            // ones so large that what it keeps to, 2^-90 of them, may be above the tile's.)
+            if (absent & kOwn) {
+              int own = -1000;
+#pragma unroll 1
+              for (int c = max(lo, 0); c < min(hi, TILE); ++c) own = max(own, (int)v_own[vs][c]);
+              v_log = fmaxf(v_log + (float)own, (float)kLeastLog);
+              v_seen = fmaxf(v_seen, v_log);
+              wide |= __any_sync(0xffffffffu, v_log > (float)(kLeastLog + 90)) ? kOwn : 0u;
+            }
+            v_log = fmaxf(v_log, fmaxf(v_seen, vinfo[vs].v_run) - 90.f);
+          }
           const float top_z = top == -INFINITY ? top : fmaf(top, unit, v_log);
           const bool grew = m != -INFINITY && top_z > m + kLazy;
           if (m == -INFINITY) m = top_z;
@@ -525,6 +557,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float more = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
           l += E4M3 ? more * ex2(-v_log) : more;
           tmem_st_wait();
+          if (E4M3 && (absent | wide) & kOwn) {  // weights times what their tokens' values were divided by, over what is in v_log
+            const int rest = (int)vinfo[vs].v_log - (int)v_log;
+#pragma unroll 1
+            for (int c = 0; c < TILE / 2; c += 4) {
+              uint32_t w[4];
+              tmem_ld_x4(at + c, w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const short2 own = absent & kOwn ? reinterpret_cast<const short2 *>(v_own[vs])[c + i] : make_short2(0, 0);
+                const auto factor = [&](int o) { return __int_as_float((127 + min(max(rest + o, -126), 0)) << 23); };  // (of tokens that are not seen at most 1)
+                const float2 e = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                w[i] = pack_f16(e.x * factor(own.x), e.y * factor(own.y));
+              }
+              tmem_st_x4(at + c, w);
+            }
+            tmem_st_wait();
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -867,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *dst = smem + t * C::kQ;
         constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows of an iteration
         if (!(ok = warp_wait(&bars.q_empty[t], ((uint32_t)c & 1u) ^ 1u, a.err))) break;
-#pragma unroll 4
+#pragma unroll C::kQRows
         for (int i = 0; i < 32 / RPI; ++i) {
           const int r = i * RPI + lane / CH, row = first + r, ch = lane % CH;
           const int64_t from = __shfl_sync(0xffffffffu, where, r);
@@ -881,6 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = first + lane;
           uint8_t *r0 = dst + row * 128;
           uint32_t top = 0;
+#pragma unroll C::kQPieces
           for (int ch = 0; ch < CH; ++ch) {
             const uint4 v = *reinterpret_cast<const uint4 *>(r0 + (ch / 8) * 128 * 128 + (((ch & 7) ^ (row & 7)) << 4));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -889,7 +940,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int ex = (int)(top >> 7) - 127;         // of the largest value
           const int up = min(max(14 - ex, -113), 126);  // factor 2^up
-          const float f = __int_as_float((up + 127) << 23);
+          const float f = __int_as_float((up + 127) << 23) * (a.softmax_scale > 0.f ? 1.f : a.softmax_scale < 0.f ? -1.f : 0.f);
+#pragma unroll C::kQPieces
           for (int ch = 0; ch < CH; ++ch) {
             uint4 *at = reinterpret_cast<uint4 *>(r0 + (ch / 8) * 128 * 128 + (((ch & 7) ^ (row & 7)) << 4));
             const uint4 v = *at;
@@ -905,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bars.q_full[t]);
       }
       if (!group_and(1, ok)) break;
-      int v_run = -1000;  // largest unit of this item's values so far
+      int v_run = -1000;  // largest v_log so far, of tokens that all rows see
       for (int j = 0; j < x.n; ++j, ++tiles) {
         const int s = tiles % ST;
         const uint32_t ph = (uint32_t)(tiles / ST) & 1u;
@@ -929,6 +981,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint4 w0 = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y), w1 = make_uint4(h[2].x, h[2].y, h[3].x, h[3].y);
           *reinterpret_cast<uint4 *>(side + first + i * (128 / RC) * 128) = sw ? w1 : w0;
           *reinterpret_cast<uint4 *>(side + second + i * (128 / RC) * 128) = sw ? w0 : w1;
+        };
+        // What a token's values are divided by besides 2^v_log, where that does not fit its scale.
+        const auto own_of = [](float scale, int v_log) {
+          const int e = (int)(__float_as_uint(scale) >> 23), off = e - 127 - v_log;
+          return e > 20 && e < 255 && (off < -14 || off > 6) ? min(max(off, kLeastLog - v_log), kMostLog - v_log) : 0;  // (e above 255: negative)
         };
         // Rows are converted one after the other by a short loop.  (Unrolled, these warps
         // wait for their instructions, which the others' push out: 60 requests, three of
@@ -965,9 +1022,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mine = 1.f;
         if (E4M3) {
           mine = th < TILE ? v_scales[th] : 0.f;
-          // the largest exponent of this warp's scales; after the barrier that of all is known
-          const uint32_t e = th < TILE && !dead(th) && mine - mine == 0.f && mine > 0.f ? __float_as_uint(mine) >> 23 : 0u, top = __reduce_max_sync(0xffffffffu, e);
+          // the largest exponent of this warp's scales, of tokens that all rows see; after the barrier that of all is known
+          const uint32_t e = th < TILE && !dead(th) && pos + th >= x.full_lo && pos + th < x.full_hi && mine - mine == 0.f && mine > 0.f ? __float_as_uint(mine) >> 23 : 0u, top = __reduce_max_sync(0xffffffffu, e);
           if (lane == 0) e_max[tiles & 1][warp - 12] = top;
+          if (th == 0) vinfo[s].absent = absent;
         }
         if (th < 4) vinfo[s].bad[th] = 0;
         if (!(ok = group_and(1, ok))) break;
@@ -977,11 +1035,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           // tile whose scales are all far below an earlier one's keeps to 2^-90 of it: a weight
           // that underflows with its scale would be missing in the sum of weights.
           const uint32_t *tops = e_max[tiles & 1], e = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-          const int here = max((e ? (int)e - 127 : 0) - 6, kLeastLog);
-          v_run = max(v_run, here);
-          const int v_log = max(here, v_run - 90);
+          int v_log = max((int)e - 133, kLeastLog);
+          if (!partial) {
+            v_run = max(v_run, v_log);
+            v_log = max(v_log, v_run - 90);
+          } else {
+            // A token that a row does not see must not decide how its own are rounded.  So where
+            // some rows see tokens that others do not, v_log goes by those that all see (here,
+            // or else before), whose largest scale becomes 1 .. 2.  A token whose scale does not
+            // fit beside that (2^-14 .. 2^7; below 2^-106 it counts as 0) is divided by a power of
+            // its own, which the rows that see it put into their weights.
+            if (e) v_run = max(v_run, v_log);
+            v_log = min(max(max(e ? (int)e - 127 : v_run + 6, kLeastLog), v_run - 90), kMostLog);
+            const int own = own_of(mine, v_log);
+            v_own[s][th] = (int16_t)(dead(th) ? -1000 : own);
+            if (!dead(th) && own) atomicOr(&vinfo[s].absent, kOwn);
+          }
           const float down = __int_as_float((127 - v_log) << 23);
-          if (th == 0) vinfo[s].absent = absent, vinfo[s].v_log = (float)v_log;
+          if (th == 0) vinfo[s].v_log = (float)v_log, vinfo[s].v_run = (float)v_run;
           // tokens whose scale is not finite
           if (th < TILE) {
             const uint32_t odd = __ballot_sync(0xffffffffu, !dead(th) && !(mine - mine == 0.f));
@@ -991,17 +1062,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.v_known[s]);
           }
-          convert(v, [&](int i, uint4 w) {
-            const int row = row0 + i * (128 / RC);
-            if (partial) {
+          if (!partial) {
+            convert(v, [&](int i, const uint4 &w) {
+              const float f = v_scales[row0 + i * (128 / RC)] * down;
+              place(v, i, w, true, __float2half2_rn(fabsf(f) <= 128.f ? f : 0.f));
+            });
+          } else {
+            convert(v, [&](int i, uint4 w) {
+              const int row = row0 + i * (128 / RC);
               const auto nan4 = [](uint32_t y) { return __vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu); };
               const bool gone = dead(row), nan = (nan4(w.x) | nan4(w.y) | nan4(w.z) | nan4(w.w)) != 0;
               if (!gone && nan) atomicOr(&vinfo[s].bad[row >> 5], 1u << (row & 31));
               if (gone || nan) w = make_uint4(0, 0, 0, 0);
-            }
-            const float f = v_scales[row] * down;
-            place(v, i, w, true, __float2half2_rn(fabsf(f) <= 128.f ? f : 0.f));
-          });
+              const float scale = v_scales[row], f = scale * 0.5f * __int_as_float((128 - v_log - own_of(scale, v_log)) << 23);  // (the power itself may be too small)
+              place(v, i, w, true, __float2half2_rn(fabsf(f) <= 128.f ? f : 0.f));
+            });
+          }
           fence_proxy_async_smem();
         } else {
           if (th == 0) vinfo[s].absent = absent;

@@ -110,3 +110,85 @@ def test_zero_values_before_and_behind_large_ones(q4k, dim, both, large):  # noq
         s.vs[page, :, place] = torch.where(zero, ZERO_SCALE, 2.0 ** large)[:, None].float()
         s.v.view(torch.uint8)[page[zero], :, place[zero]] = 0
         check(s, s.run(q4k, 0.005), 0.005)
+
+
+def steps_of(*a, change, **kw):
+    """The same step twice, the second one with scales of V changed: change(vs by [request][position])."""
+    clean, other = Step(*a, **kw), Step(*a, **kw)
+    for r, at, value in change:
+        other.vs[other.table[r, at // other.page], :, at % other.page] = value
+    return clean, other
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 4, 2), (128, 4, 2), (256, 4, 2), (64, 2, 2), (128, 2, 2), (128, 16, 1)])
+@pytest.mark.parametrize("value", [2.0 ** 30, 2.0 ** 60, 2.0 ** 120, 3.4e38, 2.0 ** -100, 1e-40, 0.0, -2.0 ** 60, math.inf, -math.inf, math.nan])
+def test_scales_of_later_tokens_stay_out_of_earlier_results(q4k, dim, heads, kv_heads, value):  # noqa: F811
+    """Whatever a later token's scale is, earlier tokens have the same bits."""
+    both = [(150, 150), (300, 40), (700, 400)]
+    places = ((0, 77), (1, 290), (2, 511), (2, 650))
+    clean, s = steps_of(53, both, heads, kv_heads, dim, 16, E4M3, change=[(r, at, value) for r, at in places])
+    want, got = clean.run(q4k, 0.1), s.run(q4k, 0.1)
+    before = torch.cat([torch.arange(77), 150 + torch.arange(30), 190 + torch.arange(211)])
+    assert torch.equal(want[0][before], got[0][before]) and torch.equal(want[1][before], got[1][before])
+    if 0 < value < 2.0 ** 100:
+        check(s, got, 0.1)
+    assert q4k.q4k_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 4, 2), (128, 4, 2), (256, 4, 2), (64, 2, 2), (128, 2, 2), (128, 16, 1)])
+@pytest.mark.parametrize("value", [2.0 ** 30, 2.0 ** 120, 2.0 ** -100, math.inf])
+def test_scales_before_the_window_stay_out(q4k, dim, heads, kv_heads, value):  # noqa: F811
+    """A token's scale does not matter once the window has passed it, nor to tokens before it."""
+    window = 200
+    clean, s = steps_of(54, [(900, 700)], heads, kv_heads, dim, 16, E4M3, change=[(0, 333, value)])
+    want, got = clean.run(q4k, 0.1, window), s.run(q4k, 0.1, window)
+    pos = torch.arange(200, 900)
+    rows = (pos < 333) | (pos >= 333 + window)
+    assert torch.equal(want[0][rows], got[0][rows]) and torch.equal(want[1][rows], got[1][rows])
+    if value < 2.0 ** 100:
+        check(s, got, 0.1, window)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("both", [[(777, 600)], [(3000, 7)], [(777, 600), (3000, 7)]])
+def test_scales_that_rise_and_fall_along_the_positions(q4k, dim, window, both):  # noqa: F811
+    """Every row against what it sees itself."""
+    for low, high in ((-60.0, 60.0), (60.0, -60.0), (-20.0, 8.0)):
+        s = Step(55, both, 4, 2, dim, 16, E4M3)
+        for r, (length, _) in enumerate(both):
+            at = torch.arange(length)
+            s.vs[s.table[r, at // 16].long(), :, at % 16] = torch.exp2(torch.linspace(low, high, length))[:, None]
+        check(s, s.run(q4k, 0.1, window), 0.1, window)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_ordinary_scales_with_a_tight_bound(q4k, dim):  # noqa: F811
+    both = [(300, 300), (1, 1), (700, 1), (513, 0), (1000, 77), (6000, 9)]
+    s = Step(56, both, 8, 2, dim, 32, E4M3)
+    check(s, s.run(q4k, dim ** -0.5), dim ** -0.5)
+    check(s, s.run(q4k, dim ** -0.5, 130), dim ** -0.5, 130)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 40, 150])
+@pytest.mark.parametrize("heads,kv_heads", [(4, 2), (2, 2), (16, 1)])
+def test_scales_of_many_orders_from_token_to_token(q4k, dim, window, heads, kv_heads):  # noqa: F811
+    """Every row against what it sees itself, where neighbours are up to 2^200 apart; values up to 2^110 in all."""
+    g = torch.Generator().manual_seed(2)
+    for low, high in ((-80.0, 105.0), (-5.0, 12.0), (90.0, 108.0)):
+        s = Step(57, [(500, 400), (1, 1), (40, 40)], heads, kv_heads, dim, 16, E4M3)
+        s.vs = torch.exp2(torch.empty(s.vs.shape).uniform_(low, high, generator=g))
+        check(s, s.run(q4k, 0.1, window), 0.1, window)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_the_largest_scales(q4k, dim):  # noqa: F811
+    """Scales next to the largest number, of values that are not: 2^-9 of 2^127 each."""
+    both = [(300, 250)]
+    s = Step(58, both, 4, 2, dim, 16, E4M3)
+    signs = torch.where(torch.rand(s.v.shape, generator=torch.Generator().manual_seed(3)) < 0.5, -1.0, 1.0)
+    s.v = (signs * 2.0 ** -9).to(E4M3)
+    s.vs.fill_(2.0 ** 127)
+    s.vs[:, :, ::3] = 2.0 ** 100
+    check(s, s.run(q4k, 0.1), 0.1)
