@@ -213,11 +213,15 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
     if (v > best || (v == best && i < best_at)) best = v, best_at = i;
     count += ahead(v, i);
     infinite += v == INFINITY;
-    if (fabsf(v) <= kPlain) {
-      const float c = v * kLog2e;
-      const Sums t = {c, 1.f, fmaf(v, kLog2e, -c)};
-      join(s, t);
+    if (!(v > 0.1f * kLow) || v == INFINITY) return;
+    const float c = v * kLog2e;
+    if (c > s.c + 12.f) {  // as below
+      const float d = fmaxf(s.c - c, -200.f), f = ex2(d);
+      s.w = f * fmaf(d, s.l, s.w), s.l *= f, s.c = c;
     }
+    // (not as 2^0 with a reference of its own: c's rounding is the same for all only where c is)
+    const float z = fmaf(v, kLog2e, -s.c), e = ex2(z);
+    s.l += e, s.w = fmaf(e, z, s.w);
   };
   const auto eight = [&](const Raw8<T> &raw, int i) {
     const float top = Eight<T>::raw_top(raw);
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
     if (!(v > -INFINITY)) return -INFINITY;
     if (infinite) return v == INFINITY ? -lg * kLn2 : -INFINITY;
     if (again) return (v - top) - lg * kLn2;
-    return fabsf(v) > kPlain ? v - (s.c + lg) * kLn2 : (fmaf(v, kLog2e, -s.c) - lg) * kLn2;
+    return v < kLow ? v - (s.c + lg) * kLn2 : (fmaf(v, kLog2e, -s.c) - lg) * kLn2;  // (v log2 e may be beyond all numbers)
   };
   if (tid == 0) {
     a.logp[row] = real ? logp_of(xt) : -INFINITY;
