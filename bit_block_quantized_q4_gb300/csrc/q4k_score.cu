@@ -88,7 +88,8 @@ __device__ __forceinline__ float one(const T *p) {
 struct Sums {
   float c, l, w;
 };
-constexpr float kNoRef = -3.0e38f;
+// (A reference stays finite, so that a vector with an infinite logit lies above any.)
+constexpr float kNoRef = -3.0e38f, kMaxRef = 1e38f;
 __device__ __forceinline__ void join(Sums &a, const Sums &b) {
   const float c = fmaxf(a.c, b.c);
   // without a token l is 0, and its reference says nothing; beyond 2^-200 a part counts for nothing
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
     const float c = v * kLog2e;
     if (c > s.c + 12.f) {  // as below
       const float d = fmaxf(s.c - c, -200.f), f = ex2(d);
-      s.w = f * fmaf(d, s.l, s.w), s.l *= f, s.c = c;
+      s.w = f * fmaf(d, s.l, s.w), s.l *= f, s.c = fminf(c, kMaxRef);
     }
     // (not as 2^0 with a reference of its own: c's rounding is the same for all only where c is)
     const float z = fmaf(v, kLog2e, -s.c), e = ex2(z);
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
         const float2 f2 = make_float2(f, f);
         w2 = __fmul2_rn(f2, __ffma2_rn(make_float2(d, d), l2, w2));
         l2 = __fmul2_rn(f2, l2);
-        s.c = ct;
+        s.c = fminf(ct, kMaxRef);
       }
     }
     float v[8];

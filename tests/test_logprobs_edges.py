@@ -1,14 +1,17 @@
-"""Scores of rows whose tokens lie beside the aligned vectors, of logits far from zero.
+"""Scores of rows whose tokens lie beside the aligned vectors, of logits far from zero and next to the
+largest number.
 
 Tolerances: as in test_logprobs: a sum good to 2^-17 per 131072 logits, a logarithm and a difference that are rounded.
 """
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
 from _gpu import DEV
-from test_logprobs import check, q4k  # noqa: F401
+from test_logprobs import BF16, F32, check, q4k  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +27,22 @@ def test_tokens_beside_the_vectors_of_far_logits(q4k, vocab, offset, top, shift)
     x.copy_(torch.randint(-16, 1, (rows, vocab), generator=g) * 0.5 + shift)
     tokens = torch.randint(0, vocab, (rows,), generator=g, dtype=torch.int32)
     check(q4k.q4k_logprobs(x, tokens.to(DEV), top=top), x, tokens, top)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab", [40, 3000, 131072])
+def test_infinite_logits_behind_the_largest_finite_ones(q4k, dtype, vocab):  # noqa: F811
+    """A thread's tokens: i, i + 2048, ...: the largest numbers in its first vectors, infinities in later ones and in the
+    same one, beside masked tokens and NaN."""
+    x = torch.randn((5, vocab), generator=torch.Generator().manual_seed(1)).to(dtype)
+    large = torch.finfo(dtype).max
+    x[0, :vocab // 2] = large
+    x[0, -7:] = math.inf
+    x[1, 8:16], x[1, vocab - 3] = large, math.inf
+    x[2, 3], x[2, 4], x[2, -1] = large, math.inf, math.inf
+    x[3], x[3, vocab // 2:] = -large, large
+    x[3, 5], x[3, 1:9:2] = math.inf, math.nan
+    x[4], x[4, ::3] = large, -math.inf
+    x = x.to(DEV)
+    tokens = torch.tensor([vocab - 1, 9, 3, 5, 1], dtype=torch.int32)
+    check(q4k.q4k_logprobs(x, tokens.to(DEV), top=9), x, tokens, 9)
