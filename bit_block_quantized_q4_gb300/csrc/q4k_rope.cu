@@ -13,8 +13,9 @@
 // Angles.  At position 10^6 an fp32 product pos f_i is off by 0.06 radians.  So
 // f_i comes as f_i / 2 pi in units of 2^-64 of a turn, an integer: its product
 // with the position, modulo 2^64, is the fraction of a turn exactly, to the 2^-65
-// that the table's rounding leaves times the position.  Its upper 32 bits, signed,
-// are the angle in (-1/2, 1/2] turns.
+// that the table's rounding leaves times the position (the table is computed in twice
+// 64 bits: from doubles alone its values are up to 182 units off, 2^-25 of a turn at
+// position 2^31).  Its upper 32 bits, signed, are the angle in (-1/2, 1/2] turns.
 //
 // What bounds it: bytes, each read and written once; so rows stay in registers, and
 // all loads of a thread go out at its start.  D / 8 lanes take a row, and up to R
@@ -360,9 +361,49 @@ cudaError_t go_lanes(int pairs, const RopeArgs &r, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+// A number as the exact sum of two doubles, the second at most half a unit in the
+// last place of the first: about 104 bits.  (Dekker 1971, Knuth: the error of a sum or
+// a product of two doubles is a double.)
+struct Two {
+  double hi, lo;
+};
+Two two_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Two times(Two a, Two b) {
+  volatile const double rounded = a.hi * b.hi;  // (not fused with the sum below)
+  const double p = rounded;
+  return two_sum(p, fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+Two plus(Two a, Two b) {
+  const Two s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+Two over(Two a, double b) {  // the quotient, and what it leaves over b
+  const double q = a.hi / b;
+  return two_sum(q, (fma(-q, b, a.hi) + a.lo) / b);
+}
+// base^(-i / n) for 0 <= i < n: the root r of r^n base^i = 1 near pow's.  With e = r^n base^i - 1,
+// of n times pow's error, the root is r (1 - e / n) to e^2.  The factors alternate, so that
+// the product stays within a factor of base.
+Two root_of(double base, int i, int n) {
+  const double r = pow(base, -(double)i / n);
+  Two p = {1.0, 0.0};
+  for (int j = 0, k = 0; j < n; ++j) {
+    p = times(p, {r, 0.0});
+    for (; k * n < (j + 1) * i; ++k) p = times(p, {base, 0.0});
+  }
+  const Two e = over(plus(p, {-1.0, 0.0}), (double)n);
+  return times({r, 0.0}, plus({1.0, 0.0}, {-e.hi, -e.lo}));
+}
+}  // namespace
+
 bool rope_steps(int rot, double base, double factor, int64_t original, double beta_fast,
                 double beta_slow, const float *factors, uint64_t *steps, float *amplitude) {
   constexpr double kPi = 3.14159265358979323846;
+  constexpr Two kTurn = {0.15915494309189535, -9.839338337591243e-18};  // 1 / 2 pi
   const bool ramp = original > 0;
   double low = 0, high = 0;
   if (ramp) {
@@ -372,14 +413,19 @@ bool rope_steps(int rot, double base, double factor, int64_t original, double be
     high = fmin((double)rot - 1, ceil(at(beta_slow)));
   }
   for (int i = 0; i < rot / 2; ++i) {
-    double f = pow(base, -2.0 * i / rot) / (factors ? (double)factors[i] : 1.0);
-    const double keep = ramp ? 1.0 - fmin(1.0, fmax(0.0, (i - low) / fmax(0.001, high - low))) : 0.0;
-    f = f / factor * (1.0 - keep) + f * keep;
-    double turns = f / (2 * kPi);
-    if (!(turns - turns == 0.0)) return false;
-    turns = (turns - floor(turns)) * 18446744073709551616.0;
-    turns = nearbyint(turns);
-    steps[i] = turns >= 18446744073709551616.0 ? 0 : (uint64_t)turns;
+    // (in twice the bits: a position multiplies the table's error by up to 2^31)
+    Two f = over(root_of(base, i, rot / 2), factors ? (double)factors[i] : 1.0);
+    const Two slow = over(f, factor);
+    const double width = fmax(0.001, high - low), from = i - low;
+    if (!ramp || from >= width) f = slow;
+    else if (from > 0) f = plus(times(f, over({width - from, 0.0}, width)), times(slow, over({from, 0.0}, width)));
+    const Two turns = times(f, kTurn);
+    if (!(turns.hi - turns.hi == 0.0)) return false;
+    // modulo 1, in units of 2^-64: both parts without their whole turns, which come off exactly
+    const Two part = two_sum(turns.hi - floor(turns.hi), turns.lo - nearbyint(turns.lo));
+    const double upper = part.hi * 4294967296.0, whole = floor(upper);
+    const double lower = nearbyint(((upper - whole) + part.lo * 4294967296.0) * 4294967296.0);
+    steps[i] = ((uint64_t)(int64_t)whole << 32) + (uint64_t)(int64_t)lower;
   }
   *amplitude = ramp ? (float)(1.0 + 0.1 * log(factor)) : 1.f;
   return true;

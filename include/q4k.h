@@ -565,7 +565,8 @@ int q4k_kv_write(const void *k, const void *v, int in_dtype, int64_t ld_token, i
  *         pairs that turn more than beta_fast times over the `original` positions
  *         keep their frequency, those that turn less than beta_slow times are
  *         slowed by factor.
- *   steps      host, rot_dim / 2 values: f_i / 2 pi, modulo 1, in units of 2^-64;
+ *   steps      host, rot_dim / 2 values: f_i / 2 pi, modulo 1, in units of 2^-64, each
+ *              rounded once (frequencies up to 2^20 turns);
  *              the caller copies them to the device
  *   amplitude  host, one value: what the caller gives the calls as amplitude, 1 or
  *              (original > 0) 1 + 0.1 ln factor
@@ -584,7 +585,7 @@ int q4k_rope_steps(int32_t rot_dim, double base, double factor, int64_t original
  *     of the first rot_dim values, the pairs (a, b), a turning by the angle
  *     pos[t] f_i:  (a cos - b sin, b cos + a sin) * amplitude
  * in fp32, each value rounded once.  Pair i is (i, i + rot_dim / 2), or with
- * interleaved (2 i, 2 i + 1).  Angles are exact to 2^-32 of a turn at any
+ * interleaved (2 i, 2 i + 1).  Angles are exact to 2^-31 of a turn at any
  * position.  The other dim - rot_dim values are only normed.  (A part of a head
  * that does not begin it is a call on that part: x and y point at its first value,
  * dim is its length.)  A token with a negative position is left alone: its row of
