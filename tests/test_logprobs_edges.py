@@ -1,5 +1,5 @@
 """Scores of rows whose tokens lie beside the aligned vectors, of logits far from zero and next to the
-largest number.
+largest number, and of the largest vocabulary.
 
 Tolerances: as in test_logprobs: a sum good to 2^-17 per 131072 logits, a logarithm and a difference that are rounded.
 """
@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from _gpu import DEV
-from test_logprobs import BF16, F32, check, q4k  # noqa: F401
+from test_logprobs import BF16, F32, check, near, plain, q4k  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,17 @@ def test_infinite_logits_behind_the_largest_finite_ones(q4k, dtype, vocab):  # n
     x = x.to(DEV)
     tokens = torch.tensor([vocab - 1, 9, 3, 5, 1], dtype=torch.int32)
     check(q4k.q4k_logprobs(x, tokens.to(DEV), top=9), x, tokens, 9)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_the_largest_vocabulary(q4k, dtype):  # noqa: F811
+    vocab = 1 << 24
+    x = torch.randn((1, vocab), generator=torch.Generator().manual_seed(2)) * 3
+    x = x.to(dtype).to(DEV)
+    x[0, 5::7] = -math.inf
+    tokens = torch.tensor([vocab - 1], dtype=torch.int32)
+    got, want = q4k.q4k_logprobs(x, tokens.to(DEV), top=32), plain(x, tokens, 32)
+    assert torch.equal(got[1].cpu().long(), want[1]) and torch.equal(got[3].cpu().long(), want[3])
+    # each of two sums of a thread has 2^24 / 8 / 256 / 2 terms one after the other: 2^12 times 2^-24
+    near(got[0], want[0], 2.0 ** -11)
+    near(got[4], want[4], 2.0 ** -11)
