@@ -19,7 +19,7 @@
 //
 // Products, both by tcgen05.mma with fp32 accumulators in tensor memory:
 //   S[128 rows, TILE keys] = Q K^T    (Q, K from shared memory)
-//   O[128 rows, D]        += P V      (P in tensor memory over S, V from shared memory)
+//   O[128 rows, D]        += P V      (P in tensor memory beside S, V from shared memory)
 //
 // Roles of a CTA's 16 warps, connected by mbarriers:
 //   0..3, 4..7  softmax of query tile 0 and 1: a thread owns a row of S
@@ -37,15 +37,25 @@
 // itself.  A CTA has at most two pieces of items that it shares with others; they
 // go to the workspace and a second launch joins them.
 //
-// What bounds it, measured.  A prompt of 8191 tokens, 64 / 8 heads x 128, bf16: 765 us,
-// 1438 TFLOP/s, 74% of the library product's rate; the tensor pipe is busy half of the
+// What bounds it, measured on replays of a graph (one call after another takes prompts and
+// windows 3 to 5% longer).  A prompt of 8191 tokens, 64 / 8 heads x 128, bf16: 750 to 770 us,
+// 1449 TFLOP/s, 74% of the library product's rate; the tensor pipe is busy half of the
 // time, and the softmax warps take longer for a tile than the products do.  4 chunks
-// of 2049 with a window of 4096, 24 / 4 x 256: 618 us, 62%, the tensor pipe busy 53% of the
+// of 2049 with a window of 4096, 24 / 4 x 256: 606 to 625 us, 62%, the tensor pipe busy 53% of the
 // time with tiles of 64 keys, the most that fit beside Q.  8 requests of up to 60000 tokens, 5
 // new ones each: 220 us, 92% of the copy rate.  e4m3, 60 requests of up to 16001 tokens,
-// three of them with 700 new ones: 880 us; the conversion's warps share the softmax's
+// three of them with 700 new ones: 914 us; the conversion's warps share the softmax's
 // instruction caches and pipes.  45 tokens behind 700: 21 to 22.5 us, a chain of lengths, table,
 // tile, products and the join.
+// The e4m3 kernels are sensitive to what stands beside their loops (of 120 KB): code that runs
+// once per item takes thousands of cycles for its instructions alone, and two such blocks
+// more in the softmax took a prompt at head size 64 from 1013 to 1318 us with the same
+// registers, warps without an instruction from 1.16 to 2.19 per issue.  So what is rare there
+// is kept short and rolled.
+//
+// Weights as one term.  A second bf16 term would double the products P V and the weights'
+// columns, and tensor memory is full at head size 128; the result is rounded to the same
+// 8 bits.  (The single-token kernel has two, its products cost nothing there.)
 // Tried: scores in halves of 64 columns (prompt 1157 us, not 1036: the shared score buffer
 // is free later); four more warps for e4m3 that convert V beside K (1375 us, not 1184);
 // two groups of softmax warps for the one query tile of head size 256, its key tiles in turn
@@ -92,7 +102,8 @@ struct Cfg {
   static constexpr int kMoreRegs = D == 256 ? 152 : 184;
   // Cost of an item's start and end, in key tiles, for the shares of the CTAs.  Measured on
   // an 8191-token prompt, bf16, head size 128: 1: 972 us, 2: 916, 4: 813, 5: 786, 6: 807,
-  // 8: 835; on 60 requests of e4m3, whose tiles cost more: 1: 929, 2: 926, 3: 922.
+  // 8: 835; on 60 requests of e4m3, whose tiles cost more: 1: 929, 2: 926, 3: 922.  (Head sizes
+  // 64 and 256 use what was measured at 128.)
   static constexpr int kItemCost = E4M3 ? 3 : 5;
   static constexpr int kParts = D / 64;               // 128-byte parts of a row
   static constexpr int kSide = kTile * D * 2;         // bytes of a tile of K or V
@@ -862,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pieces = 0;  // 16-token pieces that are absent
             for (unsigned w = need & ~have; w; w &= w - 1) {
               const int at16 = (__ffs(w) - 1) << (p.box_shift - 4);
-              pieces |= ((p.box_rows >> 4 == 32 ? 0u : 1u << (p.box_rows >> 4)) - 1u) << at16;
+              pieces |= ((1u << (p.box_rows >> 4)) - 1u) << at16;  // (a box has at most 128 rows)
             }
             if (values) v_absent[s] = pieces;
             else gone[tiles & 7] = pieces;

@@ -22,7 +22,8 @@
 // heads of the same token.  While the rows are on their way the block computes the
 // cosines and sines of its tokens, which are the same for all heads, into shared
 // memory: a thread one or a few.  Measured (of the copy rate): 8191 x 64 x 128 bf16 46 us
-// (87%), 8191 x 24 x 256 with 64 values rotated 47 us (64%), with the write of an e4m3
+// (87%), 8191 x 24 x 256 with 64 values rotated 47 us (64%; its tokens take 3 of a block's 8
+// groups of lanes each, so that a quarter of the warps have no rows), with the write of an e4m3
 // cache 8191 x (64 + 16) x 128 78 us (61%), there with issue slots 65% busy; 16 x 64 heads
 // 4.2 us, a launch and two dependent loads.
 //
