@@ -716,8 +716,9 @@ int q4k_paged_attn(const void *q, int64_t ldq, int64_t ldq_head, int32_t n, int3
  * below; and its values enter as fp16 times their scales, which are rounded to fp16
  * times a power of two per 64 or 128 tokens, or of tokens that not all of a block's
  * rows see one of its own: two roundings to 11 bits, for scales down to 2^-20 of
- * the largest that the token sees of them (of 2^-74, where that is less, as for rows
- * of zeros), and below that an error of at most 2^-31 of 448 times that scale.
+ * the largest that the token sees of them (of 2^-74, or of 2^-90 of one that it saw
+ * before, where that is less, as for rows of zeros), and below that an error of at
+ * most 2^-31 of 448 times that scale.
  * Values that are not finite in a row that a token sees show in the token's
  * result; one of V may do so as NaN in all of it.
  *   q       device, bf16, element (t, h, d) at t * ldq + h * ldq_head + d;
